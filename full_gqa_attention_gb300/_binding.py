@@ -34,6 +34,9 @@ SPARK_NOALLOC_SCRATCH_BYTES = 8 << 20
 
 SPARK_DEVERR_POSITION = 0x1
 SPARK_DEVERR_TIMEOUT = 0x2
+SPARK_DEVERR_SEQLENS = 0x4
+SPARK_DEVERR_PAGE = 0x8
+SPARK_DEVERR_ROW = 0x10
 
 
 class spark_layer_desc(ctypes.Structure):

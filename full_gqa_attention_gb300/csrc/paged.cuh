@@ -1,0 +1,43 @@
+// paged.cuh -- launch parameters and helpers of the packed and paged
+// attention calls.
+#pragma once
+
+#include "common.cuh"
+
+namespace spark {
+
+constexpr unsigned kErrSeqlens = 0x4u;  // SPARK_DEVERR_SEQLENS
+constexpr unsigned kErrPage = 0x8u;     // SPARK_DEVERR_PAGE
+
+struct PagedParams {
+    const __nv_bfloat16 *qkv;  // [N, (H+2Hkv)*256]
+    const float *gate;         // [N, H]
+    const int32_t *pos;        // [N] (decode: [B], -1 idle)
+    const int32_t *cu;         // [S + 1] (prompts)
+    const int32_t *start;      // [S]: tokens in the pages (paged prompts)
+    __nv_bfloat16 *k_pages;    // [n_pages, Hkv, page, 256]; nullptr: no cache
+    __nv_bfloat16 *v_pages;
+    const int32_t *table;      // [rows, max_pages]
+    __nv_bfloat16 *out;        // [N, H*256]
+    unsigned *status;
+    int N, S, H, Hkv, G;
+    int kind, window, gate_mode;
+    int n_pages, page_shift, max_pages;
+    RopeTable rope;
+};
+
+// The sequence whose tokens [cu[s], cu[s+1]) hold `row`, or -1 (padding, or
+// offsets that are no prefix sum).
+__device__ __forceinline__ int find_sequence(const int32_t *cu, int S, int row) {
+    int lo = 0, hi = S;  // the last s with cu[s] <= row lies in [lo, hi]
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= row)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return (lo < S && cu[lo] <= row && row < cu[lo + 1]) ? lo : -1;
+}
+
+}  // namespace spark

@@ -228,6 +228,23 @@ spark_status check_prefill(int B, int T, int H, int Hkv, const spark_layer_desc 
 
 }  // namespace
 
+// For the entry points of the other files: whether the current device is one
+// the kernels are built for, and its SM count.
+spark_status device_ready(int *sms) {
+    const spark_status st = check_device();
+    *sms = sm_count_or_default();
+    return st;
+}
+
+spark_status check_layer_desc(const spark_layer_desc *d, int H, int Hkv) {
+    return check_layer(d, H, Hkv);
+}
+
+bool encode_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box) {
+    return encode_bf16(map, base, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // Prefill, optionally filling the decode cache (k_cache != nullptr), or a
 // chunked prefill over a cache that already holds start[b] tokens.  With
 // validate_only, returns after the host-side checks and enqueues nothing.

@@ -101,6 +101,13 @@ typedef struct spark_layer_desc {
 #define SPARK_DEVERR_POSITION 0x1u /* a decode position was negative or >= cap (FULL);
                                       that sequence was skipped */
 #define SPARK_DEVERR_TIMEOUT 0x2u  /* a bounded on-chip wait ran out; results are invalid */
+#define SPARK_DEVERR_SEQLENS 0x4u  /* packed offsets that decrease or leave [0, n_tokens];
+                                      the sequences next to them were skipped */
+#define SPARK_DEVERR_PAGE 0x8u     /* a page number outside the pool was met: read as zeros,
+                                      never written */
+#define SPARK_DEVERR_ROW 0x10u     /* a page operation named a row that does not exist, forked
+                                      into a row that holds pages, or found counts (held, len)
+                                      that do not fit the table; that row was skipped */
 
 /*
  * Prefill: attention of T new tokens per sequence over themselves.
@@ -355,6 +362,169 @@ spark_status spark_attn_layer_decode(const void *x, const void *w_qkv, const voi
  */
 spark_status spark_attn_linear(const void *x, const void *w, void *y, int64_t M, int N, int K,
                                uint32_t *device_status, void *stream);
+
+/*
+ * Packed prompts and a cache in pages.
+ *
+ * A serving step holds prompts of different lengths: they lie behind one
+ * another, without padding, and cu_seqlens says where each begins.  Its cache
+ * is a pool of fixed-size pages, and a table maps the tokens of a sequence to
+ * them: token j of row r is slot j % page_size of page
+ * page_table[r][j / page_size].  Sequences that begin alike can share pages
+ * (spark_attn_pages_fork).
+ *
+ *   cu_seqlens  int32 [S + 1] (device): sequence s is the tokens
+ *               cu_seqlens[s] .. cu_seqlens[s + 1] - 1; offsets may not
+ *               decrease and lie in [0, n_tokens].  A sequence may be empty
+ *               (an idle row).  Tokens outside every sequence (the padding of
+ *               a step captured into a graph) are not read into any result,
+ *               and their rows of out stay as they were.
+ *   k_pages, v_pages  bf16 [n_pages, Hkv, page_size, 256], one layer's pool;
+ *               page_size 16, 32, 64, 128 or 256 (else SPARK_ERR_UNSUPPORTED).
+ *   page_table  int32 [rows, max_pages] (device).  Entries that hold no token
+ *               a call reads or writes may be anything (-1, say), among them
+ *               those wholly behind the window of a SLIDING layer.  A page
+ *               that is written must belong to one row alone; pages that are
+ *               only read may be shared.
+ * Keys in pages are rotated, as in the other caches.  Both layer kinds use
+ * the same addressing: a SLIDING layer's old pages can be given back, but its
+ * slots do not wrap.
+ *
+ * A value that is not finite in a place the mask hides (a later token of the
+ * same sequence, one behind the window, another sequence, a slot that no
+ * token has been written to) does not reach any output.
+ */
+
+/*
+ * Prompts in one call, no cache: what spark_attn_prefill computes, for every
+ * sequence of a packed batch on its own.
+ *
+ *   qkv   bf16 [n_tokens, (H + 2*Hkv) * 256]
+ *   gate  fp32 [n_tokens, H]
+ *   pos   int32 [n_tokens]                   RoPE positions, 0 <= pos < 2^24
+ *   out   bf16 [n_tokens, H * 256]
+ *   workspace  >= the size query's bytes, 256-byte aligned, zeroed once
+ *         before first use; calls that may overlap need one each
+ * The mask is applied on the token index inside the sequence.
+ */
+size_t spark_attn_prefill_packed_workspace_size(int n_tokens, int S, int H, int Hkv,
+                                                const spark_layer_desc *desc);
+
+spark_status spark_attn_prefill_packed(const void *qkv, const float *gate, const int32_t *pos,
+                                       const int32_t *cu_seqlens, const spark_layer_desc *desc,
+                                       int n_tokens, int S, int H, int Hkv, void *out,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Prompts, or chunks of them, on top of what their pages hold: token t of
+ * sequence s sits at index start[s] + t.  Its rotated key and its value are
+ * stored in the sequence's pages, then it attends to every earlier token of
+ * its sequence, cached ones included, under the layer's mask on those
+ * indices.  spark_attn_decode_paged at pos = start[s] + length continues the
+ * sequence.
+ *
+ *   start  int32 [S] (device): tokens in the row's pages before the call.  A
+ *          sequence with start < 0 or start + length > max_pages * page_size
+ *          is skipped and SPARK_DEVERR_POSITION set.
+ *   Other arguments as for spark_attn_prefill_packed.
+ */
+size_t spark_attn_prefill_paged_workspace_size(int n_tokens, int S, int H, int Hkv,
+                                               const spark_layer_desc *desc);
+
+spark_status spark_attn_prefill_paged(const void *qkv, const float *gate, const int32_t *pos,
+                                      const int32_t *cu_seqlens, const int32_t *start,
+                                      void *k_pages, void *v_pages, int n_pages, int page_size,
+                                      const int32_t *page_table, int max_pages,
+                                      const spark_layer_desc *desc, int n_tokens, int S, int H,
+                                      int Hkv, void *out, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/*
+ * One new token per row over its pages: what spark_attn_decode computes.
+ *
+ *   qkv   bf16 [B, (H + 2*Hkv) * 256]
+ *   gate  fp32 [B, H]
+ *   pos   int32 [B]: position of the new token = tokens cached; -1 marks an
+ *         idle row (nothing is read, its row of out stays as it was).  Other
+ *         negative positions and pos >= max_pages * page_size: the row is
+ *         skipped and SPARK_DEVERR_POSITION set.
+ *   out   bf16 [B, H * 256]
+ *   workspace  >= the size query's bytes, 256-byte aligned, zeroed once
+ *         before first use (its counters are left at 0 by every call); calls
+ *         that may overlap need one each
+ * The work is split by what the positions ask for, not by max_pages: a call
+ * captured into a graph serves every later length.
+ */
+size_t spark_attn_decode_paged_workspace_size(int B, int H, int Hkv, const spark_layer_desc *desc);
+
+spark_status spark_attn_decode_paged(const void *qkv, const float *gate, const int32_t *pos,
+                                     void *k_pages, void *v_pages, int n_pages, int page_size,
+                                     const int32_t *page_table, int max_pages,
+                                     const spark_layer_desc *desc, int B, int H, int Hkv,
+                                     void *out, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/*
+ * The pool behind the page tables: which row holds which page.  All layers
+ * share one table, so a page is the same slots of every layer.  Every array
+ * is on the device and the caller's; a fresh pool has table -1 and held, len
+ * and refs 0.  A page is free when refs is 0.
+ */
+typedef struct spark_page_pool {
+    void *k_pages, *v_pages;  /* bf16 [n_layers, n_pages, Hkv, page_size, 256] */
+    int32_t *table;           /* [n_rows, max_pages]: the pages of a row, -1 behind them */
+    int32_t *held;            /* [n_rows]: pages of the row */
+    int32_t *len;             /* [n_rows]: tokens cached; the caller adds to it after a step */
+    int32_t *refs;            /* [n_pages]: rows that hold the page */
+    int32_t n_layers, Hkv, n_pages, page_size, n_rows, max_pages;
+} spark_page_pool;
+
+/*
+ * Page operations.  Everything is read and written on the device, in stream
+ * order, so a step of a captured graph can make them; results do not depend
+ * on timing.  workspace: >= the size query's bytes, 256-byte aligned, zeroed
+ * once before first use; its status word is read with spark_attn_read_status.
+ *
+ * fork: row dst[i] becomes a copy of row src[i] that shares its pages (those
+ * of its len tokens), for n pairs.  All pairs read the rows as they were
+ * before the call.  dst[i] must hold no pages; where it does, where a row does
+ * not exist, or where an earlier pair has the same dst, the pair is skipped
+ * and SPARK_DEVERR_ROW set.
+ *
+ * reserve: makes room for add[r] more tokens behind the len[r] of every row r
+ * (add int32 [n_rows]; 0 or less: nothing; a row that would outgrow max_pages
+ * is left out and SPARK_DEVERR_ROW set).  If the row's last page holds tokens
+ * and is shared, the row gets a copy of its own, in every layer: of the rows
+ * of one call that are about to write into the same page each makes a copy,
+ * in row order, until one holder is left.  Pages are taken from the lowest
+ * free number up, rows in order, in each row the copy first.  len stays.
+ * taken: optional int32 [1]: pages taken, or -1 when the pool has too few --
+ * then nothing has changed.
+ *
+ * free: row rows[i] (n of them) keeps its first keep[i] tokens, or none where
+ * keep is NULL; pages behind them are given back and their entries set to -1.
+ * A row named twice counts once, as its first mention says.
+ *
+ * compact: the pages in use move to the lowest numbers: of n_live pages in
+ * use the i-th that has a number >= n_live goes to the i-th free one below,
+ * in every layer, and the tables follow.  live: optional int32 [1]: n_live.
+ */
+size_t spark_attn_pages_workspace_size(const spark_page_pool *pool);
+
+spark_status spark_attn_pages_fork(const spark_page_pool *pool, const int32_t *src,
+                                   const int32_t *dst, int n, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+spark_status spark_attn_pages_reserve(const spark_page_pool *pool, const int32_t *add,
+                                      int32_t *taken, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+spark_status spark_attn_pages_free(const spark_page_pool *pool, const int32_t *rows,
+                                   const int32_t *keep, int n, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+spark_status spark_attn_pages_compact(const spark_page_pool *pool, int32_t *live, void *workspace,
+                                      size_t workspace_bytes, void *stream);
 
 /*
  * Copies the sticky device status word out of a workspace (synchronizes on
