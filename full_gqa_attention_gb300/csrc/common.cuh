@@ -113,6 +113,19 @@ inline bool decode_fuses_merge(int nsplit, long long B_times_Hkv, bool have_coun
 
 // ---------------------------------------------------------------- prefill
 
+// What a packed prefill adds: sequences behind one another (B = 1, T = all
+// tokens in PrefillParams), and a list of query tiles that the kernel before
+// the attention kernel made of their offsets, longest first.
+struct PackedInfo {
+    const int32_t *cu;         // [S + 1] first token of each sequence
+    const int2 *work;          // query tiles: (sequence, first token inside it)
+    const int32_t *n_work;     // their number
+    int sure;                  // items below this are there in any case (nearly always)
+    const int32_t *table;      // [S, max_pages] (paged prompts)
+    int n_pages, page_shift, max_pages;
+    __nv_bfloat16 *out;        // [N, H*256]: ragged tiles are stored row by row
+};
+
 struct PrefillParams {
     const __nv_bfloat16 *qkv;  // [B, T, (H+2Hkv)*256]
     const float *gate;         // [B, T, H]
@@ -134,6 +147,7 @@ struct PrefillParams {
     int defer_wait;            // nonzero: a library kernel of the same call runs just
                                // before the attention kernel, so only the key/value
                                // loads wait for it (inputs are complete already)
+    PackedInfo pk;             // packed prefill only
     RopeTable rope;
 };
 

@@ -10,60 +10,194 @@ namespace spark {
 void fill_rope_table(const spark_layer_desc *d, RopeTable *t);
 spark_status device_ready(int *sms);
 spark_status check_layer_desc(const spark_layer_desc *d, int H, int Hkv);
+bool encode_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box);
+cudaError_t launch_prefill_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_kv_k,
+                                  const CUtensorMap &tm_kv_v, const CUtensorMap &tm_krot,
+                                  const CUtensorMap &tm_out, const PrefillParams &P,
+                                  long long items, cudaStream_t stream);
 
 namespace {
 
-constexpr int kStoreThreads = 256;
+constexpr int kPrepThreads = 256;
+constexpr int kBins = 1024;           // query tiles are sorted by their key tiles, up to this many
 
-// Stores the new tokens' rotated keys and their values in the pages.  One
-// thread per (token, group of 8 rotated pairs / 8 copied key dims / 8 value
-// dims), looping over the KV heads.
+// Exclusive prefix sum of one value per thread over the block, and the total.
+__device__ __forceinline__ int prep_scan(int v, int *total) {
+    __shared__ int sums[kPrepThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    __syncthreads();  // the sums of the scan before are read
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+    }
+    *total = all;
+    return before + x - v;
+}
+
+// The list of query tiles, made by one CTA: every sequence is cut into tiles
+// of tq tokens, and the tiles are put in order of the key tiles they visit,
+// most first (a counting sort), so that the long ones do not start last.  The
+// order inside a bin is whatever the atomics give; no result depends on it.
+__device__ __forceinline__ void plan_tiles(const PagedParams &P) {
+    __shared__ int bins[kBins];
+    const int tid = threadIdx.x, tq = 128 / P.G;
+    const long long cap = static_cast<long long>(P.max_pages) << P.page_shift;
+    for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
+    int base = 0;
+    for (int s0 = 0; s0 < P.S; s0 += kPrepThreads) {
+        const int s = s0 + tid;
+        int n = 0;
+        if (s < P.S) {
+            const int a = P.cu[s], b = P.cu[s + 1];
+            if (a < 0 || a > b || b > P.N) {
+                atomicOr(P.status, kErrSeqlens);
+            } else if (b > a) {
+                const long long st = P.start ? P.start[s] : 0;
+                if (st < 0 || (P.start && st + (b - a) > cap))
+                    atomicOr(P.status, kErrPosition);
+                else
+                    n = (b - a + tq - 1) / tq;
+            }
+        }
+        int total;
+        const int at = prep_scan(n, &total);
+        if (s < P.S) P.tile_base[s] = base + at;
+        base += total;
+    }
+    // offsets that overlap can ask for more tiles than the list holds
+    const int most = P.N / tq + (P.S < P.N ? P.S : P.N);
+    const int n_tiles = base < most ? base : most;
+    if (tid == 0) {
+        P.tile_base[P.S] = base;
+        *P.n_work = n_tiles;
+    }
+    __syncthreads();
+    for (int i = tid; i < n_tiles; i += kPrepThreads) {
+        int lo = 0, hi = P.S - 1;  // the last s with tile_base[s] <= i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (P.tile_base[mid] <= i)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int t0 = (i - P.tile_base[lo]) * tq;
+        const int len = P.cu[lo + 1] - P.cu[lo], st = P.start ? P.start[lo] : 0;
+        const KeyTiles kt = prefill_key_tiles(P.kind, P.window, st + t0,
+                                              st + (t0 + tq < len ? t0 + tq : len), 128,
+                                              P.start != nullptr);
+        const int bin = kBins - 1 - (kt.ntiles < kBins ? kt.ntiles : kBins - 1);
+        P.tiles[i] = make_int4(lo, t0, bin, 0);
+        atomicAdd(&bins[bin], 1);
+    }
+    __syncthreads();
+    constexpr int kPer = kBins / kPrepThreads;
+    int count[kPer], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        count[i] = bins[tid * kPer + i];
+        sum += count[i];
+    }
+    int at = prep_scan(sum, &total);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        bins[tid * kPer + i] = at;
+        at += count[i];
+    }
+    __syncthreads();
+    for (int i = tid; i < n_tiles; i += kPrepThreads) {
+        const int4 t = P.tiles[i];
+        P.work[atomicAdd(&bins[t.z], 1)] = make_int2(t.x, t.y);
+    }
+}
+
+// Whether the token of `row` has a place in the pages; where.
 template <bool kDecode>
-__global__ void __launch_bounds__(kStoreThreads) paged_store_kernel(
-    const __grid_constant__ PagedParams P) {
-    grid_dep_wait();
-    grid_dep_launch();
-    const int r = P.rope.rot_dim, half = r / 2;
-    const int n_rot = half / 8, n_kcopy = (kHeadDim - r) / 8, n_v = kHeadDim / 8;
-    const int items = n_rot + n_kcopy + n_v;
-    const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int row = static_cast<int>(idx / items);
-    const int it = static_cast<int>(idx % items);
-    if (row >= P.N) return;
+__device__ __forceinline__ bool token_slot(const PagedParams &P, int row, bool report,
+                                           size_t &base) {
     const long long cap = static_cast<long long>(P.max_pages) << P.page_shift;
     long long a;  // index in the sequence
     int seq;
     if (kDecode) {
         seq = row;
         a = P.pos[row];
-        if (a == -1) return;
+        if (a == -1) return false;
         if (a < 0 || a >= cap) {
-            if (it == 0) atomicOr(P.status, kErrPosition);
-            return;
+            if (report) atomicOr(P.status, kErrPosition);
+            return false;
         }
     } else {
         seq = find_sequence(P.cu, P.S, row);
-        if (seq < 0) return;
+        if (seq < 0) return false;
         const int t0 = P.cu[seq], t1 = P.cu[seq + 1];
-        if (t0 < 0 || t1 > P.N) return;
         const long long st = P.start[seq];
-        if (st < 0 || st + (t1 - t0) > cap) {
-            if (it == 0) atomicOr(P.status, kErrPosition);
-            return;
-        }
+        if (t0 < 0 || t1 > P.N || st < 0 || st + (t1 - t0) > cap) return false;  // the plan reports
         a = st + (row - t0);
     }
     const int page = P.table[static_cast<size_t>(seq) * P.max_pages + (a >> P.page_shift)];
     if (page < 0 || page >= P.n_pages) {
-        if (it == 0) atomicOr(P.status, kErrPage);
-        return;
+        if (report) atomicOr(P.status, kErrPage);
+        return false;
+    }
+    base = ((static_cast<size_t>(page) * P.Hkv << P.page_shift) +
+            static_cast<size_t>(a & ((1 << P.page_shift) - 1))) * kHeadDim;
+    return true;
+}
+
+// What the attention kernel needs of the new keys and values.  Paged: every
+// token's rotated key and its value go to its pages.  Packed: the leading
+// rot_w dims of every key, rotated, go to the workspace (the others are read
+// where they are).  One thread per (token, group of 8 rotated pairs / 8 copied
+// key dims / 8 value dims), looping over the KV heads so that each angle is
+// computed once.  Of a prompt's grid the first CTA makes the list of query
+// tiles instead.
+template <bool kDecode>
+__global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
+    const __grid_constant__ PagedParams P) {
+    grid_dep_wait();
+    grid_dep_launch();
+    int block = blockIdx.x;
+    if (!kDecode) {
+        if (block == 0) {
+            plan_tiles(P);
+            return;
+        }
+        --block;
+    }
+    const bool paged = P.k_pages != nullptr;
+    const int r = P.rope.rot_dim, half = r / 2;
+    const int n_rot = half / 8, n_kcopy = ((paged ? kHeadDim : P.rot_w) - r) / 8;
+    const int items = n_rot + n_kcopy + (paged ? kHeadDim / 8 : 0);
+    const long long idx = static_cast<long long>(block) * blockDim.x + threadIdx.x;
+    const long long row_l = idx / items;
+    if (row_l >= P.N) return;
+    const int row = static_cast<int>(row_l), it = static_cast<int>(idx % items);
+    __nv_bfloat16 *dst_k, *dst_v = nullptr;
+    size_t head_stride;
+    if (paged) {
+        size_t base;
+        if (!token_slot<kDecode>(P, row, it == 0, base)) return;
+        dst_k = P.k_pages + base;
+        dst_v = P.v_pages + base;
+        head_stride = static_cast<size_t>(kHeadDim) << P.page_shift;
+    } else {
+        dst_k = P.krot + static_cast<size_t>(row) * P.rot_w;
+        head_stride = static_cast<size_t>(P.N) * P.rot_w;
     }
     const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
     const __nv_bfloat16 *src_k = P.qkv + row * width + static_cast<size_t>(P.H) * kHeadDim;
     const __nv_bfloat16 *src_v = src_k + static_cast<size_t>(P.Hkv) * kHeadDim;
-    const size_t head_stride = static_cast<size_t>(kHeadDim) << P.page_shift;
-    const size_t slot = static_cast<size_t>(a & ((1 << P.page_shift) - 1));
-    const size_t base = page * (head_stride * P.Hkv) + slot * kHeadDim;
     if (it < n_rot) {
         const int k0 = it * 8;
         const int p = P.pos[row];
@@ -84,24 +218,24 @@ __global__ void __launch_bounds__(kStoreThreads) paged_store_kernel(
                 ya[i] = pack_bf16x2(y1l, y1h);
                 yb[i] = pack_bf16x2(y2l, y2h);
             }
-            __nv_bfloat16 *dst = P.k_pages + base + g * head_stride;
+            __nv_bfloat16 *dst = dst_k + g * head_stride;
             *reinterpret_cast<uint4 *>(dst + k0) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
             *reinterpret_cast<uint4 *>(dst + k0 + half) = make_uint4(yb[0], yb[1], yb[2], yb[3]);
         }
     } else if (it < n_rot + n_kcopy) {
         const int d0 = r + (it - n_rot) * 8;
         for (int g = 0; g < P.Hkv; ++g)
-            *reinterpret_cast<uint4 *>(P.k_pages + base + g * head_stride + d0) =
+            *reinterpret_cast<uint4 *>(dst_k + g * head_stride + d0) =
                 *reinterpret_cast<const uint4 *>(src_k + g * kHeadDim + d0);
     } else {
         const int d0 = (it - n_rot - n_kcopy) * 8;
         for (int g = 0; g < P.Hkv; ++g)
-            *reinterpret_cast<uint4 *>(P.v_pages + base + g * head_stride + d0) =
+            *reinterpret_cast<uint4 *>(dst_v + g * head_stride + d0) =
                 *reinterpret_cast<const uint4 *>(src_v + g * kHeadDim + d0);
     }
 }
 
-// The plain attention of every row: one warp per (token, query head), lane l
+// The plain attention of a decode step: one warp per (row, query head), lane l
 // holding dims 8l..8l+7, keys one after another with an online softmax.
 constexpr int kRowWarps = 8;
 
@@ -135,40 +269,18 @@ __device__ __forceinline__ void rotate_lane(float (&x)[8], int pos, const RopeTa
     }
 }
 
-template <bool kDecode>
 __global__ void __launch_bounds__(kRowWarps * 32) rows_attn_kernel(
     const __grid_constant__ PagedParams P) {
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31;
-    if (!kDecode && blockIdx.x == 0)
-        for (int i = threadIdx.x; i < P.S; i += kRowWarps * 32)
-            if (P.cu[i] < 0 || P.cu[i] > P.cu[i + 1] || P.cu[i + 1] > P.N)
-                atomicOr(P.status, kErrSeqlens);
     const long long w = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
     const int row = static_cast<int>(w / P.H), h = static_cast<int>(w % P.H);
     if (row >= P.N) return;
     const int g = h / P.G;
-    int seq, t0 = 0;
-    long long at;
     const long long cap = static_cast<long long>(P.max_pages) << P.page_shift;
-    if (kDecode) {
-        seq = row;
-        at = P.pos[row];
-        if (at < 0 || at >= cap) return;
-    } else {
-        seq = find_sequence(P.cu, P.S, row);
-        if (seq < 0) return;
-        t0 = P.cu[seq];
-        const int t1 = P.cu[seq + 1];
-        if (t0 < 0 || t1 > P.N) {
-            if (lane == 0 && h == 0) atomicOr(P.status, kErrSeqlens);
-            return;
-        }
-        const long long st = P.start ? P.start[seq] : 0;
-        if (st < 0 || (P.k_pages && st + (t1 - t0) > cap)) return;
-        at = st + (row - t0);
-    }
+    const long long at = P.pos[row];
+    if (at < 0 || at >= cap) return;
     const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
     float q[8], o[8], k[8], v[8];
     unpack8(*reinterpret_cast<const uint4 *>(P.qkv + row * width + h * kHeadDim + lane * 8), q);
@@ -178,22 +290,15 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_attn_kernel(
     for (int i = 0; i < 8; ++i) o[i] = 0.f;
     long long j = P.kind == kLayerSliding ? at - P.window + 1 : 0;
     for (j = j > 0 ? j : 0; j <= at; ++j) {
-        if (P.k_pages) {
-            const int page = P.table[static_cast<size_t>(seq) * P.max_pages + (j >> P.page_shift)];
-            if (page < 0 || page >= P.n_pages) {
-                if (lane == 0) atomicOr(P.status, kErrPage);
-                continue;
-            }
-            const size_t off = ((static_cast<size_t>(page) * P.Hkv + g) << P.page_shift) * kHeadDim +
-                               (j & ((1 << P.page_shift) - 1)) * kHeadDim + lane * 8;
-            unpack8(*reinterpret_cast<const uint4 *>(P.k_pages + off), k);
-            unpack8(*reinterpret_cast<const uint4 *>(P.v_pages + off), v);
-        } else {
-            const __nv_bfloat16 *src = P.qkv + (t0 + j) * width + (P.H + g) * kHeadDim + lane * 8;
-            unpack8(*reinterpret_cast<const uint4 *>(src), k);
-            unpack8(*reinterpret_cast<const uint4 *>(src + P.Hkv * kHeadDim), v);
-            if (P.rope.rot_dim > 0) rotate_lane(k, P.pos[t0 + j], P.rope, lane);
+        const int page = P.table[static_cast<size_t>(row) * P.max_pages + (j >> P.page_shift)];
+        if (page < 0 || page >= P.n_pages) {
+            if (lane == 0) atomicOr(P.status, kErrPage);
+            continue;
         }
+        const size_t off = ((static_cast<size_t>(page) * P.Hkv + g) << P.page_shift) * kHeadDim +
+                           (j & ((1 << P.page_shift) - 1)) * kHeadDim + lane * 8;
+        unpack8(*reinterpret_cast<const uint4 *>(P.k_pages + off), k);
+        unpack8(*reinterpret_cast<const uint4 *>(P.v_pages + off), v);
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) s = fmaf(q[i], k[i], s);
@@ -283,24 +388,128 @@ spark_status done(cudaError_t e) {
 }
 
 template <bool kDecode>
+spark_status launch_prep(const PagedParams &P, cudaStream_t s) {
+    const int r = P.rope.rot_dim;
+    const long long items =
+        r / 16 + ((P.k_pages ? kHeadDim : P.rot_w) - r) / 8 + (P.k_pages ? kHeadDim / 8 : 0);
+    const long long blocks = (P.N * items + kPrepThreads - 1) / kPrepThreads + (kDecode ? 0 : 1);
+    return done(launch_overlapped(paged_prep_kernel<kDecode>, dim3(static_cast<unsigned>(blocks)),
+                                  dim3(kPrepThreads), 0, s, P));
+}
+
 spark_status launch_rows(const PagedParams &P, cudaStream_t s) {
-    if (P.k_pages) {
-        const int r = P.rope.rot_dim;
-        const long long items = r / 16 + (kHeadDim - r) / 8 + kHeadDim / 8;
-        const long long blocks = (P.N * items + kStoreThreads - 1) / kStoreThreads;
-        const spark_status st =
-            done(launch_overlapped(paged_store_kernel<kDecode>, dim3(static_cast<unsigned>(blocks)),
-                                   dim3(kStoreThreads), 0, s, P));
-        if (st != SPARK_OK) return st;
-    }
+    const spark_status st = launch_prep<true>(P, s);
+    if (st != SPARK_OK) return st;
     const long long warps = static_cast<long long>(P.N) * P.H;
-    return done(launch_overlapped(rows_attn_kernel<kDecode>,
+    return done(launch_overlapped(rows_attn_kernel,
                                   dim3(static_cast<unsigned>((warps + kRowWarps - 1) / kRowWarps)),
                                   dim3(kRowWarps * 32), 0, s, P));
 }
 
-size_t packed_workspace(int, int, int, int, const spark_layer_desc *, bool) {
-    return kWorkspaceHeader;
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace of a packed or paged prefill: the status header, the query tiles,
+// and (packed) the rotated leading key dims.
+struct PackedPlan {
+    long long most;  // query tiles at most: full ones, and a ragged one per sequence
+    int rot_w;
+    size_t n_work, base, tiles, work, krot, bytes;
+};
+
+PackedPlan plan_packed(int N, int S, int H, int Hkv, const spark_layer_desc *desc, bool paged) {
+    PackedPlan pl{};
+    const int tq = 128 / (H / Hkv);
+    pl.most = static_cast<long long>(N / tq) + (S < N ? S : N);
+    pl.rot_w = paged ? 0 : (desc->rot_dim + 63) / 64 * 64;
+    pl.n_work = kWorkspaceHeader;
+    pl.base = pl.n_work + 256;
+    pl.tiles = pl.base + up256((static_cast<size_t>(S) + 1) * 4);
+    pl.work = pl.tiles + up256(static_cast<size_t>(pl.most) * sizeof(int4));
+    pl.krot = pl.work + up256(static_cast<size_t>(pl.most) * sizeof(int2));
+    pl.bytes = pl.krot + up256(static_cast<size_t>(N) * Hkv * pl.rot_w * 2);
+    return pl;
+}
+
+size_t packed_workspace(int N, int S, int H, int Hkv, const spark_layer_desc *desc, bool paged) {
+    return plan_packed(N, S, H, Hkv, desc, paged).bytes;
+}
+
+// The attention kernel's launch: its parameters and tensor maps.
+spark_status launch_packed_attn(const PagedParams &P, const PackedPlan &pl, int sms, cudaStream_t stream) {
+    const bool paged = P.k_pages != nullptr;
+    const int tq = 128 / P.G;
+    PrefillParams A;
+    std::memset(&A, 0, sizeof(A));
+    A.qkv = P.qkv;
+    A.gate = P.gate;
+    A.pos = P.pos;
+    A.v_cache = P.v_pages;
+    A.start = P.start;
+    A.status = P.status;
+    A.B = 1;
+    A.T = P.N;
+    A.H = P.H;
+    A.Hkv = P.Hkv;
+    A.G = P.G;
+    A.kind = P.kind;
+    A.window = P.window;
+    A.gate_mode = P.gate_mode;
+    A.rot_w = pl.rot_w;
+    A.wave = sms;
+    A.pk.cu = P.cu;
+    A.pk.work = P.work;
+    A.pk.n_work = P.n_work;
+    A.pk.sure = P.N / tq;
+    A.pk.table = P.table;
+    A.pk.n_pages = P.n_pages;
+    A.pk.page_shift = P.page_shift;
+    A.pk.max_pages = P.max_pages;
+    A.pk.out = P.out;
+    A.rope = P.rope;
+
+    const uint64_t heads = static_cast<uint64_t>(P.H + 2 * P.Hkv), N = P.N;
+    CUtensorMap tm_q, tm_k, tm_v, tm_krot, tm_out;
+    std::memset(&tm_krot, 0, sizeof(tm_krot));
+    {
+        // qkv as [1][N][heads][256]
+        const uint64_t dims[4] = {kHeadDim, heads, N, 1};
+        const uint64_t strides[3] = {kHeadDim * 2ull, heads * kHeadDim * 2ull,
+                                     N * heads * kHeadDim * 2ull};
+        const uint32_t box_q[4] = {64, static_cast<uint32_t>(P.G), static_cast<uint32_t>(tq), 1};
+        const uint32_t box_k[4] = {64, 1, 128, 1}, box_v[4] = {64, 1, 32, 1};
+        if (!encode_bf16_map(&tm_q, P.qkv, 4, dims, strides, box_q)) return SPARK_ERR_CUDA;
+        if (!paged && (!encode_bf16_map(&tm_k, P.qkv, 4, dims, strides, box_k) ||
+                       !encode_bf16_map(&tm_v, P.qkv, 4, dims, strides, box_v)))
+            return SPARK_ERR_CUDA;
+    }
+    if (paged) {
+        // the pool as [n_pages][Hkv][page][256]; a box never leaves its page
+        const uint64_t page = 1ull << P.page_shift;
+        const uint64_t dims[4] = {kHeadDim, page, static_cast<uint64_t>(P.Hkv),
+                                  static_cast<uint64_t>(P.n_pages)};
+        const uint64_t strides[3] = {kHeadDim * 2ull, page * kHeadDim * 2ull,
+                                     P.Hkv * page * kHeadDim * 2ull};
+        const uint32_t box_k[4] = {64, static_cast<uint32_t>(page < 128 ? page : 128), 1, 1};
+        const uint32_t box_v[4] = {64, static_cast<uint32_t>(page < 32 ? page : 32), 1, 1};
+        if (!encode_bf16_map(&tm_k, P.k_pages, 4, dims, strides, box_k) ||
+            !encode_bf16_map(&tm_v, P.v_pages, 4, dims, strides, box_v))
+            return SPARK_ERR_CUDA;
+    } else if (pl.rot_w > 0) {
+        const uint64_t dims[3] = {static_cast<uint64_t>(pl.rot_w), N,
+                                  static_cast<uint64_t>(P.Hkv)};
+        const uint64_t strides[2] = {pl.rot_w * 2ull, N * pl.rot_w * 2ull};
+        const uint32_t box[3] = {64, 128, 1};
+        if (!encode_bf16_map(&tm_krot, P.krot, 3, dims, strides, box)) return SPARK_ERR_CUDA;
+    }
+    {
+        // out as [1][N][H][256]
+        const uint64_t H = P.H;
+        const uint64_t dims[4] = {kHeadDim, H, N, 1};
+        const uint64_t strides[3] = {kHeadDim * 2ull, H * kHeadDim * 2ull, N * H * kHeadDim * 2ull};
+        const uint32_t box[4] = {64, static_cast<uint32_t>(P.G), static_cast<uint32_t>(tq), 1};
+        if (!encode_bf16_map(&tm_out, P.out, 4, dims, strides, box)) return SPARK_ERR_CUDA;
+    }
+    return done(launch_prefill_packed(tm_q, tm_k, tm_v, tm_krot, tm_out, A, pl.most, stream));
 }
 
 spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_t *pos,
@@ -321,17 +530,29 @@ spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_
         st = check_pages(k_pages, v_pages, n_pages, page_size, table, max_pages);
         if (st != SPARK_OK) return st;
     }
-    if (workspace_bytes < packed_workspace(N, S, H, Hkv, desc, paged)) return SPARK_ERR_WORKSPACE;
+    const PackedPlan pl = plan_packed(N, S, H, Hkv, desc, paged);
+    if (workspace_bytes < pl.bytes) return SPARK_ERR_WORKSPACE;
+    if (pl.most * Hkv > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;
     int sms;
     st = device_ready(&sms);
     if (st != SPARK_OK) return st;
     PagedParams P = make_params(qkv, gate, pos, desc, N, S, H, Hkv, out, workspace);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     P.cu = cu;
+    P.krot = reinterpret_cast<__nv_bfloat16 *>(ws + pl.krot);
+    P.rot_w = pl.rot_w;
+    P.tile_base = reinterpret_cast<int32_t *>(ws + pl.base);
+    P.tiles = reinterpret_cast<int4 *>(ws + pl.tiles);
+    P.work = reinterpret_cast<int2 *>(ws + pl.work);
+    P.n_work = reinterpret_cast<int32_t *>(ws + pl.n_work);
     if (paged) {
         P.start = start;
         set_pages(P, k_pages, v_pages, n_pages, page_size, table, max_pages);
     }
-    return launch_rows<false>(P, static_cast<cudaStream_t>(stream));
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    st = launch_prep<false>(P, cs);
+    if (st != SPARK_OK) return st;
+    return launch_packed_attn(P, pl, sms, cs);
 }
 
 }  // namespace
@@ -402,7 +623,7 @@ spark_status spark_attn_decode_paged(const void *qkv, const float *gate, const i
     if (st != SPARK_OK) return st;
     PagedParams P = make_params(qkv, gate, pos, desc, B, B, H, Hkv, out, workspace);
     set_pages(P, k_pages, v_pages, n_pages, page_size, page_table, max_pages);
-    return launch_rows<true>(P, static_cast<cudaStream_t>(stream));
+    return launch_rows(P, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

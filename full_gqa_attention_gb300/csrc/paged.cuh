@@ -6,9 +6,6 @@
 
 namespace spark {
 
-constexpr unsigned kErrSeqlens = 0x4u;  // SPARK_DEVERR_SEQLENS
-constexpr unsigned kErrPage = 0x8u;     // SPARK_DEVERR_PAGE
-
 struct PagedParams {
     const __nv_bfloat16 *qkv;  // [N, (H+2Hkv)*256]
     const float *gate;         // [N, H]
@@ -20,6 +17,12 @@ struct PagedParams {
     const int32_t *table;      // [rows, max_pages]
     __nv_bfloat16 *out;        // [N, H*256]
     unsigned *status;
+    __nv_bfloat16 *krot;       // [Hkv, N, rot_w]: rotated leading key dims (packed prompts)
+    int rot_w;
+    int32_t *tile_base;        // [S + 1]: query tiles before each sequence
+    int4 *tiles;               // query tiles in the sequences' order: (sequence, token, bin)
+    int2 *work;                // the same, longest first
+    int32_t *n_work;
     int N, S, H, Hkv, G;
     int kind, window, gate_mode;
     int n_pages, page_shift, max_pages;

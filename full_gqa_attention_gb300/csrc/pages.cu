@@ -15,9 +15,6 @@
 
 namespace spark {
 
-constexpr unsigned kErrPage = SPARK_DEVERR_PAGE;
-constexpr unsigned kErrRow = SPARK_DEVERR_ROW;
-
 namespace {
 
 constexpr int kPlanThreads = 1024;

@@ -206,7 +206,8 @@ constexpr int kBarODone = 6 + 2 * kSlots;
 constexpr int kBarMmaDrain = 7 + 2 * kSlots;
 constexpr int kBarOFinal = 8 + 2 * kSlots;      // every P*V done (one phase per CTA)
 constexpr int kBarMaxX = 9 + 2 * kSlots;        // 2: half-row maxima exchanged (per tile parity)
-constexpr int kNumBars = 11 + 2 * kSlots;
+constexpr int kBarVClean = 11 + 2 * kSlots;     // packed prefill: V of a tile is there and clean
+constexpr int kNumBars = 12 + 2 * kSlots;
 
 constexpr int kAttnSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + 256;
 
@@ -271,7 +272,22 @@ __device__ __forceinline__ void named_bar(int id, int n) {
 // is its own instantiation, so that no kernel carries another's addressing
 // (the ring's slot arithmetic would sit in every inlined load of the
 // producer).
-enum KvSource : int { kKvFromQkv = 0, kKvFromCache = 1, kKvFromRing = 2 };
+//
+// The packed sources: sequences of different lengths behind one another
+// (common.cuh: PackedInfo), their keys and values in the fused projection, or
+// in pages that hold the chunk and what came before it.  A key tile of the
+// last or first kind of place may then reach into another sequence, into slots
+// that no token was written to, or behind the window, and all of a tile's
+// queries share one V operand: a value there that is not finite would turn its
+// zero probability into NaN.  Warp 3, idle otherwise, clears those rows in
+// shared memory before P*V reads them (clean_v_tile).
+enum KvSource : int {
+    kKvFromQkv = 0,
+    kKvFromCache = 1,
+    kKvFromRing = 2,
+    kKvPacked = 3,
+    kKvPages = 4
+};
 
 // The layer kind is a template argument too, so that a kernel carries no
 // arithmetic of the other kind; kKindAny reads it from P.kind instead.  Which
@@ -279,6 +295,44 @@ enum KvSource : int { kKvFromQkv = 0, kKvFromCache = 1, kKvFromRing = 2 };
 // builds are faster for both chunked kinds and the one-shot sliding layer,
 // the generic one for the one-shot full layer.
 constexpr int kKindAny = -1;
+
+// Whether a packed pair of bf16 holds a value that is not finite; and the pair
+// with such values replaced by zero.
+__device__ __forceinline__ uint32_t nonfinite_mask(uint32_t w) {
+    return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
+           ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+// One warp's pass over a V slot (32 keys x 256 dims, first key key0) of a tile
+// that needs a mask, for the queries a0..a_last: rows that none of them sees
+// become zero; in rows that only some of them see, values that are not finite
+// become zero (returns true if there was one: the epilogue gives it back to the
+// rows that see it).
+__device__ __forceinline__ bool clean_v_slot(uint8_t *slot, int kind, int window, int key0,
+                                             int a0, int a_last, int lane) {
+    bool found = false;
+#pragma unroll 4
+    for (int r = 0; r < 32; ++r) {
+        const int key = key0 + r;
+        const bool all = key <= a0 && (kind == kLayerFull || a_last - key < window);
+        if (all) continue;
+        const bool none = key > a_last || (kind == kLayerSliding && a0 - key >= window);
+        uint4 *p = reinterpret_cast<uint4 *>(slot + (lane >> 3) * (kSlotBytes / 4) + r * 128 +
+                                             (lane & 7) * 16);
+        if (none) {
+            *p = make_uint4(0, 0, 0, 0);
+        } else {
+            const uint4 w = *p;
+            const uint32_t mx = nonfinite_mask(w.x), my = nonfinite_mask(w.y);
+            const uint32_t mz = nonfinite_mask(w.z), mw = nonfinite_mask(w.w);
+            if (mx | my | mz | mw) {
+                *p = make_uint4(w.x & ~mx, w.y & ~my, w.z & ~mz, w.w & ~mw);
+                found = true;
+            }
+        }
+    }
+    return found;
+}
 
 // kG: the GQA group size when fixed at compile time (the Spark-X2.5 shapes
 // all use 4), 0 to read it from P.G.  Timing chose the fixed size for the
@@ -301,6 +355,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __shared__ int abort_flag;
     __shared__ float red_max[2][2][kBM];   // [tile parity][warpgroup][row]: half-row maxima
     __shared__ float red_l[2][kBM];        // [warpgroup][row]: half-row sums
+    constexpr bool kIsPacked = kSrc == kKvPacked || kSrc == kKvPages;
+    __shared__ int cleaned_any;            // packed: a value was taken out of a partly hidden row
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int kind = kKind == kKindAny ? P.kind : kKind;
@@ -309,8 +365,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int qtile = P.n_qtiles - 1 - static_cast<int>(blockIdx.x) / units;  // longest first
     const int rem = static_cast<int>(blockIdx.x) % units;
     const int g = rem % P.Hkv, b = rem / P.Hkv;
-    const int t0 = qtile * tq;
-    const int t_end = (t0 + tq < P.T) ? t0 + tq : P.T;  // exclusive
+    int t0 = qtile * tq;
+    int t_end = (t0 + tq < P.T) ? t0 + tq : P.T;  // exclusive
+    int seq_end = P.T;                            // tokens of the sequence
+    int row0 = 0;                                 // packed: the sequence's first row
+    int seq = 0;
+    if constexpr (kIsPacked) {
+        // the grid allows for a ragged tile in every sequence: a CTA past the
+        // list has nothing to do, and finds out before it sets anything up
+        if (static_cast<int>(blockIdx.x) / units >= P.pk.sure) {
+            grid_dep_wait();
+            if (static_cast<int>(blockIdx.x) / units >= *P.pk.n_work) return;
+        }
+    }
 
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
@@ -323,6 +390,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         fence_mbar_init();
         abort_flag = 0;
+        if (kIsPacked) cleaned_any = 0;
     }
     if (warp == 1) {
         tmem_alloc(&tmem_base_sh, kTmemCols);
@@ -349,7 +417,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // Absolute indices: queries t0..t_end-1 of the chunk sit at start + t.
     int start = 0;
     bool skip = false;
-    if constexpr (kSrc != kKvFromQkv) {
+    if constexpr (kIsPacked) {
+        const int item = static_cast<int>(blockIdx.x) / units;
+        skip = item >= *P.pk.n_work;
+        if (!skip) {
+            const int2 w = P.pk.work[item];
+            seq = w.x;
+            t0 = w.y;
+            row0 = P.pk.cu[seq];
+            seq_end = P.pk.cu[seq + 1] - row0;
+            if (kSrc == kKvPages) start = P.start[seq];
+        } else {
+            t0 = 0;
+        }
+        t_end = (t0 + tq < seq_end) ? t0 + tq : seq_end;
+    } else if constexpr (kSrc != kKvFromQkv) {
         start = P.start[b];
         skip = start < 0 || (kind == kLayerFull && static_cast<long long>(start) + P.T > P.cap);
         if (skip && tid == 0 && qtile == P.n_qtiles - 1 && g == 0) atomicOr(P.status, kErrPosition);
@@ -358,7 +440,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // a ring is read in 128-key tiles aligned to its 128-slot boundaries, so
     // that no tile wraps around the end of the ring
     const KeyTiles kt = prefill_key_tiles(kind, P.window, a0, start + t_end, kBN,
-                                          kSrc == kKvFromRing);
+                                          kSrc == kKvFromRing || kSrc == kKvPages);
     const int kv_lo = kt.kv_lo;
     const int ntiles = skip ? 0 : kt.ntiles;
 
@@ -369,18 +451,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_arrive_expect_tx(&bars[kBarQFull], kQBytes);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                tma_load_4d(qbuf + c * kSlotBytes, &tm_q, &bars[kBarQFull], c * 64, g * G, t0, b);
+                tma_load_4d(qbuf + c * kSlotBytes, &tm_q, &bars[kBarQFull], c * 64, g * G,
+                            row0 + t0, b);
             // the CTA one wave later (likely the next one on this SM) finds its
             // query tile in L2 -- when this CTA is short (a sliding layer's, or
             // the last waves of a causal one); behind a long CTA the tile would
             // be evicted before use and read twice
             const long long nb = static_cast<long long>(blockIdx.x) + P.wave;
             if (P.wave > 0 && nb < gridDim.x && ntiles <= kPrefetchMaxTiles) {
-                const int nq = P.n_qtiles - 1 - static_cast<int>(nb / units);
                 const int nrem = static_cast<int>(nb % units);
+                int nt0;
+                if constexpr (kIsPacked) {
+                    const int ni = static_cast<int>(nb / units);
+                    const int2 w = ni < *P.pk.n_work ? P.pk.work[ni] : make_int2(seq, t0);
+                    nt0 = P.pk.cu[w.x] + w.y;
+                } else {
+                    nt0 = (P.n_qtiles - 1 - static_cast<int>(nb / units)) * tq;
+                }
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    tma_prefetch_l2_4d(&tm_q, c * 64, (nrem % P.Hkv) * G, nq * tq, nrem / P.Hkv);
+                    tma_prefetch_l2_4d(&tm_q, c * 64, (nrem % P.Hkv) * G, nt0, nrem / P.Hkv);
             }
             if (P.defer_wait) grid_dep_wait();  // rotated K / the cache are ready
             bool ok = true;
@@ -393,13 +483,49 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mbar_arrive_expect_tx(&bars[kBarSlotFull + slot], kSlotBytes);
                 return true;
             };
+            // The page that holds key `key` (a multiple of 16), or one past the
+            // pool where no query of this CTA sees a key of that page: the
+            // copy then reads zeros.
+            auto page_of = [&](int key) -> int {
+                const int last = start + t_end - 1;
+                const int lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
+                const int index = key >> P.pk.page_shift;
+                if (key > last || ((index + 1) << P.pk.page_shift) <= lo) return P.pk.n_pages;
+                const int id = P.pk.table[static_cast<size_t>(seq) * P.pk.max_pages + index];
+                if (id >= 0 && id < P.pk.n_pages) return id;
+                atomicOr(P.status, kErrPage);
+                return P.pk.n_pages;
+            };
             auto load_k = [&](int j) -> bool {
                 const int key0 = kv_lo + j * kBN;
+                int ids[8];
+                if constexpr (kSrc == kKvPages) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        ids[i] = i < (kBN >> P.pk.page_shift) || i == 0
+                                     ? page_of(key0 + (i << P.pk.page_shift))
+                                     : 0;
+                }
                 for (int c = 0; c < 4; ++c) {
                     int slot;
                     if (!next_slot(slot)) return false;
                     uint8_t *dst = ring + slot * kSlotBytes;
-                    if constexpr (kSrc != kKvFromQkv) {
+                    if constexpr (kSrc == kKvPages) {
+                        const int page = 1 << P.pk.page_shift;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i == 0 || i * page < kBN)
+                                tma_load_4d(dst + i * page * 128, &tm_kv_k,
+                                            &bars[kBarSlotFull + slot], c * 64, key0 & (page - 1),
+                                            g, ids[i]);
+                    } else if constexpr (kSrc == kKvPacked) {
+                        if (c * 64 < P.rot_w)
+                            tma_load_3d(dst, &tm_krot, &bars[kBarSlotFull + slot], c * 64,
+                                        row0 + key0, g);
+                        else
+                            tma_load_4d(dst, &tm_kv_k, &bars[kBarSlotFull + slot], c * 64,
+                                        P.H + g, row0 + key0, 0);
+                    } else if constexpr (kSrc != kKvFromQkv) {
                         const int slot0 =
                             kSrc == kKvFromRing ? key0 % static_cast<int>(P.cap) : key0;
                         tma_load_4d(dst, &tm_kv_k, &bars[kBarSlotFull + slot], c * 64, slot0, g,
@@ -421,7 +547,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     int slot;
                     if (!next_slot(slot)) return false;
                     uint8_t *dst = ring + slot * kSlotBytes;
-                    if constexpr (kSrc != kKvFromQkv) {
+                    if constexpr (kSrc == kKvPages) {
+                        const int page = 1 << P.pk.page_shift;
+                        const int key = key0 + vs * 32;
+                        const int id0 = page_of(key);
+                        const int id1 = page < 32 ? page_of(key + 16) : 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            tma_load_4d(dst + c * (kSlotBytes / 4), &tm_kv_v,
+                                        &bars[kBarSlotFull + slot], c * 64, key & (page - 1), g,
+                                        id0);
+                            if (page < 32)
+                                tma_load_4d(dst + c * (kSlotBytes / 4) + 16 * 128, &tm_kv_v,
+                                            &bars[kBarSlotFull + slot], c * 64, 0, g, id1);
+                        }
+                    } else if constexpr (kSrc == kKvPacked) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            tma_load_4d(dst + c * (kSlotBytes / 4), &tm_kv_v,
+                                        &bars[kBarSlotFull + slot], c * 64, P.H + P.Hkv + g,
+                                        row0 + key0 + vs * 32, 0);
+                    } else if constexpr (kSrc != kKvFromQkv) {
                         const int slot0 =
                             kSrc == kKvFromRing ? key0 % static_cast<int>(P.cap) : key0;
 #pragma unroll
@@ -508,6 +654,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             auto mma_pv = [&](int j) -> bool {
                 const uint32_t pcol = tmem + kColS + (j & 1) * kBN;
+                if (kIsPacked &&
+                    !mbar_wait(&bars[kBarVClean], j & 1, &abort_flag, P.status))
+                    return false;
                 for (int vs = 0; vs < 4; ++vs) {
                     const int slot = sc % kSlots;
                     if (!mbar_wait(&bars[kBarSlotFull + slot], (sc / kSlots) & 1, &abort_flag,
@@ -587,8 +736,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int tok = t0 + row / G;
         const int tok_abs = start + tok;                // absolute index for the mask
         const int head = g * G + row % G;
-        const bool valid = tok < P.T;
-        const size_t trow = static_cast<size_t>(b) * P.T + (valid ? tok : 0);
+        const bool valid = kIsPacked ? !skip && tok < seq_end : tok < P.T;
+        const size_t trow = kIsPacked ? static_cast<size_t>(valid ? row0 + tok : 0)
+                                      : static_cast<size_t>(b) * P.T + (valid ? tok : 0);
         const int p = valid ? P.pos[trow] : 0;
         const float gate_logit = valid ? P.gate[trow * P.H + head] : 0.f;
         bool ok = !skip && mbar_wait(&bars[kBarQFull], 0, &abort_flag, P.status);
@@ -729,12 +879,64 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         *reinterpret_cast<uint4 *>(qbuf + sw128_offset(row, (c + 32 * h) / 8 + q)) = w;
                     }
             }
+            if constexpr (kIsPacked) {
+                // a value that is not finite, taken out of a row that only some
+                // of the tile's queries see: those that do get it back
+                if (cleaned_any && valid) {
+                    const int w_lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
+                    for (int key = w_lo > 0 ? w_lo : 0; key <= tok_abs; ++key) {
+                        const bool all = key <= a0 && (kind == kLayerFull || a_last - key < P.window);
+                        if (all) {
+                            key = a0;  // no key before the causal edge is hidden from some
+                            continue;
+                        }
+                        if (!key_visible(kind, P.window, tok_abs, key)) continue;
+                        const __nv_bfloat16 *src;
+                        if constexpr (kSrc == kKvPages) {
+                            const int page = P.pk.table[static_cast<size_t>(seq) * P.pk.max_pages +
+                                                        (key >> P.pk.page_shift)];
+                            if (page < 0 || page >= P.pk.n_pages) continue;
+                            src = P.v_cache +
+                                  (((static_cast<size_t>(page) * P.Hkv + g) << P.pk.page_shift) +
+                                   (key & ((1 << P.pk.page_shift) - 1))) * kHeadDim;
+                        } else {
+                            src = P.qkv + ((static_cast<size_t>(row0) + key) * (P.H + 2 * P.Hkv) +
+                                           P.H + P.Hkv + g) * kHeadDim;
+                        }
+                        for (int q = wg * 16; q < wg * 16 + 16; ++q) {
+                            const uint4 vv = *reinterpret_cast<const uint4 *>(src + q * 8);
+                            const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
+                            uint32_t *o =
+                                reinterpret_cast<uint32_t *>(qbuf + sw128_offset(row, q));
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t m = nonfinite_mask(vw[i]);
+                                if (!m) continue;
+                                const uint32_t x = o[i];
+                                const float lo = (m & 0xFFFFu) ? bf16_lo(vw[i]) * scale : 0.f;
+                                const float hi = (m >> 16) ? bf16_hi(vw[i]) * scale : 0.f;
+                                o[i] = pack_bf16x2(bf16_lo(x) + lo, bf16_hi(x) + hi);
+                            }
+                        }
+                    }
+                }
+            }
             fence_proxy_async_smem();
             named_bar(1, kSoftmaxThreads);
-            if (sth == 0 && !abort_flag && !skip) {
+            if (kIsPacked && t_end - t0 < tq) {
+                // a ragged tile: the rows behind it belong to others
+                const int nrows = skip || abort_flag ? 0 : (t_end - t0) * G;
+                for (int i = sth; i < nrows * 32; i += kSoftmaxThreads) {
+                    const int r = i >> 5, q = i & 31;
+                    *reinterpret_cast<uint4 *>(
+                        P.pk.out +
+                        ((static_cast<size_t>(row0) + t0 + r / G) * P.H + g * G + r % G) *
+                            kHeadDim + q * 8) =
+                        *reinterpret_cast<const uint4 *>(qbuf + sw128_offset(r, q));
+                }
+            } else if (sth == 0 && !abort_flag && !skip) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    tma_store_4d(&tm_out, qbuf + c * kSlotBytes, c * 64, g * G, t0, b);
+                    tma_store_4d(&tm_out, qbuf + c * kSlotBytes, c * 64, g * G, row0 + t0, b);
                 tma_store_commit();
                 tma_store_wait_read();  // the staging buffer is read; the writes land by grid end
             }
@@ -742,7 +944,43 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc_fence_before();
         __syncthreads();
     } else {
-        // warp 3 has no role
+        // ------------------------------------------------------ V cleaner
+        // (packed sources; warp 3 has no role otherwise)  Follows the V slots of
+        // every tile in order and hands each tile to the P*V issuer, after a pass
+        // over it where the tile needs a mask.
+        if constexpr (kIsPacked) {
+            if (!skip) {
+                bool ok = true;
+                auto wait_slot = [&](int use) -> bool {
+                    return mbar_wait(&bars[kBarSlotFull + use % kSlots], (use / kSlots) & 1,
+                                     &abort_flag, P.status);
+                };
+                // K0 came first into the slots that V tiles reuse: a wait for a
+                // later phase of a barrier must not begin before its first
+                for (int i = 0; ok && i < 4; ++i) ok = wait_slot(i);
+                int sc = ntiles > 1 ? 8 : 4;
+                const int a_last = start + t_end - 1;
+                for (int j = 0; ok && j < ntiles; ++j) {
+                    const int key0 = kv_lo + j * kBN;
+                    const bool masked = tile_needs_mask(kind, P.window, key0, kBN, a0, a_last);
+                    bool found = false;
+                    for (int vs = 0; ok && vs < 4; ++vs, ++sc) {
+                        ok = wait_slot(sc);
+                        if (ok && masked)
+                            found |= clean_v_slot(ring + (sc % kSlots) * kSlotBytes, kind,
+                                                  P.window, key0 + vs * 32, a0, a_last, lane);
+                    }
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    if (masked) {
+                        if (found) cleaned_any = 1;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(&bars[kBarVClean]);
+                    if (j + 2 < ntiles) sc += 4;  // K_{j+2}
+                }
+            }
+        }
         __syncthreads();
     }
 }
@@ -811,6 +1049,26 @@ cudaError_t launch_prefill(const CUtensorMap &tm_q, const CUtensorMap &tm_kv_k,
     // fill the decode cache (it reads only qkv and pos)
     return launch_overlapped(prefill_store_kv_kernel, dim3(static_cast<unsigned>(store_blocks)),
                              dim3(kRopeThreads), 0, stream, P);
+}
+
+// The attention kernel of a packed prefill: `items` query tiles at most, per
+// KV head.  The kernel before it on the stream made the list of tiles.
+cudaError_t launch_prefill_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_kv_k,
+                                  const CUtensorMap &tm_kv_v, const CUtensorMap &tm_krot,
+                                  const CUtensorMap &tm_out, const PrefillParams &P,
+                                  long long items, cudaStream_t stream) {
+    const bool paged = P.pk.table != nullptr;
+    const bool sliding = P.kind == kLayerSliding;
+    auto kernel = paged ? (sliding ? attn_kernel_for<kKvPages, kLayerSliding>(P.G)
+                                   : attn_kernel_for<kKvPages, kLayerFull>(P.G))
+                        : (sliding ? attn_kernel_for<kKvPacked, kLayerSliding>(P.G)
+                                   : attn_kernel_for<kKvPacked, kKindAny>(P.G));
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kAttnSmemBytes);
+    if (err != cudaSuccess) return err;
+    return launch_overlapped(kernel, dim3(static_cast<unsigned>(items * P.Hkv)),
+                             dim3(kAttnThreads), kAttnSmemBytes, stream, tm_q, tm_kv_k, tm_kv_v,
+                             tm_krot, tm_out, P);
 }
 
 }  // namespace spark

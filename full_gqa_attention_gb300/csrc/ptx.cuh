@@ -11,6 +11,9 @@ namespace spark {
 // Device status bits (mirrors SPARK_DEVERR_* of the public header).
 constexpr unsigned kErrPosition = 0x1u;
 constexpr unsigned kErrTimeout = 0x2u;
+constexpr unsigned kErrSeqlens = 0x4u;
+constexpr unsigned kErrPage = 0x8u;
+constexpr unsigned kErrRow = 0x10u;
 
 // A bounded wait gives up after this long (nanoseconds of %globaltimer).
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
