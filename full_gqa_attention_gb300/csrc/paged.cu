@@ -16,6 +16,8 @@ cudaError_t launch_prefill_packed(const CUtensorMap &tm_q, const CUtensorMap &tm
                                   const CUtensorMap &tm_kv_v, const CUtensorMap &tm_krot,
                                   const CUtensorMap &tm_out, const PrefillParams &P,
                                   long long items, cudaStream_t stream);
+cudaError_t launch_decode_paged(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                                const PagedParams &P, int grid, cudaStream_t stream);
 
 namespace {
 
@@ -123,28 +125,15 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
 }
 
 // Whether the token of `row` has a place in the pages; where.
-template <bool kDecode>
 __device__ __forceinline__ bool token_slot(const PagedParams &P, int row, bool report,
                                            size_t &base) {
     const long long cap = static_cast<long long>(P.max_pages) << P.page_shift;
-    long long a;  // index in the sequence
-    int seq;
-    if (kDecode) {
-        seq = row;
-        a = P.pos[row];
-        if (a == -1) return false;
-        if (a < 0 || a >= cap) {
-            if (report) atomicOr(P.status, kErrPosition);
-            return false;
-        }
-    } else {
-        seq = find_sequence(P.cu, P.S, row);
-        if (seq < 0) return false;
-        const int t0 = P.cu[seq], t1 = P.cu[seq + 1];
-        const long long st = P.start[seq];
-        if (t0 < 0 || t1 > P.N || st < 0 || st + (t1 - t0) > cap) return false;  // the plan reports
-        a = st + (row - t0);
-    }
+    const int seq = find_sequence(P.cu, P.S, row);
+    if (seq < 0) return false;
+    const int t0 = P.cu[seq], t1 = P.cu[seq + 1];
+    const long long st = P.start[seq];
+    if (t0 < 0 || t1 > P.N || st < 0 || st + (t1 - t0) > cap) return false;  // the plan reports it
+    const long long a = st + (row - t0);  // index in the sequence
     const int page = P.table[static_cast<size_t>(seq) * P.max_pages + (a >> P.page_shift)];
     if (page < 0 || page >= P.n_pages) {
         if (report) atomicOr(P.status, kErrPage);
@@ -160,26 +149,20 @@ __device__ __forceinline__ bool token_slot(const PagedParams &P, int row, bool r
 // rot_w dims of every key, rotated, go to the workspace (the others are read
 // where they are).  One thread per (token, group of 8 rotated pairs / 8 copied
 // key dims / 8 value dims), looping over the KV heads so that each angle is
-// computed once.  Of a prompt's grid the first CTA makes the list of query
-// tiles instead.
-template <bool kDecode>
+// computed once.  The first CTA makes the list of query tiles instead.
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     const __grid_constant__ PagedParams P) {
     grid_dep_wait();
     grid_dep_launch();
-    int block = blockIdx.x;
-    if (!kDecode) {
-        if (block == 0) {
-            plan_tiles(P);
-            return;
-        }
-        --block;
+    if (blockIdx.x == 0) {
+        plan_tiles(P);
+        return;
     }
     const bool paged = P.k_pages != nullptr;
     const int r = P.rope.rot_dim, half = r / 2;
     const int n_rot = half / 8, n_kcopy = ((paged ? kHeadDim : P.rot_w) - r) / 8;
     const int items = n_rot + n_kcopy + (paged ? kHeadDim / 8 : 0);
-    const long long idx = static_cast<long long>(block) * blockDim.x + threadIdx.x;
+    const long long idx = (blockIdx.x - 1ll) * blockDim.x + threadIdx.x;
     const long long row_l = idx / items;
     if (row_l >= P.N) return;
     const int row = static_cast<int>(row_l), it = static_cast<int>(idx % items);
@@ -187,7 +170,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     size_t head_stride;
     if (paged) {
         size_t base;
-        if (!token_slot<kDecode>(P, row, it == 0, base)) return;
+        if (!token_slot(P, row, it == 0, base)) return;
         dst_k = P.k_pages + base;
         dst_v = P.v_pages + base;
         head_stride = static_cast<size_t>(kHeadDim) << P.page_shift;
@@ -233,90 +216,6 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
             *reinterpret_cast<uint4 *>(dst_v + g * head_stride + d0) =
                 *reinterpret_cast<const uint4 *>(src_v + g * kHeadDim + d0);
     }
-}
-
-// The plain attention of a decode step: one warp per (row, query head), lane l
-// holding dims 8l..8l+7, keys one after another with an online softmax.
-constexpr int kRowWarps = 8;
-
-__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(u[i]);
-        x[2 * i + 1] = bf16_hi(u[i]);
-    }
-}
-
-// Rotates this lane's 8 dims of one head (the partner dims live r/16 lanes
-// away) and rounds them to bf16.
-__device__ __forceinline__ void rotate_lane(float (&x)[8], int pos, const RopeTable &rope,
-                                            int lane) {
-    const int r = rope.rot_dim, half = r / 2, d0 = lane * 8;
-    const int partner = (d0 >= r) ? lane : (d0 < half ? lane + half / 8 : lane - half / 8);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_sync(0xffffffffu, x[i], partner);
-        if (d0 < r) {
-            float c, s, y1, y2;
-            rope_cos_sin(pos, rope.u[d0 < half ? d0 + i : d0 + i - half], c, s);
-            if (d0 < half)
-                rope_rotate(x[i], y, c, s, y1, y2);
-            else
-                rope_rotate(y, x[i], c, s, y1, y2);
-            x[i] = __bfloat162float(__float2bfloat16_rn(d0 < half ? y1 : y2));
-        }
-    }
-}
-
-__global__ void __launch_bounds__(kRowWarps * 32) rows_attn_kernel(
-    const __grid_constant__ PagedParams P) {
-    grid_dep_wait();
-    grid_dep_launch();
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-    const int row = static_cast<int>(w / P.H), h = static_cast<int>(w % P.H);
-    if (row >= P.N) return;
-    const int g = h / P.G;
-    const long long cap = static_cast<long long>(P.max_pages) << P.page_shift;
-    const long long at = P.pos[row];
-    if (at < 0 || at >= cap) return;
-    const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
-    float q[8], o[8], k[8], v[8];
-    unpack8(*reinterpret_cast<const uint4 *>(P.qkv + row * width + h * kHeadDim + lane * 8), q);
-    if (P.rope.rot_dim > 0) rotate_lane(q, P.pos[row], P.rope, lane);
-    float m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 0.f;
-    long long j = P.kind == kLayerSliding ? at - P.window + 1 : 0;
-    for (j = j > 0 ? j : 0; j <= at; ++j) {
-        const int page = P.table[static_cast<size_t>(row) * P.max_pages + (j >> P.page_shift)];
-        if (page < 0 || page >= P.n_pages) {
-            if (lane == 0) atomicOr(P.status, kErrPage);
-            continue;
-        }
-        const size_t off = ((static_cast<size_t>(page) * P.Hkv + g) << P.page_shift) * kHeadDim +
-                           (j & ((1 << P.page_shift) - 1)) * kHeadDim + lane * 8;
-        unpack8(*reinterpret_cast<const uint4 *>(P.k_pages + off), k);
-        unpack8(*reinterpret_cast<const uint4 *>(P.v_pages + off), v);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(q[i], k[i], s);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= kScaleLog2;
-        const float mn = fmaxf(m, s);
-        const float z = mn == -INFINITY ? 0.f : mn;
-        const float a = fast_exp2(m - z), p = fast_exp2(s - z);
-        l = l * a + p;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = o[i] * a + p * v[i];
-        m = mn;
-    }
-    const float scale = gate_act(P.gate[static_cast<size_t>(row) * P.H + h], P.gate_mode) / l;
-    *reinterpret_cast<uint4 *>(P.out + (static_cast<size_t>(row) * P.H + h) * kHeadDim + lane * 8) =
-        make_uint4(pack_bf16x2(o[0] * scale, o[1] * scale), pack_bf16x2(o[2] * scale, o[3] * scale),
-                   pack_bf16x2(o[4] * scale, o[5] * scale), pack_bf16x2(o[6] * scale, o[7] * scale));
 }
 
 // ---------------------------------------------------------------- host side
@@ -387,23 +286,14 @@ spark_status done(cudaError_t e) {
     return SPARK_ERR_CUDA;
 }
 
-template <bool kDecode>
 spark_status launch_prep(const PagedParams &P, cudaStream_t s) {
     const int r = P.rope.rot_dim;
     const long long items =
         r / 16 + ((P.k_pages ? kHeadDim : P.rot_w) - r) / 8 + (P.k_pages ? kHeadDim / 8 : 0);
-    const long long blocks = (P.N * items + kPrepThreads - 1) / kPrepThreads + (kDecode ? 0 : 1);
-    return done(launch_overlapped(paged_prep_kernel<kDecode>, dim3(static_cast<unsigned>(blocks)),
+    const long long blocks = (P.N * items + kPrepThreads - 1) / kPrepThreads + 1;
+    if (blocks > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;
+    return done(launch_overlapped(paged_prep_kernel, dim3(static_cast<unsigned>(blocks)),
                                   dim3(kPrepThreads), 0, s, P));
-}
-
-spark_status launch_rows(const PagedParams &P, cudaStream_t s) {
-    const spark_status st = launch_prep<true>(P, s);
-    if (st != SPARK_OK) return st;
-    const long long warps = static_cast<long long>(P.N) * P.H;
-    return done(launch_overlapped(rows_attn_kernel,
-                                  dim3(static_cast<unsigned>((warps + kRowWarps - 1) / kRowWarps)),
-                                  dim3(kRowWarps * 32), 0, s, P));
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -512,6 +402,24 @@ spark_status launch_packed_attn(const PagedParams &P, const PackedPlan &pl, int 
     return done(launch_prefill_packed(tm_q, tm_k, tm_v, tm_krot, tm_out, A, pl.most, stream));
 }
 
+// Workspace of a paged decode: the header (status word, then a byte per CTA
+// that counts the finished parts of a shared pair), two partial states per CTA.
+struct DecodePagedPlan {
+    int grid;
+    size_t ml, o, bytes;
+};
+
+DecodePagedPlan plan_decode_paged(int H, int Hkv, int sms) {
+    DecodePagedPlan pl{};
+    constexpr int most = static_cast<int>(kWorkspaceHeader) - 4;
+    pl.grid = sms < most ? sms : most;
+    const size_t parts = static_cast<size_t>(pl.grid) * 2 * (H / Hkv);
+    pl.ml = kWorkspaceHeader;
+    pl.o = pl.ml + up256(parts * 2 * 4);
+    pl.bytes = pl.o + up256(parts * kHeadDim * 4);
+    return pl;
+}
+
 spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_t *pos,
                                 const int32_t *cu, const int32_t *start, void *k_pages,
                                 void *v_pages, int n_pages, int page_size, const int32_t *table,
@@ -550,7 +458,7 @@ spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_
         set_pages(P, k_pages, v_pages, n_pages, page_size, table, max_pages);
     }
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    st = launch_prep<false>(P, cs);
+    st = launch_prep(P, cs);
     if (st != SPARK_OK) return st;
     return launch_packed_attn(P, pl, sms, cs);
 }
@@ -597,7 +505,9 @@ spark_status spark_attn_prefill_paged(const void *qkv, const float *gate, const 
 
 size_t spark_attn_decode_paged_workspace_size(int B, int H, int Hkv, const spark_layer_desc *desc) {
     if (check_layer_desc(desc, H, Hkv) != SPARK_OK || B < 0) return 0;
-    return kWorkspaceHeader;
+    int sms;
+    device_ready(&sms);
+    return plan_decode_paged(H, Hkv, sms).bytes;
 }
 
 spark_status spark_attn_decode_paged(const void *qkv, const float *gate, const int32_t *pos,
@@ -616,14 +526,29 @@ spark_status spark_attn_decode_paged(const void *qkv, const float *gate, const i
         return SPARK_ERR_ALIGN;
     st = check_pages(k_pages, v_pages, n_pages, page_size, page_table, max_pages);
     if (st != SPARK_OK) return st;
-    if (workspace_bytes < spark_attn_decode_paged_workspace_size(B, H, Hkv, desc))
-        return SPARK_ERR_WORKSPACE;
     int sms;
-    st = device_ready(&sms);
-    if (st != SPARK_OK) return st;
+    const spark_status ready = device_ready(&sms);
+    const DecodePagedPlan pl = plan_decode_paged(H, Hkv, sms);
+    if (workspace_bytes < pl.bytes) return SPARK_ERR_WORKSPACE;
+    if (ready != SPARK_OK) return ready;
     PagedParams P = make_params(qkv, gate, pos, desc, B, B, H, Hkv, out, workspace);
     set_pages(P, k_pages, v_pages, n_pages, page_size, page_table, max_pages);
-    return launch_rows(P, static_cast<cudaStream_t>(stream));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    P.counters = reinterpret_cast<unsigned *>(ws) + 1;
+    P.part_ml = reinterpret_cast<float *>(ws + pl.ml);
+    P.part_o = reinterpret_cast<float *>(ws + pl.o);
+    // the pool as [n_pages][Hkv][page][256]; boxes of a page's share of a tile
+    const uint64_t page = static_cast<uint64_t>(page_size);
+    const uint64_t dims[4] = {kHeadDim, page, static_cast<uint64_t>(Hkv),
+                              static_cast<uint64_t>(n_pages)};
+    const uint64_t strides[3] = {kHeadDim * 2ull, page * kHeadDim * 2ull,
+                                 Hkv * page * kHeadDim * 2ull};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(page < 64 ? page : 64), 1, 1};
+    CUtensorMap tm_k, tm_v;
+    if (!encode_bf16_map(&tm_k, k_pages, 4, dims, strides, box) ||
+        !encode_bf16_map(&tm_v, v_pages, 4, dims, strides, box))
+        return SPARK_ERR_CUDA;
+    return done(launch_decode_paged(tm_k, tm_v, P, pl.grid, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

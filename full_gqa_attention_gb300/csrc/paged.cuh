@@ -23,6 +23,9 @@ struct PagedParams {
     int4 *tiles;               // query tiles in the sequences' order: (sequence, token, bin)
     int2 *work;                // the same, longest first
     int32_t *n_work;
+    float *part_ml;            // decode: [grid, 2, G, 2] running max (base-2 units), sum
+    float *part_o;             // decode: [grid, 2, G, 256] unnormalised outputs
+    unsigned *counters;        // decode: a byte per CTA, left at 0 by every call
     int N, S, H, Hkv, G;
     int kind, window, gate_mode;
     int n_pages, page_shift, max_pages;

@@ -450,8 +450,8 @@ spark_status spark_attn_prefill_paged(const void *qkv, const float *gate, const 
  *         skipped and SPARK_DEVERR_POSITION set.
  *   out   bf16 [B, H * 256]
  *   workspace  >= the size query's bytes, 256-byte aligned, zeroed once
- *         before first use (its counters are left at 0 by every call); calls
- *         that may overlap need one each
+ *         before first use (the counters in its first 256 bytes are left at 0
+ *         by every call); calls that may overlap need one each
  * The work is split by what the positions ask for, not by max_pages: a call
  * captured into a graph serves every later length.
  */
