@@ -116,11 +116,17 @@ inline bool decode_fuses_merge(int nsplit, long long B_times_Hkv, bool have_coun
 // What a packed prefill adds: sequences behind one another (B = 1, T = all
 // tokens in PrefillParams), and a list of query tiles that the kernel before
 // the attention kernel made of their offsets, longest first.
+struct __align__(16) PackedItem {
+    int seq;                   // its sequence, -1: no tile
+    int t0;                    // its first token inside the sequence
+    int row0, len;             // the sequence's first row, its tokens
+    int start;                 // tokens in its pages before the call
+    int bin, pad[2];
+};
+
 struct PackedInfo {
-    const int32_t *cu;         // [S + 1] first token of each sequence
-    const int2 *work;          // query tiles: (sequence, first token inside it)
-    const int32_t *n_work;     // their number
-    int sure;                  // items below this are there in any case (nearly always)
+    const PackedItem *work;
+    int sure;                  // the list is nearly always at least this long
     const int32_t *table;      // [S, max_pages] (paged prompts)
     int n_pages, page_shift, max_pages;
     __nv_bfloat16 *out;        // [N, H*256]: ragged tiles are stored row by row

@@ -78,12 +78,9 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
         base += total;
     }
     // offsets that overlap can ask for more tiles than the list holds
-    const int most = P.N / tq + (P.S < P.N ? P.S : P.N);
-    const int n_tiles = base < most ? base : most;
-    if (tid == 0) {
-        P.tile_base[P.S] = base;
-        *P.n_work = n_tiles;
-    }
+    const int n_tiles = base < P.most ? base : P.most;
+    for (int i = n_tiles + tid; i < P.most; i += kPrepThreads)
+        P.work[i] = PackedItem{-1, 0, 0, 0, 0, 0, {0, 0}};
     __syncthreads();
     for (int i = tid; i < n_tiles; i += kPrepThreads) {
         int lo = 0, hi = P.S - 1;  // the last s with tile_base[s] <= i
@@ -94,13 +91,13 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
             else
                 hi = mid - 1;
         }
-        const int t0 = (i - P.tile_base[lo]) * tq;
-        const int len = P.cu[lo + 1] - P.cu[lo], st = P.start ? P.start[lo] : 0;
+        const int t0 = (i - P.tile_base[lo]) * tq, row0 = P.cu[lo];
+        const int len = P.cu[lo + 1] - row0, st = P.start ? P.start[lo] : 0;
         const KeyTiles kt = prefill_key_tiles(P.kind, P.window, st + t0,
                                               st + (t0 + tq < len ? t0 + tq : len), 128,
                                               P.start != nullptr);
         const int bin = kBins - 1 - (kt.ntiles < kBins ? kt.ntiles : kBins - 1);
-        P.tiles[i] = make_int4(lo, t0, bin, 0);
+        P.tiles[i] = PackedItem{lo, t0, row0, len, st, bin, {0, 0}};
         atomicAdd(&bins[bin], 1);
     }
     __syncthreads();
@@ -119,8 +116,8 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
     }
     __syncthreads();
     for (int i = tid; i < n_tiles; i += kPrepThreads) {
-        const int4 t = P.tiles[i];
-        P.work[atomicAdd(&bins[t.z], 1)] = make_int2(t.x, t.y);
+        const PackedItem t = P.tiles[i];
+        P.work[atomicAdd(&bins[t.bin], 1)] = t;
     }
 }
 
@@ -303,7 +300,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct PackedPlan {
     long long most;  // query tiles at most: full ones, and a ragged one per sequence
     int rot_w;
-    size_t n_work, base, tiles, work, krot, bytes;
+    size_t base, tiles, work, krot, bytes;
 };
 
 PackedPlan plan_packed(int N, int S, int H, int Hkv, const spark_layer_desc *desc, bool paged) {
@@ -311,11 +308,10 @@ PackedPlan plan_packed(int N, int S, int H, int Hkv, const spark_layer_desc *des
     const int tq = 128 / (H / Hkv);
     pl.most = static_cast<long long>(N / tq) + (S < N ? S : N);
     pl.rot_w = paged ? 0 : (desc->rot_dim + 63) / 64 * 64;
-    pl.n_work = kWorkspaceHeader;
-    pl.base = pl.n_work + 256;
+    pl.base = kWorkspaceHeader;
     pl.tiles = pl.base + up256((static_cast<size_t>(S) + 1) * 4);
-    pl.work = pl.tiles + up256(static_cast<size_t>(pl.most) * sizeof(int4));
-    pl.krot = pl.work + up256(static_cast<size_t>(pl.most) * sizeof(int2));
+    pl.work = pl.tiles + up256(static_cast<size_t>(pl.most) * sizeof(PackedItem));
+    pl.krot = pl.work + up256(static_cast<size_t>(pl.most) * sizeof(PackedItem));
     pl.bytes = pl.krot + up256(static_cast<size_t>(N) * Hkv * pl.rot_w * 2);
     return pl;
 }
@@ -346,9 +342,7 @@ spark_status launch_packed_attn(const PagedParams &P, const PackedPlan &pl, int 
     A.gate_mode = P.gate_mode;
     A.rot_w = pl.rot_w;
     A.wave = sms;
-    A.pk.cu = P.cu;
     A.pk.work = P.work;
-    A.pk.n_work = P.n_work;
     A.pk.sure = P.N / tq;
     A.pk.table = P.table;
     A.pk.n_pages = P.n_pages;
@@ -440,7 +434,7 @@ spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_
     }
     const PackedPlan pl = plan_packed(N, S, H, Hkv, desc, paged);
     if (workspace_bytes < pl.bytes) return SPARK_ERR_WORKSPACE;
-    if (pl.most * Hkv > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;
+    if (pl.most * Hkv > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;  // the grid
     int sms;
     st = device_ready(&sms);
     if (st != SPARK_OK) return st;
@@ -450,9 +444,9 @@ spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_
     P.krot = reinterpret_cast<__nv_bfloat16 *>(ws + pl.krot);
     P.rot_w = pl.rot_w;
     P.tile_base = reinterpret_cast<int32_t *>(ws + pl.base);
-    P.tiles = reinterpret_cast<int4 *>(ws + pl.tiles);
-    P.work = reinterpret_cast<int2 *>(ws + pl.work);
-    P.n_work = reinterpret_cast<int32_t *>(ws + pl.n_work);
+    P.tiles = reinterpret_cast<PackedItem *>(ws + pl.tiles);
+    P.work = reinterpret_cast<PackedItem *>(ws + pl.work);
+    P.most = static_cast<int>(pl.most);
     if (paged) {
         P.start = start;
         set_pages(P, k_pages, v_pages, n_pages, page_size, table, max_pages);

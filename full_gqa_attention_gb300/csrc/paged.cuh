@@ -20,9 +20,9 @@ struct PagedParams {
     __nv_bfloat16 *krot;       // [Hkv, N, rot_w]: rotated leading key dims (packed prompts)
     int rot_w;
     int32_t *tile_base;        // [S + 1]: query tiles before each sequence
-    int4 *tiles;               // query tiles in the sequences' order: (sequence, token, bin)
-    int2 *work;                // the same, longest first
-    int32_t *n_work;
+    PackedItem *tiles;         // query tiles in the sequences' order
+    PackedItem *work;          // the same, longest first, and -1 behind them
+    int most;                  // places in the lists
     float *part_ml;            // decode: [grid, 2, G, 2] running max (base-2 units), sum
     float *part_o;             // decode: [grid, 2, G, 256] unnormalised outputs
     unsigned *counters;        // decode: a byte per CTA, left at 0 by every call

@@ -30,6 +30,8 @@
 //       band / window are never visited; boundary tiles are masked per element.
 //       Online softmax in base 2 with a lazy rescale: the reference maximum
 //       moves only when a row's maximum grows by more than 2^8.
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace spark {
@@ -206,8 +208,7 @@ constexpr int kBarODone = 6 + 2 * kSlots;
 constexpr int kBarMmaDrain = 7 + 2 * kSlots;
 constexpr int kBarOFinal = 8 + 2 * kSlots;      // every P*V done (one phase per CTA)
 constexpr int kBarMaxX = 9 + 2 * kSlots;        // 2: half-row maxima exchanged (per tile parity)
-constexpr int kBarVClean = 11 + 2 * kSlots;     // packed prefill: V of a tile is there and clean
-constexpr int kNumBars = 12 + 2 * kSlots;
+constexpr int kNumBars = 11 + 2 * kSlots;
 
 constexpr int kAttnSmemBytes = 1024 + kQBytes + kSlots * kSlotBytes + 256;
 
@@ -279,8 +280,9 @@ __device__ __forceinline__ void named_bar(int id, int n) {
 // last or first kind of place may then reach into another sequence, into slots
 // that no token was written to, or behind the window, and all of a tile's
 // queries share one V operand: a value there that is not finite would turn its
-// zero probability into NaN.  Warp 3, idle otherwise, clears those rows in
-// shared memory before P*V reads them (clean_v_tile).
+// zero probability into NaN.  The softmax warps clear those rows in shared
+// memory before they hand the tile's probabilities over (clean_v_rows, boundary
+// tiles only; one warp doing it alone took 10 us a tile).
 enum KvSource : int {
     kKvFromQkv = 0,
     kKvFromCache = 1,
@@ -303,32 +305,32 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t w) {
            ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// One warp's pass over a V slot (32 keys x 256 dims, first key key0) of a tile
-// that needs a mask, for the queries a0..a_last: rows that none of them sees
-// become zero; in rows that only some of them see, values that are not finite
-// become zero (returns true if there was one: the epilogue gives it back to the
-// rows that see it).
-__device__ __forceinline__ bool clean_v_slot(uint8_t *slot, int kind, int window, int key0,
-                                             int a0, int a_last, int lane) {
+// A softmax warp's share (16 rows from row0) of the V tile of a key tile that
+// needs a mask (kBN keys x 256 dims from key0, in the four ring slots from `use`
+// on), for the queries a0..a_last: rows that none of them sees become zero; in
+// rows that only some of them see, values that are not finite become zero
+// (returns true if this lane met one: the epilogue gives it back to the rows
+// that see it).
+__device__ __noinline__ bool clean_v_rows(uint8_t *ring, int use, int kind, int window,
+                                             int key0, int a0, int a_last, int row0, int lane) {
+    uint8_t *slot = ring + ((use + (row0 >> 5)) % kSlots) * kSlotBytes +
+                    (lane >> 3) * (kSlotBytes / 4) + (row0 & 31) * 128 + (lane & 7) * 16;
     bool found = false;
 #pragma unroll 4
-    for (int r = 0; r < 32; ++r) {
-        const int key = key0 + r;
-        const bool all = key <= a0 && (kind == kLayerFull || a_last - key < window);
-        if (all) continue;
-        const bool none = key > a_last || (kind == kLayerSliding && a0 - key >= window);
-        uint4 *p = reinterpret_cast<uint4 *>(slot + (lane >> 3) * (kSlotBytes / 4) + r * 128 +
-                                             (lane & 7) * 16);
-        if (none) {
+    for (int r = 0; r < 16; ++r) {
+        const int key = key0 + row0 + r;
+        if (key <= a0 && (kind == kLayerFull || a_last - key < window)) continue;  // seen by all
+        uint4 *p = reinterpret_cast<uint4 *>(slot + r * 128);
+        if (key > a_last || (kind == kLayerSliding && a0 - key >= window)) {
             *p = make_uint4(0, 0, 0, 0);
-        } else {
-            const uint4 w = *p;
-            const uint32_t mx = nonfinite_mask(w.x), my = nonfinite_mask(w.y);
-            const uint32_t mz = nonfinite_mask(w.z), mw = nonfinite_mask(w.w);
-            if (mx | my | mz | mw) {
-                *p = make_uint4(w.x & ~mx, w.y & ~my, w.z & ~mz, w.w & ~mw);
-                found = true;
-            }
+            continue;
+        }
+        const uint4 w = *p;
+        const uint32_t mx = nonfinite_mask(w.x), my = nonfinite_mask(w.y);
+        const uint32_t mz = nonfinite_mask(w.z), mw = nonfinite_mask(w.w);
+        if (mx | my | mz | mw) {
+            *p = make_uint4(w.x & ~mx, w.y & ~my, w.z & ~mz, w.w & ~mw);
+            found = true;
         }
     }
     return found;
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // list has nothing to do, and finds out before it sets anything up
         if (static_cast<int>(blockIdx.x) / units >= P.pk.sure) {
             grid_dep_wait();
-            if (static_cast<int>(blockIdx.x) / units >= *P.pk.n_work) return;
+            if (P.pk.work[static_cast<int>(blockIdx.x) / units].seq < 0) return;
         }
     }
 
@@ -418,18 +420,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int start = 0;
     bool skip = false;
     if constexpr (kIsPacked) {
-        const int item = static_cast<int>(blockIdx.x) / units;
-        skip = item >= *P.pk.n_work;
-        if (!skip) {
-            const int2 w = P.pk.work[item];
-            seq = w.x;
-            t0 = w.y;
-            row0 = P.pk.cu[seq];
-            seq_end = P.pk.cu[seq + 1] - row0;
-            if (kSrc == kKvPages) start = P.start[seq];
-        } else {
-            t0 = 0;
-        }
+        const PackedItem w = P.pk.work[static_cast<int>(blockIdx.x) / units];
+        skip = w.seq < 0;
+        seq = w.seq;
+        t0 = w.t0;
+        row0 = w.row0;
+        seq_end = w.len;
+        start = w.start;
         t_end = (t0 + tq < seq_end) ? t0 + tq : seq_end;
     } else if constexpr (kSrc != kKvFromQkv) {
         start = P.start[b];
@@ -462,9 +459,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int nrem = static_cast<int>(nb % units);
                 int nt0;
                 if constexpr (kIsPacked) {
-                    const int ni = static_cast<int>(nb / units);
-                    const int2 w = ni < *P.pk.n_work ? P.pk.work[ni] : make_int2(seq, t0);
-                    nt0 = P.pk.cu[w.x] + w.y;
+                    const PackedItem w = P.pk.work[nb / units];
+                    nt0 = w.row0 + w.t0;
                 } else {
                     nt0 = (P.n_qtiles - 1 - static_cast<int>(nb / units)) * tq;
                 }
@@ -483,42 +479,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mbar_arrive_expect_tx(&bars[kBarSlotFull + slot], kSlotBytes);
                 return true;
             };
-            // The page that holds key `key` (a multiple of 16), or one past the
-            // pool where no query of this CTA sees a key of that page: the
-            // copy then reads zeros.
-            auto page_of = [&](int key) -> int {
-                const int last = start + t_end - 1;
-                const int lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
-                const int index = key >> P.pk.page_shift;
-                if (key > last || ((index + 1) << P.pk.page_shift) <= lo) return P.pk.n_pages;
-                const int id = P.pk.table[static_cast<size_t>(seq) * P.pk.max_pages + index];
-                if (id >= 0 && id < P.pk.n_pages) return id;
-                atomicOr(P.status, kErrPage);
-                return P.pk.n_pages;
-            };
             auto load_k = [&](int j) -> bool {
                 const int key0 = kv_lo + j * kBN;
-                int ids[8];
-                if constexpr (kSrc == kKvPages) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        ids[i] = i < (kBN >> P.pk.page_shift) || i == 0
-                                     ? page_of(key0 + (i << P.pk.page_shift))
-                                     : 0;
-                }
                 for (int c = 0; c < 4; ++c) {
                     int slot;
                     if (!next_slot(slot)) return false;
                     uint8_t *dst = ring + slot * kSlotBytes;
-                    if constexpr (kSrc == kKvPages) {
-                        const int page = 1 << P.pk.page_shift;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i == 0 || i * page < kBN)
-                                tma_load_4d(dst + i * page * 128, &tm_kv_k,
-                                            &bars[kBarSlotFull + slot], c * 64, key0 & (page - 1),
-                                            g, ids[i]);
-                    } else if constexpr (kSrc == kKvPacked) {
+                    if constexpr (kSrc == kKvPacked) {
                         if (c * 64 < P.rot_w)
                             tma_load_3d(dst, &tm_krot, &bars[kBarSlotFull + slot], c * 64,
                                         row0 + key0, g);
@@ -547,21 +514,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     int slot;
                     if (!next_slot(slot)) return false;
                     uint8_t *dst = ring + slot * kSlotBytes;
-                    if constexpr (kSrc == kKvPages) {
-                        const int page = 1 << P.pk.page_shift;
-                        const int key = key0 + vs * 32;
-                        const int id0 = page_of(key);
-                        const int id1 = page < 32 ? page_of(key + 16) : 0;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            tma_load_4d(dst + c * (kSlotBytes / 4), &tm_kv_v,
-                                        &bars[kBarSlotFull + slot], c * 64, key & (page - 1), g,
-                                        id0);
-                            if (page < 32)
-                                tma_load_4d(dst + c * (kSlotBytes / 4) + 16 * 128, &tm_kv_v,
-                                            &bars[kBarSlotFull + slot], c * 64, 0, g, id1);
-                        }
-                    } else if constexpr (kSrc == kKvPacked) {
+                    if constexpr (kSrc == kKvPacked) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             tma_load_4d(dst + c * (kSlotBytes / 4), &tm_kv_v,
@@ -585,11 +538,115 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 return true;
             };
-            ok = load_k(0);
-            if (ok && ntiles > 1) ok = load_k(1);
-            for (int j = 0; ok && j < ntiles; ++j) {
-                ok = load_v(j);
-                if (ok && j + 2 < ntiles) ok = load_k(j + 2);
+            if constexpr (kSrc != kKvPages) {
+                ok = load_k(0);
+                if (ok && ntiles > 1) ok = load_k(1);
+                for (int j = 0; ok && j < ntiles; ++j) {
+                    ok = load_v(j);
+                    if (ok && j + 2 < ntiles) ok = load_k(j + 2);
+                }
+            } else {
+                // Keys and values in pages: a tile is kPieces boxes, one per page.
+                // What stands between a slot's release and its refill delays
+                // every tile (the ring is two tiles deep), so the page numbers
+                // are looked up a tile ahead and kept in registers, and the
+                // number of pieces is fixed at compile time: looking them up
+                // behind the wait took 860 us where the contiguous cache takes
+                // 475 (2048 tokens on 16384), issuing from several lanes 1390.
+                const int shift = P.pk.page_shift, pmask = (1 << shift) - 1;
+                const int last = start + t_end - 1;
+                const int lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
+                const int32_t *pages = P.pk.table + static_cast<size_t>(seq) * P.pk.max_pages;
+                const int none = P.pk.n_pages;  // past the pool: the copy reads zeros
+                bool bad = false;
+                auto walk = [&](auto count) {
+                    constexpr int kPieces = decltype(count)::value;
+                    constexpr int kStep = kBN / kPieces;  // keys per piece
+                    int idv[kPieces], idv1[kPieces], idk[kPieces], next[kPieces];
+                    // the pages of a tile; those that no query sees a key of are
+                    // not looked up
+                    auto seen = [&](int key) { return key <= last && (key | pmask) >= lo; };
+                    auto fetch = [&](int tile, int(&id)[kPieces]) {
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            const int key = kv_lo + tile * kBN + i * kStep;
+                            id[i] = none;
+                            if (seen(key)) id[i] = pages[key >> shift];
+                        }
+                    };
+                    auto check = [&](int tile, int(&id)[kPieces]) {
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(none) &&
+                                seen(kv_lo + tile * kBN + i * kStep)) {
+                                bad = true;
+                                id[i] = none;
+                            }
+                        }
+                    };
+                    auto k_tile = [&](int j, const int(&id)[kPieces]) -> bool {
+                        const int at = (kv_lo + j * kBN) & pmask;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            int slot;
+                            if (!next_slot(slot)) return false;
+#pragma unroll
+                            for (int i = 0; i < kPieces; ++i)
+                                tma_load_4d(ring + slot * kSlotBytes + i * kStep * 128, &tm_kv_k,
+                                            &bars[kBarSlotFull + slot], c * 64, at, g, id[i]);
+                            ++sc;
+                        }
+                        return true;
+                    };
+                    auto v_tile = [&](int j, const int(&id)[kPieces]) -> bool {
+                        const int at = (kv_lo + j * kBN) & pmask;
+#pragma unroll
+                        for (int vs = 0; vs < 4; ++vs) {
+                            int slot;
+                            if (!next_slot(slot)) return false;
+                            // 32 keys: part of a piece, one, or two of 16
+                            constexpr int kBox = kStep < 32 ? kStep : 32;
+#pragma unroll
+                            for (int i = 0; i < 32 / kBox; ++i) {
+                                const int r = vs * 32 + i * kBox;
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    tma_load_4d(ring + slot * kSlotBytes +
+                                                    c * (kSlotBytes / 4) + i * kBox * 128,
+                                                &tm_kv_v, &bars[kBarSlotFull + slot], c * 64,
+                                                at + r % kStep, g, id[r / kStep]);
+                            }
+                            ++sc;
+                        }
+                        return true;
+                    };
+                    fetch(0, idv);
+                    fetch(1, idv1);
+                    fetch(2, idk);
+                    check(0, idv);
+                    check(1, idv1);
+                    ok = k_tile(0, idv);
+                    if (ok && ntiles > 1) ok = k_tile(1, idv1);
+                    for (int j = 0; ok && j < ntiles; ++j) {
+                        fetch(j + 3, next);
+                        check(j + 2, idk);
+                        ok = v_tile(j, idv);
+                        if (ok && j + 2 < ntiles) ok = k_tile(j + 2, idk);
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            idv[i] = idv1[i];
+                            idv1[i] = idk[i];
+                            idk[i] = next[i];
+                        }
+                    }
+                };
+                switch (shift) {
+                    case 4: walk(std::integral_constant<int, 8>()); break;
+                    case 5: walk(std::integral_constant<int, 4>()); break;
+                    case 6: walk(std::integral_constant<int, 2>()); break;
+                    default: walk(std::integral_constant<int, 1>()); break;
+                }
+                if (bad) atomicOr(P.status, kErrPage);
             }
         }
         __syncwarp();
@@ -654,9 +711,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             auto mma_pv = [&](int j) -> bool {
                 const uint32_t pcol = tmem + kColS + (j & 1) * kBN;
-                if (kIsPacked &&
-                    !mbar_wait(&bars[kBarVClean], j & 1, &abort_flag, P.status))
-                    return false;
                 for (int vs = 0; vs < 4; ++vs) {
                     const int slot = sc % kSlots;
                     if (!mbar_wait(&bars[kBarSlotFull + slot], (sc / kSlots) & 1, &abort_flag,
@@ -842,6 +896,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_st32(sbase + wg * 64, pk);
             tmem_st_wait();
             tc_fence_before();
+            if constexpr (kIsPacked) {
+                if (tile_needs_mask(kind, P.window, key0, kBN, a0, a_last)) {
+                    // V_j comes after min(ntiles, j + 2) K tiles and j V tiles.
+                    // The slots' use before it was K_j (the last tile: S_j says
+                    // that it landed), K0 (the first) or V_{j-1}, which P*V of
+                    // tile j-1 says: a parity wait must not begin a phase early.
+                    const int use = 4 * ((ntiles < j + 2 ? ntiles : j + 2) + j);
+                    if (j > 0 && j + 1 < ntiles)
+                        ok = mbar_wait(&bars[kBarODone], (j - 1) & 1, &abort_flag, P.status);
+                    const int slot = use + ((warp - kSoftmaxWarp0) >> 1);  // 32 keys each
+                    if (ok)
+                        ok = mbar_wait(&bars[kBarSlotFull + slot % kSlots], (slot / kSlots) & 1,
+                                       &abort_flag, P.status);
+                    if (!ok) break;
+                    if (clean_v_rows(ring, use, kind, P.window, key0, a0, a_last,
+                                     (warp - kSoftmaxWarp0) * 16, lane))
+                        cleaned_any = 1;
+                    fence_proxy_async_smem();
+                }
+            }
             mbar_arrive(&bars[kBarPReady + (j & 1)]);
         }
 
@@ -944,43 +1018,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc_fence_before();
         __syncthreads();
     } else {
-        // ------------------------------------------------------ V cleaner
-        // (packed sources; warp 3 has no role otherwise)  Follows the V slots of
-        // every tile in order and hands each tile to the P*V issuer, after a pass
-        // over it where the tile needs a mask.
-        if constexpr (kIsPacked) {
-            if (!skip) {
-                bool ok = true;
-                auto wait_slot = [&](int use) -> bool {
-                    return mbar_wait(&bars[kBarSlotFull + use % kSlots], (use / kSlots) & 1,
-                                     &abort_flag, P.status);
-                };
-                // K0 came first into the slots that V tiles reuse: a wait for a
-                // later phase of a barrier must not begin before its first
-                for (int i = 0; ok && i < 4; ++i) ok = wait_slot(i);
-                int sc = ntiles > 1 ? 8 : 4;
-                const int a_last = start + t_end - 1;
-                for (int j = 0; ok && j < ntiles; ++j) {
-                    const int key0 = kv_lo + j * kBN;
-                    const bool masked = tile_needs_mask(kind, P.window, key0, kBN, a0, a_last);
-                    bool found = false;
-                    for (int vs = 0; ok && vs < 4; ++vs, ++sc) {
-                        ok = wait_slot(sc);
-                        if (ok && masked)
-                            found |= clean_v_slot(ring + (sc % kSlots) * kSlotBytes, kind,
-                                                  P.window, key0 + vs * 32, a0, a_last, lane);
-                    }
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    if (masked) {
-                        if (found) cleaned_any = 1;
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (lane == 0) mbar_arrive(&bars[kBarVClean]);
-                    if (j + 2 < ntiles) sc += 4;  // K_{j+2}
-                }
-            }
-        }
+        // warp 3 has no role
         __syncthreads();
     }
 }
