@@ -305,36 +305,243 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t w) {
            ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// A softmax warp's share (16 rows from row0) of the V tile of a key tile that
-// needs a mask (kBN keys x 256 dims from key0, in the four ring slots from `use`
-// on), for the queries a0..a_last: rows that none of them sees become zero; in
-// rows that only some of them see, values that are not finite become zero
-// (returns true if this lane met one: the epilogue gives it back to the rows
+// The rows of a key tile (kBN keys from key0) for the queries a0..a_last:
+// [none_lo, none_hi) are seen by some of them, [all_lo, all_hi) by all.
+struct TileRows {
+    int none_lo, none_hi, all_lo, all_hi;
+};
+
+__device__ __forceinline__ TileRows tile_rows(int kind, int window, int key0, int a0, int a_last) {
+    auto clamp = [](int x) { return x < 0 ? 0 : (x < kBN ? x : kBN); };
+    TileRows t;
+    t.none_lo = kind == kLayerSliding ? clamp(a0 - window + 1 - key0) : 0;
+    t.all_lo = kind == kLayerSliding ? clamp(a_last - window + 1 - key0) : 0;
+    t.all_hi = clamp(a0 + 1 - key0);
+    t.none_hi = clamp(a_last + 1 - key0);
+    return t;
+}
+
+// A softmax warp's share of V of a key tile that needs a mask (in the four
+// ring slots from `use` on): the rows that not every query sees.  Those that no
+// query sees become zero; in the others, values that are not finite become zero
+// (returns true if this lane met one: the epilogue gives it back to the queries
 // that see it).
-__device__ __noinline__ bool clean_v_rows(uint8_t *ring, int use, int kind, int window,
-                                             int key0, int a0, int a_last, int row0, int lane) {
-    uint8_t *slot = ring + ((use + (row0 >> 5)) % kSlots) * kSlotBytes +
-                    (lane >> 3) * (kSlotBytes / 4) + (row0 & 31) * 128 + (lane & 7) * 16;
+__device__ __forceinline__ bool clean_v_rows(uint8_t *ring, int use, const TileRows &t, int w,
+                                             int lane) {
+    // Row w + 8 i is at a constant distance from row w (`use` is a multiple of
+    // 4, so the slots do not wrap): bit i of a mask stands for it, and the
+    // passes unroll to plain stores and loads.
+    uint8_t *base = ring + (use % kSlots) * kSlotBytes + (lane >> 3) * (kSlotBytes / 4) +
+                    w * 128 + (lane & 7) * 16;
+    auto at = [&](int i) {
+        return reinterpret_cast<uint4 *>(base + (i >> 2) * kSlotBytes + (i & 3) * 1024);
+    };
+    auto below = [&](int row) -> uint32_t {  // rows w + 8 i < row
+        const int n = (row - w + 7) >> 3;
+        return (1u << (n < 0 ? 0 : (n < 16 ? n : 16))) - 1u;
+    };
+    const uint32_t none = (below(t.none_lo) | ~below(t.none_hi)) & 0xFFFFu;
+    const uint32_t all = below(t.all_hi) & ~below(t.all_lo);
+    const uint32_t part = ~(none | all) & 0xFFFFu;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (none >> i & 1u) *at(i) = make_uint4(0, 0, 0, 0);
     bool found = false;
-#pragma unroll 4
-    for (int r = 0; r < 16; ++r) {
-        const int key = key0 + row0 + r;
-        if (key <= a0 && (kind == kLayerFull || a_last - key < window)) continue;  // seen by all
-        uint4 *p = reinterpret_cast<uint4 *>(slot + r * 128);
-        if (key > a_last || (kind == kLayerSliding && a0 - key >= window)) {
-            *p = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        const uint4 w = *p;
-        const uint32_t mx = nonfinite_mask(w.x), my = nonfinite_mask(w.y);
-        const uint32_t mz = nonfinite_mask(w.z), mw = nonfinite_mask(w.w);
-        if (mx | my | mz | mw) {
-            *p = make_uint4(w.x & ~mx, w.y & ~my, w.z & ~mz, w.w & ~mw);
-            found = true;
+#pragma unroll
+    for (int i0 = 0; i0 < 16; i0 += 4) {
+        if (!(part >> i0 & 15u)) continue;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = part >> (i0 + i) & 1u ? *at(i0 + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // an exponent of all ones carries into the sign's place
+            const uint32_t hit = ((v[i].x & 0x7F807F80u) + 0x00800080u) |
+                                 ((v[i].y & 0x7F807F80u) + 0x00800080u) |
+                                 ((v[i].z & 0x7F807F80u) + 0x00800080u) |
+                                 ((v[i].w & 0x7F807F80u) + 0x00800080u);
+            if (hit & 0x80008000u) {
+                *at(i0 + i) = make_uint4(
+                    v[i].x & ~nonfinite_mask(v[i].x), v[i].y & ~nonfinite_mask(v[i].y),
+                    v[i].z & ~nonfinite_mask(v[i].z), v[i].w & ~nonfinite_mask(v[i].w));
+                found = true;
+            }
         }
     }
     return found;
 }
+
+// The copies of a packed source's key and value tiles into the ring, by one
+// thread in the order of the issuers: K0, K1, then V_j and K_{j+2} for every
+// tile j.
+//
+// With pages a tile is a box per page.  What stands between a slot's release
+// and its refill delays every tile, so the page numbers are looked up a tile
+// ahead and kept in registers, and the number of pieces is fixed at compile
+// time: looking them up behind the wait took 860 us where the contiguous cache
+// takes 475 (2048 tokens on 16384), issuing from several lanes 1390.  A second
+// thread for V was 5 % slower: its copies then queue behind K tiles that are
+// not urgent.  Pages of 16 need 64 small copies a tile, which the copy engine
+// itself bounds (890 us).
+template <int kSrc>
+struct PackedTiles {
+    const CUtensorMap &tm_k, &tm_v, &tm_krot;
+    const PrefillParams &P;
+    uint8_t *ring;
+    uint64_t *bars;
+    volatile int *abort_flag;
+    int kind, ntiles, kv_lo, a0, last;  // last: index of the last query
+    int row0, seq, g;
+
+    // Waits until ring use `sc` may be filled, and arms its barrier.
+    __device__ __forceinline__ bool take(int sc, int &slot) const {
+        slot = sc % kSlots;
+        if (sc >= kSlots && !mbar_wait(&bars[kBarSlotEmpty + slot], ((sc / kSlots) - 1) & 1,
+                                       abort_flag, P.status))
+            return false;
+        mbar_arrive_expect_tx(&bars[kBarSlotFull + slot], kSlotBytes);
+        return true;
+    }
+
+    // Copies every tile; returns the ring uses that were begun.
+    __device__ __forceinline__ int load() const {
+        if constexpr (kSrc == kKvPages) {
+            switch (P.pk.page_shift) {
+                case 4: return load_pages<8>();
+                case 5: return load_pages<4>();
+                case 6: return load_pages<2>();
+                default: return load_pages<1>();
+            }
+        } else {
+            int sc = 0;
+            auto k_tile = [&](int j) -> bool {
+                const int row = row0 + kv_lo + j * kBN;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    int slot;
+                    if (!take(sc, slot)) return false;
+                    uint8_t *dst = ring + slot * kSlotBytes;
+                    if (c * 64 < P.rot_w)
+                        tma_load_3d(dst, &tm_krot, &bars[kBarSlotFull + slot], c * 64, row, g);
+                    else
+                        tma_load_4d(dst, &tm_k, &bars[kBarSlotFull + slot], c * 64, P.H + g, row,
+                                    0);
+                    ++sc;
+                }
+                return true;
+            };
+            auto v_tile = [&](int j) -> bool {
+                const int row = row0 + kv_lo + j * kBN;
+                for (int vs = 0; vs < 4; ++vs) {
+                    int slot;
+                    if (!take(sc, slot)) return false;
+                    uint8_t *dst = ring + slot * kSlotBytes;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tma_load_4d(dst + c * (kSlotBytes / 4), &tm_v, &bars[kBarSlotFull + slot],
+                                    c * 64, P.H + P.Hkv + g, row + vs * 32, 0);
+                    ++sc;
+                }
+                return true;
+            };
+            bool ok = k_tile(0);
+            if (ok && ntiles > 1) ok = k_tile(1);
+            for (int j = 0; ok && j < ntiles; ++j) {
+                ok = v_tile(j);
+                if (ok && j + 2 < ntiles) ok = k_tile(j + 2);
+            }
+            return sc;
+        }
+    }
+
+    template <int kPieces>
+    __device__ __forceinline__ int load_pages() const {
+        constexpr int kStep = kBN / kPieces;  // keys per piece
+        constexpr int kBox = kStep < 32 ? kStep : 32;  // keys per V box
+        const int shift = P.pk.page_shift, pmask = (1 << shift) - 1;
+        const int lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
+        const int32_t *pages = P.pk.table + static_cast<size_t>(seq) * P.pk.max_pages;
+        const int none = P.pk.n_pages;  // past the pool: the copy reads zeros
+        int idv[kPieces], idv1[kPieces], idk[kPieces], next[kPieces];
+        int sc = 0;
+        bool bad = false;
+        // pages that no query sees a key of are not looked up
+        auto seen = [&](int key) { return key <= last && (key | pmask) >= lo; };
+        auto fetch = [&](int tile, int(&id)[kPieces]) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int key = kv_lo + tile * kBN + i * kStep;
+                id[i] = none;
+                if (seen(key)) id[i] = pages[key >> shift];
+            }
+        };
+        auto check = [&](int tile, int(&id)[kPieces]) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(none) &&
+                    seen(kv_lo + tile * kBN + i * kStep)) {
+                    bad = true;
+                    id[i] = none;
+                }
+        };
+        auto k_tile = [&](int j, const int(&id)[kPieces]) -> bool {
+            const int at = (kv_lo + j * kBN) & pmask;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                int slot;
+                if (!take(sc, slot)) return false;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    tma_load_4d(ring + slot * kSlotBytes + i * kStep * 128, &tm_k,
+                                &bars[kBarSlotFull + slot], c * 64, at, g, id[i]);
+                ++sc;
+            }
+            return true;
+        };
+        auto v_tile = [&](int j, const int(&id)[kPieces]) -> bool {
+            const int at = (kv_lo + j * kBN) & pmask;
+#pragma unroll
+            for (int vs = 0; vs < 4; ++vs) {
+                int slot;
+                if (!take(sc, slot)) return false;
+#pragma unroll
+                for (int i = 0; i < 32 / kBox; ++i) {
+                    const int r = vs * 32 + i * kBox;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tma_load_4d(ring + slot * kSlotBytes + c * (kSlotBytes / 4) +
+                                        i * kBox * 128,
+                                    &tm_v, &bars[kBarSlotFull + slot], c * 64, at + r % kStep, g,
+                                    id[r / kStep]);
+                }
+                ++sc;
+            }
+            return true;
+        };
+        fetch(0, idv);
+        fetch(1, idv1);
+        fetch(2, idk);
+        check(0, idv);
+        bool ok = k_tile(0, idv);
+        check(1, idv1);
+        if (ok && ntiles > 1) ok = k_tile(1, idv1);
+        for (int j = 0; ok && j < ntiles; ++j) {
+            fetch(j + 3, next);
+            check(j + 2, idk);
+            ok = v_tile(j, idv);
+            if (ok && j + 2 < ntiles) ok = k_tile(j + 2, idk);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                idv[i] = idv1[i];
+                idv1[i] = idk[i];
+                idk[i] = next[i];
+            }
+        }
+        if (bad) atomicOr(P.status, kErrPage);
+        return sc;
+    }
+};
 
 // kG: the GQA group size when fixed at compile time (the Spark-X2.5 shapes
 // all use 4), 0 to read it from P.G.  Timing chose the fixed size for the
@@ -440,6 +647,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                           kSrc == kKvFromRing || kSrc == kKvPages);
     const int kv_lo = kt.kv_lo;
     const int ntiles = skip ? 0 : kt.ntiles;
+    const PackedTiles<kSrc> packed_tiles{tm_kv_k, tm_kv_v, tm_krot, P, ring, bars, &abort_flag,
+                                         kind, ntiles, kv_lo, a0, start + t_end - 1, row0, seq, g};
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -485,14 +694,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     int slot;
                     if (!next_slot(slot)) return false;
                     uint8_t *dst = ring + slot * kSlotBytes;
-                    if constexpr (kSrc == kKvPacked) {
-                        if (c * 64 < P.rot_w)
-                            tma_load_3d(dst, &tm_krot, &bars[kBarSlotFull + slot], c * 64,
-                                        row0 + key0, g);
-                        else
-                            tma_load_4d(dst, &tm_kv_k, &bars[kBarSlotFull + slot], c * 64,
-                                        P.H + g, row0 + key0, 0);
-                    } else if constexpr (kSrc != kKvFromQkv) {
+                    if constexpr (kSrc != kKvFromQkv) {
                         const int slot0 =
                             kSrc == kKvFromRing ? key0 % static_cast<int>(P.cap) : key0;
                         tma_load_4d(dst, &tm_kv_k, &bars[kBarSlotFull + slot], c * 64, slot0, g,
@@ -514,13 +716,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     int slot;
                     if (!next_slot(slot)) return false;
                     uint8_t *dst = ring + slot * kSlotBytes;
-                    if constexpr (kSrc == kKvPacked) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            tma_load_4d(dst + c * (kSlotBytes / 4), &tm_kv_v,
-                                        &bars[kBarSlotFull + slot], c * 64, P.H + P.Hkv + g,
-                                        row0 + key0 + vs * 32, 0);
-                    } else if constexpr (kSrc != kKvFromQkv) {
+                    if constexpr (kSrc != kKvFromQkv) {
                         const int slot0 =
                             kSrc == kKvFromRing ? key0 % static_cast<int>(P.cap) : key0;
 #pragma unroll
@@ -538,7 +734,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 return true;
             };
-            if constexpr (kSrc != kKvPages) {
+            if constexpr (!kIsPacked) {
                 ok = load_k(0);
                 if (ok && ntiles > 1) ok = load_k(1);
                 for (int j = 0; ok && j < ntiles; ++j) {
@@ -546,107 +742,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (ok && j + 2 < ntiles) ok = load_k(j + 2);
                 }
             } else {
-                // Keys and values in pages: a tile is kPieces boxes, one per page.
-                // What stands between a slot's release and its refill delays
-                // every tile (the ring is two tiles deep), so the page numbers
-                // are looked up a tile ahead and kept in registers, and the
-                // number of pieces is fixed at compile time: looking them up
-                // behind the wait took 860 us where the contiguous cache takes
-                // 475 (2048 tokens on 16384), issuing from several lanes 1390.
-                const int shift = P.pk.page_shift, pmask = (1 << shift) - 1;
-                const int last = start + t_end - 1;
-                const int lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
-                const int32_t *pages = P.pk.table + static_cast<size_t>(seq) * P.pk.max_pages;
-                const int none = P.pk.n_pages;  // past the pool: the copy reads zeros
-                bool bad = false;
-                auto walk = [&](auto count) {
-                    constexpr int kPieces = decltype(count)::value;
-                    constexpr int kStep = kBN / kPieces;  // keys per piece
-                    int idv[kPieces], idv1[kPieces], idk[kPieces], next[kPieces];
-                    // the pages of a tile; those that no query sees a key of are
-                    // not looked up
-                    auto seen = [&](int key) { return key <= last && (key | pmask) >= lo; };
-                    auto fetch = [&](int tile, int(&id)[kPieces]) {
-#pragma unroll
-                        for (int i = 0; i < kPieces; ++i) {
-                            const int key = kv_lo + tile * kBN + i * kStep;
-                            id[i] = none;
-                            if (seen(key)) id[i] = pages[key >> shift];
-                        }
-                    };
-                    auto check = [&](int tile, int(&id)[kPieces]) {
-#pragma unroll
-                        for (int i = 0; i < kPieces; ++i) {
-                            if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(none) &&
-                                seen(kv_lo + tile * kBN + i * kStep)) {
-                                bad = true;
-                                id[i] = none;
-                            }
-                        }
-                    };
-                    auto k_tile = [&](int j, const int(&id)[kPieces]) -> bool {
-                        const int at = (kv_lo + j * kBN) & pmask;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            int slot;
-                            if (!next_slot(slot)) return false;
-#pragma unroll
-                            for (int i = 0; i < kPieces; ++i)
-                                tma_load_4d(ring + slot * kSlotBytes + i * kStep * 128, &tm_kv_k,
-                                            &bars[kBarSlotFull + slot], c * 64, at, g, id[i]);
-                            ++sc;
-                        }
-                        return true;
-                    };
-                    auto v_tile = [&](int j, const int(&id)[kPieces]) -> bool {
-                        const int at = (kv_lo + j * kBN) & pmask;
-#pragma unroll
-                        for (int vs = 0; vs < 4; ++vs) {
-                            int slot;
-                            if (!next_slot(slot)) return false;
-                            // 32 keys: part of a piece, one, or two of 16
-                            constexpr int kBox = kStep < 32 ? kStep : 32;
-#pragma unroll
-                            for (int i = 0; i < 32 / kBox; ++i) {
-                                const int r = vs * 32 + i * kBox;
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    tma_load_4d(ring + slot * kSlotBytes +
-                                                    c * (kSlotBytes / 4) + i * kBox * 128,
-                                                &tm_kv_v, &bars[kBarSlotFull + slot], c * 64,
-                                                at + r % kStep, g, id[r / kStep]);
-                            }
-                            ++sc;
-                        }
-                        return true;
-                    };
-                    fetch(0, idv);
-                    fetch(1, idv1);
-                    fetch(2, idk);
-                    check(0, idv);
-                    check(1, idv1);
-                    ok = k_tile(0, idv);
-                    if (ok && ntiles > 1) ok = k_tile(1, idv1);
-                    for (int j = 0; ok && j < ntiles; ++j) {
-                        fetch(j + 3, next);
-                        check(j + 2, idk);
-                        ok = v_tile(j, idv);
-                        if (ok && j + 2 < ntiles) ok = k_tile(j + 2, idk);
-#pragma unroll
-                        for (int i = 0; i < kPieces; ++i) {
-                            idv[i] = idv1[i];
-                            idv1[i] = idk[i];
-                            idk[i] = next[i];
-                        }
-                    }
-                };
-                switch (shift) {
-                    case 4: walk(std::integral_constant<int, 8>()); break;
-                    case 5: walk(std::integral_constant<int, 4>()); break;
-                    case 6: walk(std::integral_constant<int, 2>()); break;
-                    default: walk(std::integral_constant<int, 1>()); break;
-                }
-                if (bad) atomicOr(P.status, kErrPage);
+                sc = packed_tiles.load();
             }
         }
         __syncwarp();
@@ -905,13 +1001,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     const int use = 4 * ((ntiles < j + 2 ? ntiles : j + 2) + j);
                     if (j > 0 && j + 1 < ntiles)
                         ok = mbar_wait(&bars[kBarODone], (j - 1) & 1, &abort_flag, P.status);
-                    const int slot = use + ((warp - kSoftmaxWarp0) >> 1);  // 32 keys each
-                    if (ok)
-                        ok = mbar_wait(&bars[kBarSlotFull + slot % kSlots], (slot / kSlots) & 1,
-                                       &abort_flag, P.status);
+                    const TileRows rows = tile_rows(kind, P.window, key0, a0, a_last);
+                    for (int vs = 0; ok && vs < 4; ++vs)
+                        ok = mbar_wait(&bars[kBarSlotFull + (use + vs) % kSlots],
+                                       ((use + vs) / kSlots) & 1, &abort_flag, P.status);
                     if (!ok) break;
-                    if (clean_v_rows(ring, use, kind, P.window, key0, a0, a_last,
-                                     (warp - kSoftmaxWarp0) * 16, lane))
+                    if (clean_v_rows(ring, use, rows, warp - kSoftmaxWarp0, lane))
                         cleaned_any = 1;
                     fence_proxy_async_smem();
                 }
