@@ -121,12 +121,19 @@ struct __align__(16) PackedItem {
     int t0;                    // its first token inside the sequence
     int row0, len;             // the sequence's first row, its tokens
     int start;                 // tokens in its pages before the call
-    int bin, pad[2];
+    int bin;
+    unsigned call;             // the call's number: which word of odd_values is its own
+    int pad;
 };
 
 struct PackedInfo {
     const PackedItem *work;
-    int sure;                  // the list is nearly always at least this long
+    // Whether any value V of the call is not finite (no cache: the kernel before
+    // the attention kernel looks at all of them).  Two words take turns: a call
+    // sets its own and clears the next one's.  Whatever they held before, the
+    // worst is a needless pass over boundary tiles.
+    const unsigned *odd_values;
+    unsigned *call;            // calls so far (modulo anything even)
     const int32_t *table;      // [S, max_pages] (paged prompts)
     int n_pages, page_shift, max_pages;
     __nv_bfloat16 *out;        // [N, H*256]: ragged tiles are stored row by row

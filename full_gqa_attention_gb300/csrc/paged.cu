@@ -56,6 +56,8 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
     const int tid = threadIdx.x, tq = 128 / P.G;
     const long long cap = static_cast<long long>(P.max_pages) << P.page_shift;
     for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
+    const unsigned call = *P.call;  // the attention kernel counts it on
+    if (tid == 0) P.odd_values[(call + 1) & 1] = 0;
     int base = 0;
     for (int s0 = 0; s0 < P.S; s0 += kPrepThreads) {
         const int s = s0 + tid;
@@ -80,7 +82,7 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
     // offsets that overlap can ask for more tiles than the list holds
     const int n_tiles = base < P.most ? base : P.most;
     for (int i = n_tiles + tid; i < P.most; i += kPrepThreads)
-        P.work[i] = PackedItem{-1, 0, 0, 0, 0, 0, {0, 0}};
+        P.work[i] = PackedItem{-1, 0, 0, 0, 0, 0, call, 0};
     __syncthreads();
     for (int i = tid; i < n_tiles; i += kPrepThreads) {
         int lo = 0, hi = P.S - 1;  // the last s with tile_base[s] <= i
@@ -97,7 +99,7 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
                                               st + (t0 + tq < len ? t0 + tq : len), 128,
                                               P.start != nullptr);
         const int bin = kBins - 1 - (kt.ntiles < kBins ? kt.ntiles : kBins - 1);
-        P.tiles[i] = PackedItem{lo, t0, row0, len, st, bin, {0, 0}};
+        P.tiles[i] = PackedItem{lo, t0, row0, len, st, bin, call, 0};
         atomicAdd(&bins[bin], 1);
     }
     __syncthreads();
@@ -144,7 +146,8 @@ __device__ __forceinline__ bool token_slot(const PagedParams &P, int row, bool r
 // What the attention kernel needs of the new keys and values.  Paged: every
 // token's rotated key and its value go to its pages.  Packed: the leading
 // rot_w dims of every key, rotated, go to the workspace (the others are read
-// where they are).  One thread per (token, group of 8 rotated pairs / 8 copied
+// where they are), and the values are looked over for one that is not finite
+// (with none, no boundary tile needs a pass over V).  One thread per (token, group of 8 rotated pairs / 8 copied
 // key dims / 8 value dims), looping over the KV heads so that each angle is
 // computed once.  The first CTA makes the list of query tiles instead.
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     const bool paged = P.k_pages != nullptr;
     const int r = P.rope.rot_dim, half = r / 2;
     const int n_rot = half / 8, n_kcopy = ((paged ? kHeadDim : P.rot_w) - r) / 8;
-    const int items = n_rot + n_kcopy + (paged ? kHeadDim / 8 : 0);
+    const int items = n_rot + n_kcopy + kHeadDim / 8;
     const long long idx = (blockIdx.x - 1ll) * blockDim.x + threadIdx.x;
     const long long row_l = idx / items;
     if (row_l >= P.N) return;
@@ -209,9 +212,16 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
                 *reinterpret_cast<const uint4 *>(src_k + g * kHeadDim + d0);
     } else {
         const int d0 = (it - n_rot - n_kcopy) * 8;
-        for (int g = 0; g < P.Hkv; ++g)
-            *reinterpret_cast<uint4 *>(dst_v + g * head_stride + d0) =
-                *reinterpret_cast<const uint4 *>(src_v + g * kHeadDim + d0);
+        uint32_t hit = 0;
+        for (int g = 0; g < P.Hkv; ++g) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src_v + g * kHeadDim + d0);
+            if (paged)
+                *reinterpret_cast<uint4 *>(dst_v + g * head_stride + d0) = v;
+            // an exponent of all ones carries into the sign's place
+            hit |= ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
+                   ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
+        }
+        if (!paged && (hit & 0x80008000u)) atomicOr(&P.odd_values[*P.call & 1], 1u);
     }
 }
 
@@ -285,8 +295,7 @@ spark_status done(cudaError_t e) {
 
 spark_status launch_prep(const PagedParams &P, cudaStream_t s) {
     const int r = P.rope.rot_dim;
-    const long long items =
-        r / 16 + ((P.k_pages ? kHeadDim : P.rot_w) - r) / 8 + (P.k_pages ? kHeadDim / 8 : 0);
+    const long long items = r / 16 + ((P.k_pages ? kHeadDim : P.rot_w) - r) / 8 + kHeadDim / 8;
     const long long blocks = (P.N * items + kPrepThreads - 1) / kPrepThreads + 1;
     if (blocks > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;
     return done(launch_overlapped(paged_prep_kernel, dim3(static_cast<unsigned>(blocks)),
@@ -300,7 +309,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct PackedPlan {
     long long most;  // query tiles at most: full ones, and a ragged one per sequence
     int rot_w;
-    size_t base, tiles, work, krot, bytes;
+    size_t flags, base, tiles, work, krot, bytes;
 };
 
 PackedPlan plan_packed(int N, int S, int H, int Hkv, const spark_layer_desc *desc, bool paged) {
@@ -308,7 +317,8 @@ PackedPlan plan_packed(int N, int S, int H, int Hkv, const spark_layer_desc *des
     const int tq = 128 / (H / Hkv);
     pl.most = static_cast<long long>(N / tq) + (S < N ? S : N);
     pl.rot_w = paged ? 0 : (desc->rot_dim + 63) / 64 * 64;
-    pl.base = kWorkspaceHeader;
+    pl.flags = kWorkspaceHeader;
+    pl.base = pl.flags + 256;
     pl.tiles = pl.base + up256((static_cast<size_t>(S) + 1) * 4);
     pl.work = pl.tiles + up256(static_cast<size_t>(pl.most) * sizeof(PackedItem));
     pl.krot = pl.work + up256(static_cast<size_t>(pl.most) * sizeof(PackedItem));
@@ -343,7 +353,8 @@ spark_status launch_packed_attn(const PagedParams &P, const PackedPlan &pl, int 
     A.rot_w = pl.rot_w;
     A.wave = sms;
     A.pk.work = P.work;
-    A.pk.sure = P.N / tq;
+    A.pk.odd_values = P.odd_values;
+    A.pk.call = P.call;
     A.pk.table = P.table;
     A.pk.n_pages = P.n_pages;
     A.pk.page_shift = P.page_shift;
@@ -360,7 +371,7 @@ spark_status launch_packed_attn(const PagedParams &P, const PackedPlan &pl, int 
         const uint64_t strides[3] = {kHeadDim * 2ull, heads * kHeadDim * 2ull,
                                      N * heads * kHeadDim * 2ull};
         const uint32_t box_q[4] = {64, static_cast<uint32_t>(P.G), static_cast<uint32_t>(tq), 1};
-        const uint32_t box_k[4] = {64, 1, 128, 1}, box_v[4] = {64, 1, 32, 1};
+        const uint32_t box_k[4] = {64, 1, 128, 1}, box_v[4] = {64, 1, 64, 1};
         if (!encode_bf16_map(&tm_q, P.qkv, 4, dims, strides, box_q)) return SPARK_ERR_CUDA;
         if (!paged && (!encode_bf16_map(&tm_k, P.qkv, 4, dims, strides, box_k) ||
                        !encode_bf16_map(&tm_v, P.qkv, 4, dims, strides, box_v)))
@@ -374,7 +385,7 @@ spark_status launch_packed_attn(const PagedParams &P, const PackedPlan &pl, int 
         const uint64_t strides[3] = {kHeadDim * 2ull, page * kHeadDim * 2ull,
                                      P.Hkv * page * kHeadDim * 2ull};
         const uint32_t box_k[4] = {64, static_cast<uint32_t>(page < 128 ? page : 128), 1, 1};
-        const uint32_t box_v[4] = {64, static_cast<uint32_t>(page < 32 ? page : 32), 1, 1};
+        const uint32_t box_v[4] = {64, static_cast<uint32_t>(page < 64 ? page : 64), 1, 1};
         if (!encode_bf16_map(&tm_k, P.k_pages, 4, dims, strides, box_k) ||
             !encode_bf16_map(&tm_v, P.v_pages, 4, dims, strides, box_v))
             return SPARK_ERR_CUDA;
@@ -447,6 +458,8 @@ spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_
     P.tiles = reinterpret_cast<PackedItem *>(ws + pl.tiles);
     P.work = reinterpret_cast<PackedItem *>(ws + pl.work);
     P.most = static_cast<int>(pl.most);
+    P.call = reinterpret_cast<unsigned *>(ws + pl.flags);
+    P.odd_values = P.call + 1;
     if (paged) {
         P.start = start;
         set_pages(P, k_pages, v_pages, n_pages, page_size, table, max_pages);

@@ -23,6 +23,8 @@ struct PagedParams {
     PackedItem *tiles;         // query tiles in the sequences' order
     PackedItem *work;          // the same, longest first, and -1 behind them
     int most;                  // places in the lists
+    unsigned *odd_values;      // common.cuh: PackedInfo
+    unsigned *call;
     float *part_ml;            // decode: [grid, 2, G, 2] running max (base-2 units), sum
     float *part_o;             // decode: [grid, 2, G, 256] unnormalised outputs
     unsigned *counters;        // decode: a byte per CTA, left at 0 by every call

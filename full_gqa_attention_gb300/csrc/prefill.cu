@@ -331,10 +331,10 @@ __device__ __forceinline__ bool clean_v_rows(uint8_t *ring, int use, const TileR
     // Row w + 8 i is at a constant distance from row w (`use` is a multiple of
     // 4, so the slots do not wrap): bit i of a mask stands for it, and the
     // passes unroll to plain stores and loads.
-    uint8_t *base = ring + (use % kSlots) * kSlotBytes + (lane >> 3) * (kSlotBytes / 4) +
+    uint8_t *base = ring + (use % kSlots) * kSlotBytes + (lane >> 3) * (kSlotBytes / 2) +
                     w * 128 + (lane & 7) * 16;
     auto at = [&](int i) {
-        return reinterpret_cast<uint4 *>(base + (i >> 2) * kSlotBytes + (i & 3) * 1024);
+        return reinterpret_cast<uint4 *>(base + (i >> 3) * 2 * kSlotBytes + (i & 7) * 1024);
     };
     auto below = [&](int row) -> uint32_t {  // rows w + 8 i < row
         const int n = (row - w + 7) >> 3;
@@ -374,7 +374,9 @@ __device__ __forceinline__ bool clean_v_rows(uint8_t *ring, int use, const TileR
 
 // The copies of a packed source's key and value tiles into the ring, by one
 // thread in the order of the issuers: K0, K1, then V_j and K_{j+2} for every
-// tile j.
+// tile j.  A V tile is two halves of 64 keys, each in two slots of two 64-dim
+// chunks (the other sources: four slots of 32 keys): the copy engine takes
+// about as long for a box of 32 rows as for one of 64.
 //
 // With pages a tile is a box per page.  What stands between a slot's release
 // and its refill delays every tile, so the page numbers are looked up a tile
@@ -433,14 +435,16 @@ struct PackedTiles {
             };
             auto v_tile = [&](int j) -> bool {
                 const int row = row0 + kv_lo + j * kBN;
-                for (int vs = 0; vs < 4; ++vs) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
                     int slot;
                     if (!take(sc, slot)) return false;
                     uint8_t *dst = ring + slot * kSlotBytes;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tma_load_4d(dst + c * (kSlotBytes / 4), &tm_v, &bars[kBarSlotFull + slot],
-                                    c * 64, P.H + P.Hkv + g, row + vs * 32, 0);
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_4d(dst + c * (kSlotBytes / 2), &tm_v, &bars[kBarSlotFull + slot],
+                                    ((q & 1) * 2 + c) * 64, P.H + P.Hkv + g, row + (q >> 1) * 64,
+                                    0);
                     ++sc;
                 }
                 return true;
@@ -458,7 +462,7 @@ struct PackedTiles {
     template <int kPieces>
     __device__ __forceinline__ int load_pages() const {
         constexpr int kStep = kBN / kPieces;  // keys per piece
-        constexpr int kBox = kStep < 32 ? kStep : 32;  // keys per V box
+        constexpr int kBox = kStep < 64 ? kStep : 64;  // keys per V box
         const int shift = P.pk.page_shift, pmask = (1 << shift) - 1;
         const int lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
         const int32_t *pages = P.pk.table + static_cast<size_t>(seq) * P.pk.max_pages;
@@ -502,18 +506,18 @@ struct PackedTiles {
         auto v_tile = [&](int j, const int(&id)[kPieces]) -> bool {
             const int at = (kv_lo + j * kBN) & pmask;
 #pragma unroll
-            for (int vs = 0; vs < 4; ++vs) {
+            for (int q = 0; q < 4; ++q) {
                 int slot;
                 if (!take(sc, slot)) return false;
 #pragma unroll
-                for (int i = 0; i < 32 / kBox; ++i) {
-                    const int r = vs * 32 + i * kBox;
+                for (int i = 0; i < 64 / kBox; ++i) {
+                    const int r = (q >> 1) * 64 + i * kBox;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tma_load_4d(ring + slot * kSlotBytes + c * (kSlotBytes / 4) +
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_4d(ring + slot * kSlotBytes + c * (kSlotBytes / 2) +
                                         i * kBox * 128,
-                                    &tm_v, &bars[kBarSlotFull + slot], c * 64, at + r % kStep, g,
-                                    id[r / kStep]);
+                                    &tm_v, &bars[kBarSlotFull + slot], ((q & 1) * 2 + c) * 64,
+                                    at + r % kStep, g, id[r / kStep]);
                 }
                 ++sc;
             }
@@ -579,15 +583,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int seq_end = P.T;                            // tokens of the sequence
     int row0 = 0;                                 // packed: the sequence's first row
     int seq = 0;
+    PackedItem item = {};
     if constexpr (kIsPacked) {
-        // the grid allows for a ragged tile in every sequence: a CTA past the
-        // list has nothing to do, and finds out before it sets anything up
-        if (static_cast<int>(blockIdx.x) / units >= P.pk.sure) {
-            grid_dep_wait();
-            if (P.pk.work[static_cast<int>(blockIdx.x) / units].seq < 0) return;
-        }
+        // The tile comes from the list that the kernel before made: its latency
+        // overlaps the set-up below.  The grid allows for a ragged tile in every
+        // sequence: a CTA past the list has nothing to do.
+        grid_dep_wait();
+        item = P.pk.work[static_cast<int>(blockIdx.x) / units];
+        if (item.seq < 0) return;
     }
-
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t count = 1;
@@ -621,19 +625,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // it waited for the call's inputs before letting this kernel start, so only
     // the producer waits, before its first key/value load.  Otherwise every
     // thread waits here, before reading any input.
-    if (!P.defer_wait) grid_dep_wait();
+    if (!kIsPacked && !P.defer_wait) grid_dep_wait();
 
     // Absolute indices: queries t0..t_end-1 of the chunk sit at start + t.
     int start = 0;
     bool skip = false;
     if constexpr (kIsPacked) {
-        const PackedItem w = P.pk.work[static_cast<int>(blockIdx.x) / units];
-        skip = w.seq < 0;
-        seq = w.seq;
-        t0 = w.t0;
-        row0 = w.row0;
-        seq_end = w.len;
-        start = w.start;
+        seq = item.seq;
+        t0 = item.t0;
+        row0 = item.row0;
+        seq_end = item.len;
+        start = item.start;
         t_end = (t0 + tq < seq_end) ? t0 + tq : seq_end;
     } else if constexpr (kSrc != kKvFromQkv) {
         start = P.start[b];
@@ -773,6 +775,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const uint64_t q_desc = smem_desc_sw128(smem_u32(qbuf), 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024);
             const uint64_t v_desc = smem_desc_sw128(smem_u32(ring), kSlotBytes / 4, 1024);
+            const uint64_t vp_desc = smem_desc_sw128(smem_u32(ring), kSlotBytes / 2, 1024);
             // (the full-layer cache instance measured faster building each
             // descriptor in place)
             constexpr bool kDescInPlace = kSrc == kKvFromCache;
@@ -807,6 +810,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             auto mma_pv = [&](int j) -> bool {
                 const uint32_t pcol = tmem + kColS + (j & 1) * kBN;
+                if constexpr (kIsPacked) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // halves of 64 keys, two slots each
+                        const int slot = sc % kSlots;
+                        const uint32_t parity = (sc / kSlots) & 1;
+                        if (!mbar_wait(&bars[kBarSlotFull + slot], parity, &abort_flag,
+                                       P.status) ||
+                            !mbar_wait(&bars[kBarSlotFull + slot + 1], parity, &abort_flag,
+                                       P.status))
+                            return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            // P of keys 0..63 sits in packed columns 0..31, of 64..127 in 64..95
+                            mma_ts(tmem + kColO, pcol + h * 64 + kk * 8,
+                                   vp_desc + static_cast<uint32_t>((slot * kSlotBytes + kk * 2048) >> 4),
+                                   kIdescPV, (j > 0 || h + kk > 0));
+                        }
+                        tc_commit(&bars[kBarSlotEmpty + slot]);
+                        tc_commit(&bars[kBarSlotEmpty + slot + 1]);
+                        sc += 2;
+                    }
+                    tc_commit(&bars[kBarODone]);
+                    return true;
+                }
                 for (int vs = 0; vs < 4; ++vs) {
                     const int slot = sc % kSlots;
                     if (!mbar_wait(&bars[kBarSlotFull + slot], (sc / kSlots) & 1, &abort_flag,
@@ -917,6 +945,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // raw equivalent of 2^8.
         constexpr float kLazyRaw = 8.0f / kScaleLog2;
         const int a_last = start + t_end - 1;
+        // (without a cache the kernel before has looked at every value)
+        const bool clean = kSrc == kKvPages || (kIsPacked && P.pk.odd_values[item.call & 1] != 0);
         const int col0 = wg * 64;                       // first score column of this thread
         float m_run = -INFINITY, l_part = 0.f;
         for (int j = 0; ok && j < ntiles; ++j) {
@@ -993,7 +1023,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             if constexpr (kIsPacked) {
-                if (tile_needs_mask(kind, P.window, key0, kBN, a0, a_last)) {
+                if (clean && tile_needs_mask(kind, P.window, key0, kBN, a0, a_last)) {
                     // V_j comes after min(ntiles, j + 2) K tiles and j V tiles.
                     // The slots' use before it was K_j (the last tile: S_j says
                     // that it landed), K0 (the first) or V_{j-1}, which P*V of
@@ -1014,6 +1044,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_arrive(&bars[kBarPReady + (j & 1)]);
         }
 
+        if (kIsPacked && blockIdx.x == 0 && sth == 0) *P.pk.call = item.call + 1;
         // epilogue: O / l * sigmoid(gate) -> bf16 -> staged in the Q buffer -> TMA store
         if (sth == 0) grid_dep_launch();
         if (ok) ok = mbar_wait(&bars[kBarOFinal], 0, &abort_flag, P.status);
