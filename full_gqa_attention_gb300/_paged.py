@@ -46,25 +46,41 @@ for _name, _args, _res in (
     _f.argtypes, _f.restype = _args, _res
 
 
-def _need_on(device, t, dtype, name: str):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+# The current stream's handle and the current device's number.  The public
+# calls build objects (2.8 us for a stream), which is most of a short launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _device_of(t, name: str):
+def _device_of(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
+
+
+def _refuse(dev: int, t, dtype, name: str):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _check(dev: int, *wanted):
+    """Each (tensor, dtype, name): contiguous, of that type, on that device."""
+    for t, dtype, name in wanted:
+        if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev
+                or not t.is_contiguous()):
+            _refuse(dev, t, dtype, name)
 
 
 @contextlib.contextmanager
-def _elsewhere(device, stream):
+def _elsewhere(dev: int, stream):
     """The device and stream of a call that are not the current ones."""
-    with torch.cuda.device(device):
+    with torch.cuda.device(dev):
         if stream is None:
             yield
         else:
@@ -75,27 +91,25 @@ def _elsewhere(device, stream):
 _HERE = contextlib.nullcontext()
 
 
-def _where(device, stream):
+def _where(dev: int, stream):
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return _elsewhere(device, stream)
-    if torch.cuda.current_device() != device.index:
-        return _elsewhere(device, None)
-    return _HERE
+        if stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+        return _elsewhere(dev, stream)
+    return _HERE if _current_device() == dev else _elsewhere(dev, None)
 
 
-def _run(name: str, device, workspace, nbytes: int, stream, call):
-    """Calls call(workspace pointer, bytes, stream pointer) with the caller's
-    workspace or one of its own."""
-    owned = workspace is None
-    if owned:
-        workspace = new_workspace(nbytes, device)
-    else:
-        _need_on(device, workspace, torch.uint8, "workspace")
-    st = call(workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream().cuda_stream)
-    if st != SPARK_OK:
-        raise SparkError(st, name)
+def _workspace(dev: int, workspace, nbytes):
+    """The caller's workspace, or one of nbytes() bytes; whether it is ours."""
+    if workspace is None:
+        return new_workspace(nbytes(), torch.device("cuda", dev)), True
+    _check(dev, (workspace, _U8, "workspace"))
+    return workspace, False
+
+
+def _done(name: str, status: int, workspace, owned: bool):
+    if status != SPARK_OK:
+        raise SparkError(status, name)
     if owned:
         _check_owned(workspace, name, None)
 
@@ -113,24 +127,21 @@ def _heads(qkv, gate):
     return n, H, Hkv
 
 
-def _pages(device, k_pages, v_pages, page_table, rows: int, Hkv: int):
+def _pages(k_pages, v_pages, page_table, rows: int, Hkv: int):
     """n_pages, page_size, max_pages of a layer's pool and its table."""
-    _need_on(device, k_pages, torch.bfloat16, "k_pages")
-    _need_on(device, v_pages, torch.bfloat16, "v_pages")
-    _need_on(device, page_table, torch.int32, "page_table")
-    shape = k_pages.shape
+    shape, table = k_pages.shape, page_table.shape
     if len(shape) != 4 or v_pages.shape != shape or shape[1] != Hkv or shape[3] != HEAD_DIM:
         raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page_size, 256]")
-    if page_table.dim() != 2 or page_table.shape[0] != rows:
+    if len(table) != 2 or table[0] != rows:
         raise ValueError("page_table must be [rows, max_pages]")
-    return shape[0], shape[2], page_table.shape[1]
+    return shape[0], shape[2], table[1]
 
 
-def _new_out(out, n: int, H: int, device):
+def _out(dev: int, out, n: int, H: int):
     if out is None:
         # rows that no sequence covers stay as they are: they begin as zeros
-        return torch.zeros((n, H * HEAD_DIM), dtype=torch.bfloat16, device=device)
-    _need_on(device, out, torch.bfloat16, "out")
+        return torch.zeros((n, H * HEAD_DIM), dtype=_BF16, device=torch.device("cuda", dev))
+    _check(dev, (out, _BF16, "out"))
     if out.shape != (n, H * HEAD_DIM):
         raise ValueError("out must be [tokens, H * 256]")
     return out
@@ -160,23 +171,21 @@ def spark_attn_prefill_packed(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.
     -> out bf16 [n,H*256].  Rows of out that no sequence covers stay as they
     were (zeros in one that the call allocates)."""
     dev = _device_of(qkv, "qkv")
-    _need_on(dev, qkv, torch.bfloat16, "qkv")
-    _need_on(dev, gate, torch.float32, "gate")
-    _need_on(dev, pos, torch.int32, "pos")
-    _need_on(dev, cu_seqlens, torch.int32, "cu_seqlens")
+    _check(dev, (qkv, _BF16, "qkv"), (gate, _F32, "gate"), (pos, _I32, "pos"),
+           (cu_seqlens, _I32, "cu_seqlens"))
     n, H, Hkv = _heads(qkv, gate)
     S = cu_seqlens.numel() - 1
     if pos.shape != (n,) or cu_seqlens.dim() != 1 or S < 0:
         raise ValueError("pos must be [tokens], cu_seqlens [S + 1]")
     d = ctypes.byref(as_desc(layer))
     with _where(dev, stream):
-        out = _new_out(out, n, H, dev)
-        need = (lib.spark_attn_prefill_packed_workspace_size(n, S, H, Hkv, d)
-                if workspace is None else 0)
-        _run("spark_attn_prefill_packed", dev, workspace, need, stream,
-             lambda ws, size, s: lib.spark_attn_prefill_packed(
-                 qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(), d, n, S,
-                 H, Hkv, out.data_ptr(), ws, size, s))
+        out = _out(dev, out, n, H)
+        ws, owned = _workspace(
+            dev, workspace, lambda: lib.spark_attn_prefill_packed_workspace_size(n, S, H, Hkv, d))
+        st = lib.spark_attn_prefill_packed(
+            qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(), d, n, S, H,
+            Hkv, out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        _done("spark_attn_prefill_packed", st, ws, owned)
     return out
 
 
@@ -190,26 +199,25 @@ def spark_attn_prefill_paged(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.T
     place; page_table int32 [S,max_pages]); the rest as for
     spark_attn_prefill_packed."""
     dev = _device_of(qkv, "qkv")
-    _need_on(dev, qkv, torch.bfloat16, "qkv")
-    _need_on(dev, gate, torch.float32, "gate")
-    _need_on(dev, pos, torch.int32, "pos")
-    _need_on(dev, cu_seqlens, torch.int32, "cu_seqlens")
-    _need_on(dev, start, torch.int32, "start")
+    _check(dev, (qkv, _BF16, "qkv"), (gate, _F32, "gate"), (pos, _I32, "pos"),
+           (cu_seqlens, _I32, "cu_seqlens"), (start, _I32, "start"), (k_pages, _BF16, "k_pages"),
+           (v_pages, _BF16, "v_pages"), (page_table, _I32, "page_table"))
     n, H, Hkv = _heads(qkv, gate)
     S = cu_seqlens.numel() - 1
     if pos.shape != (n,) or cu_seqlens.dim() != 1 or S < 0 or start.shape != (S,):
         raise ValueError("pos must be [tokens], cu_seqlens [S + 1], start [S]")
-    n_pages, page_size, max_pages = _pages(dev, k_pages, v_pages, page_table, S, Hkv)
+    n_pages, page_size, max_pages = _pages(k_pages, v_pages, page_table, S, Hkv)
     d = ctypes.byref(as_desc(layer))
     with _where(dev, stream):
-        out = _new_out(out, n, H, dev)
-        need = (lib.spark_attn_prefill_paged_workspace_size(n, S, H, Hkv, d)
-                if workspace is None else 0)
-        _run("spark_attn_prefill_paged", dev, workspace, need, stream,
-             lambda ws, size, s: lib.spark_attn_prefill_paged(
-                 qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(),
-                 start.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page_size,
-                 page_table.data_ptr(), max_pages, d, n, S, H, Hkv, out.data_ptr(), ws, size, s))
+        out = _out(dev, out, n, H)
+        ws, owned = _workspace(
+            dev, workspace, lambda: lib.spark_attn_prefill_paged_workspace_size(n, S, H, Hkv, d))
+        st = lib.spark_attn_prefill_paged(
+            qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(),
+            start.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page_size,
+            page_table.data_ptr(), max_pages, d, n, S, H, Hkv, out.data_ptr(), ws.data_ptr(),
+            ws.numel(), _raw_stream(dev))
+        _done("spark_attn_prefill_paged", st, ws, owned)
     return out
 
 
@@ -222,23 +230,23 @@ def spark_attn_decode_paged(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.Te
     [n_pages,Hkv,page_size,256] (updated in place), page_table int32
     [B,max_pages] -> out bf16 [B,H*256]."""
     dev = _device_of(qkv, "qkv")
-    _need_on(dev, qkv, torch.bfloat16, "qkv")
-    _need_on(dev, gate, torch.float32, "gate")
-    _need_on(dev, pos, torch.int32, "pos")
+    _check(dev, (qkv, _BF16, "qkv"), (gate, _F32, "gate"), (pos, _I32, "pos"),
+           (k_pages, _BF16, "k_pages"), (v_pages, _BF16, "v_pages"),
+           (page_table, _I32, "page_table"))
     B, H, Hkv = _heads(qkv, gate)
     if pos.shape != (B,):
         raise ValueError("pos must be [B]")
-    n_pages, page_size, max_pages = _pages(dev, k_pages, v_pages, page_table, B, Hkv)
+    n_pages, page_size, max_pages = _pages(k_pages, v_pages, page_table, B, Hkv)
     d = ctypes.byref(as_desc(layer))
     with _where(dev, stream):
-        out = _new_out(out, B, H, dev)
-        need = (lib.spark_attn_decode_paged_workspace_size(B, H, Hkv, d)
-                if workspace is None else 0)
-        _run("spark_attn_decode_paged", dev, workspace, need, stream,
-             lambda ws, size, s: lib.spark_attn_decode_paged(
-                 qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), k_pages.data_ptr(),
-                 v_pages.data_ptr(), n_pages, page_size, page_table.data_ptr(), max_pages, d, B,
-                 H, Hkv, out.data_ptr(), ws, size, s))
+        out = _out(dev, out, B, H)
+        ws, owned = _workspace(
+            dev, workspace, lambda: lib.spark_attn_decode_paged_workspace_size(B, H, Hkv, d))
+        st = lib.spark_attn_decode_paged(
+            qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), k_pages.data_ptr(),
+            v_pages.data_ptr(), n_pages, page_size, page_table.data_ptr(), max_pages, d, B, H,
+            Hkv, out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        _done("spark_attn_decode_paged", st, ws, owned)
     return out
 
 
@@ -249,15 +257,14 @@ class PagePool:
     The tensors are the caller's and keep their storage; add to `len` in place
     after a step."""
 
-    __slots__ = ("k_pages", "v_pages", "table", "held", "len", "refs", "device", "_c")
+    __slots__ = ("k_pages", "v_pages", "table", "held", "len", "refs", "_dev", "_c", "_rows")
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
                  held: torch.Tensor, len: torch.Tensor, refs: torch.Tensor):
         dev = _device_of(k_pages, "k_pages")
-        _need_on(dev, k_pages, torch.bfloat16, "k_pages")
-        _need_on(dev, v_pages, torch.bfloat16, "v_pages")
-        for t, name in ((table, "table"), (held, "held"), (len, "len"), (refs, "refs")):
-            _need_on(dev, t, torch.int32, name)
+        _check(dev, (k_pages, _BF16, "k_pages"), (v_pages, _BF16, "v_pages"),
+               (table, _I32, "table"), (held, _I32, "held"), (len, _I32, "len"),
+               (refs, _I32, "refs"))
         if (k_pages.dim() != 5 or v_pages.shape != k_pages.shape
                 or k_pages.shape[4] != HEAD_DIM):
             raise ValueError("k_pages and v_pages must be [n_layers, n_pages, Hkv, page_size, 256]")
@@ -266,7 +273,7 @@ class PagePool:
                 or refs.shape != (n_pages,)):
             raise ValueError("table must be [n_rows, max_pages], held and len [n_rows], "
                              "refs [n_pages]")
-        self.k_pages, self.v_pages, self.device = k_pages, v_pages, dev
+        self.k_pages, self.v_pages, self._dev, self._rows = k_pages, v_pages, dev, held.shape[0]
         self.table, self.held, self.len, self.refs = table, held, len, refs
         self._c = spark_page_pool(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(),
                                   held.data_ptr(), len.data_ptr(), refs.data_ptr(), n_layers, Hkv,
@@ -286,17 +293,19 @@ class PagePool:
                    torch.zeros(n_rows, **i32), torch.zeros(n_pages, **i32))
 
 
-def _rows(pool: PagePool, t, name: str, n: int | None = None):
-    _need_on(pool.device, t, torch.int32, name)
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+def _rows(pool: PagePool, t, name: str, n: int | None = None) -> int:
+    """The number of entries of an int32 list on the pool's device."""
+    _check(pool._dev, (t, _I32, name))
+    shape = t.shape
+    if len(shape) != 1 or (n is not None and shape[0] != n):
         raise ValueError(f"{name} must be one-dimensional" + (f", of {n}" if n is not None else ""))
-    return t.data_ptr()
+    return shape[0]
 
 
 def _one(pool: PagePool, t, name: str):
     if t is None:
         return None
-    _need_on(pool.device, t, torch.int32, name)
+    _check(pool._dev, (t, _I32, name))
     if t.numel() != 1:
         raise ValueError(f"{name} must hold one value")
     return t.data_ptr()
@@ -306,21 +315,22 @@ def spark_attn_pages_workspace_size(pool: PagePool) -> int:
     return lib.spark_attn_pages_workspace_size(ctypes.byref(pool._c))
 
 
-def _run_pages(name: str, pool: PagePool, workspace, stream, call):
-    with _where(pool.device, stream):
-        need = spark_attn_pages_workspace_size(pool) if workspace is None else 0
-        _run(name, pool.device, workspace, need, stream, call)
+def _pages_call(name: str, call, pool: PagePool, args, workspace, stream):
+    dev = pool._dev
+    with _where(dev, stream):
+        ws, owned = _workspace(dev, workspace, lambda: spark_attn_pages_workspace_size(pool))
+        st = call(ctypes.byref(pool._c), *args, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        _done(name, st, ws, owned)
 
 
 def spark_attn_pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor,
                           workspace: torch.Tensor | None = None, stream=None) -> None:
     """Rows dst[i] (which hold no pages) become copies of rows src[i] that
     share their pages; src, dst int32 [n]."""
-    s = _rows(pool, src, "src")
-    t = _rows(pool, dst, "dst", src.shape[0])
-    _run_pages("spark_attn_pages_fork", pool, workspace, stream,
-               lambda ws, size, st: lib.spark_attn_pages_fork(
-                   ctypes.byref(pool._c), s, t, src.shape[0], ws, size, st))
+    n = _rows(pool, src, "src")
+    _rows(pool, dst, "dst", n)
+    _pages_call("spark_attn_pages_fork", lib.spark_attn_pages_fork, pool,
+                (src.data_ptr(), dst.data_ptr(), n), workspace, stream)
 
 
 def spark_attn_pages_reserve(pool: PagePool, add: torch.Tensor,
@@ -330,29 +340,25 @@ def spark_attn_pages_reserve(pool: PagePool, add: torch.Tensor,
     [n_rows]), with a copy of a shared page that is about to be written.
     taken: one int32, the pages taken, or -1 (and nothing changed) when the
     pool has too few."""
-    a = _rows(pool, add, "add", pool.held.shape[0])
-    t = _one(pool, taken, "taken")
-    _run_pages("spark_attn_pages_reserve", pool, workspace, stream,
-               lambda ws, size, st: lib.spark_attn_pages_reserve(
-                   ctypes.byref(pool._c), a, t, ws, size, st))
+    _rows(pool, add, "add", pool._rows)
+    _pages_call("spark_attn_pages_reserve", lib.spark_attn_pages_reserve, pool,
+                (add.data_ptr(), _one(pool, taken, "taken")), workspace, stream)
 
 
 def spark_attn_pages_free(pool: PagePool, rows: torch.Tensor, keep: torch.Tensor | None = None,
                           workspace: torch.Tensor | None = None, stream=None) -> None:
     """Gives back the pages of rows (int32 [n]) behind their first keep[i]
     tokens (none kept without `keep`)."""
-    r = _rows(pool, rows, "rows")
-    k = None if keep is None else _rows(pool, keep, "keep", rows.shape[0])
-    _run_pages("spark_attn_pages_free", pool, workspace, stream,
-               lambda ws, size, st: lib.spark_attn_pages_free(
-                   ctypes.byref(pool._c), r, k, rows.shape[0], ws, size, st))
+    n = _rows(pool, rows, "rows")
+    if keep is not None:
+        _rows(pool, keep, "keep", n)
+    _pages_call("spark_attn_pages_free", lib.spark_attn_pages_free, pool,
+                (rows.data_ptr(), None if keep is None else keep.data_ptr(), n), workspace, stream)
 
 
 def spark_attn_pages_compact(pool: PagePool, live: torch.Tensor | None = None,
                              workspace: torch.Tensor | None = None, stream=None) -> None:
     """Moves the pages in use to the lowest numbers.  live: one int32, the
     number of pages in use."""
-    n = _one(pool, live, "live")
-    _run_pages("spark_attn_pages_compact", pool, workspace, stream,
-               lambda ws, size, st: lib.spark_attn_pages_compact(
-                   ctypes.byref(pool._c), n, ws, size, st))
+    _pages_call("spark_attn_pages_compact", lib.spark_attn_pages_compact, pool,
+                (_one(pool, live, "live"),), workspace, stream)

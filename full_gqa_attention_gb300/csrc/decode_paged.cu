@@ -30,7 +30,8 @@ namespace spark {
 
 namespace {
 
-constexpr int kMinShare = 1;                              // tiles a CTA takes at least
+constexpr int kMinShare = 1;                              // units a CTA takes at least
+constexpr int kPairCost = 3;                              // a pair's own units (Row::units)
 constexpr int kTile = 64;                                 // slots per stage
 constexpr int kStages = 3;
 constexpr int kWarps = 4;                                 // consumers, 16 slots each
@@ -51,6 +52,11 @@ __device__ __forceinline__ void consumer_bar() {
 struct Row {
     int pos, lo, tiles;
     __device__ __forceinline__ int slot0() const { return lo & ~(kTile - 1); }
+    // Units of one of its pairs in the list: its tiles, and what setting a pair
+    // up and finishing it costs besides, in tiles.
+    __device__ __forceinline__ long long units() const {
+        return tiles ? tiles + kPairCost : 0;
+    }
 };
 
 __device__ __forceinline__ Row row_of(const PagedParams &P, int b) {
@@ -65,33 +71,36 @@ __device__ __forceinline__ Row row_of(const PagedParams &P, int b) {
     return r;
 }
 
-// A CTA's walk over its stretch of the list: the pair (b, g), the tiles
-// [t0, t1) of it, and where the pair begins in the list.
+// A CTA's walk over its stretch of the list: the pair (b, g) and the tiles
+// [t0, t1) of it.  A pair's units are kPairCost for itself, then its tiles.
 struct Walk {
     long long u, end;   // next unit of the stretch, its end
     long long base;     // first unit of row b
+    long long first;    // first unit of the pair
     int b, g, t0, t1;
     Row row;
 
-    __device__ __forceinline__ long long pair_first() const {
-        return base + static_cast<long long>(g) * row.tiles;
-    }
-    // The pair that holds unit u; false at the end.  b and base are at or
-    // before it.
+    // The next pair with tiles in the stretch, from unit u on; false at the
+    // end.  b and base are at or before it.
     __device__ __forceinline__ bool load(const PagedParams &P) {
-        if (u >= end) return false;
-        while (u >= base + static_cast<long long>(P.Hkv) * row.tiles) {
-            if (b + 1 >= P.N) return false;  // the positions changed under the call
-            base += static_cast<long long>(P.Hkv) * row.tiles;
-            row = row_of(P, ++b);
+        while (u < end) {
+            while (u >= base + P.Hkv * row.units()) {
+                if (b + 1 >= P.N) return false;  // the positions changed under the call
+                base += P.Hkv * row.units();
+                row = row_of(P, ++b);
+            }
+            const long long n = row.units();
+            g = static_cast<int>((u - base) / n);
+            first = base + g * n;
+            const int from = static_cast<int>(u - first) - kPairCost;
+            const int to = static_cast<int>(end - first < n ? end - first : n) - kPairCost;
+            u = first + to + kPairCost;
+            t0 = from > 0 ? from : 0;
+            t1 = to;
+            if (t1 > t0) return true;
         }
-        g = static_cast<int>((u - base) / row.tiles);
-        const long long first = pair_first();
-        t0 = static_cast<int>(u - first);
-        t1 = end - first < row.tiles ? static_cast<int>(end - first) : row.tiles;
-        return true;
+        return false;
     }
-    __device__ __forceinline__ void next() { u += t1 - t0; }
 };
 
 // The running state of one query head: this lane's 8 dims.
@@ -149,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p = P.pos[b];
         if (blockIdx.x == 0 && (p < -1 || p >= P.max_pages << P.page_shift))
             atomicOr(P.status, kErrPosition);
-        mine += row_of(P, b).tiles;
+        mine += row_of(P, b).units();
     }
     long long before = mine;
 #pragma unroll
@@ -176,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int b = b0;
         long long base = before * P.Hkv;
         for (;; ++b) {
-            const long long n = static_cast<long long>(P.Hkv) * row_of(P, b).tiles;
+            const long long n = P.Hkv * row_of(P, b).units();
             if (wk.u < base + n) break;
             base += n;
         }
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int piece = lane >> 3, which = (lane >> 2) & 1, c = lane & 3;
         int it = 0;
         bool ok = true;
-        for (; ok && wk.load(P); wk.next()) {
+        while (ok && wk.load(P)) {
             const int32_t *row = P.table + static_cast<size_t>(wk.b) * P.max_pages;
             const int slot0 = wk.row.slot0();
             int ids = 0;
@@ -260,25 +269,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4 *>(qs + i * 8) = make_uint4(0, 0, 0, 0);
     int it = 0;
     bool aborted = false;  // the same in every consumer thread
-    for (; wk.load(P); wk.next()) {
-        const Row row = wk.row;
-        // q of the group's heads and the new key, rotated and rounded to bf16,
-        // and the new value
-        for (int i = tid; i < (P.G + 2) * (kHeadDim / 8); i += kWarps * 32) {
-            const int hh = i / (kHeadDim / 8), v = i % (kHeadDim / 8);
-            const int head = hh < P.G ? wk.g * P.G + hh : P.H + (hh - P.G) * P.Hkv + wk.g;
-            const uint4 val = *reinterpret_cast<const uint4 *>(
-                P.qkv + wk.b * width + static_cast<size_t>(head) * kHeadDim + v * 8);
-            __nv_bfloat16 *dst = hh < P.G ? qs + hh * kHeadDim : hh == P.G ? kn : vn;
-            *reinterpret_cast<uint4 *>(dst + v * 8) = val;
-        }
-        float gate[2];
+    // The projections of a pair's new token -- q of the group's heads, the key,
+    // the value -- and its gates, loaded a pair ahead: warp w brings rows w,
+    // w + 4, ... of them.
+    uint4 raw[3];
+    float gate[2];
+    auto fetch = [&](const Walk &w) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            gate[i] = warp + i * kRedHeads < P.G
-                          ? P.gate[static_cast<size_t>(wk.b) * P.H + wk.g * P.G + warp +
-                                   i * kRedHeads]
-                          : 0.f;
+        for (int i = 0; i < 3; ++i) {
+            const int hh = warp + i * kWarps;
+            if (hh >= P.G + 2) break;
+            const int head = hh < P.G ? w.g * P.G + hh : P.H + (hh - P.G) * P.Hkv + w.g;
+            raw[i] = *reinterpret_cast<const uint4 *>(
+                P.qkv + w.b * width + static_cast<size_t>(head) * kHeadDim + lane * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int hq = warp + i * kRedHeads;
+            if (hq < P.G) gate[i] = P.gate[static_cast<size_t>(w.b) * P.H + w.g * P.G + hq];
+        }
+    };
+    Walk nx = wk;
+    bool more = nx.load(P);
+    if (more) fetch(nx);
+    while (more) {
+        wk = nx;
+        const Row row = wk.row;
+        // q and the new key, rotated and rounded to bf16, and the new value
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int hh = warp + i * kWarps;
+            if (hh >= P.G + 2) break;
+            __nv_bfloat16 *dst = hh < P.G ? qs + hh * kHeadDim : hh == P.G ? kn : vn;
+            *reinterpret_cast<uint4 *>(dst + lane * 8) = raw[i];
+        }
+        const float gate_now[2] = {gate[0], gate[1]};
+        more = nx.load(P);
+        if (more) fetch(nx);
         consumer_bar();
         for (int k = tid; k < half; k += kWarps * 32) {
             float c, s;
@@ -456,13 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // ------------------------------------------------------ finish or hand over
-        const long long pair = wk.pair_first();
-        const int c0 = static_cast<int>(pair / share);
-        const int c1 = static_cast<int>((pair + row.tiles - 1) / share);
+        const int c0 = static_cast<int>((wk.first + kPairCost) / share);
+        const int c1 = static_cast<int>((wk.first + row.units() - 1) / share);
         bool finish = c0 == c1;
         if (!finish) {
             // this CTA's partial state, then the count
-            const int place = wk.u == share * blockIdx.x ? 0 : 1;
+            const int place = share * blockIdx.x < wk.first ? 1 : 0;  // not its first pair
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int hq = warp + i * kRedHeads;
@@ -496,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (hq >= P.G) break;
                     HeadState &h = st[i];
                     auto at = [&](int cta) {
-                        const int pl = static_cast<long long>(cta) * share < pair ? 1 : 0;
+                        const int pl = static_cast<long long>(cta) * share < wk.first ? 1 : 0;
                         return (static_cast<size_t>(cta) * 2 + pl) * P.G + hq;
                     };
                     float m = -INFINITY;
@@ -552,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m = fmaxf(h.m, x);
                 const float z = m == -INFINITY ? 0.f : m;
                 const float wo = h.m == -INFINITY ? 0.f : fast_exp2(h.m - z), wn = fast_exp2(x - z);
-                const float scale = gate_act(gate[i], P.gate_mode) / (h.l * wo + wn);
+                const float scale = gate_act(gate_now[i], P.gate_mode) / (h.l * wo + wn);
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] = (h.o[j] * wo + v[j] * wn) * scale;

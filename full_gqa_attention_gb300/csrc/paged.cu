@@ -123,35 +123,39 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
     }
 }
 
-// Whether the token of `row` has a place in the pages; where.
-__device__ __forceinline__ bool token_slot(const PagedParams &P, int row, bool report,
-                                           size_t &base) {
+// Where the token of `row` goes in the pages (elements), or -1: padding, or a
+// place that does not exist.  One warp; lane 0 reports.
+__device__ __forceinline__ long long token_slot(const PagedParams &P, int row, int lane) {
     const long long cap = static_cast<long long>(P.max_pages) << P.page_shift;
-    const int seq = find_sequence(P.cu, P.S, row);
-    if (seq < 0) return false;
+    const int seq = find_sequence(P.cu, P.S, row, lane);
+    if (seq < 0) return -1;
     const int t0 = P.cu[seq], t1 = P.cu[seq + 1];
     const long long st = P.start[seq];
-    if (t0 < 0 || t1 > P.N || st < 0 || st + (t1 - t0) > cap) return false;  // the plan reports it
+    if (t0 < 0 || t1 > P.N || st < 0 || st + (t1 - t0) > cap) return -1;  // the plan reports it
     const long long a = st + (row - t0);  // index in the sequence
     const int page = P.table[static_cast<size_t>(seq) * P.max_pages + (a >> P.page_shift)];
     if (page < 0 || page >= P.n_pages) {
-        if (report) atomicOr(P.status, kErrPage);
-        return false;
+        if (lane == 0) atomicOr(P.status, kErrPage);
+        return -1;
     }
-    base = ((static_cast<size_t>(page) * P.Hkv << P.page_shift) +
-            static_cast<size_t>(a & ((1 << P.page_shift) - 1))) * kHeadDim;
-    return true;
+    return ((static_cast<long long>(page) * P.Hkv << P.page_shift) +
+            (a & ((1 << P.page_shift) - 1))) * kHeadDim;
 }
+
+constexpr int kPrepRows = kPrepThreads / 32;  // tokens per CTA: a warp finds each one's place
+constexpr int kPrepHeads = 4;                 // KV heads whose loads are in flight at once
 
 // What the attention kernel needs of the new keys and values.  Paged: every
 // token's rotated key and its value go to its pages.  Packed: the leading
 // rot_w dims of every key, rotated, go to the workspace (the others are read
 // where they are), and the values are looked over for one that is not finite
-// (with none, no boundary tile needs a pass over V).  One thread per (token, group of 8 rotated pairs / 8 copied
-// key dims / 8 value dims), looping over the KV heads so that each angle is
-// computed once.  The first CTA makes the list of query tiles instead.
+// (with none, no boundary tile needs a pass over V).  One thread per (token,
+// group of 8 rotated pairs / 8 copied key dims / 8 value dims), over the KV
+// heads, so that each angle is computed once.  The first CTA makes the list of
+// query tiles instead.
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     const __grid_constant__ PagedParams P) {
+    __shared__ long long place[kPrepRows];
     grid_dep_wait();
     grid_dep_launch();
     if (blockIdx.x == 0) {
@@ -162,67 +166,91 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     const int r = P.rope.rot_dim, half = r / 2;
     const int n_rot = half / 8, n_kcopy = ((paged ? kHeadDim : P.rot_w) - r) / 8;
     const int items = n_rot + n_kcopy + kHeadDim / 8;
-    const long long idx = (blockIdx.x - 1ll) * blockDim.x + threadIdx.x;
-    const long long row_l = idx / items;
-    if (row_l >= P.N) return;
-    const int row = static_cast<int>(row_l), it = static_cast<int>(idx % items);
-    __nv_bfloat16 *dst_k, *dst_v = nullptr;
-    size_t head_stride;
+    const long long first = (blockIdx.x - 1ll) * kPrepRows;
     if (paged) {
-        size_t base;
-        if (!token_slot(P, row, it == 0, base)) return;
-        dst_k = P.k_pages + base;
-        dst_v = P.v_pages + base;
-        head_stride = static_cast<size_t>(kHeadDim) << P.page_shift;
-    } else {
-        dst_k = P.krot + static_cast<size_t>(row) * P.rot_w;
-        head_stride = static_cast<size_t>(P.N) * P.rot_w;
+        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const long long at =
+            first + w < P.N ? token_slot(P, static_cast<int>(first + w), lane) : -1;
+        if (lane == 0) place[w] = at;
+        __syncthreads();
     }
     const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
-    const __nv_bfloat16 *src_k = P.qkv + row * width + static_cast<size_t>(P.H) * kHeadDim;
-    const __nv_bfloat16 *src_v = src_k + static_cast<size_t>(P.Hkv) * kHeadDim;
-    if (it < n_rot) {
-        const int k0 = it * 8;
-        const int p = P.pos[row];
-        float c[8], s[8];
+    const size_t head_stride = paged ? static_cast<size_t>(kHeadDim) << P.page_shift
+                                     : static_cast<size_t>(P.N) * P.rot_w;
+    uint32_t hit = 0;
+    for (int i = threadIdx.x; i < kPrepRows * items; i += kPrepThreads) {
+        const int w = i / items, it = i % items;
+        if (first + w >= P.N) break;
+        const int row = static_cast<int>(first + w);
+        if (paged && place[w] < 0) continue;
+        const size_t base = paged ? static_cast<size_t>(place[w])
+                                  : static_cast<size_t>(row) * P.rot_w;
+        __nv_bfloat16 *dst_k = (paged ? P.k_pages : P.krot) + base;
+        __nv_bfloat16 *dst_v = P.v_pages + (paged ? base : 0);
+        const __nv_bfloat16 *src_k = P.qkv + row * width + static_cast<size_t>(P.H) * kHeadDim;
+        const __nv_bfloat16 *src_v = src_k + static_cast<size_t>(P.Hkv) * kHeadDim;
+        if (it < n_rot) {
+            const int k0 = it * 8;
+            const int p = P.pos[row];
+            float c[8], s[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rope_cos_sin(p, P.rope.u[k0 + i], c[i], s[i]);
-        for (int g = 0; g < P.Hkv; ++g) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(src_k + g * kHeadDim + k0);
-            const uint4 y = *reinterpret_cast<const uint4 *>(src_k + g * kHeadDim + k0 + half);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-            const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-            uint32_t ya[4], yb[4];
+            for (int j = 0; j < 8; ++j) rope_cos_sin(p, P.rope.u[k0 + j], c[j], s[j]);
+            for (int g0 = 0; g0 < P.Hkv; g0 += kPrepHeads) {
+                uint4 x[kPrepHeads], y[kPrepHeads];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y1l, y2l, y1h, y2h;
-                rope_rotate(bf16_lo(xw[i]), bf16_lo(yw[i]), c[2 * i], s[2 * i], y1l, y2l);
-                rope_rotate(bf16_hi(xw[i]), bf16_hi(yw[i]), c[2 * i + 1], s[2 * i + 1], y1h, y2h);
-                ya[i] = pack_bf16x2(y1l, y1h);
-                yb[i] = pack_bf16x2(y2l, y2h);
+                for (int g = 0; g < kPrepHeads; ++g) {
+                    if (g0 + g >= P.Hkv) break;
+                    const __nv_bfloat16 *src = src_k + (g0 + g) * kHeadDim + k0;
+                    x[g] = *reinterpret_cast<const uint4 *>(src);
+                    y[g] = *reinterpret_cast<const uint4 *>(src + half);
+                }
+#pragma unroll
+                for (int g = 0; g < kPrepHeads; ++g) {
+                    if (g0 + g >= P.Hkv) break;
+                    const uint32_t xw[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+                    const uint32_t yw[4] = {y[g].x, y[g].y, y[g].z, y[g].w};
+                    uint32_t ya[4], yb[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float y1l, y2l, y1h, y2h;
+                        rope_rotate(bf16_lo(xw[j]), bf16_lo(yw[j]), c[2 * j], s[2 * j], y1l, y2l);
+                        rope_rotate(bf16_hi(xw[j]), bf16_hi(yw[j]), c[2 * j + 1], s[2 * j + 1],
+                                    y1h, y2h);
+                        ya[j] = pack_bf16x2(y1l, y1h);
+                        yb[j] = pack_bf16x2(y2l, y2h);
+                    }
+                    __nv_bfloat16 *dst = dst_k + (g0 + g) * head_stride + k0;
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+                    *reinterpret_cast<uint4 *>(dst + half) = make_uint4(yb[0], yb[1], yb[2], yb[3]);
+                }
             }
-            __nv_bfloat16 *dst = dst_k + g * head_stride;
-            *reinterpret_cast<uint4 *>(dst + k0) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
-            *reinterpret_cast<uint4 *>(dst + k0 + half) = make_uint4(yb[0], yb[1], yb[2], yb[3]);
+        } else {
+            const bool key = it < n_rot + n_kcopy;
+            const int d0 = key ? r + (it - n_rot) * 8 : (it - n_rot - n_kcopy) * 8;
+            const __nv_bfloat16 *src = (key ? src_k : src_v) + d0;
+            __nv_bfloat16 *dst = (key ? dst_k : dst_v) + d0;
+            for (int g0 = 0; g0 < P.Hkv; g0 += kPrepHeads) {
+                uint4 v[kPrepHeads];
+#pragma unroll
+                for (int g = 0; g < kPrepHeads; ++g)
+                    v[g] = g0 + g < P.Hkv ? *reinterpret_cast<const uint4 *>(
+                                                src + (g0 + g) * kHeadDim)
+                                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int g = 0; g < kPrepHeads; ++g) {
+                    if (g0 + g >= P.Hkv) break;
+                    if (key || paged)
+                        *reinterpret_cast<uint4 *>(dst + (g0 + g) * head_stride) = v[g];
+                    else  // an exponent of all ones carries into the sign's place
+                        hit |= ((v[g].x & 0x7F807F80u) + 0x00800080u) |
+                               ((v[g].y & 0x7F807F80u) + 0x00800080u) |
+                               ((v[g].z & 0x7F807F80u) + 0x00800080u) |
+                               ((v[g].w & 0x7F807F80u) + 0x00800080u);
+                }
+            }
         }
-    } else if (it < n_rot + n_kcopy) {
-        const int d0 = r + (it - n_rot) * 8;
-        for (int g = 0; g < P.Hkv; ++g)
-            *reinterpret_cast<uint4 *>(dst_k + g * head_stride + d0) =
-                *reinterpret_cast<const uint4 *>(src_k + g * kHeadDim + d0);
-    } else {
-        const int d0 = (it - n_rot - n_kcopy) * 8;
-        uint32_t hit = 0;
-        for (int g = 0; g < P.Hkv; ++g) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src_v + g * kHeadDim + d0);
-            if (paged)
-                *reinterpret_cast<uint4 *>(dst_v + g * head_stride + d0) = v;
-            // an exponent of all ones carries into the sign's place
-            hit |= ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
-                   ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
-        }
-        if (!paged && (hit & 0x80008000u)) atomicOr(&P.odd_values[*P.call & 1], 1u);
     }
+    if (hit & 0x80008000u) atomicOr(&P.odd_values[*P.call & 1], 1u);
 }
 
 // ---------------------------------------------------------------- host side
@@ -294,10 +322,7 @@ spark_status done(cudaError_t e) {
 }
 
 spark_status launch_prep(const PagedParams &P, cudaStream_t s) {
-    const int r = P.rope.rot_dim;
-    const long long items = r / 16 + ((P.k_pages ? kHeadDim : P.rot_w) - r) / 8 + kHeadDim / 8;
-    const long long blocks = (P.N * items + kPrepThreads - 1) / kPrepThreads + 1;
-    if (blocks > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;
+    const long long blocks = (static_cast<long long>(P.N) + kPrepRows - 1) / kPrepRows + 1;
     return done(launch_overlapped(paged_prep_kernel, dim3(static_cast<unsigned>(blocks)),
                                   dim3(kPrepThreads), 0, s, P));
 }

@@ -35,15 +35,16 @@ struct PagedParams {
 };
 
 // The sequence whose tokens [cu[s], cu[s+1]) hold `row`, or -1 (padding, or
-// offsets that are no prefix sum).
-__device__ __forceinline__ int find_sequence(const int32_t *cu, int S, int row) {
-    int lo = 0, hi = S;  // the last s with cu[s] <= row lies in [lo, hi]
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] <= row)
-            lo = mid;
-        else
-            hi = mid - 1;
+// offsets that are no prefix sum), by one warp: 32 probes a step.
+__device__ __forceinline__ int find_sequence(const int32_t *cu, int S, int row, int lane) {
+    int lo = 0, n = S + 1;  // the last s with cu[s] <= row lies in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lane * step;
+        const unsigned hit = __ballot_sync(0xffffffffu, at < n && cu[lo + at] <= row);
+        const int last = hit ? 31 - __clz(hit) : 0;
+        lo += last * step;
+        n = n - last * step < step ? n - last * step : step;
     }
     return (lo < S && cu[lo] <= row && row < cu[lo + 1]) ? lo : -1;
 }

@@ -832,10 +832,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         tc_commit(&bars[kBarSlotEmpty + slot + 1]);
                         sc += 2;
                     }
-                    tc_commit(&bars[kBarODone]);
-                    return true;
                 }
-                for (int vs = 0; vs < 4; ++vs) {
+                for (int vs = 0; !kIsPacked && vs < 4; ++vs) {
                     const int slot = sc % kSlots;
                     if (!mbar_wait(&bars[kBarSlotFull + slot], (sc / kSlots) & 1, &abort_flag,
                                    P.status))
