@@ -32,6 +32,7 @@ struct PoolParams {
     unsigned *status;
     // workspace
     int32_t *n_copies;          // copies listed
+    int32_t *n_live;            // pages in use (compact)
     int32_t *copy_src, *copy_dst;   // [n_pages]
     int32_t *map;               // [n_pages]: where a page goes (compact)
     int32_t *row_a, *row_b, *row_c;   // [n_rows]
@@ -69,71 +70,93 @@ __device__ __forceinline__ int pages_of(int tokens, int page_size) {
 
 // Whether a row's counts fit the table (a pool that was not set up, or written
 // over, must not lead outside it).
-__device__ __forceinline__ bool row_sane(const PoolParams &P, int row, int held, int len) {
+__device__ __forceinline__ bool row_sane(const PoolParams &P, int held, int len) {
     return held >= 0 && held <= P.max_pages && len >= 0 && pages_of(len, P.page_size) <= held;
 }
 
 // ---------------------------------------------------------------- fork
 
-// Decides every pair before any row changes: row_a[i % ...] cannot hold more
-// pairs than rows, since a row is the target of one pair at most; pairs past
-// n_rows repeat a target and are refused here.
-__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(
-    const __grid_constant__ PoolParams P, const int32_t *src, const int32_t *dst, int n) {
-    grid_dep_wait();
-    grid_dep_launch();
-    // row_a[r]: the pair that forks into row r, or -1; row_b[r]: its pages;
-    // row_c[r]: its tokens
+// Decides every pair before any row changes.  row_a[r]: the first pair that
+// forks into row r; row_b[r]: its pages (-1: refused); row_c[r]: its tokens.
+__device__ __forceinline__ void fork_plan(const PoolParams &P, const int32_t *src,
+                                          const int32_t *dst, int n) {
     for (int r = threadIdx.x; r < P.n_rows; r += kPlanThreads) P.row_a[r] = n;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int d = dst[i];
-        if (d >= 0 && d < P.n_rows) atomicMin(&P.row_a[d], i);  // the first mention
+        if (d >= 0 && d < P.n_rows) atomicMin(&P.row_a[d], i);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int s = src[i], d = dst[i];
-        bool ok = s >= 0 && s < P.n_rows && d >= 0 && d < P.n_rows;
-        if (ok) ok = P.row_a[d] == i;
-        if (ok) ok = P.held[d] == 0 && row_sane(P, s, P.held[s], P.len[s]);
-        if (!ok) {
-            atomicOr(P.status, kErrRow);
-            // a pair that comes first but is refused leaves the row alone
-            if (d >= 0 && d < P.n_rows && P.row_a[d] == i) P.row_b[d] = -1;
-        } else {
-            P.row_b[d] = pages_of(P.len[s], P.page_size);
-            P.row_c[d] = P.len[s];
+        const bool row = d >= 0 && d < P.n_rows;
+        const bool first = row && P.row_a[d] == i;
+        int pages = -1;
+        if (first && s >= 0 && s < P.n_rows && P.held[d] == 0) {
+            const int held = P.held[s], len = P.len[s];
+            if (row_sane(P, held, len)) {
+                pages = pages_of(len, P.page_size);
+                P.row_c[d] = len;
+            }
         }
+        if (pages < 0) atomicOr(P.status, kErrRow);
+        if (first) P.row_b[d] = pages;
     }
 }
 
-// One CTA per pair: the table row and the counts.
+// The table row and the counts of pair i, by the threads t, t + step, ...
+__device__ __forceinline__ void fork_apply(const PoolParams &P, const int32_t *src,
+                                           const int32_t *dst, int i, int t, int step) {
+    const int d = dst[i];
+    if (d < 0 || d >= P.n_rows || P.row_a[d] != i) return;
+    const int count = P.row_b[d];
+    if (count < 0) return;
+    const int32_t *from = P.table + static_cast<size_t>(src[i]) * P.max_pages;
+    int32_t *to = P.table + static_cast<size_t>(d) * P.max_pages;
+    for (int j = t; j < P.max_pages; j += step) {
+        int p = -1;
+        if (j < count) {
+            p = from[j];
+            if (p < 0 || p >= P.n_pages)
+                atomicOr(P.status, kErrPage);
+            else
+                atomicAdd(&P.refs[p], 1);
+        }
+        to[j] = p;
+    }
+    if (t == 0) {
+        P.held[d] = count;
+        P.len[d] = P.row_c[d];
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(
+    const __grid_constant__ PoolParams P, const int32_t *src, const int32_t *dst, int n) {
+    grid_dep_wait();
+    grid_dep_launch();
+    fork_plan(P, src, dst, n);
+}
+
 __global__ void __launch_bounds__(kRowThreads) fork_apply_kernel(
     const __grid_constant__ PoolParams P, const int32_t *src, const int32_t *dst, int n) {
     grid_dep_wait();
     grid_dep_launch();
-    const int i = blockIdx.x;
-    const int d = dst[i];
-    if (d < 0 || d >= P.n_rows || P.row_a[d] != i || P.row_b[d] < 0) return;
-    const int count = P.row_b[d];
-    const int32_t *from = P.table + static_cast<size_t>(src[i]) * P.max_pages;
-    int32_t *to = P.table + static_cast<size_t>(d) * P.max_pages;
-    for (int j = threadIdx.x; j < P.max_pages; j += kRowThreads) {
-        int p = -1;
-        if (j < count) {
-            p = from[j];
-            if (p < 0 || p >= P.n_pages) {
-                atomicOr(P.status, kErrPage);
-            } else {
-                atomicAdd(&P.refs[p], 1);
-            }
-        }
-        to[j] = p;
-    }
-    if (threadIdx.x == 0) {
-        P.held[d] = count;
-        P.len[d] = P.row_c[d];
-    }
+    fork_apply(P, src, dst, blockIdx.x, threadIdx.x, kRowThreads);
+}
+
+// Both in one CTA, a warp per pair, where there are few table entries to write:
+// one launch less, against a CTA per pair for many.
+constexpr long long kForkSmall = 32768;
+
+__global__ void __launch_bounds__(kPlanThreads) fork_kernel(const __grid_constant__ PoolParams P,
+                                                            const int32_t *src, const int32_t *dst,
+                                                            int n) {
+    grid_dep_wait();
+    grid_dep_launch();
+    fork_plan(P, src, dst, n);
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < n; i += kPlanThreads / 32)
+        fork_apply(P, src, dst, i, threadIdx.x & 31, 32);
 }
 
 // ---------------------------------------------------------------- free
@@ -153,7 +176,7 @@ __global__ void __launch_bounds__(kRowThreads) free_kernel(const __grid_constant
     for (int j = threadIdx.x; j < i; j += kRowThreads) first = first && rows[j] != r;
     if (!__syncthreads_and(first)) return;
     const int held = P.held[r], len = P.len[r];
-    if (!row_sane(P, r, held, len)) {
+    if (!row_sane(P, held, len)) {
         if (threadIdx.x == 0) atomicOr(P.status, kErrRow);
         return;
     }
@@ -178,174 +201,221 @@ __global__ void __launch_bounds__(kRowThreads) free_kernel(const __grid_constant
 
 // ---------------------------------------------------------------- reserve
 
-// One CTA.  row_a[r]: the page row r is about to write into although it holds
-// tokens already (-1: none); row_b[r]: pages wanted, the copy in bit 30;
-// row_c[r]: exclusive prefix of the wants.
+constexpr int kScanPages = 4 * kPlanThreads;  // pages a scan step looks at, four per thread
+
+// Which of the four pages 4 tid .. 4 tid + 3 behind p0 are free, as bits.
+__device__ __forceinline__ unsigned free_bits(const PoolParams &P, int p0) {
+    unsigned bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = p0 + 4 * static_cast<int>(threadIdx.x) + i;
+        if (p < P.n_pages && P.refs[p] == 0) bits |= 1u << i;
+    }
+    return bits;
+}
+
+// What row r asks for: the page it is about to write into although it holds
+// tokens already (-1: none), and the fresh pages behind the ones it holds.
+__device__ __forceinline__ void row_wish(const PoolParams &P, const int32_t *add, int r, int &page,
+                                         int &fresh) {
+    page = -1;
+    fresh = 0;
+    const int more = add[r], held = P.held[r], len = P.len[r];
+    if (more <= 0) return;
+    const long long end = static_cast<long long>(len) + more;
+    if (!row_sane(P, held, len) || end > static_cast<long long>(P.max_pages) * P.page_size) {
+        atomicOr(P.status, kErrRow);
+        return;
+    }
+    if (len % P.page_size) {
+        page = P.table[static_cast<size_t>(r) * P.max_pages + len / P.page_size];
+        if (page < 0 || page >= P.n_pages) {
+            atomicOr(P.status, kErrPage);
+            page = -1;
+            return;
+        }
+    }
+    const int need = static_cast<int>((end + P.page_size - 1) / P.page_size);
+    fresh = need > held ? need - held : 0;
+    if (fresh > P.n_pages) fresh = P.n_pages + 1;  // too many, whatever the sum
+}
+
+// One CTA, a row per thread at a time.  Rows of the first kPlanThreads keep
+// their wishes in registers; the arrays in the workspace serve pools with more
+// (a trip through L2 costs half a microsecond, and there are several).
 __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(
     const __grid_constant__ PoolParams P, const int32_t *add, int32_t *taken) {
     __shared__ int warp_sums[32];
     __shared__ long long wide_sums[32];
+    __shared__ int s_page[kPlanThreads];  // row_wish's pages of this chunk of rows
+    __shared__ int s_map[kPlanThreads];   // the first pages taken
     constexpr int kCopyBit = 1 << 30;
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x;
-    for (int r = tid; r < P.n_rows; r += kPlanThreads) {
-        int page = -1, fresh = 0;
-        const int more = add[r];
-        if (more > 0) {
-            const int held = P.held[r], len = P.len[r];
-            const long long end = static_cast<long long>(len) + more;
-            if (!row_sane(P, r, held, len) ||
-                end > static_cast<long long>(P.max_pages) * P.page_size) {
-                atomicOr(P.status, kErrRow);
-            } else {
-                const int need = static_cast<int>((end + P.page_size - 1) / P.page_size);
-                fresh = need > held ? need - held : 0;
-                if (fresh > P.n_pages) fresh = P.n_pages + 1;  // too many, whatever the sum
-                if (len % P.page_size) {
-                    page = P.table[static_cast<size_t>(r) * P.max_pages + len / P.page_size];
-                    if (page < 0 || page >= P.n_pages) {
-                        atomicOr(P.status, kErrPage);
-                        page = -1;
-                        fresh = 0;
-                    }
-                }
-            }
-        }
-        P.row_a[r] = page;
-        P.row_b[r] = fresh;
-    }
-    __syncthreads();
-    // copies: all rows that share the page but the last holder
-    for (int r = tid; r < P.n_rows; r += kPlanThreads) {
-        const int page = P.row_a[r];
-        if (page < 0) continue;
-        const int refs = P.refs[page];
-        if (refs <= 1) continue;
-        int before = 0;
-        for (int q = 0; q < r; ++q) before += P.row_a[q] == page;
-        if (refs - before > 1) P.row_b[r] |= kCopyBit;
-    }
-    __syncthreads();
-    // prefix sum of the wants, and of the copies, over the rows
+    const bool one = P.n_rows <= kPlanThreads;
+    const unsigned first_free = free_bits(P, 0);  // (its latency overlaps the rows')
+    int my_want = 0, my_at = 0;                   // of the chunk's row
     long long base = 0;
     int copies = 0;
     for (int r0 = 0; r0 < P.n_rows; r0 += kPlanThreads) {
         const int r = r0 + tid;
-        const int w = r < P.n_rows ? P.row_b[r] : 0;
-        const int cp = (w & kCopyBit) ? 1 : 0;
+        int page = -1, fresh = 0, refs = 0;
+        if (r < P.n_rows) row_wish(P, add, r, page, fresh);
+        if (page >= 0) refs = P.refs[page];
+        s_page[tid] = page;
+        if (!one && r < P.n_rows) P.row_a[r] = page;
+        __syncthreads();
+        // a copy for all rows that are about to write into the page but the
+        // last holder
+        int copy = 0;
+        if (refs > 1) {
+            int before = 0;
+            for (int q = 0; q < r0; ++q) before += P.row_a[q] == page;
+            for (int q = 0; q < tid; ++q) before += s_page[q] == page;
+            copy = refs - before > 1;
+        }
         long long total;
         int ctotal;
-        const long long at =
-            base + block_scan<long long>((w & ~kCopyBit) + cp, &total, wide_sums);
-        const int cat = copies + block_scan(cp, &ctotal, warp_sums);
+        const long long at = base + block_scan<long long>(fresh + copy, &total, wide_sums);
+        const int cat = copies + block_scan(copy, &ctotal, warp_sums);
         // past n_pages the call will be refused: nothing of it is used
-        if (r < P.n_rows) P.row_c[r] = static_cast<int>(at < P.n_pages ? at : P.n_pages);
-        if (cp && cat < P.n_pages) {
-            P.copy_src[cat] = P.row_a[r];
-            P.copy_dst[cat] = static_cast<int>(at < P.n_pages ? at : P.n_pages);  // a rank, for now
+        my_want = fresh | (copy ? kCopyBit : 0);
+        my_at = static_cast<int>(at < P.n_pages ? at : P.n_pages);
+        if (copy && cat < P.n_pages) {
+            P.copy_src[cat] = page;
+            P.copy_dst[cat] = my_at;  // its rank among the free pages, for now
+        }
+        if (!one && r < P.n_rows) {
+            P.row_b[r] = my_want;
+            P.row_c[r] = my_at;
         }
         base += total;
         copies += ctotal;
     }
     const int want = static_cast<int>(base <= P.n_pages ? base : P.n_pages + 1);
-    // the first `want` free pages, in map[]
+    // the first `want` free pages
+    int32_t *map = want <= kPlanThreads ? s_map : P.map;
     int found = 0;
-    for (int p0 = 0; p0 < P.n_pages && found < want; p0 += kPlanThreads) {
-        const int p = p0 + tid;
-        const int is_free = p < P.n_pages && P.refs[p] == 0;
+    for (int p0 = 0; p0 < P.n_pages && found < want; p0 += kScanPages) {
+        const unsigned bits = p0 == 0 ? first_free : free_bits(P, p0);
         int total;
-        const int at = block_scan(is_free, &total, warp_sums);
-        if (is_free && found + at < want) P.map[found + at] = p;
+        int at = found + block_scan(__popc(bits), &total, warp_sums);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (bits >> i & 1u) {
+                if (at < want) map[at] = p0 + 4 * tid + i;
+                ++at;
+            }
         found += total;
     }
     __syncthreads();
-    if (found < want) {
-        if (tid == 0) {
-            *P.n_copies = 0;
-            if (taken) *taken = -1;
-        }
-        return;
-    }
+    const bool ok = found >= want;
     if (tid == 0) {
-        *P.n_copies = copies;
-        if (taken) *taken = want;
+        *P.n_copies = ok ? copies : 0;
+        if (taken) *taken = ok ? want : -1;
     }
-    for (int i = tid; i < want; i += kPlanThreads) P.refs[P.map[i]] = 1;
+    if (!ok) return;
+    for (int i = tid; i < want; i += kPlanThreads) P.refs[map[i]] = 1;
     for (int i = tid; i < copies; i += kPlanThreads) {
-        P.copy_dst[i] = P.map[P.copy_dst[i]];
+        P.copy_dst[i] = map[P.copy_dst[i]];
         atomicSub(&P.refs[P.copy_src[i]], 1);
     }
     for (int r = tid; r < P.n_rows; r += kPlanThreads) {
-        const int w = P.row_b[r];
+        const int w = one ? my_want : P.row_b[r];
         if (!w) continue;
-        int at = P.row_c[r];
+        int at = one ? my_at : P.row_c[r];
         int32_t *row = P.table + static_cast<size_t>(r) * P.max_pages;
-        if (w & kCopyBit) row[P.len[r] / P.page_size] = P.map[at++];
+        if (w & kCopyBit) row[P.len[r] / P.page_size] = map[at++];
         const int fresh = w & ~kCopyBit, held = P.held[r];
-        for (int j = 0; j < fresh; ++j) row[held + j] = P.map[at + j];
-        P.held[r] = held + fresh;
+        for (int j = 0; j < fresh; ++j) row[held + j] = map[at + j];
+        if (fresh) P.held[r] = held + fresh;
     }
 }
 
 // ---------------------------------------------------------------- compact
 
+// With U(p) the pages in use below p, of n_live in all: a free page p < n_live
+// is hole number p - U(p), a used page p >= n_live mover number U(p) - U(n_live),
+// and there are as many of one as of the other.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(
     const __grid_constant__ PoolParams P, int32_t *live) {
     __shared__ int warp_sums[32];
+    __shared__ int s_below;  // U(n_live)
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x;
+    auto used_bits = [&](int p0) {
+        unsigned bits = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + 4 * tid + i;
+            if (p < P.n_pages && P.refs[p] > 0) bits |= 1u << i;
+        }
+        return bits;
+    };
+    const unsigned first = used_bits(0);
     int n = 0;
-    for (int p = tid; p < P.n_pages; p += kPlanThreads) n += P.refs[p] > 0;
+    for (int p0 = 0; p0 < P.n_pages; p0 += kScanPages)
+        n += __popc(p0 == 0 ? first : used_bits(p0));
     int n_live;
     block_scan(n, &n_live, warp_sums);
-    int holes = 0, movers = 0;
-    for (int p0 = 0; p0 < P.n_pages; p0 += kPlanThreads) {
-        const int p = p0 + tid;
-        const bool used = p < P.n_pages && P.refs[p] > 0;
-        const int hole = p < n_live && !used, mover = p >= n_live && used;
+    if (tid == 0 && n_live >= P.n_pages) s_below = n_live;
+    int before = 0;
+    for (int p0 = 0; p0 < P.n_pages; p0 += kScanPages) {
+        const unsigned bits = p0 == 0 ? first : used_bits(p0);
         int total;
-        int at = block_scan(hole, &total, warp_sums);
-        if (hole) P.copy_dst[holes + at] = p;
-        holes += total;
-        at = block_scan(mover, &total, warp_sums);
-        if (mover) P.copy_src[movers + at] = p;
-        if (p < P.n_pages) P.map[p] = p;
-        movers += total;
+        int u = before + block_scan(__popc(bits), &total, warp_sums);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + 4 * tid + i;
+            if (p >= P.n_pages) break;
+            const bool used = bits >> i & 1u;
+            if (p == n_live) s_below = u;
+            if (p < n_live) {
+                if (!used) P.copy_dst[p - u] = p;
+            } else {
+                P.map[p] = used ? u : p;  // U(p) of a mover, for now
+            }
+            u += used;
+        }
+        before += total;
     }
     __syncthreads();
-    for (int i = tid; i < movers; i += kPlanThreads) {  // as many holes as movers
-        const int s = P.copy_src[i], d = P.copy_dst[i];
-        P.map[s] = d;
-        P.refs[d] = P.refs[s];
-        P.refs[s] = 0;
+    const int below = s_below, movers = n_live - below;
+    for (int p = n_live + tid; p < P.n_pages; p += kPlanThreads) {
+        const int refs = P.refs[p];
+        if (refs <= 0) continue;
+        const int i = P.map[p] - below, to = P.copy_dst[i];
+        P.copy_src[i] = p;
+        P.map[p] = to;
+        P.refs[to] = refs;
+        P.refs[p] = 0;
     }
     if (tid == 0) {
         *P.n_copies = movers;
+        *P.n_live = n_live;
         if (live) *live = n_live;
-        P.row_a[0] = n_live;
     }
 }
 
-// The tables follow their pages: one CTA per row.
-__global__ void __launch_bounds__(kRowThreads) compact_table_kernel(
-    const __grid_constant__ PoolParams P) {
-    grid_dep_wait();
-    grid_dep_launch();
-    const int r = blockIdx.x, n_live = P.row_a[0];
-    const int held = P.held[r];
-    if (held < 0 || held > P.max_pages) {
-        if (threadIdx.x == 0) atomicOr(P.status, kErrRow);
-        return;
-    }
-    int32_t *row = P.table + static_cast<size_t>(r) * P.max_pages;
-    for (int j = threadIdx.x; j < held; j += kRowThreads) {
-        const int p = row[j];
-        if (p < 0 || p >= P.n_pages)
-            atomicOr(P.status, kErrPage);
-        else if (p >= n_live)
-            row[j] = P.map[p];
+// The tables follow their pages: rows r, r + step, ..., one CTA each.
+__device__ __forceinline__ void compact_tables(const PoolParams &P) {
+    const int n_live = *P.n_live;
+    for (int r = blockIdx.x; r < P.n_rows; r += gridDim.x) {
+        const int held = P.held[r];
+        if (held < 0 || held > P.max_pages) {
+            if (threadIdx.x == 0) atomicOr(P.status, kErrRow);
+            continue;
+        }
+        int32_t *row = P.table + static_cast<size_t>(r) * P.max_pages;
+        for (int j = threadIdx.x; j < held; j += blockDim.x) {
+            const int p = row[j];
+            if (p < 0 || p >= P.n_pages)
+                atomicOr(P.status, kErrPage);
+            else if (p >= n_live)
+                row[j] = P.map[p];
+        }
     }
 }
 
@@ -354,10 +424,12 @@ __global__ void __launch_bounds__(kRowThreads) compact_table_kernel(
 // The listed page copies in every layer, K and V, in chunks of 32 KB (or the
 // page, where it is smaller).  No page is the source of one copy and the
 // target of another, so their order does not matter.
+template <bool kTables>
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(
     const __grid_constant__ PoolParams P) {
     grid_dep_wait();
     grid_dep_launch();
+    if (kTables) compact_tables(P);
     const long long per_page = (P.page_bytes + kCopyChunk - 1) / kCopyChunk;
     const long long total = per_page * 2 * P.n_layers * *P.n_copies;
     for (long long c = blockIdx.x; c < total; c += gridDim.x) {
@@ -453,6 +525,7 @@ PoolParams pool_params(const spark_page_pool *pool, void *workspace) {
     P.page_bytes = static_cast<long long>(pool->Hkv) * pool->page_size * kHeadDim * 2;
     P.status = reinterpret_cast<unsigned *>(ws);
     P.n_copies = reinterpret_cast<int32_t *>(ws + pl.counts);
+    P.n_live = P.n_copies + 1;
     P.copy_src = reinterpret_cast<int32_t *>(ws + pl.copy_src);
     P.copy_dst = reinterpret_cast<int32_t *>(ws + pl.copy_dst);
     P.map = reinterpret_cast<int32_t *>(ws + pl.map);
@@ -468,11 +541,14 @@ spark_status done(cudaError_t e) {
     return SPARK_ERR_CUDA;
 }
 
+// The copies listed, `most` at most; with kTables the rows' tables too.
+template <bool kTables>
 cudaError_t launch_copies(const PoolParams &P, long long most, int sms, cudaStream_t stream) {
     const long long per_page = (P.page_bytes + kCopyChunk - 1) / kCopyChunk;
-    long long grid = static_cast<long long>(sms) * 4;
-    if (grid > per_page * 2 * P.n_layers * most) grid = per_page * 2 * P.n_layers * most;
-    return launch_overlapped(page_copy_kernel, dim3(static_cast<unsigned>(grid)),
+    long long work = per_page * 2 * P.n_layers * most;
+    if (kTables && work < P.n_rows) work = P.n_rows;
+    const long long grid = work < sms * 4ll ? work : sms * 4ll;
+    return launch_overlapped(page_copy_kernel<kTables>, dim3(static_cast<unsigned>(grid)),
                              dim3(kCopyThreads), 0, stream, P);
 }
 
@@ -507,6 +583,9 @@ spark_status spark_attn_pages_fork(const spark_page_pool *pool, const int32_t *s
     if (st != SPARK_OK) return st;
     const PoolParams P = pool_params(pool, workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (static_cast<long long>(n) * pool->max_pages <= kForkSmall)
+        return done(launch_overlapped(fork_kernel, dim3(1), dim3(kPlanThreads), 0, s, P, src, dst,
+                                      n));
     st = done(launch_overlapped(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, P, src, dst,
                                 n));
     if (st != SPARK_OK) return st;
@@ -531,7 +610,7 @@ spark_status spark_attn_pages_reserve(const spark_page_pool *pool, const int32_t
                                 taken));
     const long long most = pool->n_rows < pool->n_pages ? pool->n_rows : pool->n_pages;
     if (st != SPARK_OK || most == 0) return st;
-    return done(launch_copies(P, most, sms, s));
+    return done(launch_copies<false>(P, most, sms, s));
 }
 
 spark_status spark_attn_pages_free(const spark_page_pool *pool, const int32_t *rows,
@@ -564,10 +643,7 @@ spark_status spark_attn_pages_compact(const spark_page_pool *pool, int32_t *live
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = done(launch_overlapped(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, P, live));
     if (st != SPARK_OK || pool->n_rows == 0 || pool->n_pages == 0) return st;
-    st = done(launch_overlapped(compact_table_kernel, dim3(pool->n_rows), dim3(kRowThreads), 0, s,
-                                P));
-    if (st != SPARK_OK) return st;
-    return done(launch_copies(P, pool->n_pages / 2 + 1, sms, s));
+    return done(launch_copies<true>(P, pool->n_pages / 2 + 1, sms, s));
 }
 
 }  // extern "C"

@@ -121,6 +121,16 @@ def test_fork_refuses_rows_in_use_and_rows_that_do_not_exist(cuda):
     p.check(fga.SPARK_DEVERR_ROW)
 
 
+def test_fork_of_many_long_rows(cuda):
+    """More table entries than one CTA writes."""
+    p = Pair(n_layers=1, n_pages=700, Hkv=1, n_rows=400, max_pages=130)
+    p.append([2000, 1999, 5] + [0] * 397)
+    p.fork([(r % 3, r) for r in range(3, 400)] + [(0, 5), (400, 2), (1, 399)])
+    p.check(fga.SPARK_DEVERR_ROW)
+    p.append([1, 0, 1] + [r % 2 for r in range(397)])
+    p.check()
+
+
 def test_reserve_all_or_nothing(cuda):
     p = Pair(n_pages=6)
     p.append([50, 0, 0, 0, 0, 0])          # 4 pages
