@@ -121,9 +121,12 @@ struct __align__(16) PackedItem {
     int t0;                    // its first token inside the sequence
     int row0, len;             // the sequence's first row, its tokens
     int start;                 // tokens in its pages before the call
-    int bin;
     unsigned call;             // the call's number: which word of odd_values is its own
-    int pad;
+    // Its key tiles [k0, k0 + tiles) of those the query tile visits.  Where a
+    // query tile is split, `parts` items share it: part `part` of KV head g
+    // leaves its state at slot + g * parts + part.
+    int k0, tiles;
+    int part, parts, slot, pad;
 };
 
 struct PackedInfo {
@@ -137,6 +140,10 @@ struct PackedInfo {
     const int32_t *table;      // [S, max_pages] (paged prompts)
     int n_pages, page_shift, max_pages;
     __nv_bfloat16 *out;        // [N, H*256]: ragged tiles are stored row by row
+    float2 *part_ml;           // [slots][128] maximum (raw units), sum
+    float4 *part_o;            // [slots][64][128] unnormalised outputs, four dims each
+    const PackedItem *splits;  // the split query tiles (their first parts)
+    const int *n_splits;
 };
 
 struct PrefillParams {

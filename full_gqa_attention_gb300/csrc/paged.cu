@@ -51,13 +51,34 @@ __device__ __forceinline__ int prep_scan(int v, int *total) {
 // of tq tokens, and the tiles are put in order of the key tiles they visit,
 // most first (a counting sort), so that the long ones do not start last.  The
 // order inside a bin is whatever the atomics give; no result depends on it.
+//
+// A query tile that would outlast the others is split along its keys into
+// parts of L key tiles or fewer.  With no more query tiles than SMs, L is the
+// least that still fits them all in one wave; else it is an SM's share of all
+// the work and kPartCost besides, what a part costs in key tiles (set-up,
+// leaving its state, joining).  So uniform batches are not split, and a short
+// chunk on top of a long prefix fills the GPU.
+constexpr int kMinPart = 6;
+constexpr int kPartCost = 8;
+constexpr int kPlanSeqs = 1024;       // sequences whose offsets fit in shared memory
+constexpr int kMaxSms = 256;
+
 __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
     __shared__ int bins[kBins];
+    __shared__ int s_base[kPlanSeqs + 1];
+    __shared__ int s_n[kMaxSms];
+    __shared__ int s_limit, s_slots, s_splits, s_max;
+    __shared__ unsigned long long s_total;
     const int tid = threadIdx.x, tq = 128 / P.G;
     const long long cap = static_cast<long long>(P.max_pages) << P.page_shift;
+    int *tile_base = P.S <= kPlanSeqs ? s_base : P.tile_base;
     for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
     const unsigned call = *P.call;  // the attention kernel counts it on
-    if (tid == 0) P.odd_values[(call + 1) & 1] = 0;
+    if (tid == 0) {
+        P.odd_values[(call + 1) & 1] = 0;
+        s_total = 0;
+        s_max = s_slots = s_splits = 0;
+    }
     int base = 0;
     for (int s0 = 0; s0 < P.S; s0 += kPrepThreads) {
         const int s = s0 + tid;
@@ -76,51 +97,136 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
         }
         int total;
         const int at = prep_scan(n, &total);
-        if (s < P.S) P.tile_base[s] = base + at;
+        if (s < P.S) tile_base[s] = base + at;
         base += total;
     }
     // offsets that overlap can ask for more tiles than the list holds
-    const int n_tiles = base < P.most ? base : P.most;
-    for (int i = n_tiles + tid; i < P.most; i += kPrepThreads)
-        P.work[i] = PackedItem{-1, 0, 0, 0, 0, 0, call, 0};
+    const int extra = P.slots > 0 ? P.sms / P.Hkv + 1 : 0;
+    const int n_tiles = base < P.most - extra ? base : P.most - extra;
     __syncthreads();
-    for (int i = tid; i < n_tiles; i += kPrepThreads) {
+    auto tile = [&](int i) {
         int lo = 0, hi = P.S - 1;  // the last s with tile_base[s] <= i
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (P.tile_base[mid] <= i)
+            if (tile_base[mid] <= i)
                 lo = mid;
             else
                 hi = mid - 1;
         }
-        const int t0 = (i - P.tile_base[lo]) * tq, row0 = P.cu[lo];
-        const int len = P.cu[lo + 1] - row0, st = P.start ? P.start[lo] : 0;
-        const KeyTiles kt = prefill_key_tiles(P.kind, P.window, st + t0,
-                                              st + (t0 + tq < len ? t0 + tq : len), 128,
-                                              P.start != nullptr);
-        const int bin = kBins - 1 - (kt.ntiles < kBins ? kt.ntiles : kBins - 1);
-        P.tiles[i] = PackedItem{lo, t0, row0, len, st, bin, call, 0};
-        atomicAdd(&bins[bin], 1);
+        PackedItem t;
+        t.seq = lo;
+        t.t0 = (i - tile_base[lo]) * tq;
+        t.row0 = P.cu[lo];
+        t.len = P.cu[lo + 1] - t.row0;
+        t.start = P.start ? P.start[lo] : 0;
+        t.call = call;
+        t.k0 = 0;
+        t.tiles = prefill_key_tiles(P.kind, P.window, t.start + t.t0,
+                                    t.start + (t.t0 + tq < t.len ? t.t0 + tq : t.len), 128,
+                                    P.start != nullptr).ntiles;
+        t.part = t.slot = t.pad = 0;
+        t.parts = 1;
+        return t;
+    };
+    PackedItem first = {};  // the thread's first tile: in most calls its only one
+    if (tid < n_tiles) first = tile(tid);
+    const bool wave = static_cast<long long>(n_tiles) * P.Hkv <= P.sms;
+    if (P.slots > 0) {
+        unsigned long long sum = 0;
+        int most = 0;
+        for (int i = tid; i < n_tiles; i += kPrepThreads) {
+            const int n = i == tid ? first.tiles : tile(i).tiles;
+            sum += n;
+            most = n > most ? n : most;
+            if (wave) s_n[i] = n;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+        }
+        if ((tid & 31) == 0) {
+            atomicAdd(&s_total, sum);
+            atomicMax(&s_max, most);
+        }
+        __syncthreads();
+    }
+    if (tid < 32) {
+        // the longest part
+        int limit = 1 << 30;
+        if (P.slots > 0 && s_max > kMinPart) {
+            limit = s_max;
+            if (wave) {
+                int lo = kMinPart, hi = s_max;  // hi fits
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    int parts = 0;
+                    for (int i = tid; i < n_tiles; i += 32) parts += (s_n[i] + mid - 1) / mid;
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+                        parts += __shfl_xor_sync(0xffffffffu, parts, off);
+                    if (parts * P.Hkv <= P.sms)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                if (hi + kPartCost < limit) limit = hi;
+            } else {
+                const unsigned long long share =
+                    (s_total * P.Hkv + P.sms - 1) / P.sms + kPartCost;
+                if (share < static_cast<unsigned long long>(limit))
+                    limit = static_cast<int>(share);
+            }
+        }
+        if (tid == 0) s_limit = limit;
+    }
+    __syncthreads();
+    const int limit = s_limit;
+    auto bin_of = [&](int n) { return kBins - 1 - (n < kBins ? n : kBins - 1); };
+    for (int i = tid; i < n_tiles; i += kPrepThreads) {
+        const int n = i == tid ? first.tiles : tile(i).tiles;
+        const int parts = (n + limit - 1) / limit;
+        atomicAdd(&bins[bin_of((n + parts - 1) / parts)], parts);
     }
     __syncthreads();
     constexpr int kPer = kBins / kPrepThreads;
-    int count[kPer], sum = 0, total;
+    int count[kPer], mine = 0, total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         count[i] = bins[tid * kPer + i];
-        sum += count[i];
+        mine += count[i];
     }
-    int at = prep_scan(sum, &total);
+    int at = prep_scan(mine, &total);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         bins[tid * kPer + i] = at;
         at += count[i];
     }
     __syncthreads();
-    for (int i = tid; i < n_tiles; i += kPrepThreads) {
-        const PackedItem t = P.tiles[i];
-        P.work[atomicAdd(&bins[t.bin], 1)] = t;
+    for (int i = total + tid; i < P.most; i += kPrepThreads) {
+        PackedItem t = {};
+        t.seq = -1;
+        t.call = call;
+        P.work[i] = t;
     }
+    for (int i = tid; i < n_tiles; i += kPrepThreads) {
+        PackedItem t = i == tid ? first : tile(i);
+        const int n = t.tiles, parts = (n + limit - 1) / limit;
+        int place = atomicAdd(&bins[bin_of((n + parts - 1) / parts)], parts);
+        if (parts > 1) {
+            t.parts = parts;
+            t.slot = atomicAdd(&s_slots, parts * P.Hkv);
+            P.splits[atomicAdd(&s_splits, 1)] = t;
+        }
+        for (int p = 0; p < parts; ++p) {
+            t.part = p;
+            t.k0 = static_cast<int>(static_cast<long long>(n) * p / parts);
+            t.tiles = static_cast<int>(static_cast<long long>(n) * (p + 1) / parts) - t.k0;
+            P.work[place++] = t;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) *P.n_splits = s_splits;
 }
 
 // Where the token of `row` goes in the pages (elements), or -1: padding, or a
@@ -332,27 +438,41 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // Workspace of a packed or paged prefill: the status header, the query tiles,
 // and (packed) the rotated leading key dims.
 struct PackedPlan {
-    long long most;  // query tiles at most: full ones, and a ragged one per sequence
-    int rot_w;
-    size_t flags, base, tiles, work, krot, bytes;
+    long long most;  // items at most: full query tiles, a ragged one per sequence, parts
+    int rot_w, slots;
+    size_t flags, base, splits, work, krot, ml, o, bytes;
 };
 
-PackedPlan plan_packed(int N, int S, int H, int Hkv, const spark_layer_desc *desc, bool paged) {
+// Query tiles are split where keys are many: always possible over pages, and in
+// a packed prompt of more than kMinPart key tiles.  At most two parts per SM
+// then have a state to leave (plan_tiles: a tile is split into parts of at
+// least an SM's share, or all parts fit in one wave).
+PackedPlan plan_packed(int N, int S, int H, int Hkv, const spark_layer_desc *desc, bool paged,
+                       int sms) {
     PackedPlan pl{};
     const int tq = 128 / (H / Hkv);
     pl.most = static_cast<long long>(N / tq) + (S < N ? S : N);
     pl.rot_w = paged ? 0 : (desc->rot_dim + 63) / 64 * 64;
+    const bool long_rows = desc->kind == SPARK_LAYER_FULL || desc->window > 128 * kMinPart;
+    if (long_rows && (paged || N > 128 * kMinPart) && sms <= kMaxSms) {
+        pl.slots = 2 * sms;
+        pl.most += sms / Hkv + 1;
+    }
     pl.flags = kWorkspaceHeader;
     pl.base = pl.flags + 256;
-    pl.tiles = pl.base + up256((static_cast<size_t>(S) + 1) * 4);
-    pl.work = pl.tiles + up256(static_cast<size_t>(pl.most) * sizeof(PackedItem));
+    pl.splits = pl.base + up256((static_cast<size_t>(S) + 1) * 4);
+    pl.work = pl.splits + up256((pl.slots > 0 ? sms : 0) * sizeof(PackedItem));
     pl.krot = pl.work + up256(static_cast<size_t>(pl.most) * sizeof(PackedItem));
-    pl.bytes = pl.krot + up256(static_cast<size_t>(N) * Hkv * pl.rot_w * 2);
+    pl.ml = pl.krot + up256(static_cast<size_t>(N) * Hkv * pl.rot_w * 2);
+    pl.o = pl.ml + static_cast<size_t>(pl.slots) * 128 * sizeof(float2);
+    pl.bytes = pl.o + static_cast<size_t>(pl.slots) * 128 * kHeadDim * sizeof(float);
     return pl;
 }
 
 size_t packed_workspace(int N, int S, int H, int Hkv, const spark_layer_desc *desc, bool paged) {
-    return plan_packed(N, S, H, Hkv, desc, paged).bytes;
+    int sms;
+    device_ready(&sms);
+    return plan_packed(N, S, H, Hkv, desc, paged, sms).bytes;
 }
 
 // The attention kernel's launch: its parameters and tensor maps.
@@ -378,6 +498,12 @@ spark_status launch_packed_attn(const PagedParams &P, const PackedPlan &pl, int 
     A.rot_w = pl.rot_w;
     A.wave = sms;
     A.pk.work = P.work;
+    if (pl.slots > 0) {
+        A.pk.part_ml = reinterpret_cast<float2 *>(P.part_ml);
+        A.pk.part_o = reinterpret_cast<float4 *>(P.part_o);
+        A.pk.splits = P.splits;
+        A.pk.n_splits = P.n_splits;
+    }
     A.pk.odd_values = P.odd_values;
     A.pk.call = P.call;
     A.pk.table = P.table;
@@ -468,11 +594,11 @@ spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_
         st = check_pages(k_pages, v_pages, n_pages, page_size, table, max_pages);
         if (st != SPARK_OK) return st;
     }
-    const PackedPlan pl = plan_packed(N, S, H, Hkv, desc, paged);
-    if (workspace_bytes < pl.bytes) return SPARK_ERR_WORKSPACE;
-    if (pl.most * Hkv > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;  // the grid
     int sms;
     st = device_ready(&sms);
+    const PackedPlan pl = plan_packed(N, S, H, Hkv, desc, paged, sms);
+    if (workspace_bytes < pl.bytes) return SPARK_ERR_WORKSPACE;
+    if (pl.most * Hkv > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;  // the grid
     if (st != SPARK_OK) return st;
     PagedParams P = make_params(qkv, gate, pos, desc, N, S, H, Hkv, out, workspace);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -480,11 +606,16 @@ spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_
     P.krot = reinterpret_cast<__nv_bfloat16 *>(ws + pl.krot);
     P.rot_w = pl.rot_w;
     P.tile_base = reinterpret_cast<int32_t *>(ws + pl.base);
-    P.tiles = reinterpret_cast<PackedItem *>(ws + pl.tiles);
     P.work = reinterpret_cast<PackedItem *>(ws + pl.work);
     P.most = static_cast<int>(pl.most);
+    P.sms = sms;
+    P.slots = pl.slots;
+    P.part_ml = reinterpret_cast<float *>(ws + pl.ml);
+    P.part_o = reinterpret_cast<float *>(ws + pl.o);
     P.call = reinterpret_cast<unsigned *>(ws + pl.flags);
     P.odd_values = P.call + 1;
+    P.n_splits = reinterpret_cast<int *>(P.call) + 3;
+    P.splits = reinterpret_cast<PackedItem *>(ws + pl.splits);
     if (paged) {
         P.start = start;
         set_pages(P, k_pages, v_pages, n_pages, page_size, table, max_pages);

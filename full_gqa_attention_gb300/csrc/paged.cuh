@@ -20,13 +20,16 @@ struct PagedParams {
     __nv_bfloat16 *krot;       // [Hkv, N, rot_w]: rotated leading key dims (packed prompts)
     int rot_w;
     int32_t *tile_base;        // [S + 1]: query tiles before each sequence
-    PackedItem *tiles;         // query tiles in the sequences' order
-    PackedItem *work;          // the same, longest first, and -1 behind them
-    int most;                  // places in the lists
+    PackedItem *work;          // query tiles, longest first, and -1 behind them
+    int most;                  // places in the list
+    int sms, slots;            // CTAs at a time, places for states of split tiles
+    PackedItem *splits;        // common.cuh: PackedInfo
+    int *n_splits;
     unsigned *odd_values;      // common.cuh: PackedInfo
     unsigned *call;
     float *part_ml;            // decode: [grid, 2, G, 2] running max (base-2 units), sum
     float *part_o;             // decode: [grid, 2, G, 256] unnormalised outputs
+                               // (prompts: states of split query tiles, PackedInfo)
     unsigned *counters;        // decode: a byte per CTA, left at 0 by every call
     int N, S, H, Hkv, G;
     int kind, window, gate_mode;

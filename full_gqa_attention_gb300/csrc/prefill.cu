@@ -547,6 +547,70 @@ struct PackedTiles {
     }
 };
 
+// Gives values of V that are not finite, which clean_v_rows took out, back to
+// a row that sees them: adds them to this thread's 128 dims of the row's
+// output (TMEM columns from taddr on).  Warp-collective, and rare.  `lo` and
+// `end` bound the keys of this CTA, of which only those hidden from some of the
+// tile's queries a0..a_last were touched.
+template <typename Src>
+__device__ __forceinline__ void give_back(uint32_t taddr, bool valid, int kind, int window, int at,
+                                          int a0, int a_last, int lo, int end, Src v_row) {
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(taddr + c, o);
+        tmem_ld_wait();
+        for (int key = lo; valid && key < end; ++key) {
+            if (key <= a0 && (kind == kLayerFull || a_last - key < window)) continue;
+            if (!key_visible(kind, window, at, key)) continue;
+            const __nv_bfloat16 *src = v_row(key);
+            if (!src) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(src + c + q * 8);
+                const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t m = nonfinite_mask(vw[i]);
+                    uint32_t &x = o[q * 8 + 2 * i], &y = o[q * 8 + 2 * i + 1];
+                    if (m & 0xFFFFu) x = __float_as_uint(__uint_as_float(x) + bf16_lo(vw[i]));
+                    if (m >> 16) y = __float_as_uint(__uint_as_float(y) + bf16_hi(vw[i]));
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st32(taddr + c, o);
+    }
+    tmem_st_wait();
+}
+
+// The same out of line, for the paged kernels: inlined there it makes the
+// softmax spill (the packed ones are 4 % faster with it inlined).
+template <typename Src>
+__device__ __noinline__ void give_back_call(uint32_t taddr, bool valid, int kind, int window,
+                                            int at, int a0, int a_last, int lo, int end,
+                                            Src v_row) {
+    give_back(taddr, valid, kind, window, at, a0, a_last, lo, end, v_row);
+}
+
+// Split query tiles: this thread's 128 dims of a row's unnormalised output
+// (TMEM columns from taddr on) to the part's state, rows side by side.
+__device__ __forceinline__ void leave_part(float4 *o, uint32_t taddr, bool store, bool ok) {
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(taddr + c, v);
+        tmem_ld_wait();
+        if (!store) continue;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            o[(c / 4 + q) * kBM] =
+                ok ? make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                 __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+
 // kG: the GQA group size when fixed at compile time (the Spark-X2.5 shapes
 // all use 4), 0 to read it from P.G.  Timing chose the fixed size for the
 // sliding-kind kernels only; the full-kind ones measured faster without it.
@@ -570,6 +634,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __shared__ float red_l[2][kBM];        // [warpgroup][row]: half-row sums
     constexpr bool kIsPacked = kSrc == kKvPacked || kSrc == kKvPages;
     __shared__ int cleaned_any;            // packed: a value was taken out of a partly hidden row
+    // packed: the item, read from here where it is needed (held in registers
+    // through the softmax it made the kernel spill)
+    __shared__ PackedItem s_item;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int kind = kKind == kKindAny ? P.kind : kKind;
@@ -583,14 +650,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int seq_end = P.T;                            // tokens of the sequence
     int row0 = 0;                                 // packed: the sequence's first row
     int seq = 0;
-    PackedItem item = {};
     if constexpr (kIsPacked) {
         // The tile comes from the list that the kernel before made: its latency
         // overlaps the set-up below.  The grid allows for a ragged tile in every
         // sequence: a CTA past the list has nothing to do.
         grid_dep_wait();
-        item = P.pk.work[static_cast<int>(blockIdx.x) / units];
+        const PackedItem item = P.pk.work[static_cast<int>(blockIdx.x) / units];
         if (item.seq < 0) return;
+        if (tid == 0) s_item = item;
     }
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
@@ -631,11 +698,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int start = 0;
     bool skip = false;
     if constexpr (kIsPacked) {
-        seq = item.seq;
-        t0 = item.t0;
-        row0 = item.row0;
-        seq_end = item.len;
-        start = item.start;
+        seq = s_item.seq;
+        t0 = s_item.t0;
+        row0 = s_item.row0;
+        seq_end = s_item.len;
+        start = s_item.start;
         t_end = (t0 + tq < seq_end) ? t0 + tq : seq_end;
     } else if constexpr (kSrc != kKvFromQkv) {
         start = P.start[b];
@@ -647,8 +714,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // that no tile wraps around the end of the ring
     const KeyTiles kt = prefill_key_tiles(kind, P.window, a0, start + t_end, kBN,
                                           kSrc == kKvFromRing || kSrc == kKvPages);
-    const int kv_lo = kt.kv_lo;
-    const int ntiles = skip ? 0 : kt.ntiles;
+    const int kv_lo = kt.kv_lo + (kIsPacked ? s_item.k0 * kBN : 0);
+    const int ntiles = skip ? 0 : (kIsPacked ? s_item.tiles : kt.ntiles);
     const PackedTiles<kSrc> packed_tiles{tm_kv_k, tm_kv_v, tm_krot, P, ring, bars, &abort_flag,
                                          kind, ntiles, kv_lo, a0, start + t_end - 1, row0, seq, g};
 
@@ -944,7 +1011,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         constexpr float kLazyRaw = 8.0f / kScaleLog2;
         const int a_last = start + t_end - 1;
         // (without a cache the kernel before has looked at every value)
-        const bool clean = kSrc == kKvPages || (kIsPacked && P.pk.odd_values[item.call & 1] != 0);
+        const bool clean = kSrc == kKvPages || (kIsPacked && P.pk.odd_values[s_item.call & 1] != 0);
         const int col0 = wg * 64;                       // first score column of this thread
         float m_run = -INFINITY, l_part = 0.f;
         for (int j = 0; ok && j < ntiles; ++j) {
@@ -1042,7 +1109,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_arrive(&bars[kBarPReady + (j & 1)]);
         }
 
-        if (kIsPacked && blockIdx.x == 0 && sth == 0) *P.pk.call = item.call + 1;
+        if (kIsPacked && blockIdx.x == 0 && sth == 0) *P.pk.call = s_item.call + 1;
         // epilogue: O / l * sigmoid(gate) -> bf16 -> staged in the Q buffer -> TMA store
         if (sth == 0) grid_dep_launch();
         if (ok) ok = mbar_wait(&bars[kBarOFinal], 0, &abort_flag, P.status);
@@ -1054,9 +1121,48 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // only the store below depends on the abort flag
             tc_fence_after();
             const float l_row = l_part + red_l[wg ^ 1][row];
+            bool whole = true;  // the same in every softmax thread
+            if constexpr (kIsPacked) {
+                if (cleaned_any && ok) {
+                    const int end = kv_lo + ntiles * kBN < a_last + 1 ? kv_lo + ntiles * kBN
+                                                                      : a_last + 1;
+                    auto v_row = [&](int key) -> const __nv_bfloat16 * {
+                        if constexpr (kSrc == kKvPages) {
+                            const int page = P.pk.table[static_cast<size_t>(seq) * P.pk.max_pages +
+                                                        (key >> P.pk.page_shift)];
+                            if (page < 0 || page >= P.pk.n_pages) return nullptr;
+                            return P.v_cache +
+                                   (((static_cast<size_t>(page) * P.Hkv + g) << P.pk.page_shift) +
+                                    (key & ((1 << P.pk.page_shift) - 1))) * kHeadDim + wg * 128;
+                        } else {
+                            return P.qkv + ((static_cast<size_t>(row0) + key) * (P.H + 2 * P.Hkv) +
+                                            P.H + P.Hkv + g) * kHeadDim + wg * 128;
+                        }
+                    };
+                    const uint32_t taddr = lane_base + kColO + wg * 128;
+                    if constexpr (kSrc == kKvPages)
+                        give_back_call(taddr, valid, kind, P.window, tok_abs, a0, a_last, kv_lo,
+                                       end, v_row);
+                    else
+                        give_back(taddr, valid, kind, P.window, tok_abs, a0, a_last, kv_lo, end,
+                                  v_row);
+                }
+                whole = s_item.parts == 1;
+                if (!whole) {
+                    // one of several parts of the query tile: its state goes to
+                    // the workspace, and the kernel behind this one joins them
+                    const size_t slot =
+                        s_item.slot + static_cast<size_t>(g) * s_item.parts + s_item.part;
+                    if (wg == 0)
+                        P.pk.part_ml[slot * kBM + row] =
+                            ok ? make_float2(m_run, l_row) : make_float2(-INFINITY, 0.f);
+                    leave_part(P.pk.part_o + (slot * 64 + wg * 32) * kBM + row,
+                               lane_base + kColO + wg * 128, valid, ok);
+                }
+            }
             const float scale = valid ? gate_act(gate_logit, P.gate_mode) / l_row : 0.f;
             // two 32-column loads in flight per wait (the loads' latency overlaps)
-            for (int c = wg * 128; c < wg * 128 + 128; c += 64) {
+            for (int c = wg * 128; whole && c < wg * 128 + 128; c += 64) {
                 uint32_t ov[2][32];
                 tmem_ld32(lane_base + kColO + c, ov[0]);
                 tmem_ld32(lane_base + kColO + c + 32, ov[1]);
@@ -1077,52 +1183,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         *reinterpret_cast<uint4 *>(qbuf + sw128_offset(row, (c + 32 * h) / 8 + q)) = w;
                     }
             }
-            if constexpr (kIsPacked) {
-                // a value that is not finite, taken out of a row that only some
-                // of the tile's queries see: those that do get it back
-                if (cleaned_any && valid) {
-                    const int w_lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
-                    for (int key = w_lo > 0 ? w_lo : 0; key <= tok_abs; ++key) {
-                        const bool all = key <= a0 && (kind == kLayerFull || a_last - key < P.window);
-                        if (all) {
-                            key = a0;  // no key before the causal edge is hidden from some
-                            continue;
-                        }
-                        if (!key_visible(kind, P.window, tok_abs, key)) continue;
-                        const __nv_bfloat16 *src;
-                        if constexpr (kSrc == kKvPages) {
-                            const int page = P.pk.table[static_cast<size_t>(seq) * P.pk.max_pages +
-                                                        (key >> P.pk.page_shift)];
-                            if (page < 0 || page >= P.pk.n_pages) continue;
-                            src = P.v_cache +
-                                  (((static_cast<size_t>(page) * P.Hkv + g) << P.pk.page_shift) +
-                                   (key & ((1 << P.pk.page_shift) - 1))) * kHeadDim;
-                        } else {
-                            src = P.qkv + ((static_cast<size_t>(row0) + key) * (P.H + 2 * P.Hkv) +
-                                           P.H + P.Hkv + g) * kHeadDim;
-                        }
-                        for (int q = wg * 16; q < wg * 16 + 16; ++q) {
-                            const uint4 vv = *reinterpret_cast<const uint4 *>(src + q * 8);
-                            const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
-                            uint32_t *o =
-                                reinterpret_cast<uint32_t *>(qbuf + sw128_offset(row, q));
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t m = nonfinite_mask(vw[i]);
-                                if (!m) continue;
-                                const uint32_t x = o[i];
-                                const float lo = (m & 0xFFFFu) ? bf16_lo(vw[i]) * scale : 0.f;
-                                const float hi = (m >> 16) ? bf16_hi(vw[i]) * scale : 0.f;
-                                o[i] = pack_bf16x2(bf16_lo(x) + lo, bf16_hi(x) + hi);
-                            }
-                        }
-                    }
-                }
-            }
             fence_proxy_async_smem();
             named_bar(1, kSoftmaxThreads);
             if (kIsPacked && t_end - t0 < tq) {
                 // a ragged tile: the rows behind it belong to others
-                const int nrows = skip || abort_flag ? 0 : (t_end - t0) * G;
+                const int nrows = skip || abort_flag || !whole ? 0 : (t_end - t0) * G;
                 for (int i = sth; i < nrows * 32; i += kSoftmaxThreads) {
                     const int r = i >> 5, q = i & 31;
                     *reinterpret_cast<uint4 *>(
@@ -1131,7 +1196,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             kHeadDim + q * 8) =
                         *reinterpret_cast<const uint4 *>(qbuf + sw128_offset(r, q));
                 }
-            } else if (sth == 0 && !abort_flag && !skip) {
+            } else if (sth == 0 && !abort_flag && !skip && whole) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     tma_store_4d(&tm_out, qbuf + c * kSlotBytes, c * 64, g * G, row0 + t0, b);
@@ -1144,6 +1209,65 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else {
         // warp 3 has no role
         __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- joining
+
+// Joins the states of split query tiles: out = sigma(gate) * sum_p w_p O_p /
+// sum_p w_p l_p with w_p = exp2((m_p - max m) / 16 log2 e).  A task is 32 rows
+// of one tile and KV head and half the dims; lane = row, so that the states
+// are read 512 bytes at a time, and each warp takes 16 dims.  Where no tile was
+// split there are no tasks.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(
+    const __grid_constant__ PrefillParams P) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = *P.pk.n_splits, tq = kBM / P.G;
+    const int per_tile = P.Hkv * (kBM / 32) * 2;
+    for (int task = blockIdx.x; task < n * per_tile; task += gridDim.x) {
+        const PackedItem t = P.pk.splits[task / per_tile];
+        const int u = task % per_tile;
+        const int g = u / (2 * (kBM / 32)), row = (u >> 1) % (kBM / 32) * 32 + lane;
+        const int tokens = t.len - t.t0 < tq ? t.len - t.t0 : tq;
+        if (row >= tokens * P.G) continue;
+        const size_t slot0 = t.slot + static_cast<size_t>(g) * t.parts;
+        const float2 *ml = P.pk.part_ml + slot0 * kBM + row;
+        float m = -INFINITY, l = 0.f;
+        for (int p = 0; p < t.parts; ++p) m = fmaxf(m, ml[p * kBM].x);
+        const int dim = (u & 1) * 128 + warp * 16;
+        const float4 *o = P.pk.part_o + (slot0 * 64 + dim / 4) * kBM + row;
+        float acc[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < t.parts; ++p) {
+            const float2 x = ml[p * kBM];
+            const float w = x.x == -INFINITY ? 0.f : fast_exp2((x.x - m) * kScaleLog2);
+            l += x.y * w;
+            const float4 *src = o + static_cast<size_t>(p) * (kBM * 64);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 y = src[q * kBM];
+                acc[4 * q] += y.x * w;
+                acc[4 * q + 1] += y.y * w;
+                acc[4 * q + 2] += y.z * w;
+                acc[4 * q + 3] += y.w * w;
+            }
+        }
+        const size_t token = static_cast<size_t>(t.row0) + t.t0 + row / P.G;
+        const size_t head = token * P.H + g * P.G + row % P.G;
+        const float scale = gate_act(P.gate[head], P.gate_mode) / l;
+        uint4 *dst = reinterpret_cast<uint4 *>(P.pk.out + head * kHeadDim + dim);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            dst[q] = make_uint4(pack_bf16x2(acc[8 * q] * scale, acc[8 * q + 1] * scale),
+                                pack_bf16x2(acc[8 * q + 2] * scale, acc[8 * q + 3] * scale),
+                                pack_bf16x2(acc[8 * q + 4] * scale, acc[8 * q + 5] * scale),
+                                pack_bf16x2(acc[8 * q + 6] * scale, acc[8 * q + 7] * scale));
     }
 }
 
@@ -1213,8 +1337,9 @@ cudaError_t launch_prefill(const CUtensorMap &tm_q, const CUtensorMap &tm_kv_k,
                              dim3(kRopeThreads), 0, stream, P);
 }
 
-// The attention kernel of a packed prefill: `items` query tiles at most, per
-// KV head.  The kernel before it on the stream made the list of tiles.
+// The attention kernel of a packed prefill: `items` query tiles (and parts of
+// them) at most, per KV head, from the list that the kernel before it made; and
+// where tiles may be split, the kernel that joins them.
 cudaError_t launch_prefill_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_kv_k,
                                   const CUtensorMap &tm_kv_v, const CUtensorMap &tm_krot,
                                   const CUtensorMap &tm_out, const PrefillParams &P,
@@ -1224,13 +1349,16 @@ cudaError_t launch_prefill_packed(const CUtensorMap &tm_q, const CUtensorMap &tm
     auto kernel = paged ? (sliding ? attn_kernel_for<kKvPages, kLayerSliding>(P.G)
                                    : attn_kernel_for<kKvPages, kLayerFull>(P.G))
                         : (sliding ? attn_kernel_for<kKvPacked, kLayerSliding>(P.G)
-                                   : attn_kernel_for<kKvPacked, kKindAny>(P.G));
+                                   : attn_kernel_for<kKvPacked, kLayerFull>(P.G));
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            kAttnSmemBytes);
     if (err != cudaSuccess) return err;
-    return launch_overlapped(kernel, dim3(static_cast<unsigned>(items * P.Hkv)),
-                             dim3(kAttnThreads), kAttnSmemBytes, stream, tm_q, tm_kv_k, tm_kv_v,
-                             tm_krot, tm_out, P);
+    err = launch_overlapped(kernel, dim3(static_cast<unsigned>(items * P.Hkv)),
+                            dim3(kAttnThreads), kAttnSmemBytes, stream, tm_q, tm_kv_k, tm_kv_v,
+                            tm_krot, tm_out, P);
+    if (err != cudaSuccess || P.pk.part_o == nullptr) return err;
+    return launch_overlapped(join_parts_kernel, dim3(static_cast<unsigned>(P.wave)),
+                             dim3(kJoinThreads), 0, stream, P);
 }
 
 }  // namespace spark

@@ -342,6 +342,48 @@ def test_paged_bad_rows_are_skipped_and_flagged(cuda):
         check_close(out[50:], want[50:], "behind")
 
 
+@pytest.mark.parametrize("G,Hkv", [(1, 1), (4, 1), (8, 2), (2, 3)])
+@pytest.mark.parametrize("kind", ["full", "sliding"])
+def test_few_queries_on_many_keys_are_split(cuda, kind, G, Hkv):
+    """Short chunks on top of long prefixes: a query tile's keys are shared by several CTAs."""
+    layer = layer_of(kind, window=2500)
+    for new, old in (([1], [4000]), ([3, 0, 40], [3500, 0, 100]), ([33, 1], [2047, 2999])):
+        s = Step(new, old, H=G * Hkv, Hkv=Hkv, page=64, seed=G + old[0])
+        ws = fga.new_workspace(
+            fga.spark_attn_prefill_paged_workspace_size(sum(new), len(new), G * Hkv, Hkv, layer))
+        for _ in range(2):   # the counters come back to 0
+            out, k, v = run_paged(s, layer, workspace=ws)
+            s.check_out(out, layer, f"split {kind} G={G} {new} on {old}")
+        s.check_pages(k, v, layer)
+        assert fga.spark_attn_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_split_hidden_values(cuda, value):
+    """Values that are not finite in cached tokens, over split query tiles."""
+    layer = layer_of("sliding", window=2000)
+    s = Step([40], [3000], H=4, Hkv=1, page=32, seed=5)
+    clean, _, _ = run_paged(s, layer)
+    at = 1020                            # hidden from the queries behind 1020 + 1999 = 3019
+    s.v[s.rows[0][at // 32], :, at % 32, 5:8] = value
+    got, _, _ = run_paged(s, layer)
+    for i in range(40):
+        x, y = got[i].view(4, D), clean[i].view(4, D)
+        if i <= 19:
+            assert not torch.isfinite(x[:, 5:8]).any(), i
+            assert torch.equal(x[:, 8:], y[:, 8:]), i
+        else:
+            assert torch.equal(x, y), i
+
+
+def test_packed_few_long_prompts_are_split(cuda):
+    layer = layer_of("full")
+    s = Step([1500, 3], H=2, Hkv=1, seed=21, pad=2)
+    s.check_out(run_packed(s, layer), layer, "packed, split")
+    again = run_packed(s, layer)
+    assert torch.equal(again, run_packed(s, layer))
+
+
 @pytest.mark.parametrize("kind", ["full", "sliding"])
 def test_paged_in_chunks_then_decode(cuda, kind):
     """A prompt in chunks of odd sizes equals the prompt at once; decode goes on from there."""
