@@ -39,6 +39,7 @@ constexpr int kThreads = (kWarps + 1) * 32;               // + one producer warp
 constexpr int kTileBytes = kTile * kHeadDim * 2;          // 32 KB (K or V)
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kQBytes = 8 * kHeadDim * 2;                 // 8 (padded) query heads
+constexpr int kJoin = 6;                                  // partial states joined at once
 constexpr int kRedHeads = 4;                              // heads reduced over the warps at once
 constexpr int kRedBytes = kWarps * kRedHeads * kHeadDim * 4;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kQBytes + 2 * kHeadDim * 2 + kRedBytes +
@@ -383,10 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[db][2] *= r0;
                 o[db][3] *= r1;
             }
-            // P^T as the B operand of O^T += V^T P^T (probabilities rounded to
-            // bf16, the type of V; the sums l stay in 32 bits)
-            const uint32_t pb0 = movmatrix_trans(pack_bf16x2(p0, p1));
-            const uint32_t pb1 = movmatrix_trans(pack_bf16x2(p2, p3));
+            // P^T as the B operand of O^T += V^T P^T, in two bf16 terms: the
+            // product's operands have V's type, one term would round the
+            // probabilities by 2^-9, and the second costs no time while HBM
+            // bounds the step.  The sums l stay in 32 bits.
+            const uint32_t ph0 = pack_bf16x2(p0, p1), ph1 = pack_bf16x2(p2, p3);
+            const uint32_t pb0 = movmatrix_trans(ph0), pb1 = movmatrix_trans(ph1);
+            const uint32_t pl0 =
+                movmatrix_trans(pack_bf16x2(p0 - bf16_lo(ph0), p1 - bf16_hi(ph0)));
+            const uint32_t pl1 =
+                movmatrix_trans(pack_bf16x2(p2 - bf16_lo(ph1), p3 - bf16_hi(ph1)));
             ok = mbar_wait(&fullv[s], (it / kStages) & 1, &abort_flag, P.status);
             if (!ok) break;
             // Slots that hold no visible token may hold anything, and 0 * NaN is
@@ -411,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t a0, a1, a2, a3;
                 ldmatrix_x4_trans(addr, a0, a1, a2, a3);
                 mma_bf16_16816(o[db], a0, a1, a2, a3, pb0, pb1);
+                mma_bf16_16816(o[db], a0, a1, a2, a3, pl0, pl1);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
@@ -525,27 +533,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int pl = static_cast<long long>(cta) * share < wk.first ? 1 : 0;
                         return (static_cast<size_t>(cta) * 2 + pl) * P.G + hq;
                     };
-                    float m = -INFINITY;
-                    for (int cta = c0 + lane; cta <= c1; cta += 32)
-                        m = fmaxf(m, __ldcg(P.part_ml + 2 * at(cta)));
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1)
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                    h.m = m;
+                    // kJoin states at a time, all their loads in flight
+                    h.m = -INFINITY;
                     h.l = 0.f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) h.o[j] = 0.f;
-#pragma unroll 4
-                    for (int cta = c0; cta <= c1; ++cta) {
-                        const size_t a = at(cta);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + a);
-                        const float4 *src =
-                            reinterpret_cast<const float4 *>(P.part_o + a * kHeadDim + lane * 8);
-                        const float4 x = __ldcg(src), y = __ldcg(src + 1);
-                        const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-                        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                        h.l += ml.y * w;
-                        add_scaled(h, w, v);
+                    for (int cta = c0; cta <= c1; cta += kJoin) {
+                        float2 ml[kJoin];
+                        float4 x[kJoin], y[kJoin];
+#pragma unroll
+                        for (int k = 0; k < kJoin; ++k) {
+                            ml[k] = make_float2(-INFINITY, 0.f);
+                            x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (cta + k > c1) continue;
+                            const size_t a = at(cta + k);
+                            ml[k] = __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + a);
+                            const float4 *src = reinterpret_cast<const float4 *>(
+                                P.part_o + a * kHeadDim + lane * 8);
+                            x[k] = __ldcg(src);
+                            y[k] = __ldcg(src + 1);
+                        }
+                        float m = h.m;
+#pragma unroll
+                        for (int k = 0; k < kJoin; ++k) m = fmaxf(m, ml[k].x);
+                        const float z = m == -INFINITY ? 0.f : m;
+                        const float wo = fast_exp2(h.m - z);
+                        h.m = m;
+                        h.l *= wo;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) h.o[j] *= wo;
+#pragma unroll
+                        for (int k = 0; k < kJoin; ++k) {
+                            const float w = fast_exp2(ml[k].x - z);
+                            const float v[8] = {x[k].x, x[k].y, x[k].z, x[k].w,
+                                                y[k].x, y[k].y, y[k].z, y[k].w};
+                            h.l += ml[k].y * w;
+                            add_scaled(h, w, v);
+                        }
                     }
                 }
             }
