@@ -255,10 +255,11 @@ constexpr int kPrepHeads = 4;                 // KV heads whose loads are in fli
 // token's rotated key and its value go to its pages.  Packed: the leading
 // rot_w dims of every key, rotated, go to the workspace (the others are read
 // where they are), and the values are looked over for one that is not finite
-// (with none, no boundary tile needs a pass over V).  One thread per (token,
-// group of 8 rotated pairs / 8 copied key dims / 8 value dims), over the KV
-// heads, so that each angle is computed once.  The first CTA makes the list of
-// query tiles instead.
+// (with none, no boundary tile needs a pass over V).  A CTA takes kPrepRows
+// tokens; one thread per (token, 4 rotated pairs) or (token, 8 copied key dims
+// or value dims), over the KV heads, so that each angle is computed once; the
+// rotations come first, so that few warps do both.  The first CTA makes the
+// list of query tiles instead.
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     const __grid_constant__ PagedParams P) {
     __shared__ long long place[kPrepRows];
@@ -270,8 +271,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     }
     const bool paged = P.k_pages != nullptr;
     const int r = P.rope.rot_dim, half = r / 2;
-    const int n_rot = half / 8, n_kcopy = ((paged ? kHeadDim : P.rot_w) - r) / 8;
-    const int items = n_rot + n_kcopy + kHeadDim / 8;
+    const int n_rot = half / 4, n_kcopy = ((paged ? kHeadDim : P.rot_w) - r) / 8;
+    const int n_copy = n_kcopy + kHeadDim / 8;
     const long long first = (blockIdx.x - 1ll) * kPrepRows;
     if (paged) {
         const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -283,76 +284,81 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
     const size_t head_stride = paged ? static_cast<size_t>(kHeadDim) << P.page_shift
                                      : static_cast<size_t>(P.N) * P.rot_w;
-    uint32_t hit = 0;
-    for (int i = threadIdx.x; i < kPrepRows * items; i += kPrepThreads) {
-        const int w = i / items, it = i % items;
-        if (first + w >= P.N) break;
+    auto dst_of = [&](int w, int row) {
+        return paged ? static_cast<size_t>(place[w]) : static_cast<size_t>(row) * P.rot_w;
+    };
+    auto there = [&](int w) { return first + w < P.N && (!paged || place[w] >= 0); };
+    for (int i = threadIdx.x; i < kPrepRows * n_rot; i += kPrepThreads) {
+        const int w = i / n_rot, k0 = i % n_rot * 4;
+        if (!there(w)) continue;
         const int row = static_cast<int>(first + w);
-        if (paged && place[w] < 0) continue;
-        const size_t base = paged ? static_cast<size_t>(place[w])
-                                  : static_cast<size_t>(row) * P.rot_w;
-        __nv_bfloat16 *dst_k = (paged ? P.k_pages : P.krot) + base;
-        __nv_bfloat16 *dst_v = P.v_pages + (paged ? base : 0);
-        const __nv_bfloat16 *src_k = P.qkv + row * width + static_cast<size_t>(P.H) * kHeadDim;
-        const __nv_bfloat16 *src_v = src_k + static_cast<size_t>(P.Hkv) * kHeadDim;
-        if (it < n_rot) {
-            const int k0 = it * 8;
-            const int p = P.pos[row];
-            float c[8], s[8];
+        const __nv_bfloat16 *src = P.qkv + row * width + static_cast<size_t>(P.H) * kHeadDim + k0;
+        __nv_bfloat16 *dst = (paged ? P.k_pages : P.krot) + dst_of(w, row) + k0;
+        const int p = P.pos[row];
+        uint2 x[kPrepHeads], y[kPrepHeads];
+        auto load = [&](int g0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) rope_cos_sin(p, P.rope.u[k0 + j], c[j], s[j]);
-            for (int g0 = 0; g0 < P.Hkv; g0 += kPrepHeads) {
-                uint4 x[kPrepHeads], y[kPrepHeads];
-#pragma unroll
-                for (int g = 0; g < kPrepHeads; ++g) {
-                    if (g0 + g >= P.Hkv) break;
-                    const __nv_bfloat16 *src = src_k + (g0 + g) * kHeadDim + k0;
-                    x[g] = *reinterpret_cast<const uint4 *>(src);
-                    y[g] = *reinterpret_cast<const uint4 *>(src + half);
-                }
-#pragma unroll
-                for (int g = 0; g < kPrepHeads; ++g) {
-                    if (g0 + g >= P.Hkv) break;
-                    const uint32_t xw[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
-                    const uint32_t yw[4] = {y[g].x, y[g].y, y[g].z, y[g].w};
-                    uint32_t ya[4], yb[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float y1l, y2l, y1h, y2h;
-                        rope_rotate(bf16_lo(xw[j]), bf16_lo(yw[j]), c[2 * j], s[2 * j], y1l, y2l);
-                        rope_rotate(bf16_hi(xw[j]), bf16_hi(yw[j]), c[2 * j + 1], s[2 * j + 1],
-                                    y1h, y2h);
-                        ya[j] = pack_bf16x2(y1l, y1h);
-                        yb[j] = pack_bf16x2(y2l, y2h);
-                    }
-                    __nv_bfloat16 *dst = dst_k + (g0 + g) * head_stride + k0;
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
-                    *reinterpret_cast<uint4 *>(dst + half) = make_uint4(yb[0], yb[1], yb[2], yb[3]);
-                }
+            for (int g = 0; g < kPrepHeads; ++g) {
+                if (g0 + g >= P.Hkv) break;
+                x[g] = *reinterpret_cast<const uint2 *>(src + (g0 + g) * kHeadDim);
+                y[g] = *reinterpret_cast<const uint2 *>(src + (g0 + g) * kHeadDim + half);
             }
-        } else {
-            const bool key = it < n_rot + n_kcopy;
-            const int d0 = key ? r + (it - n_rot) * 8 : (it - n_rot - n_kcopy) * 8;
-            const __nv_bfloat16 *src = (key ? src_k : src_v) + d0;
-            __nv_bfloat16 *dst = (key ? dst_k : dst_v) + d0;
-            for (int g0 = 0; g0 < P.Hkv; g0 += kPrepHeads) {
-                uint4 v[kPrepHeads];
+        };
+        load(0);
+        float c[4], s[4];
 #pragma unroll
-                for (int g = 0; g < kPrepHeads; ++g)
-                    v[g] = g0 + g < P.Hkv ? *reinterpret_cast<const uint4 *>(
-                                                src + (g0 + g) * kHeadDim)
-                                          : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) rope_cos_sin(p, P.rope.u[k0 + j], c[j], s[j]);
+        for (int g0 = 0; g0 < P.Hkv; g0 += kPrepHeads) {
+            if (g0) load(g0);
 #pragma unroll
-                for (int g = 0; g < kPrepHeads; ++g) {
-                    if (g0 + g >= P.Hkv) break;
-                    if (key || paged)
-                        *reinterpret_cast<uint4 *>(dst + (g0 + g) * head_stride) = v[g];
-                    else  // an exponent of all ones carries into the sign's place
-                        hit |= ((v[g].x & 0x7F807F80u) + 0x00800080u) |
-                               ((v[g].y & 0x7F807F80u) + 0x00800080u) |
-                               ((v[g].z & 0x7F807F80u) + 0x00800080u) |
-                               ((v[g].w & 0x7F807F80u) + 0x00800080u);
+            for (int g = 0; g < kPrepHeads; ++g) {
+                if (g0 + g >= P.Hkv) break;
+                const uint32_t xw[2] = {x[g].x, x[g].y}, yw[2] = {y[g].x, y[g].y};
+                uint32_t ya[2], yb[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float y1l, y2l, y1h, y2h;
+                    rope_rotate(bf16_lo(xw[j]), bf16_lo(yw[j]), c[2 * j], s[2 * j], y1l, y2l);
+                    rope_rotate(bf16_hi(xw[j]), bf16_hi(yw[j]), c[2 * j + 1], s[2 * j + 1], y1h,
+                                y2h);
+                    ya[j] = pack_bf16x2(y1l, y1h);
+                    yb[j] = pack_bf16x2(y2l, y2h);
                 }
+                __nv_bfloat16 *to = dst + (g0 + g) * head_stride;
+                *reinterpret_cast<uint2 *>(to) = make_uint2(ya[0], ya[1]);
+                *reinterpret_cast<uint2 *>(to + half) = make_uint2(yb[0], yb[1]);
+            }
+        }
+    }
+    uint32_t hit = 0;
+    // (from the last thread down: the first ones have rotations behind them)
+    for (int i = kPrepThreads - 1 - threadIdx.x; i < kPrepRows * n_copy; i += kPrepThreads) {
+        const int w = i / n_copy, it = i % n_copy;
+        if (!there(w)) continue;
+        const int row = static_cast<int>(first + w);
+        const bool key = it < n_kcopy;
+        const int d0 = key ? r + it * 8 : (it - n_kcopy) * 8;
+        const __nv_bfloat16 *src =
+            P.qkv + row * width + static_cast<size_t>(P.H + (key ? 0 : P.Hkv)) * kHeadDim + d0;
+        __nv_bfloat16 *dst = (key ? (paged ? P.k_pages : P.krot) : P.v_pages) + d0;
+        if (key || paged) dst += dst_of(w, row);
+        for (int g0 = 0; g0 < P.Hkv; g0 += kPrepHeads) {
+            uint4 v[kPrepHeads];
+#pragma unroll
+            for (int g = 0; g < kPrepHeads; ++g)
+                v[g] = g0 + g < P.Hkv
+                           ? *reinterpret_cast<const uint4 *>(src + (g0 + g) * kHeadDim)
+                           : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int g = 0; g < kPrepHeads; ++g) {
+                if (g0 + g >= P.Hkv) break;
+                if (key || paged)
+                    *reinterpret_cast<uint4 *>(dst + (g0 + g) * head_stride) = v[g];
+                else  // an exponent of all ones carries into the sign's place
+                    hit |= ((v[g].x & 0x7F807F80u) + 0x00800080u) |
+                           ((v[g].y & 0x7F807F80u) + 0x00800080u) |
+                           ((v[g].z & 0x7F807F80u) + 0x00800080u) |
+                           ((v[g].w & 0x7F807F80u) + 0x00800080u);
             }
         }
     }
