@@ -279,6 +279,14 @@ class PagePool:
                                   held.data_ptr(), len.data_ptr(), refs.data_ptr(), n_layers, Hkv,
                                   n_pages, page_size, table.shape[0], table.shape[1])
 
+    def __setattr__(self, name, value):
+        # `pool.len += add` keeps the storage; another tensor would leave the
+        # library with the old one
+        old = getattr(self, name, None)
+        if isinstance(old, torch.Tensor) and value is not old:
+            raise AttributeError(f"{name} keeps its storage: write into it")
+        super().__setattr__(name, value)
+
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, Hkv: int, page_size: int, n_rows: int,
               max_pages: int, device=None) -> "PagePool":

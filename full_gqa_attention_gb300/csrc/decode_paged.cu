@@ -116,6 +116,27 @@ __device__ __forceinline__ void add_scaled(HeadState &s, float w, const float *o
 
 }  // namespace
 
+// The sum of the values of the slots [lo, pos) that are not finite, for a lane's
+// 8 dims (from d0) of a pair: with a visible value of +-inf the two terms of its
+// probability can make NaN where the sum is infinite.  Rare.
+__device__ __noinline__ void sum_nonfinite(const PagedParams &P, int b, int g, int lo, int pos,
+                                           int d0, float (&s)[8]) {
+    for (int j = lo; j < pos; ++j) {
+        const int id = P.table[static_cast<size_t>(b) * P.max_pages + (j >> P.page_shift)];
+        if (id < 0 || id >= P.n_pages) continue;
+        const uint4 w = *reinterpret_cast<const uint4 *>(
+            P.v_pages + (((static_cast<size_t>(id) * P.Hkv + g) << P.page_shift) +
+                         (j & ((1 << P.page_shift) - 1))) * kHeadDim + d0);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = bf16_lo(u[i]), c = bf16_hi(u[i]);
+            if (!isfinite(a)) s[2 * i] += a;
+            if (!isfinite(c)) s[2 * i + 1] += c;
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
@@ -604,8 +625,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float wo = h.m == -INFINITY ? 0.f : fast_exp2(h.m - z), wn = fast_exp2(x - z);
                 const float scale = gate_act(gate_now[i], P.gate_mode) / (h.l * wo + wn);
                 float y[8];
+                bool odd = false;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = (h.o[j] * wo + v[j] * wn) * scale;
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = (h.o[j] * wo + v[j] * wn) * scale;
+                    odd = odd || isnan(y[j]);
+                }
+                if (odd && isfinite(scale)) {
+                    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    sum_nonfinite(P, wk.b, wk.g, row.lo, row.pos, lane * 8, s);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (!isfinite(v[j])) s[j] += v[j];
+                        if (isnan(y[j])) y[j] = s[j] * scale;
+                    }
+                }
                 *reinterpret_cast<uint4 *>(
                     P.out + (static_cast<size_t>(wk.b) * P.H + head) * kHeadDim + lane * 8) =
                     make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),

@@ -411,7 +411,12 @@ PagedParams make_params(const void *qkv, const float *gate, const int32_t *pos,
     P.Hkv = Hkv;
     P.G = H / Hkv;
     P.kind = desc->kind;
-    P.window = desc->kind == SPARK_LAYER_SLIDING ? desc->window : 0;
+    // (indices stay below 2^30: a wider window is no narrower, and sums with it
+    // stay in 32 bits)
+    constexpr int kMostWindow = 1 << 30;
+    P.window = desc->kind != SPARK_LAYER_SLIDING  ? 0
+               : desc->window < kMostWindow ? desc->window
+                                            : kMostWindow;
     P.gate_mode = desc->gate_mode;
     fill_rope_table(desc, &P.rope);
     return P;

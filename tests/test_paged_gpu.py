@@ -521,6 +521,29 @@ def test_decode_old_pages_gone_and_hidden_values(cuda):
     check_close(out, want, "decode, old pages gone")
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_decode_visible_values_that_are_not_finite(cuda, value):
+    s = decode_step([500, 80], H=4, Hkv=1, page=16, seed=4)
+    clean, _, _ = run_decode(s, FULL)
+    s.v[s.rows[0][30], :, 5, 3:9] = value
+    got, _, _ = run_decode(s, FULL)
+    assert torch.equal(got[1], clean[1])
+    x, y = got[0].view(4, D), clean[0].view(4, D)
+    assert torch.equal(x[:, 9:], y[:, 9:]) and torch.equal(x[:, :3], y[:, :3])
+    assert torch.isnan(x[:, 3:9]).all() if value != value else (x[:, 3:9] == value).all()
+
+
+def test_a_window_wider_than_any_position(cuda):
+    layer = layer_of("sliding", window=2 ** 31 - 1)
+    s = Step([40, 3], [500, 250], H=4, Hkv=1, page=16, seed=4)
+    out, _, _ = run_paged(s, layer)
+    s.check_out(out, layer, "paged, all of it in the window")
+    p = Step([300, 5], H=4, Hkv=1, seed=4)
+    p.check_out(run_packed(p, layer), layer, "packed, all of it in the window")
+    d = decode_step([400, 7], page=32, seed=2)
+    check_decode(d, layer, run_decode(d, layer)[0], "decode, all of it in the window")
+
+
 def test_decode_bad_rows_are_flagged(cuda):
     s = decode_step([100, 37, 200], page=16, seed=6)
     ws = fga.new_workspace(fga.spark_attn_decode_paged_workspace_size(3, 4, 1, FULL))

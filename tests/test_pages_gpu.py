@@ -243,6 +243,21 @@ def test_a_pool_that_was_not_set_up_leads_nowhere(cuda):
     assert torch.equal(p.gpu.k_pages.view(torch.int16), p.k)
 
 
+def test_a_pool_keeps_its_tensors(cuda):
+    p = Pair()
+    p.gpu.len += 0
+    with pytest.raises(AttributeError):
+        p.gpu.len = p.gpu.len + 1
+    with pytest.raises(ValueError):
+        fga.spark_attn_pages_reserve(p.gpu, p.i32([1, 2]), workspace=p.ws)
+    with pytest.raises(TypeError):
+        fga.spark_attn_pages_free(p.gpu, torch.tensor([0], device=cuda), workspace=p.ws)
+    with pytest.raises(ValueError):
+        fga.spark_attn_pages_fork(p.gpu, p.i32([1, 2]), p.i32([1]), workspace=p.ws)
+    with pytest.raises(fga.SparkError):
+        fga.spark_attn_pages_compact(p.gpu, workspace=p.ws[:256])
+
+
 def test_empty_calls(cuda):
     p = Pair()
     none = torch.empty(0, dtype=torch.int32, device=cuda)
