@@ -257,7 +257,7 @@ class PagePool:
     The tensors are the caller's and keep their storage; add to `len` in place
     after a step."""
 
-    __slots__ = ("k_pages", "v_pages", "table", "held", "len", "refs", "_dev", "_c", "_rows")
+    __slots__ = ("k_pages", "v_pages", "table", "held", "len", "refs", "_dev", "_c", "_ref", "_rows")
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
                  held: torch.Tensor, len: torch.Tensor, refs: torch.Tensor):
@@ -278,6 +278,7 @@ class PagePool:
         self._c = spark_page_pool(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(),
                                   held.data_ptr(), len.data_ptr(), refs.data_ptr(), n_layers, Hkv,
                                   n_pages, page_size, table.shape[0], table.shape[1])
+        self._ref = ctypes.byref(self._c)
 
     def __setattr__(self, name, value):
         # `pool.len += add` keeps the storage; another tensor would leave the
@@ -320,14 +321,14 @@ def _one(pool: PagePool, t, name: str):
 
 
 def spark_attn_pages_workspace_size(pool: PagePool) -> int:
-    return lib.spark_attn_pages_workspace_size(ctypes.byref(pool._c))
+    return lib.spark_attn_pages_workspace_size(pool._ref)
 
 
 def _pages_call(name: str, call, pool: PagePool, args, workspace, stream):
     dev = pool._dev
     with _where(dev, stream):
         ws, owned = _workspace(dev, workspace, lambda: spark_attn_pages_workspace_size(pool))
-        st = call(ctypes.byref(pool._c), *args, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        st = call(pool._ref, *args, ws.data_ptr(), ws.numel(), _raw_stream(dev))
         _done(name, st, ws, owned)
 
 
