@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         consumer_bar();
         for (int k = tid; k < half; k += kWarps * 32) {
             float c, s;
-            rope_cos_sin(row.pos, P.rope.u[k], c, s);
+            rope_cos_sin_fine(row.pos, P.rope.u[k], c, s);
             for (int hh = 0; hh <= P.G; ++hh) {
                 __nv_bfloat16 *x = hh < P.G ? qs + hh * kHeadDim : kn;
                 float y1, y2;

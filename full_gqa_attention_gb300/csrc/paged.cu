@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
         load(0);
         float c[4], s[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) rope_cos_sin(p, P.rope.u[k0 + j], c[j], s[j]);
+        for (int j = 0; j < 4; ++j) rope_cos_sin_fine(p, P.rope.u[k0 + j], c[j], s[j]);
         for (int g0 = 0; g0 < P.Hkv; g0 += kPrepHeads) {
             if (g0) load(g0);
 #pragma unroll

@@ -37,6 +37,26 @@ struct PagedParams {
     RopeTable rope;
 };
 
+// rope_cos_sin with the last rounding of the angle given back: the sum f + g of
+// the reduced angle's two parts (rope_math.cuh: rope_turns) is off by up to
+// 2^-25 turns, 2e-7 rad, which TwoSum recovers exactly and a first-order step
+// applies.  For keys that go to pages: the angle error then no longer flips the
+// last bit of a stored bf16 more often than 32-bit products do.
+__device__ __forceinline__ void rope_cos_sin_fine(int pos, float2 u, float &c, float &s) {
+    const float fp = static_cast<float>(pos);
+    const float p = __fmul_rn(fp, u.x);
+    const float f = __fadd_rn(p, -rintf(p));
+    const float g = __fmaf_rn(fp, u.y, __fmaf_rn(fp, u.x, -p));
+    const float t = __fadd_rn(f, g);
+    const float b = __fadd_rn(t, -f);
+    const float err = __fadd_rn(__fadd_rn(f, -__fadd_rn(t, -b)), __fadd_rn(g, -b));
+    float c0, s0;
+    sincospif(__fmul_rn(2.0f, t), &s0, &c0);
+    const float d = err * 6.283185307f;
+    c = __fmaf_rn(-d, s0, c0);
+    s = __fmaf_rn(d, c0, s0);
+}
+
 // The sequence whose tokens [cu[s], cu[s+1]) hold `row`, or -1 (padding, or
 // offsets that are no prefix sum), by one warp: 32 probes a step.
 __device__ __forceinline__ int find_sequence(const int32_t *cu, int S, int row, int lane) {
