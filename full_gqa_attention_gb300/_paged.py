@@ -88,23 +88,11 @@ def _elsewhere(dev: int, stream):
                 yield
 
 
-_HERE = contextlib.nullcontext()
-
-
 def _where(dev: int, stream):
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
-        return _elsewhere(dev, stream)
-    return _HERE if _current_device() == dev else _elsewhere(dev, None)
-
-
-def _workspace(dev: int, workspace, nbytes):
-    """The caller's workspace, or one of nbytes() bytes; whether it is ours."""
-    if workspace is None:
-        return new_workspace(nbytes(), torch.device("cuda", dev)), True
-    _check(dev, (workspace, _U8, "workspace"))
-    return workspace, False
+    """Where a call runs that gives a stream or is for another device."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+    return _elsewhere(dev, stream)
 
 
 def _done(name: str, status: int, workspace, owned: bool):
@@ -137,14 +125,20 @@ def _pages(k_pages, v_pages, page_table, rows: int, Hkv: int):
     return shape[0], shape[2], table[1]
 
 
-def _out(dev: int, out, n: int, H: int):
+def _buffers(dev: int, out, n: int, H: int, workspace, size, *args):
+    """The output and the workspace of a call, the caller's or (workspace:
+    size(*args) bytes) new ones, and whether the workspace is ours."""
     if out is None:
         # rows that no sequence covers stay as they are: they begin as zeros
-        return torch.zeros((n, H * HEAD_DIM), dtype=_BF16, device=torch.device("cuda", dev))
-    _check(dev, (out, _BF16, "out"))
-    if out.shape != (n, H * HEAD_DIM):
-        raise ValueError("out must be [tokens, H * 256]")
-    return out
+        out = torch.zeros((n, H * HEAD_DIM), dtype=_BF16, device=torch.device("cuda", dev))
+    else:
+        _check(dev, (out, _BF16, "out"))
+        if out.shape != (n, H * HEAD_DIM):
+            raise ValueError("out must be [tokens, H * 256]")
+    if workspace is None:
+        return out, new_workspace(size(*args), torch.device("cuda", dev)), True
+    _check(dev, (workspace, _U8, "workspace"))
+    return out, workspace, False
 
 
 def spark_attn_prefill_packed_workspace_size(n_tokens: int, S: int, H: int, Hkv: int,
@@ -171,6 +165,9 @@ def spark_attn_prefill_packed(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.
     -> out bf16 [n,H*256].  Rows of out that no sequence covers stay as they
     were (zeros in one that the call allocates)."""
     dev = _device_of(qkv, "qkv")
+    if stream is not None or _current_device() != dev:
+        with _where(dev, stream):
+            return spark_attn_prefill_packed(qkv, gate, pos, cu_seqlens, layer, out, workspace)
     _check(dev, (qkv, _BF16, "qkv"), (gate, _F32, "gate"), (pos, _I32, "pos"),
            (cu_seqlens, _I32, "cu_seqlens"))
     n, H, Hkv = _heads(qkv, gate)
@@ -178,13 +175,12 @@ def spark_attn_prefill_packed(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.
     if pos.shape != (n,) or cu_seqlens.dim() != 1 or S < 0:
         raise ValueError("pos must be [tokens], cu_seqlens [S + 1]")
     d = ctypes.byref(as_desc(layer))
-    with _where(dev, stream):
-        out = _out(dev, out, n, H)
-        ws, owned = _workspace(
-            dev, workspace, lambda: lib.spark_attn_prefill_packed_workspace_size(n, S, H, Hkv, d))
-        st = lib.spark_attn_prefill_packed(
-            qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(), d, n, S, H,
-            Hkv, out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    out, ws, owned = _buffers(dev, out, n, H, workspace,
+                              lib.spark_attn_prefill_packed_workspace_size, n, S, H, Hkv, d)
+    st = lib.spark_attn_prefill_packed(
+        qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(), d, n, S, H, Hkv,
+        out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if st or owned:
         _done("spark_attn_prefill_packed", st, ws, owned)
     return out
 
@@ -199,6 +195,10 @@ def spark_attn_prefill_paged(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.T
     place; page_table int32 [S,max_pages]); the rest as for
     spark_attn_prefill_packed."""
     dev = _device_of(qkv, "qkv")
+    if stream is not None or _current_device() != dev:
+        with _where(dev, stream):
+            return spark_attn_prefill_paged(qkv, gate, pos, cu_seqlens, start, k_pages, v_pages,
+                                            page_table, layer, out, workspace)
     _check(dev, (qkv, _BF16, "qkv"), (gate, _F32, "gate"), (pos, _I32, "pos"),
            (cu_seqlens, _I32, "cu_seqlens"), (start, _I32, "start"), (k_pages, _BF16, "k_pages"),
            (v_pages, _BF16, "v_pages"), (page_table, _I32, "page_table"))
@@ -208,15 +208,13 @@ def spark_attn_prefill_paged(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.T
         raise ValueError("pos must be [tokens], cu_seqlens [S + 1], start [S]")
     n_pages, page_size, max_pages = _pages(k_pages, v_pages, page_table, S, Hkv)
     d = ctypes.byref(as_desc(layer))
-    with _where(dev, stream):
-        out = _out(dev, out, n, H)
-        ws, owned = _workspace(
-            dev, workspace, lambda: lib.spark_attn_prefill_paged_workspace_size(n, S, H, Hkv, d))
-        st = lib.spark_attn_prefill_paged(
-            qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(),
-            start.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page_size,
-            page_table.data_ptr(), max_pages, d, n, S, H, Hkv, out.data_ptr(), ws.data_ptr(),
-            ws.numel(), _raw_stream(dev))
+    out, ws, owned = _buffers(dev, out, n, H, workspace,
+                              lib.spark_attn_prefill_paged_workspace_size, n, S, H, Hkv, d)
+    st = lib.spark_attn_prefill_paged(
+        qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(), start.data_ptr(),
+        k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page_size, page_table.data_ptr(),
+        max_pages, d, n, S, H, Hkv, out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if st or owned:
         _done("spark_attn_prefill_paged", st, ws, owned)
     return out
 
@@ -230,6 +228,10 @@ def spark_attn_decode_paged(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.Te
     [n_pages,Hkv,page_size,256] (updated in place), page_table int32
     [B,max_pages] -> out bf16 [B,H*256]."""
     dev = _device_of(qkv, "qkv")
+    if stream is not None or _current_device() != dev:
+        with _where(dev, stream):
+            return spark_attn_decode_paged(qkv, gate, pos, k_pages, v_pages, page_table, layer,
+                                           out, workspace)
     _check(dev, (qkv, _BF16, "qkv"), (gate, _F32, "gate"), (pos, _I32, "pos"),
            (k_pages, _BF16, "k_pages"), (v_pages, _BF16, "v_pages"),
            (page_table, _I32, "page_table"))
@@ -238,14 +240,13 @@ def spark_attn_decode_paged(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.Te
         raise ValueError("pos must be [B]")
     n_pages, page_size, max_pages = _pages(k_pages, v_pages, page_table, B, Hkv)
     d = ctypes.byref(as_desc(layer))
-    with _where(dev, stream):
-        out = _out(dev, out, B, H)
-        ws, owned = _workspace(
-            dev, workspace, lambda: lib.spark_attn_decode_paged_workspace_size(B, H, Hkv, d))
-        st = lib.spark_attn_decode_paged(
-            qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), k_pages.data_ptr(),
-            v_pages.data_ptr(), n_pages, page_size, page_table.data_ptr(), max_pages, d, B, H,
-            Hkv, out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    out, ws, owned = _buffers(dev, out, B, H, workspace,
+                              lib.spark_attn_decode_paged_workspace_size, B, H, Hkv, d)
+    st = lib.spark_attn_decode_paged(
+        qkv.data_ptr(), gate.data_ptr(), pos.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        n_pages, page_size, page_table.data_ptr(), max_pages, d, B, H, Hkv, out.data_ptr(),
+        ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if st or owned:
         _done("spark_attn_decode_paged", st, ws, owned)
     return out
 
@@ -326,10 +327,17 @@ def spark_attn_pages_workspace_size(pool: PagePool) -> int:
 
 def _pages_call(name: str, call, pool: PagePool, args, workspace, stream):
     dev = pool._dev
-    with _where(dev, stream):
-        ws, owned = _workspace(dev, workspace, lambda: spark_attn_pages_workspace_size(pool))
-        st = call(pool._ref, *args, ws.data_ptr(), ws.numel(), _raw_stream(dev))
-        _done(name, st, ws, owned)
+    if stream is not None or _current_device() != dev:
+        with _where(dev, stream):
+            return _pages_call(name, call, pool, args, workspace, None)
+    owned = workspace is None
+    if owned:
+        workspace = new_workspace(spark_attn_pages_workspace_size(pool), torch.device("cuda", dev))
+    else:
+        _check(dev, (workspace, _U8, "workspace"))
+    st = call(pool._ref, *args, workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
+    if st or owned:
+        _done(name, st, workspace, owned)
 
 
 def spark_attn_pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor,
