@@ -380,7 +380,9 @@ spark_status spark_attn_linear(const void *x, const void *w, void *y, int64_t M,
  *               a step captured into a graph) are not read into any result,
  *               and their rows of out stay as they were.
  *   k_pages, v_pages  bf16 [n_pages, Hkv, page_size, 256], one layer's pool;
- *               page_size 16, 32, 64, 128 or 256 (else SPARK_ERR_UNSUPPORTED).
+ *               page_size 16, 32, 64, 128 or 256 (else SPARK_ERR_UNSUPPORTED),
+ *               n_pages and max_pages at least 1 (else SPARK_ERR_CAPACITY).
+ *               Pages of 64 and more are fastest.
  *   page_table  int32 [rows, max_pages] (device).  Entries that hold no token
  *               a call reads or writes may be anything (-1, say), among them
  *               those wholly behind the window of a SLIDING layer.  A page
