@@ -631,13 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     y[j] = (h.o[j] * wo + v[j] * wn) * scale;
                     odd = odd || isnan(y[j]);
                 }
-                if (odd && isfinite(scale)) {
+                if (odd && isfinite(scale) && h.m != -INFINITY) {
                     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     sum_nonfinite(P, wk.b, wk.g, row.lo, row.pos, lane * 8, s);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         if (!isfinite(v[j])) s[j] += v[j];
-                        if (isnan(y[j])) y[j] = s[j] * scale;
+                        if (isnan(y[j]) && !isfinite(s[j])) y[j] = s[j] * scale;
                     }
                 }
                 *reinterpret_cast<uint4 *>(

@@ -181,6 +181,18 @@ def test_packed_rotated_widths_and_silu(cuda, rot):
     s.check_out(run_packed(s, layer), layer, f"packed rot {rot}")
 
 
+def test_packed_many_sequences(cuda):
+    """More sequences than the plan keeps in shared memory, most of them empty."""
+    g = torch.Generator().manual_seed(4)
+    new = [int(x) if x < 4 else 0 for x in torch.randint(0, 12, (1500,), generator=g)]
+    new[700], new[1499] = 70, 33
+    for page in (0, 16):
+        s = Step(new, [3 * (i % 5) if page else 0 for i in range(1500)], H=2, Hkv=1, page=page,
+                 seed=1, pad=2)
+        out = run_paged(s, FULL)[0] if page else run_packed(s, FULL)
+        s.check_out(out, FULL, f"1500 sequences, page {page}")
+
+
 def test_packed_equals_one_prompt_at_a_time(cuda):
     """A sequence's result does not depend on its neighbours: bit for bit."""
     for layer in (FULL, SLIDING):
@@ -533,6 +545,16 @@ def test_decode_visible_values_that_are_not_finite(cuda, value):
     assert torch.isnan(x[:, 3:9]).all() if value != value else (x[:, 3:9] == value).all()
 
 
+def test_decode_visible_keys_that_are_not_finite(cuda):
+    """A NaN key makes every dim of its row's heads NaN, as a softmax over it does."""
+    s = decode_step([500, 80], H=4, Hkv=1, page=16, seed=4)
+    clean, _, _ = run_decode(s, FULL)
+    s.k[s.rows[0][30], :, 5, 100] = float("nan")
+    got, _, _ = run_decode(s, FULL)
+    assert torch.isnan(got[0]).all()
+    assert torch.equal(got[1], clean[1])
+
+
 def test_a_window_wider_than_any_position(cuda):
     layer = layer_of("sliding", window=2 ** 31 - 1)
     s = Step([40, 3], [500, 250], H=4, Hkv=1, page=16, seed=4)
@@ -651,6 +673,44 @@ def test_packed_in_a_graph_serves_other_lengths(cuda):
         out.view(torch.int16).fill_(SENTINEL)
         graph.replay()
         s.check_out(out, layer, "replayed")
+    assert fga.spark_attn_read_status(ws) == 0
+
+
+def test_two_graphs_share_a_workspace(cuda):
+    """Captured calls of different kinds over one workspace, replayed in turn."""
+    layer = FULL
+    d = decode_step([1500, 40, 700], H=8, Hkv=2, page=32, seed=12)
+    p = Step([900, 5, 60], H=8, Hkv=2, seed=3)
+    need = max(fga.spark_attn_decode_paged_workspace_size(3, 8, 2, layer),
+               fga.spark_attn_prefill_packed_workspace_size(965, 3, 8, 2, layer))
+    ws = fga.new_workspace(need)
+    dd, out_d = d.cuda("qkv", "gate", "pos", "k", "v", "table"), blank(d)
+    pp, out_p = p.cuda("qkv", "gate", "pos"), blank(p)
+    cu = torch.tensor(p.cu, dtype=torch.int32, device=cuda)
+    side = torch.cuda.Stream()
+
+    def decode():
+        fga.spark_attn_decode_paged(*dd, layer, out=out_d, workspace=ws)
+
+    def prompt():
+        fga.spark_attn_prefill_packed(*pp, cu, layer, out=out_p, workspace=ws)
+
+    graphs = []
+    for call in (decode, prompt):
+        with torch.cuda.stream(side):
+            call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call()
+        graphs.append(g)
+    for i in range(6):
+        out_d.view(torch.int16).fill_(SENTINEL)
+        out_p.view(torch.int16).fill_(SENTINEL)
+        for g in (graphs if i % 2 else graphs[::-1]):
+            g.replay()
+        check_decode(d, layer, out_d, "decode, workspace shared")
+        p.check_out(out_p, layer, "packed, workspace shared")
     assert fga.spark_attn_read_status(ws) == 0
 
 
