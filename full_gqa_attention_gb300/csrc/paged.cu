@@ -254,8 +254,9 @@ constexpr int kPrepHeads = 4;                 // KV heads whose loads are in fli
 // What the attention kernel needs of the new keys and values.  Paged: every
 // token's rotated key and its value go to its pages.  Packed: the leading
 // rot_w dims of every key, rotated, go to the workspace (the others are read
-// where they are), and the values are looked over for one that is not finite
-// (with none, no boundary tile needs a pass over V).  A CTA takes kPrepRows
+// where they are).  The values are looked over for one that is not finite:
+// with none, a boundary tile needs no pass over its V but for slots from before
+// the call and behind the sequence's end.  A CTA takes kPrepRows
 // tokens; one thread per (token, 4 rotated pairs) or (token, 8 copied key dims
 // or value dims), over the KV heads, so that each angle is computed once; the
 // rotations come first, so that few warps do both.  The first CTA makes the
@@ -352,9 +353,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
 #pragma unroll
             for (int g = 0; g < kPrepHeads; ++g) {
                 if (g0 + g >= P.Hkv) break;
-                if (key || paged)
-                    *reinterpret_cast<uint4 *>(dst + (g0 + g) * head_stride) = v[g];
-                else  // an exponent of all ones carries into the sign's place
+                if (key || paged) *reinterpret_cast<uint4 *>(dst + (g0 + g) * head_stride) = v[g];
+                if (!key)  // an exponent of all ones carries into the sign's place
                     hit |= ((v[g].x & 0x7F807F80u) + 0x00800080u) |
                            ((v[g].y & 0x7F807F80u) + 0x00800080u) |
                            ((v[g].z & 0x7F807F80u) + 0x00800080u) |
@@ -540,14 +540,14 @@ spark_status launch_packed_attn(const PagedParams &P, const PackedPlan &pl, int 
             return SPARK_ERR_CUDA;
     }
     if (paged) {
-        // the pool as [n_pages][Hkv][page][256]; a box never leaves its page
+        // the pool as groups of 8 slots, [groups][4 chunks of 64 dims][8 slots][64]:
+        // a box of a few whole groups, which never leaves its page
         const uint64_t page = 1ull << P.page_shift;
-        const uint64_t dims[4] = {kHeadDim, page, static_cast<uint64_t>(P.Hkv),
-                                  static_cast<uint64_t>(P.n_pages)};
-        const uint64_t strides[3] = {kHeadDim * 2ull, page * kHeadDim * 2ull,
-                                     P.Hkv * page * kHeadDim * 2ull};
-        const uint32_t box_k[4] = {64, static_cast<uint32_t>(page < 128 ? page : 128), 1, 1};
-        const uint32_t box_v[4] = {64, static_cast<uint32_t>(page < 64 ? page : 64), 1, 1};
+        const uint64_t dims[4] = {64, 8, kHeadDim / 64,
+                                  static_cast<uint64_t>(P.n_pages) * P.Hkv * page / 8};
+        const uint64_t strides[3] = {kHeadDim * 2ull, 128, 8 * kHeadDim * 2ull};
+        const uint32_t box_k[4] = {64, 8, 2, static_cast<uint32_t>(page < 64 ? page : 64) / 8};
+        const uint32_t box_v[4] = {64, 8, 4, static_cast<uint32_t>(page < 32 ? page : 32) / 8};
         if (!encode_bf16_map(&tm_k, P.k_pages, 4, dims, strides, box_k) ||
             !encode_bf16_map(&tm_v, P.v_pages, 4, dims, strides, box_v))
             return SPARK_ERR_CUDA;
@@ -604,6 +604,8 @@ spark_status prefill_paged_impl(const void *qkv, const float *gate, const int32_
     if (paged) {
         st = check_pages(k_pages, v_pages, n_pages, page_size, table, max_pages);
         if (st != SPARK_OK) return st;
+        // a box's coordinate counts groups of 8 slots (8.8 TB of them)
+        if ((n_pages + 1ll) * Hkv * (page_size / 8) > 0x7fffffffLL) return SPARK_ERR_UNSUPPORTED;
     }
     int sms;
     st = device_ready(&sms);

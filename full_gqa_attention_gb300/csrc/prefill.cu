@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(kRopeThreads) cache_zero_tail_kernel(
 
 constexpr int kBM = 128;                  // query rows per tile
 constexpr int kBN = 128;                  // keys per tile
-constexpr int kSlotBytes = 16384;         // ring slot: 128 keys x 64 dims (K) or 32 keys x 256 (V)
+constexpr int kSlotBytes = 16384;         // ring slot: 128 keys x 64 dims (K) or 32 keys x 256 (V);
+                                          // from pages 32 keys x 256 (both)
 constexpr int kSlots = 8;
+constexpr int kGroupBytes = 4096;         // from pages: 8 keys, as 4 chunks of 64 dims
 constexpr int kQBytes = 4 * kSlotBytes;   // 128 rows x 256 dims, as 4 chunks of 64 dims
 constexpr int kAttnThreads = 384;
 constexpr int kPrefetchMaxTiles = 8;      // CTAs this short pull the next wave's Q into L2
@@ -325,24 +327,29 @@ __device__ __forceinline__ TileRows tile_rows(int kind, int window, int key0, in
 // ring slots from `use` on): the rows that not every query sees.  Those that no
 // query sees become zero; in the others, values that are not finite become zero
 // (returns true if this lane met one: the epilogue gives it back to the queries
-// that see it).
-__device__ __forceinline__ bool clean_v_rows(uint8_t *ring, int use, const TileRows &t, int w,
-                                             int lane) {
+// that see it).  Rows [finite_lo, finite_hi) hold finite values only and are
+// left alone (pages).
+template <bool kPages>
+__device__ __forceinline__ bool clean_v_rows(uint8_t *ring, int use, const TileRows &t,
+                                             int finite_lo, int finite_hi, int w, int lane) {
     // Row w + 8 i is at a constant distance from row w (`use` is a multiple of
     // 4, so the slots do not wrap): bit i of a mask stands for it, and the
     // passes unroll to plain stores and loads.
-    uint8_t *base = ring + (use % kSlots) * kSlotBytes + (lane >> 3) * (kSlotBytes / 2) +
-                    w * 128 + (lane & 7) * 16;
+    uint8_t *base = ring + (use % kSlots) * kSlotBytes +
+                    (lane >> 3) * (kPages ? 1024 : kSlotBytes / 2) + w * 128 + (lane & 7) * 16;
     auto at = [&](int i) {
-        return reinterpret_cast<uint4 *>(base + (i >> 3) * 2 * kSlotBytes + (i & 7) * 1024);
+        return reinterpret_cast<uint4 *>(
+            base + (kPages ? i * kGroupBytes : (i >> 3) * 2 * kSlotBytes + (i & 7) * 1024));
     };
     auto below = [&](int row) -> uint32_t {  // rows w + 8 i < row
         const int n = (row - w + 7) >> 3;
         return (1u << (n < 0 ? 0 : (n < 16 ? n : 16))) - 1u;
     };
-    const uint32_t none = (below(t.none_lo) | ~below(t.none_hi)) & 0xFFFFu;
+    const uint32_t unseen = below(t.none_lo) | ~below(t.none_hi);
     const uint32_t all = below(t.all_hi) & ~below(t.all_lo);
-    const uint32_t part = ~(none | all) & 0xFFFFu;
+    const uint32_t look = kPages ? ~(below(finite_hi) & ~below(finite_lo)) & 0xFFFFu : 0xFFFFu;
+    const uint32_t none = unseen & look;
+    const uint32_t part = ~(unseen | all) & look;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         if (none >> i & 1u) *at(i) = make_uint4(0, 0, 0, 0);
@@ -395,6 +402,7 @@ struct PackedTiles {
     volatile int *abort_flag;
     int kind, ntiles, kv_lo, a0, last;  // last: index of the last query
     int row0, seq, g;
+    int *groups;  // pages: where the pieces of the tiles of two batches begin
 
     // Waits until ring use `sc` may be filled, and arms its barrier.
     __device__ __forceinline__ bool take(int sc, int &slot) const {
@@ -459,88 +467,91 @@ struct PackedTiles {
         }
     }
 
+    // By the whole warp: lane l looks up piece l of the next kBatch tiles, a
+    // batch ahead; lane 0 waits and copies.
     template <int kPieces>
     __device__ __forceinline__ int load_pages() const {
-        constexpr int kStep = kBN / kPieces;  // keys per piece
-        constexpr int kBox = kStep < 64 ? kStep : 64;  // keys per V box
+        constexpr int kStep = kBN / kPieces;            // keys per piece
+        constexpr int kBatch = 32 / kPieces;            // tiles per lookup
+        constexpr int kBoxK = kStep < 64 ? kStep : 64;  // keys per K box
+        constexpr int kBoxV = kStep < 32 ? kStep : 32;  // keys per V box
+        static_assert(kBatch > 2, "V_j is copied after K_{j+2}'s batch has come");
+        const int lane = threadIdx.x & 31;
         const int shift = P.pk.page_shift, pmask = (1 << shift) - 1;
         const int lo = kind == kLayerSliding ? a0 - P.window + 1 : 0;
         const int32_t *pages = P.pk.table + static_cast<size_t>(seq) * P.pk.max_pages;
-        const int none = P.pk.n_pages;  // past the pool: the copy reads zeros
-        int idv[kPieces], idv1[kPieces], idk[kPieces], next[kPieces];
-        int sc = 0;
-        bool bad = false;
         // pages that no query sees a key of are not looked up
+        auto key_of = [&](int n) { return kv_lo + (n * 32 + lane) * kStep; };
         auto seen = [&](int key) { return key <= last && (key | pmask) >= lo; };
-        auto fetch = [&](int tile, int(&id)[kPieces]) {
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int key = kv_lo + tile * kBN + i * kStep;
-                id[i] = none;
-                if (seen(key)) id[i] = pages[key >> shift];
+        auto look = [&](int n) {
+            const int key = key_of(n);
+            return seen(key) ? pages[key >> shift] : -1;
+        };
+        bool bad = false;
+        auto place = [&](int n, int id) {  // the piece's first group of 8 slots
+            const int key = key_of(n);
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(P.pk.n_pages)) {
+                bad = bad || seen(key);
+                id = P.pk.n_pages;  // past the pool: the copy reads zeros
             }
+            groups[(n & 1) * 32 + lane] =
+                ((id * P.Hkv + g) << (shift - 3)) + ((key & pmask) >> 3);
         };
-        auto check = [&](int tile, int(&id)[kPieces]) {
+        int sc = 0;
+        auto k_tile = [&](int j) -> bool {
+            int at[kPieces];
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(none) &&
-                    seen(kv_lo + tile * kBN + i * kStep)) {
-                    bad = true;
-                    id[i] = none;
-                }
-        };
-        auto k_tile = [&](int j, const int(&id)[kPieces]) -> bool {
-            const int at = (kv_lo + j * kBN) & pmask;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                int slot;
-                if (!take(sc, slot)) return false;
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-                    tma_load_4d(ring + slot * kSlotBytes + i * kStep * 128, &tm_k,
-                                &bars[kBarSlotFull + slot], c * 64, at, g, id[i]);
-                ++sc;
-            }
-            return true;
-        };
-        auto v_tile = [&](int j, const int(&id)[kPieces]) -> bool {
-            const int at = (kv_lo + j * kBN) & pmask;
+            for (int i = 0; i < kPieces; ++i) at[i] = groups[(j * kPieces + i) & 63];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 int slot;
                 if (!take(sc, slot)) return false;
 #pragma unroll
-                for (int i = 0; i < 64 / kBox; ++i) {
-                    const int r = (q >> 1) * 64 + i * kBox;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        tma_load_4d(ring + slot * kSlotBytes + c * (kSlotBytes / 2) +
-                                        i * kBox * 128,
-                                    &tm_v, &bars[kBarSlotFull + slot], ((q & 1) * 2 + c) * 64,
-                                    at + r % kStep, g, id[r / kStep]);
+                for (int i = 0; i < 64 / kBoxK; ++i) {
+                    const int r = (q & 1) * 64 + i * kBoxK;
+                    tma_load_4d(ring + slot * kSlotBytes + i * (kBoxK / 8) * (kGroupBytes / 2),
+                                &tm_k, &bars[kBarSlotFull + slot], 0, 0, q & 2,
+                                at[r / kStep] + r % kStep / 8);
                 }
                 ++sc;
             }
             return true;
         };
-        fetch(0, idv);
-        fetch(1, idv1);
-        fetch(2, idk);
-        check(0, idv);
-        bool ok = k_tile(0, idv);
-        check(1, idv1);
-        if (ok && ntiles > 1) ok = k_tile(1, idv1);
-        for (int j = 0; ok && j < ntiles; ++j) {
-            fetch(j + 3, next);
-            check(j + 2, idk);
-            ok = v_tile(j, idv);
-            if (ok && j + 2 < ntiles) ok = k_tile(j + 2, idk);
+        auto v_tile = [&](int j) -> bool {
+            int at[kPieces];
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                idv[i] = idv1[i];
-                idv1[i] = idk[i];
-                idk[i] = next[i];
+            for (int i = 0; i < kPieces; ++i) at[i] = groups[(j * kPieces + i) & 63];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                int slot;
+                if (!take(sc, slot)) return false;
+#pragma unroll
+                for (int i = 0; i < 32 / kBoxV; ++i) {
+                    const int r = q * 32 + i * kBoxV;
+                    tma_load_4d(ring + slot * kSlotBytes + i * (kBoxV / 8) * kGroupBytes, &tm_v,
+                                &bars[kBarSlotFull + slot], 0, 0, 0,
+                                at[r / kStep] + r % kStep / 8);
+                }
+                ++sc;
             }
+            return true;
+        };
+        place(0, look(0));
+        int next = look(1);
+        __syncwarp();
+        bool ok = true;
+        if (lane == 0) ok = k_tile(0) && (ntiles == 1 || k_tile(1));
+        for (int j = 0; j < ntiles; ++j) {
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if ((j + 2) % kBatch == 0) {
+                const int n = (j + 2) / kBatch;
+                __syncwarp();  // the batch before the last is read
+                place(n, next);
+                next = look(n + 1);
+                __syncwarp();
+            }
+            if (lane == 0) ok = v_tile(j) && (j + 2 >= ntiles || k_tile(j + 2));
         }
         if (bad) atomicOr(P.status, kErrPage);
         return sc;
@@ -637,6 +648,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // packed: the item, read from here where it is needed (held in registers
     // through the softmax it made the kernel spill)
     __shared__ PackedItem s_item;
+    __shared__ int s_groups[kSrc == kKvPages ? 64 : 1];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int kind = kKind == kKindAny ? P.kind : kKind;
@@ -717,7 +729,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int kv_lo = kt.kv_lo + (kIsPacked ? s_item.k0 * kBN : 0);
     const int ntiles = skip ? 0 : (kIsPacked ? s_item.tiles : kt.ntiles);
     const PackedTiles<kSrc> packed_tiles{tm_kv_k, tm_kv_v, tm_krot, P, ring, bars, &abort_flag,
-                                         kind, ntiles, kv_lo, a0, start + t_end - 1, row0, seq, g};
+                                         kind, ntiles, kv_lo, a0, start + t_end - 1, row0, seq, g,
+                                         s_groups};
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -810,11 +823,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     ok = load_v(j);
                     if (ok && j + 2 < ntiles) ok = load_k(j + 2);
                 }
-            } else {
+            } else if constexpr (kSrc == kKvPacked) {
                 sc = packed_tiles.load();
             }
         }
         __syncwarp();
+        if constexpr (kSrc == kKvPages) sc = packed_tiles.load();
         tc_fence_before();
         __syncthreads();
         // after an abort, copies in flight must land before shared memory is released
@@ -840,8 +854,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // below 2^18, so an operand at byte offset o from a base has the
             // base's descriptor plus o / 16.  This keeps the issue loop short.
             const uint64_t q_desc = smem_desc_sw128(smem_u32(qbuf), 16, 1024);
-            const uint64_t k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(smem_u32(ring), kSlotBytes / 4, 1024);
+            constexpr bool kPages = kSrc == kKvPages;  // tiles of 8-key groups
+            const uint64_t k_desc =
+                smem_desc_sw128(smem_u32(ring), 16, kPages ? kGroupBytes / 2 : 1024);
+            const uint64_t v_desc = smem_desc_sw128(smem_u32(ring), kPages ? 1024 : kSlotBytes / 4,
+                                                    kPages ? kGroupBytes : 1024);
             const uint64_t vp_desc = smem_desc_sw128(smem_u32(ring), kSlotBytes / 2, 1024);
             // (the full-layer cache instance measured faster building each
             // descriptor in place)
@@ -851,7 +868,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bool ok = true;
             auto mma_qk = [&](int j) -> bool {
                 const uint32_t d = tmem + kColS + (j & 1) * kBN;
-                for (int c = 0; c < 4; ++c) {
+                for (int h = 0; kPages && h < 2; ++h) {  // halves of 128 dims, two slots each
+                    const int slot = sc % kSlots;
+                    const uint32_t parity = (sc / kSlots) & 1;
+                    if (!mbar_wait(&bars[kBarSlotFull + slot], parity, &abort_flag, P.status) ||
+                        !mbar_wait(&bars[kBarSlotFull + slot + 1], parity, &abort_flag, P.status))
+                        return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)  // 16 dims a step
+                        mma_ss(d,
+                               q_desc + static_cast<uint32_t>(
+                                            ((2 * h + (i >> 2)) * kSlotBytes + (i & 3) * 32) >> 4),
+                               k_desc + static_cast<uint32_t>(
+                                            (slot * kSlotBytes + (i >> 2) * 1024 + (i & 3) * 32) >>
+                                            4),
+                               kIdescQK, (h | i) != 0);
+                    tc_commit(&bars[kBarSlotEmpty + slot]);
+                    tc_commit(&bars[kBarSlotEmpty + slot + 1]);
+                    sc += 2;
+                }
+                for (int c = 0; !kPages && c < 4; ++c) {
                     const int slot = sc % kSlots;
                     if (!mbar_wait(&bars[kBarSlotFull + slot], (sc / kSlots) & 1, &abort_flag,
                                    P.status))
@@ -877,7 +914,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             auto mma_pv = [&](int j) -> bool {
                 const uint32_t pcol = tmem + kColS + (j & 1) * kBN;
-                if constexpr (kIsPacked) {
+                if constexpr (kSrc == kKvPacked) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // halves of 64 keys, two slots each
                         const int slot = sc % kSlots;
@@ -900,7 +937,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         sc += 2;
                     }
                 }
-                for (int vs = 0; !kIsPacked && vs < 4; ++vs) {
+                for (int vs = 0; kSrc != kKvPacked && vs < 4; ++vs) {
                     const int slot = sc % kSlots;
                     if (!mbar_wait(&bars[kBarSlotFull + slot], (sc / kSlots) & 1, &abort_flag,
                                    P.status))
@@ -913,7 +950,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             kDescInPlace
                                 ? smem_desc_sw128(ring_addr + slot * kSlotBytes + kk * 2048,
                                                   kSlotBytes / 4, 1024)
-                                : v_desc + static_cast<uint32_t>((slot * kSlotBytes + kk * 2048) >> 4);
+                                : v_desc + static_cast<uint32_t>(
+                                               (slot * kSlotBytes +
+                                                kk * (kPages ? 2 * kGroupBytes : 2048)) >> 4);
                         // P of keys 0..63 sits in packed columns 0..31, keys 64..127 in 64..95
                         const uint32_t acol = pcol + (ks < 4 ? ks * 8 : 64 + (ks - 4) * 8);
                         mma_ts(tmem + kColO, acol, bd, kIdescPV, (j > 0 || ks > 0));
@@ -1010,8 +1049,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // raw equivalent of 2^8.
         constexpr float kLazyRaw = 8.0f / kScaleLog2;
         const int a_last = start + t_end - 1;
-        // (without a cache the kernel before has looked at every value)
-        const bool clean = kSrc == kKvPages || (kIsPacked && P.pk.odd_values[s_item.call & 1] != 0);
+        // The kernel before has looked over the values of the call's tokens.
+        // Without a cache there are no others; in pages, these are the indices
+        // from `start` to finite_end.
+        const bool odd = kIsPacked && P.pk.odd_values[s_item.call & 1] != 0;
+        const int finite_end = odd ? -1 : start + seq_end;
         const int col0 = wg * 64;                       // first score column of this thread
         float m_run = -INFINITY, l_part = 0.f;
         for (int j = 0; ok && j < ntiles; ++j) {
@@ -1088,6 +1130,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             if constexpr (kIsPacked) {
+                // (of a page's older slots only the window's start can be hidden)
+                const bool clean =
+                    kSrc == kKvPages
+                        ? key0 + kBN > finite_end || (kind == kLayerSliding && key0 < start &&
+                                                      key0 < a_last - P.window + 1)
+                        : odd;
                 if (clean && tile_needs_mask(kind, P.window, key0, kBN, a0, a_last)) {
                     // V_j comes after min(ntiles, j + 2) K tiles and j V tiles.
                     // The slots' use before it was K_j (the last tile: S_j says
@@ -1101,7 +1149,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         ok = mbar_wait(&bars[kBarSlotFull + (use + vs) % kSlots],
                                        ((use + vs) / kSlots) & 1, &abort_flag, P.status);
                     if (!ok) break;
-                    if (clean_v_rows(ring, use, rows, warp - kSoftmaxWarp0, lane))
+                    if (clean_v_rows<kSrc == kKvPages>(ring, use, rows, start - key0,
+                                                       finite_end - key0, warp - kSoftmaxWarp0,
+                                                       lane))
                         cleaned_any = 1;
                     fence_proxy_async_smem();
                 }

@@ -315,6 +315,45 @@ def test_paged_edges(cuda, kind):
         s.check_pages(k, v, layer)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("kind", ["full", "sliding"])
+def test_paged_hidden_values_reach_nothing(cuda, kind, value):
+    """A value that is not finite, cached or new: the queries that see it, and they alone,
+    have it.  One workspace serves the calls in turn, a finite one after each."""
+    layer = layer_of(kind, window=40)
+    H, Hkv = 4, 1
+    s = Step([50, 70, 0, 33], [100, 383, 5, 0], H=H, Hkv=Hkv, page=16, seed=19, pad=5)
+    ws = fga.new_workspace(fga.spark_attn_prefill_paged_workspace_size(
+        len(s.qkv), len(s.new), H, Hkv, layer))
+    clean, _, _ = run_paged(s, layer, workspace=ws)
+    old, row = s.old[1], s.cu[1]
+    for at in (345, 360, 380, 382, old, old + 20, old + 69):
+        if at < old:
+            place = s.v[s.rows[1][at // 16], 0, at % 16, 3:9]
+        else:
+            place = s.qkv[row + at - old, (H + Hkv) * D + 3:(H + Hkv) * D + 9]
+        kept = place.clone()
+        place.fill_(value)
+        got, _, _ = run_paged(s, layer, workspace=ws)
+        place.copy_(kept)
+        assert torch.equal(run_paged(s, layer, workspace=ws)[0].view(torch.int16),
+                           clean.view(torch.int16)), at
+        w = layer.window if kind == "sliding" else 10 ** 6
+        for i in range(70):
+            x, y = got[row + i].view(H, D), clean[row + i].view(H, D)
+            if at <= old + i < at + w:
+                assert torch.equal(x[:, 9:], y[:, 9:]) and torch.equal(x[:, :3], y[:, :3]), (at, i)
+                if value == value:
+                    assert (x[:, 3:9] == value).all(), (at, i)
+                else:
+                    assert torch.isnan(x[:, 3:9]).all(), (at, i)
+            else:
+                assert torch.equal(x, y), (at, i)
+        m = s.covered()
+        m[row:row + 70] = False
+        assert torch.equal(got.cpu()[m], clean.cpu()[m]), at
+
+
 def test_paged_sliding_pages_behind_the_window_may_be_gone(cuda):
     layer = layer_of("sliding", window=70)
     s = Step([40, 3], [500, 250], H=4, Hkv=1, page=16, seed=4)
