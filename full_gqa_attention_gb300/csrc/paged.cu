@@ -98,9 +98,10 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
         int total;
         const int at = prep_scan(n, &total);
         if (s < P.S) tile_base[s] = base + at;
-        base += total;
+        // offsets that overlap can ask for more tiles than the list holds, and
+        // many times more than 32 bits do
+        base = base + total < P.most ? base + total : P.most;
     }
-    // offsets that overlap can ask for more tiles than the list holds
     const int extra = P.slots > 0 ? P.sms / P.Hkv + 1 : 0;
     const int n_tiles = base < P.most - extra ? base : P.most - extra;
     __syncthreads();

@@ -280,6 +280,24 @@ def test_packed_bad_offsets_are_flagged(cuda):
     check_close(run, s.expected(FULL)[0], "after the bad ones")
 
 
+def test_packed_offsets_that_overlap_without_end(cuda):
+    """Offsets that jump back two million times ask for 2^31 query tiles and more."""
+    n = 1 << 18
+    layer = layer_of("sliding", window=1)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    qkv = torch.randn((n, 3 * D), generator=g, device=cuda).to(torch.bfloat16)
+    gate = torch.randn((n, 1), generator=g, device=cuda)
+    pos = torch.arange(n, device=cuda, dtype=torch.int32)
+    want = fga.spark_attn_prefill_packed(
+        qkv, gate, pos, torch.tensor([0, n], dtype=torch.int32, device=cuda), layer)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=cuda).repeat((1 << 20) + 4096)
+    ws = fga.new_workspace(fga.spark_attn_prefill_packed_workspace_size(
+        n, cu.numel() - 1, 1, 1, layer))
+    got = fga.spark_attn_prefill_packed(qkv, gate, pos, cu, layer, workspace=ws)
+    assert fga.spark_attn_read_status(ws) == fga.SPARK_DEVERR_SEQLENS
+    assert torch.equal(got, want)        # the first sequence is whole, the others repeat it
+
+
 # ---------------------------------------------------------------- paged prompts
 
 @pytest.mark.parametrize("kind", ["full", "sliding"])
