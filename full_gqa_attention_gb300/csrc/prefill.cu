@@ -379,20 +379,65 @@ __device__ __forceinline__ bool clean_v_rows(uint8_t *ring, int use, const TileR
     return found;
 }
 
+// The same for tile j of ntiles, once its V has landed; false after a wait that
+// ran out.
+template <bool kPages>
+__device__ __forceinline__ bool clean_tile(uint8_t *ring, uint64_t *bars,
+                                           volatile int *abort_flag, unsigned *status,
+                                           int *cleaned_any, int j, int ntiles,
+                                           int kind, int window, int key0, int a0, int a_last,
+                                           int finite_lo, int finite_end, int w, int lane) {
+    // V_j comes after min(ntiles, j + 2) K tiles and j V tiles.  The slots' use
+    // before it was K_j (the last tile: S_j says that it landed), K0 (the first)
+    // or V_{j-1}, which P*V of tile j-1 says: a parity wait must not begin a
+    // phase early.
+    const int use = 4 * ((ntiles < j + 2 ? ntiles : j + 2) + j);
+    bool ok = true;
+    if (j > 0 && j + 1 < ntiles) ok = mbar_wait(&bars[kBarODone], (j - 1) & 1, abort_flag, status);
+    for (int vs = 0; ok && vs < 4; ++vs)
+        ok = mbar_wait(&bars[kBarSlotFull + (use + vs) % kSlots], ((use + vs) / kSlots) & 1,
+                       abort_flag, status);
+    if (!ok) return false;
+    if (clean_v_rows<kPages>(ring, use, tile_rows(kind, window, key0, a0, a_last),
+                             finite_lo - key0, finite_end - key0, w, lane))
+        *cleaned_any = 1;
+    fence_proxy_async_smem();
+    return true;
+}
+
+// The same out of line, for the packed kernels: inlined it slows the softmax
+// loop, which needs it only where a value is not finite (sliding prompt of 8192
+// tokens 146 -> 141 us; over pages of 16 inlining is 4 % faster).
+__device__ __noinline__ bool clean_tile_call(uint8_t *ring, uint64_t *bars,
+                                             volatile int *abort_flag, unsigned *status,
+                                             int *cleaned_any, int j, int ntiles, int kind,
+                                             int window, int key0, int a0, int a_last, int w,
+                                             int lane) {
+    return clean_tile<false>(ring, bars, abort_flag, status, cleaned_any, j, ntiles, kind, window,
+                             key0, a0, a_last, 0, 0, w, lane);
+}
+
 // The copies of a packed source's key and value tiles into the ring, by one
 // thread in the order of the issuers: K0, K1, then V_j and K_{j+2} for every
 // tile j.  A V tile is two halves of 64 keys, each in two slots of two 64-dim
 // chunks (the other sources: four slots of 32 keys): the copy engine takes
 // about as long for a box of 32 rows as for one of 64.
 //
-// With pages a tile is a box per page.  What stands between a slot's release
-// and its refill delays every tile, so the page numbers are looked up a tile
-// ahead and kept in registers, and the number of pieces is fixed at compile
-// time: looking them up behind the wait took 860 us where the contiguous cache
-// takes 475 (2048 tokens on 16384), issuing from several lanes 1390.  A second
-// thread for V was 5 % slower: its copies then queue behind K tiles that are
-// not urgent.  Pages of 16 need 64 small copies a tile, which the copy engine
-// itself bounds (890 us).
+// With pages, a K or V tile is in groups of 8 keys, each 4 KB of the pool, and
+// a box takes several of them: it brings its keys' 64-dim chunks one behind the
+// other, so that the groups stand where the products expect them, at a constant
+// distance whatever the page size.  V slots hold 32 keys, K slots 64 keys and
+// half of the dims, so that QK^T begins with half a tile.  A box per page and
+// chunk instead left pages of 16 and 32 bound by the number of copies (64 and
+// 32 a tile; 1783 and 1139 us where pages of 64 take 848, chunks of up to 2048
+// tokens on up to 24,576; now 980, 872 and 865).  K in boxes of all dims made
+// pages of 64 11 % slower.
+//
+// What stands between a slot's release and its refill delays every tile, so
+// the page numbers are looked up ahead, by the warp's other lanes, and left in
+// shared memory: one thread that looked up pages of 16 by itself took 10 %
+// longer.  A second thread for V was 5 % slower: its copies then queue behind
+// K tiles that are not urgent.
 template <int kSrc>
 struct PackedTiles {
     const CUtensorMap &tm_k, &tm_v, &tm_krot;
@@ -1137,23 +1182,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                                       key0 < a_last - P.window + 1)
                         : odd;
                 if (clean && tile_needs_mask(kind, P.window, key0, kBN, a0, a_last)) {
-                    // V_j comes after min(ntiles, j + 2) K tiles and j V tiles.
-                    // The slots' use before it was K_j (the last tile: S_j says
-                    // that it landed), K0 (the first) or V_{j-1}, which P*V of
-                    // tile j-1 says: a parity wait must not begin a phase early.
-                    const int use = 4 * ((ntiles < j + 2 ? ntiles : j + 2) + j);
-                    if (j > 0 && j + 1 < ntiles)
-                        ok = mbar_wait(&bars[kBarODone], (j - 1) & 1, &abort_flag, P.status);
-                    const TileRows rows = tile_rows(kind, P.window, key0, a0, a_last);
-                    for (int vs = 0; ok && vs < 4; ++vs)
-                        ok = mbar_wait(&bars[kBarSlotFull + (use + vs) % kSlots],
-                                       ((use + vs) / kSlots) & 1, &abort_flag, P.status);
+                    if constexpr (kSrc == kKvPages)
+                        ok = clean_tile<true>(ring, bars, &abort_flag, P.status, &cleaned_any, j,
+                                              ntiles, kind, P.window, key0, a0, a_last, start,
+                                              finite_end, warp - kSoftmaxWarp0, lane);
+                    else
+                        ok = clean_tile_call(ring, bars, &abort_flag, P.status, &cleaned_any, j,
+                                             ntiles, kind, P.window, key0, a0, a_last,
+                                             warp - kSoftmaxWarp0, lane);
                     if (!ok) break;
-                    if (clean_v_rows<kSrc == kKvPages>(ring, use, rows, start - key0,
-                                                       finite_end - key0, warp - kSoftmaxWarp0,
-                                                       lane))
-                        cleaned_any = 1;
-                    fence_proxy_async_smem();
                 }
             }
             mbar_arrive(&bars[kBarPReady + (j & 1)]);

@@ -382,7 +382,7 @@ spark_status spark_attn_linear(const void *x, const void *w, void *y, int64_t M,
  *   k_pages, v_pages  bf16 [n_pages, Hkv, page_size, 256], one layer's pool;
  *               page_size 16, 32, 64, 128 or 256 (else SPARK_ERR_UNSUPPORTED),
  *               n_pages and max_pages at least 1 (else SPARK_ERR_CAPACITY).
- *               Pages of 64 and more are fastest.
+ *               Pages of 32 and more are fastest.
  *   page_table  int32 [rows, max_pages] (device).  Entries that hold no token
  *               a call reads or writes may be anything (-1, say), among them
  *               those wholly behind the window of a SLIDING layer.  A page
@@ -498,7 +498,8 @@ typedef struct spark_page_pool {
  * is left out and SPARK_DEVERR_ROW set).  If the row's last page holds tokens
  * and is shared, the row gets a copy of its own, in every layer: of the rows
  * of one call that are about to write into the same page each makes a copy,
- * in row order, until one holder is left.  Pages are taken from the lowest
+ * in row order, until one holder is left.  A fork shares the last page again:
+ * both rows reserve anew before they write.  Pages are taken from the lowest
  * free number up, rows in order, in each row the copy first.  len stays.
  * taken: optional int32 [1]: pages taken, or -1 when the pool has too few --
  * then nothing has changed.
