@@ -183,32 +183,30 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
     }
     __syncthreads();
     const int limit = s_limit;
-    auto bin_of = [&](int n) { return kBins - 1 - (n < kBins ? n : kBins - 1); };
-    for (int i = tid; i < n_tiles; i += kPrepThreads) {
-        const int n = i == tid ? first.tiles : tile(i).tiles;
-        const int parts = (n + limit - 1) / limit;
-        atomicAdd(&bins[bin_of((n + parts - 1) / parts)], parts);
-    }
-    __syncthreads();
-    constexpr int kPer = kBins / kPrepThreads;
-    int count[kPer], mine = 0, total;
+    // (tiles of a single wave start together: they need no order, one bin does)
+    auto bin_of = [&](int n) { return wave ? 0 : kBins - 1 - (n < kBins ? n : kBins - 1); };
+    int total = 0;
+    if (!wave) {
+        for (int i = tid; i < n_tiles; i += kPrepThreads) {
+            const int n = i == tid ? first.tiles : tile(i).tiles;
+            const int parts = (n + limit - 1) / limit;
+            atomicAdd(&bins[bin_of((n + parts - 1) / parts)], parts);
+        }
+        __syncthreads();
+        constexpr int kPer = kBins / kPrepThreads;
+        int count[kPer], mine = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        count[i] = bins[tid * kPer + i];
-        mine += count[i];
-    }
-    int at = prep_scan(mine, &total);
+        for (int i = 0; i < kPer; ++i) {
+            count[i] = bins[tid * kPer + i];
+            mine += count[i];
+        }
+        int at = prep_scan(mine, &total);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        bins[tid * kPer + i] = at;
-        at += count[i];
-    }
-    __syncthreads();
-    for (int i = total + tid; i < P.most; i += kPrepThreads) {
-        PackedItem t = {};
-        t.seq = -1;
-        t.call = call;
-        P.work[i] = t;
+        for (int i = 0; i < kPer; ++i) {
+            bins[tid * kPer + i] = at;
+            at += count[i];
+        }
+        __syncthreads();
     }
     for (int i = tid; i < n_tiles; i += kPrepThreads) {
         PackedItem t = i == tid ? first : tile(i);
@@ -227,6 +225,13 @@ __device__ __forceinline__ void plan_tiles(const PagedParams &P) {
         }
     }
     __syncthreads();
+    if (wave) total = bins[0];
+    for (int i = total + tid; i < P.most; i += kPrepThreads) {
+        PackedItem t = {};
+        t.seq = -1;
+        t.call = call;
+        P.work[i] = t;
+    }
     if (tid == 0) *P.n_splits = s_splits;
 }
 
