@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     __shared__ long long place[kPrepRows];
     grid_dep_wait();
     grid_dep_launch();
+    grid_dep_launch();
     if (blockIdx.x == 0) {
         plan_tiles(P);
         return;
