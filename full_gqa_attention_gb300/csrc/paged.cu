@@ -270,6 +270,9 @@ constexpr int kPrepHeads = 4;                 // KV heads whose loads are in fli
 __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     const __grid_constant__ PagedParams P) {
     __shared__ long long place[kPrepRows];
+    // (the lanes' frequencies differ: from the parameters, constant memory, they
+    // would come one lane after another)
+    __shared__ __align__(16) float2 freq[kHeadDim / 2];
     grid_dep_wait();
     grid_dep_launch();
     grid_dep_launch();
@@ -287,8 +290,9 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
         const long long at =
             first + w < P.N ? token_slot(P, static_cast<int>(first + w), lane) : -1;
         if (lane == 0) place[w] = at;
-        __syncthreads();
     }
+    if (threadIdx.x < half) freq[threadIdx.x] = P.rope.u[threadIdx.x];
+    __syncthreads();
     const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
     const size_t head_stride = paged ? static_cast<size_t>(kHeadDim) << P.page_shift
                                      : static_cast<size_t>(P.N) * P.rot_w;
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
         load(0);
         float c[4], s[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) rope_cos_sin_fine(p, P.rope.u[k0 + j], c[j], s[j]);
+        for (int j = 0; j < 4; ++j) rope_cos_sin_fine(p, freq[k0 + j], c[j], s[j]);
         for (int g0 = 0; g0 < P.Hkv; g0 += kPrepHeads) {
             if (g0) load(g0);
 #pragma unroll
