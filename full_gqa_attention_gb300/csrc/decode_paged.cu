@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ long long s_base;
     __shared__ long long warp_sum[kThreads / 32];
     __shared__ float red_m[kWarps][8], red_l[kWarps][8];
+    __shared__ float2 freq[kHeadDim / 2];  // (read by lane: constant memory is slow at that)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -170,6 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
+    const int half = P.rope.rot_dim / 2;
+    if (tid < half) freq[tid] = P.rope.u[tid];
     grid_dep_wait();  // positions, tables and pages may come from the kernel before
 
     // ---------------------------------------------------------- this CTA's stretch
@@ -282,7 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---------------------------------------------------------- consumers
     const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
-    const int half = P.rope.rot_dim / 2;
     const int arow = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;  // K rows (ldmatrix)
     const int vrow = warp * 16 + (lane & 7) + (lane >> 4) * 8;        // V rows (ldmatrix.trans)
     const int h0 = 2 * (lane & 3), h1 = h0 + 1;                       // this thread's two heads
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         consumer_bar();
         for (int k = tid; k < half; k += kWarps * 32) {
             float c, s;
-            rope_cos_sin_fine(row.pos, P.rope.u[k], c, s);
+            rope_cos_sin_fine(row.pos, freq[k], c, s);
             for (int hh = 0; hh <= P.G; ++hh) {
                 __nv_bfloat16 *x = hh < P.G ? qs + hh * kHeadDim : kn;
                 float y1, y2;
