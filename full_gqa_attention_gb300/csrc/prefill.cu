@@ -430,7 +430,7 @@ __device__ __noinline__ bool clean_tile_call(uint8_t *ring, uint64_t *bars,
 // half of the dims, so that QK^T begins with half a tile.  A box per page and
 // chunk instead left pages of 16 and 32 bound by the number of copies (64 and
 // 32 a tile; 1783 and 1139 us where pages of 64 take 848, chunks of up to 2048
-// tokens on up to 24,576; now 980, 872 and 865).  K in boxes of all dims made
+// tokens on up to 24,576; now 1014, 872 and 865).  K in boxes of all dims made
 // pages of 64 11 % slower.
 //
 // What stands between a slot's release and its refill delays every tile, so
