@@ -131,7 +131,7 @@ struct __align__(16) PackedItem {
 
 struct PackedInfo {
     const PackedItem *work;
-    // Whether any value V of the call is not finite (no cache: the kernel before
+    // Whether any value V of the call's tokens is not finite (the kernel before
     // the attention kernel looks at all of them).  Two words take turns: a call
     // sets its own and clears the next one's.  Whatever they held before, the
     // worst is a needless pass over boundary tiles.
