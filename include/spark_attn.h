@@ -382,7 +382,9 @@ spark_status spark_attn_linear(const void *x, const void *w, void *y, int64_t M,
  *   k_pages, v_pages  bf16 [n_pages, Hkv, page_size, 256], one layer's pool;
  *               page_size 16, 32, 64, 128 or 256 (else SPARK_ERR_UNSUPPORTED),
  *               n_pages and max_pages at least 1 (else SPARK_ERR_CAPACITY).
- *               Pages of 32 and more are fastest.
+ *               Pages of 32 and more are fastest.  A prompt's pool holds less than
+ *               2^31 groups of 8 slots over all KV heads (8.8 TB of keys; else
+ *               SPARK_ERR_UNSUPPORTED).
  *   page_table  int32 [rows, max_pages] (device).  Entries that hold no token
  *               a call reads or writes may be anything (-1, say), among them
  *               those wholly behind the window of a SLIDING layer.  A page

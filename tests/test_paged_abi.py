@@ -204,3 +204,10 @@ def test_the_binding_refuses_host_tensors():
         fga.spark_attn_decode_paged(x, torch.zeros(4, 16), i, x, x, i, desc())
     with pytest.raises(TypeError):
         fga.PagePool(x, x, i, i, i, i)
+
+
+def test_a_pool_past_the_copies_coordinates_is_refused():
+    """A prompt's copies count groups of 8 slots in 31 bits (8.8 TB of keys)."""
+    most = (2 ** 31 - 1) // (4 * 8)                  # 4 KV heads, pages of 64
+    assert paged(n_pages=most) == bnd.SPARK_ERR_UNSUPPORTED
+    assert paged(n_pages=most - 1, ws_bytes=255) == bnd.SPARK_ERR_WORKSPACE
