@@ -114,25 +114,47 @@ __device__ __forceinline__ void add_scaled(HeadState &s, float w, const float *o
     for (int i = 0; i < 8; ++i) s.o[i] += o[i] * w;
 }
 
+// Values that are not finite.  A visible infinity is infinite in its dims,
+// however small its weight, but not in these products: a weight that 32 bits
+// hold as zero, or the two terms of a probability, which can have different
+// signs, make NaN of it.  So where a sum is not finite, the values that are not
+// are added up without weights and take its place: in each CTA's state
+// (sum_nonfinite), where states are joined, and where the new token joins.  A
+// NaN score makes the sum of the weights NaN, and with it the row.
+__device__ __forceinline__ float nonfinite_part(float x) { return isfinite(x) ? 0.f : x; }
+
 }  // namespace
 
-// The sum of the values of the slots [lo, pos) that are not finite, for a lane's
-// 8 dims (from d0) of a pair: with a visible value of +-inf the two terms of its
-// probability can make NaN where the sum is infinite.  Rare.
-__device__ __noinline__ void sum_nonfinite(const PagedParams &P, int b, int g, int lo, int pos,
-                                           int d0, float (&s)[8]) {
-    for (int j = lo; j < pos; ++j) {
-        const int id = P.table[static_cast<size_t>(b) * P.max_pages + (j >> P.page_shift)];
-        if (id < 0 || id >= P.n_pages) continue;
-        const uint4 w = *reinterpret_cast<const uint4 *>(
+// The sum of the values of the slots [lo, hi) of a pair that are not finite, over
+// this warp's share of them, for a lane's 8 dims (from d0).  Groups of 8 slots
+// (which lie in one page) are the warps' in turn: one table entry and 8 rows in
+// flight.  Rare, and bounded by the CTA's stretch, so that a call takes twice as
+// long at most: 108 us for a row of 120,000 tokens with one such value (75
+// without, and 61 ms where one warp walked the row), 0.42 ms for 262,139 tokens
+// with many (0.19 without).
+__device__ __noinline__ void sum_nonfinite(const PagedParams &P, int b, int g, int lo, int hi,
+                                           int warp, int d0, float (&s)[8]) {
+    const int32_t *row = P.table + static_cast<size_t>(b) * P.max_pages;
+    for (int j0 = (lo & ~7) + warp * 8; j0 < hi; j0 += kWarps * 8) {
+        const int id = row[j0 >> P.page_shift];
+        if (id < 0 || id >= P.n_pages) continue;  // read as zeros
+        const __nv_bfloat16 *src =
             P.v_pages + (((static_cast<size_t>(id) * P.Hkv + g) << P.page_shift) +
-                         (j & ((1 << P.page_shift) - 1))) * kHeadDim + d0);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                         (j0 & ((1 << P.page_shift) - 1))) * kHeadDim + d0;
+        uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = bf16_lo(u[i]), c = bf16_hi(u[i]);
-            if (!isfinite(a)) s[2 * i] += a;
-            if (!isfinite(c)) s[2 * i + 1] += c;
+        for (int r = 0; r < 8; ++r)
+            w[r] = j0 + r >= lo && j0 + r < hi
+                       ? *reinterpret_cast<const uint4 *>(src + r * kHeadDim)
+                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[2 * i] += nonfinite_part(bf16_lo(u[i]));
+                s[2 * i + 1] += nonfinite_part(bf16_hi(u[i]));
+            }
         }
     }
 }
@@ -151,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(red_o) + kRedBytes);
     uint64_t *fullv = full + kStages;
     uint64_t *empty = fullv + kStages;
-    __shared__ int abort_flag, seg_bad, last_cta;
+    __shared__ int abort_flag, seg_bad, seg_odd, last_cta;
     __shared__ int s_row;
     __shared__ long long s_base;
     __shared__ long long warp_sum[kThreads / 32];
@@ -168,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         abort_flag = 0;
         seg_bad = 0;
+        seg_odd = 0;
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
@@ -459,9 +482,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             red_l[warp][h0] = l0;
             red_l[warp][h1] = l1;
         }
+        // (a product with zero is NaN where a sum is not finite)
+        float odd0 = 0.f, odd1 = 0.f;
+#pragma unroll
+        for (int db = 0; db < 16; ++db) {
+            odd0 += (o[db][0] + o[db][2]) * 0.f;
+            odd1 += (o[db][1] + o[db][3]) * 0.f;
+        }
+        if ((isnan(odd0) && isfinite(l0)) || (isnan(odd1) && isfinite(l1))) seg_odd = 1;
         if (!ok) seg_bad = 1;
         consumer_bar();
         aborted = seg_bad != 0;  // written before the barrier, never reset
+        const bool odd = seg_odd != 0 && !aborted;
         float M0 = red_m[0][h0], M1 = red_m[0][h1];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) {
@@ -510,6 +542,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
                     add_scaled(h, 1.f, v);
                 }
+            }
+        }
+
+        if (tid == 0) seg_odd = 0;  // (everyone has read it: a barrier lies between)
+        if (odd) {
+            // the values of this stretch that are not finite, dims 8l..8l+7 in every warp
+            float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const int at = row.slot0() + wk.t0 * kTile;
+            const int end = row.slot0() + wk.t1 * kTile;
+            sum_nonfinite(P, wk.b, wk.g, at > row.lo ? at : row.lo, end < row.pos ? end : row.pos,
+                          warp, lane * 8, s);
+            consumer_bar();  // the heads' sums are read
+#pragma unroll
+            for (int j = 0; j < 8; ++j) red_o[warp * kHeadDim + lane * 8 + j] = s[j];
+            consumer_bar();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[j] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) s[j] += red_o[w * kHeadDim + lane * 8 + j];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    // (with scores of -inf alone the weights are zero in earnest)
+                    if (warp + i * kRedHeads < P.G && st[i].m != -INFINITY &&
+                        !isfinite(s[j]) && !isfinite(st[i].o[j]))
+                        st[i].o[j] = s[j];
             }
         }
 
@@ -594,6 +652,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             add_scaled(h, w, v);
                         }
                     }
+                    float any = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) any += h.o[j] * 0.f;
+                    if (isnan(any)) {
+                        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        for (int cta = c0; cta <= c1; ++cta) {
+                            const float4 *src = reinterpret_cast<const float4 *>(
+                                P.part_o + at(cta) * kHeadDim + lane * 8);
+                            const float4 a = __ldcg(src), c = __ldcg(src + 1);
+                            const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) s[j] += nonfinite_part(v[j]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (!isfinite(s[j])) h.o[j] = s[j];
+                    }
                 }
             }
         }
@@ -627,20 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float wo = h.m == -INFINITY ? 0.f : fast_exp2(h.m - z), wn = fast_exp2(x - z);
                 const float scale = gate_act(gate_now[i], P.gate_mode) / (h.l * wo + wn);
                 float y[8];
-                bool odd = false;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     y[j] = (h.o[j] * wo + v[j] * wn) * scale;
-                    odd = odd || isnan(y[j]);
-                }
-                if (odd && isfinite(scale) && h.m != -INFINITY) {
-                    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    sum_nonfinite(P, wk.b, wk.g, row.lo, row.pos, lane * 8, s);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (!isfinite(v[j])) s[j] += v[j];
-                        if (isnan(y[j]) && !isfinite(s[j])) y[j] = s[j] * scale;
-                    }
+                    const float s = nonfinite_part(h.o[j]) + nonfinite_part(v[j]);
+                    if (!isfinite(s)) y[j] = s * scale;
                 }
                 *reinterpret_cast<uint4 *>(
                     P.out + (static_cast<size_t>(wk.b) * P.H + head) * kHeadDim + lane * 8) =
