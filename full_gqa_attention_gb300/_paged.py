@@ -224,7 +224,7 @@ def spark_attn_decode_paged(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.Te
                             page_table: torch.Tensor, layer, out: torch.Tensor | None = None,
                             workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """One new token per row over its pages: qkv bf16 [B,(H+2Hkv)*256], gate
-    fp32 [B,H], pos int32 [B] (-1: idle row), pages bf16
+    fp32 [B,H], pos int32 [B] (-1: idle row; below 2^24 on layers that rotate), pages bf16
     [n_pages,Hkv,page_size,256] (updated in place), page_table int32
     [B,max_pages] -> out bf16 [B,H*256]."""
     dev = _device_of(qkv, "qkv")

@@ -65,7 +65,7 @@ __device__ __forceinline__ Row row_of(const PagedParams &P, int b) {
     r.pos = P.pos[b];
     r.lo = 0;
     r.tiles = 0;
-    if (r.pos < 0 || r.pos >= P.max_pages << P.page_shift) return r;
+    if (r.pos < 0 || r.pos >= P.pos_end) return r;
     if (P.kind == kLayerSliding && r.pos >= P.window) r.lo = r.pos - P.window + 1;
     const int n = (r.pos - r.slot0() + kTile - 1) / kTile;
     r.tiles = n > 0 ? n : 1;  // a row with nothing cached still has its new token
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long mine = 0;
     for (int b = b0; b < b0 + per && b < P.N; ++b) {
         const int p = P.pos[b];
-        if (blockIdx.x == 0 && (p < -1 || p >= P.max_pages << P.page_shift))
+        if (blockIdx.x == 0 && (p < -1 || p >= P.pos_end))
             atomicOr(P.status, kErrPosition);
         mine += row_of(P, b).units();
     }

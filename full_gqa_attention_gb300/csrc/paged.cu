@@ -721,6 +721,8 @@ spark_status spark_attn_decode_paged(const void *qkv, const float *gate, const i
     PagedParams P = make_params(qkv, gate, pos, desc, B, B, H, Hkv, out, workspace);
     set_pages(P, k_pages, v_pages, n_pages, page_size, page_table, max_pages);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    P.pos_end = max_pages << P.page_shift;
+    if (P.rope.rot_dim > 0 && P.pos_end > kRopePositions) P.pos_end = kRopePositions;
     P.counters = reinterpret_cast<unsigned *>(ws) + 1;
     P.part_ml = reinterpret_cast<float *>(ws + pl.ml);
     P.part_o = reinterpret_cast<float *>(ws + pl.o);

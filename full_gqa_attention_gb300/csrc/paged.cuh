@@ -34,8 +34,12 @@ struct PagedParams {
     int N, S, H, Hkv, G;
     int kind, window, gate_mode;
     int n_pages, page_shift, max_pages;
+    int pos_end;               // decode: positions end here (the table, the rotation)
     RopeTable rope;
 };
+
+// Positions that RoPE takes: fp32 holds them (rope_math.cuh).
+constexpr int kRopePositions = 1 << 24;
 
 // rope_cos_sin with the last rounding of the angle given back: the sum f + g of
 // the reduced angle's two parts (rope_math.cuh: rope_turns) is off by up to

@@ -98,8 +98,9 @@ typedef struct spark_layer_desc {
 } spark_layer_desc;
 
 /* Bits of the device status word in the workspace. */
-#define SPARK_DEVERR_POSITION 0x1u /* a decode position was negative or >= cap (FULL);
-                                      that sequence was skipped */
+#define SPARK_DEVERR_POSITION 0x1u /* a decode position was negative or >= cap (FULL), or
+                                      outside what a paged call takes; that sequence was
+                                      skipped */
 #define SPARK_DEVERR_TIMEOUT 0x2u  /* a bounded on-chip wait ran out; results are invalid */
 #define SPARK_DEVERR_SEQLENS 0x4u  /* packed offsets that decrease or leave [0, n_tokens];
                                       the sequences next to them were skipped */
@@ -450,8 +451,9 @@ spark_status spark_attn_prefill_paged(const void *qkv, const float *gate, const 
  *   gate  fp32 [B, H]
  *   pos   int32 [B]: position of the new token = tokens cached; -1 marks an
  *         idle row (nothing is read, its row of out stays as it was).  Other
- *         negative positions and pos >= max_pages * page_size: the row is
- *         skipped and SPARK_DEVERR_POSITION set.
+ *         negative positions, pos >= max_pages * page_size, and, on layers
+ *         that rotate (rot_dim > 0), pos >= 2^24, whose angles fp32 does not
+ *         hold: the row is skipped and SPARK_DEVERR_POSITION set.
  *   out   bf16 [B, H * 256]
  *   workspace  >= the size query's bytes, 256-byte aligned, zeroed once
  *         before first use (the counters in its first 256 bytes are left at 0
