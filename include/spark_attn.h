@@ -102,8 +102,9 @@ typedef struct spark_layer_desc {
                                       outside what a paged call takes; that sequence was
                                       skipped */
 #define SPARK_DEVERR_TIMEOUT 0x2u  /* a bounded on-chip wait ran out; results are invalid */
-#define SPARK_DEVERR_SEQLENS 0x4u  /* packed offsets that decrease or leave [0, n_tokens];
-                                      the sequences next to them were skipped */
+#define SPARK_DEVERR_SEQLENS 0x4u  /* packed offsets that decrease or leave [0, n_tokens]; a
+                                      sequence with such a pair of offsets was skipped, and
+                                      rows that several others then claim hold anything */
 #define SPARK_DEVERR_PAGE 0x8u     /* a page number outside the pool was met: read as zeros,
                                       never written */
 #define SPARK_DEVERR_ROW 0x10u     /* a page operation named a row that does not exist, forked
@@ -383,9 +384,10 @@ spark_status spark_attn_linear(const void *x, const void *w, void *y, int64_t M,
  *   k_pages, v_pages  bf16 [n_pages, Hkv, page_size, 256], one layer's pool;
  *               page_size 16, 32, 64, 128 or 256 (else SPARK_ERR_UNSUPPORTED),
  *               n_pages and max_pages at least 1 (else SPARK_ERR_CAPACITY).
- *               Pages of 32 and more are fastest.  A prompt's pool holds less than
- *               2^31 groups of 8 slots over all KV heads (8.8 TB of keys; else
- *               SPARK_ERR_UNSUPPORTED).
+ *               Pages of 32 and more are fastest.  A row's table holds less
+ *               than 2^30 tokens: max_pages < 2^30 / page_size.  A prompt's pool
+ *               holds less than 2^31 groups of 8 slots over all KV heads (8.8 TB
+ *               of keys).  Past either: SPARK_ERR_UNSUPPORTED.
  *   page_table  int32 [rows, max_pages] (device).  Entries that hold no token
  *               a call reads or writes may be anything (-1, say), among them
  *               those wholly behind the window of a SLIDING layer.  A page
@@ -410,7 +412,12 @@ spark_status spark_attn_linear(const void *x, const void *w, void *y, int64_t M,
  *   out   bf16 [n_tokens, H * 256]
  *   workspace  >= the size query's bytes, 256-byte aligned, zeroed once
  *         before first use; calls that may overlap need one each
- * The mask is applied on the token index inside the sequence.
+ * The mask is applied on the token index inside the sequence.  How the work is
+ * split depends on the whole batch, so a long sequence's result can differ in
+ * its last bits from the same sequence's in another batch; one call's results
+ * repeat bit for bit.
+ * Query tiles (of 128 / (H / Hkv) tokens, and one more per sequence) times Hkv
+ * stay below 2^31 (else SPARK_ERR_UNSUPPORTED).
  */
 size_t spark_attn_prefill_packed_workspace_size(int n_tokens, int S, int H, int Hkv,
                                                 const spark_layer_desc *desc);
@@ -483,6 +490,8 @@ typedef struct spark_page_pool {
     int32_t *len;             /* [n_rows]: tokens cached; the caller adds to it after a step */
     int32_t *refs;            /* [n_pages]: rows that hold the page */
     int32_t n_layers, Hkv, n_pages, page_size, n_rows, max_pages;
+                              /* n_pages < 2^29, max_pages < 2^30 / page_size (else
+                                 SPARK_ERR_UNSUPPORTED) */
 } spark_page_pool;
 
 /*
