@@ -115,7 +115,8 @@ inline bool decode_fuses_merge(int nsplit, long long B_times_Hkv, bool have_coun
 
 // What a packed prefill adds: sequences behind one another (B = 1, T = all
 // tokens in PrefillParams), and a list of query tiles that the kernel before
-// the attention kernel made of their offsets, longest first.
+// the attention kernel made of their offsets: longest first, or in no order
+// where all of them run at once.
 struct __align__(16) PackedItem {
     int seq;                   // its sequence, -1: no tile
     int t0;                    // its first token inside the sequence

@@ -30,7 +30,6 @@ namespace spark {
 
 namespace {
 
-constexpr int kMinShare = 1;                              // units a CTA takes at least
 constexpr int kPairCost = 3;                              // a pair's own units (Row::units)
 constexpr int kTile = 64;                                 // slots per stage
 constexpr int kStages = 3;
@@ -223,8 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         total += warp_sum[w];
     }
     total *= P.Hkv;
-    long long share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < kMinShare) share = kMinShare;
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
     Walk wk;
     wk.u = share * blockIdx.x;
     wk.end = wk.u + share < total ? wk.u + share : total;

@@ -49,8 +49,9 @@ __device__ __forceinline__ int prep_scan(int v, int *total) {
 
 // The list of query tiles, made by one CTA: every sequence is cut into tiles
 // of tq tokens, and the tiles are put in order of the key tiles they visit,
-// most first (a counting sort), so that the long ones do not start last.  The
-// order inside a bin is whatever the atomics give; no result depends on it.
+// most first (a counting sort), so that the long ones do not start last.  Tiles
+// that all run at once need no order and get none.  The order inside a bin is
+// whatever the atomics give; no result depends on it.
 //
 // A query tile that would outlast the others is split along its keys into
 // parts of L key tiles or fewer.  With no more query tiles than SMs, L is the
@@ -274,7 +275,6 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     // would come one lane after another)
     __shared__ __align__(16) float2 freq[kHeadDim / 2];
     grid_dep_wait();
-    grid_dep_launch();
     grid_dep_launch();
     if (blockIdx.x == 0) {
         plan_tiles(P);

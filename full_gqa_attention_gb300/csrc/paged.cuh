@@ -20,7 +20,7 @@ struct PagedParams {
     __nv_bfloat16 *krot;       // [Hkv, N, rot_w]: rotated leading key dims (packed prompts)
     int rot_w;
     int32_t *tile_base;        // [S + 1]: query tiles before each sequence
-    PackedItem *work;          // query tiles, longest first, and -1 behind them
+    PackedItem *work;          // query tiles (common.cuh: PackedItem), and -1 behind them
     int most;                  // places in the list
     int sms, slots;            // CTAs at a time, places for states of split tiles
     PackedItem *splits;        // common.cuh: PackedInfo
