@@ -145,8 +145,10 @@ __global__ void __launch_bounds__(kRowThreads) fork_apply_kernel(
 }
 
 // Both in one CTA, a warp per pair, where there are few table entries to write:
-// one launch less, against a CTA per pair for many.
-constexpr long long kForkSmall = 32768;
+// one launch less, against a CTA per pair for many (fork and free, in one CTA
+// and in two launches: 16 x 64 entries 9.9 and 11.0 us, 64 x 256 9.9 and 10.7,
+// 128 x 256 13.6 and 10.6, 256 x 256 23 and 10.6).
+constexpr long long kForkSmall = 16384;
 
 __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const __grid_constant__ PoolParams P,
                                                             const int32_t *src, const int32_t *dst,
