@@ -226,7 +226,11 @@ __device__ __forceinline__ uint32_t sw128_offset(int row, int gran) {
 }
 
 // RoPE of one query row held in shared memory (the 128-byte-swizzled Q tile),
-// for the pair groups of warpgroup `wg`.  The G lanes holding the G heads of
+// for the pair groups of warpgroup `wg`.  The rotated query is rounded to bf16
+// once: it is an operand of K's type.  Its angle may be off by 2e-7 rad
+// (rope_turns), which moves a query by a ten-thousandth of that rounding; keys
+// that are stored in pages take it finer (rope_cos_sin_fine), so that their
+// bits agree with 32-bit products.  The G lanes holding the G heads of
 // one token compute 8/G of the 8 angles of a group each and exchange them by
 // shuffles, so each angle is computed once per token.
 template <int G>
@@ -1179,6 +1183,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
             }
             const float neg = (m_run == -INFINITY) ? 0.f : -m_run * kScaleLog2;
+            // Probabilities are rounded to bf16 for P*V, an operand of V's type: with
+            // the output's own rounding the error against 64 bits is 2.1e-3 of the
+            // output instead of 1.7e-3.  A second term, as in decode, would double
+            // the products that bound this kernel.  Their sum stays in 32 bits.
             uint32_t pk[32];
             float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
