@@ -131,8 +131,8 @@ __device__ __forceinline__ float nonfinite_part(float x) { return isfinite(x) ? 
 // The sum of the values of the slots [lo, hi) of a pair that are not finite, over
 // this warp's share of them, for a lane's 8 dims (from d0).  Groups of 8 slots
 // (which lie in one page) are the warps' in turn: one table entry and 8 rows in
-// flight.  Rare, and bounded by the CTA's stretch, so that a call takes twice as
-// long at most: 108 us for a row of 120,000 tokens with one such value (75
+// flight.  Rare, and bounded by the CTA's stretch, so that a call takes about
+// twice as long: 108 us for a row of 120,000 tokens with one such value (75
 // without, and 61 ms where one warp walked the row), 0.42 ms for 262,139 tokens
 // with many (0.19 without).
 __device__ __noinline__ void sum_nonfinite(const PagedParams &P, int b, int g, int lo, int hi,
