@@ -41,10 +41,14 @@ for _name, _args, _res in (
         ("pages_fork", [_POOL, _P, _P, _i32, _P, _sz, _P], _i32),
         ("pages_reserve", [_POOL, _P, _P, _P, _sz, _P], _i32),
         ("pages_free", [_POOL, _P, _P, _i32, _P, _sz, _P], _i32),
-        ("pages_compact", [_POOL, _P, _P, _sz, _P], _i32)):
+        ("pages_compact", [_POOL, _P, _P, _sz, _P], _i32),
+        ("kv4_pages_reserve", [_POOL, _P, _P, _P, _sz, _P], _i32),
+        ("kv4_pages_compact", [_POOL, _P, _P, _sz, _P], _i32)):
     _f = getattr(lib, "spark_attn_" + _name)
     _f.argtypes, _f.restype = _args, _res
 
+
+KV4_TOKEN_BYTES = HEAD_DIM // 2 + HEAD_DIM // 16   # a key, or value, of a KV head in 4 bits
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
@@ -253,22 +257,26 @@ def spark_attn_decode_paged(qkv: torch.Tensor, gate: torch.Tensor, pos: torch.Te
 
 class PagePool:
     """A KV cache in pages and the tables behind it (spark_page_pool of the C
-    header): k_pages, v_pages bf16 [n_layers,n_pages,Hkv,page_size,256]; table
+    header): k_pages, v_pages bf16 [n_layers,n_pages,Hkv,page_size,256], or
+    uint8 [n_layers,n_pages,Hkv,page_size,144] (a cache in 4 bits); table
     int32 [n_rows,max_pages]; held, len int32 [n_rows]; refs int32 [n_pages].
     The tensors are the caller's and keep their storage; add to `len` in place
     after a step."""
 
-    __slots__ = ("k_pages", "v_pages", "table", "held", "len", "refs", "_dev", "_c", "_ref", "_rows")
+    __slots__ = ("k_pages", "v_pages", "table", "held", "len", "refs", "_dev", "_c", "_ref", "_rows",
+                 "_reserve", "_compact")
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
                  held: torch.Tensor, len: torch.Tensor, refs: torch.Tensor):
         dev = _device_of(k_pages, "k_pages")
-        _check(dev, (k_pages, _BF16, "k_pages"), (v_pages, _BF16, "v_pages"),
+        narrow = k_pages.dtype is _U8
+        dtype, width = (_U8, KV4_TOKEN_BYTES) if narrow else (_BF16, HEAD_DIM)
+        _check(dev, (k_pages, dtype, "k_pages"), (v_pages, dtype, "v_pages"),
                (table, _I32, "table"), (held, _I32, "held"), (len, _I32, "len"),
                (refs, _I32, "refs"))
-        if (k_pages.dim() != 5 or v_pages.shape != k_pages.shape
-                or k_pages.shape[4] != HEAD_DIM):
-            raise ValueError("k_pages and v_pages must be [n_layers, n_pages, Hkv, page_size, 256]")
+        if k_pages.dim() != 5 or v_pages.shape != k_pages.shape or k_pages.shape[4] != width:
+            raise ValueError("k_pages and v_pages must be "
+                             f"[n_layers, n_pages, Hkv, page_size, {width}]")
         n_layers, n_pages, Hkv, page_size, _ = k_pages.shape
         if (table.dim() != 2 or held.shape != table.shape[:1] or len.shape != held.shape
                 or refs.shape != (n_pages,)):
@@ -280,6 +288,8 @@ class PagePool:
                                   held.data_ptr(), len.data_ptr(), refs.data_ptr(), n_layers, Hkv,
                                   n_pages, page_size, table.shape[0], table.shape[1])
         self._ref = ctypes.byref(self._c)
+        self._reserve = lib.spark_attn_kv4_pages_reserve if narrow else lib.spark_attn_pages_reserve
+        self._compact = lib.spark_attn_kv4_pages_compact if narrow else lib.spark_attn_pages_compact
 
     def __setattr__(self, name, value):
         # `pool.len += add` keeps the storage; another tensor would leave the
@@ -291,13 +301,17 @@ class PagePool:
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, Hkv: int, page_size: int, n_rows: int,
-              max_pages: int, device=None) -> "PagePool":
-        """A fresh pool; the pages themselves are not initialised."""
+              max_pages: int, device=None, bits: int = 16) -> "PagePool":
+        """A fresh pool of bf16 (bits 16) or of 4 bits; the pages themselves are
+        not initialised."""
+        if bits not in (4, 16):
+            raise ValueError("bits must be 4 or 16")
         dev = torch.device(device or "cuda")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        shape = (n_layers, n_pages, Hkv, page_size, HEAD_DIM)
-        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+        shape = (n_layers, n_pages, Hkv, page_size, HEAD_DIM if bits == 16 else KV4_TOKEN_BYTES)
+        k, v = (torch.empty(shape, dtype=_BF16 if bits == 16 else _U8, device=dev)
+                for _ in range(2))
         i32 = dict(dtype=torch.int32, device=dev)
         return cls(k, v, torch.full((n_rows, max_pages), -1, **i32), torch.zeros(n_rows, **i32),
                    torch.zeros(n_rows, **i32), torch.zeros(n_pages, **i32))
@@ -358,7 +372,7 @@ def spark_attn_pages_reserve(pool: PagePool, add: torch.Tensor,
     taken: one int32, the pages taken, or -1 (and nothing changed) when the
     pool has too few."""
     _rows(pool, add, "add", pool._rows)
-    _pages_call("spark_attn_pages_reserve", lib.spark_attn_pages_reserve, pool,
+    _pages_call("spark_attn_pages_reserve", pool._reserve, pool,
                 (add.data_ptr(), _one(pool, taken, "taken")), workspace, stream)
 
 
@@ -377,5 +391,5 @@ def spark_attn_pages_compact(pool: PagePool, live: torch.Tensor | None = None,
                              workspace: torch.Tensor | None = None, stream=None) -> None:
     """Moves the pages in use to the lowest numbers.  live: one int32, the
     number of pages in use."""
-    _pages_call("spark_attn_pages_compact", lib.spark_attn_pages_compact, pool,
+    _pages_call("spark_attn_pages_compact", pool._compact, pool,
                 (_one(pool, live, "live"),), workspace, stream)

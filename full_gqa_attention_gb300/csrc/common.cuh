@@ -17,6 +17,10 @@ namespace spark {
 constexpr int kHeadDim = 256;
 constexpr int kMaxRopePairs = kHeadDim / 2;
 
+// Bytes of a token's key, or value, of one KV head in a cache in 4 bits: codes,
+// and a scale per 16 dims (kv4.cuh).
+constexpr int kKv4TokenBytes = kHeadDim / 2 + kHeadDim / 16;
+
 // log2(e) / sqrt(256): scores are kept in base-2 units, s * kScaleLog2.
 constexpr float kScaleLog2 = 1.4426950408889634f / 16.0f;
 

@@ -1,0 +1,514 @@
+// kv4.cu -- a cache in 4 bits: tokens quantised as they are stored, and read
+// back, and the host side of the calls on such a cache (format: kv4.cuh).
+//
+//   store  reads the K and V columns of the projections (1024 bytes per token
+//          and KV head), writes 288: HBM bounds it
+//   load   reads 288, writes 1024
+//
+// Both walk the groups of 16 slots that the call touches.  The groups of all
+// rows behind one another are a list, which the CTAs share out evenly; a warp
+// takes 4 tokens of a KV head's keys or values at a time, a lane 8 dims.
+#include <cmath>
+#include <cstring>
+
+#include "kv4.cuh"
+#include "spark_attn.h"
+
+namespace spark {
+
+void fill_rope_table(const spark_layer_desc *d, RopeTable *t);
+spark_status device_ready(int *sms);
+spark_status check_layer_desc(const spark_layer_desc *d, int H, int Hkv);
+bool aligned(const void *p, size_t a);
+int page_shift_of(int page_size);
+spark_status check_pages(const void *k_pages, const void *v_pages, int n_pages, int page_size,
+                         const int32_t *table, int max_pages);
+cudaError_t launch_decode_kv4(const Kv4Params &P, int grid, cudaStream_t stream);
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// A CTA's stretch [u, end) of a list of units, row behind row, and the row that
+// unit u belongs to (whose first unit is base).
+struct Stretch {
+    long long u, end, base;
+    int r;
+};
+
+// units(r, report): units of row r; report: the one place to note a fault of it.
+// False where nothing is left for this CTA.  All threads.
+template <typename Units>
+__device__ __forceinline__ bool stretch_of(int S, Units &&units, Stretch &st) {
+    __shared__ long long sums[kWarps];
+    __shared__ long long s_base;
+    __shared__ int s_row;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (S + kThreads - 1) / kThreads;
+    const int r0 = tid * per;
+    long long mine = 0;
+    for (int r = r0; r < r0 + per && r < S; ++r) mine += units(r, blockIdx.x == 0);
+    long long before = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += y;
+    }
+    if (lane == 31) sums[warp] = before;
+    before -= mine;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    st.u = share * blockIdx.x;
+    st.end = st.u + share < total ? st.u + share : total;
+    if (st.u >= st.end) return false;
+    if (st.u >= before && st.u < before + mine) {
+        int r = r0;
+        long long base = before;
+        for (; r + 1 < S; ++r) {
+            const long long n = units(r, false);
+            if (st.u < base + n) break;
+            base += n;
+        }
+        s_row = r;
+        s_base = base;
+    }
+    __syncthreads();
+    st.r = s_row;
+    st.base = s_base;
+    return true;
+}
+
+// Groups of 16 slots that tokens [a, b) touch.
+__device__ __forceinline__ int groups_of(int a, int b) {
+    return a < b ? ((b + kKv4Group - 1) >> 4) - (a >> 4) : 0;
+}
+
+// ---------------------------------------------------------------- store
+
+// Tokens of sequence r: [a, b) of its slots, its first packed row.
+struct StoreRow {
+    int a, b, row;
+};
+
+__device__ __forceinline__ StoreRow store_row(const Kv4Params &P, int r, bool report) {
+    StoreRow s{0, 0, 0};
+    const int c0 = P.cu[r], c1 = P.cu[r + 1];
+    if (c0 < 0 || c1 < c0 || c1 > P.N) {
+        if (report) atomicOr(P.status, kErrSeqlens);
+        return s;
+    }
+    if (c1 == c0) return s;
+    const int start = P.begin[r];
+    const int slots = P.pg.max_pages << P.pg.page_shift;
+    if (start < 0 || start > slots - (c1 - c0)) {
+        if (report) atomicOr(P.status, kErrPosition);
+        return s;
+    }
+    return StoreRow{start, start + (c1 - c0), c0};
+}
+
+__global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_constant__ Kv4Params P) {
+    __shared__ float2 freq[kMaxRopePairs];
+    __shared__ float2 cs[kKv4Group][kMaxRopePairs];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int half = P.rope.rot_dim / 2;
+    if (tid < half) freq[tid] = P.rope.u[tid];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int parts = (P.Hkv + P.heads - 1) / P.heads;
+    auto units = [&](int r, bool report) {
+        const StoreRow s = store_row(P, r, report);
+        return static_cast<long long>(groups_of(s.a, s.b)) * parts;
+    };
+    Stretch st;
+    if (!stretch_of(P.S, units, st)) return;
+    const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
+    StoreRow row = store_row(P, st.r, false);
+    for (; st.u < st.end; ++st.u) {
+        while (st.u >= st.base + static_cast<long long>(groups_of(row.a, row.b)) * parts) {
+            st.base += static_cast<long long>(groups_of(row.a, row.b)) * parts;
+            if (++st.r >= P.S) return;  // the offsets changed under the call
+            row = store_row(P, st.r, false);
+        }
+        const int at = static_cast<int>(st.u - st.base);
+        const int slot0 = ((row.a >> 4) + at / parts) << 4;
+        const int h0 = at % parts * P.heads;
+        const int heads = P.Hkv - h0 < P.heads ? P.Hkv - h0 : P.heads;
+        const int t_lo = row.a > slot0 ? row.a - slot0 : 0;
+        const int t_hi = row.b - slot0 < kKv4Group ? row.b - slot0 : kKv4Group;
+        const int first = row.row + (slot0 - row.a);  // packed row of slot 0 of the group
+        const int id = P.pg.table[static_cast<size_t>(st.r) * P.pg.max_pages +
+                                  (slot0 >> P.pg.page_shift)];
+        if (id < 0 || id >= P.pg.n_pages) {
+            if (tid == 0) atomicOr(P.status, kErrPage);
+            continue;
+        }
+        __syncthreads();  // (the angles of the unit before are read)
+        for (int i = tid; i < (t_hi - t_lo) * half; i += kThreads) {
+            const int t = t_lo + i / half, k = i % half;
+            float2 c;
+            rope_cos_sin_fine(P.pos[first + t], freq[k], c.x, c.y);
+            cs[t][k] = c;
+        }
+        __syncthreads();
+        for (int task = warp; task < heads * 8; task += kWarps) {
+            const int h = h0 + (task >> 3), quad = task & 3;
+            const bool key = !(task & 4);
+            uint4 raw[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = 4 * quad + j;
+                raw[j] = make_uint4(0, 0, 0, 0);
+                if (t >= t_lo && t < t_hi)
+                    raw[j] = __ldcs(reinterpret_cast<const uint4 *>(
+                        P.qkv + (first + t) * width +
+                        static_cast<size_t>(P.H + (key ? 0 : P.Hkv) + h) * kHeadDim + lane * 8));
+            }
+            uint8_t *group = (key ? P.pg.k : P.pg.v) + P.pg.group(id, h, P.Hkv, slot0);
+            if (key) {
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    const int t = 4 * quad + j;
+                    if (t < t_lo || t >= t_hi) continue;
+                    const uint4 x = j == 0 ? raw[0] : j == 1 ? raw[1] : j == 2 ? raw[2] : raw[3];
+                    const int pos = half ? P.pos[first + t] : 0;
+                    const KeyTurn turn = kv4_key_turn(x, P.rope.rot_dim, pos, lane);
+                    float y[8];
+                    uint32_t codes;
+                    unsigned byte;
+                    kv4_key_row(turn, cs[t], pos, P.turns, y, codes, byte);
+                    *reinterpret_cast<uint32_t *>(group + kv4_key_at(lane, t)) = codes;
+                    if (!(lane & 1))
+                        group[kv4_key_scale_at(lane >> 1, t)] = static_cast<uint8_t>(byte);
+                }
+            } else {
+                uint32_t codes[4];
+                unsigned scales = 0, keep = 0;  // keep: of the group's slots, as masks
+                uint32_t mask = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = 4 * quad + j;
+                    unsigned byte;
+                    kv4_value_row(raw[j], codes[j], byte);
+                    scales |= byte << (8 * (2 * (j & 1) + (j >> 1)));
+                    if (t < t_lo || t >= t_hi) {
+                        keep |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
+                        mask |= (j & 1 ? 0xf0f0u : 0x0f0fu) << (16 * (j >> 1));
+                    }
+                }
+                if (mask == 0xffffffffu) continue;
+                // dims 2 i, 2 i + 1 of slots 0 and 1, then of 2 and 3
+                uint32_t e[2], o[2];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const uint32_t a = codes[2 * p], b = codes[2 * p + 1];
+                    e[p] = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
+                    o[p] = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+                }
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = __byte_perm(e[0], o[0], i | (i + 4) << 4);
+                    const uint32_t hi = __byte_perm(e[1], o[1], i | (i + 4) << 4);
+                    w[i] = __byte_perm(lo, hi, 0x5410);
+                }
+                uint4 *dst = reinterpret_cast<uint4 *>(group + kv4_value_at(lane, quad));
+                uint32_t *sdst = reinterpret_cast<uint32_t *>(
+                    group + kv4_value_scale_at(lane >> 1, quad));
+                if (mask) {  // slots beside the call's keep what they hold
+                    const uint4 old = *dst;
+                    w[0] = (w[0] & ~mask) | (old.x & mask);
+                    w[1] = (w[1] & ~mask) | (old.y & mask);
+                    w[2] = (w[2] & ~mask) | (old.z & mask);
+                    w[3] = (w[3] & ~mask) | (old.w & mask);
+                    scales = (scales & ~keep) | (*sdst & keep);
+                }
+                *dst = make_uint4(w[0], w[1], w[2], w[3]);
+                if (!(lane & 1)) *sdst = scales;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- load
+
+struct LoadRow {
+    int a, b;
+};
+
+__device__ __forceinline__ LoadRow load_row(const Kv4Params &P, int r, bool report) {
+    const int a = P.begin[r], b = P.end[r];
+    if (a == b) return LoadRow{0, 0};
+    const int from = P.pg.max_pages << P.pg.page_shift, to = P.to_max_pages << P.to_page_shift;
+    if (a < 0 || b < a || b > from || b > to) {
+        if (report) atomicOr(P.status, kErrPosition);
+        return LoadRow{0, 0};
+    }
+    return LoadRow{a, b};
+}
+
+// Codes of dims 8 l .. and their scale as 8 bf16 (exact).
+__device__ __forceinline__ uint4 kv4_to_bf16(uint32_t codes, unsigned byte) {
+    uint32_t h[4], w[4];
+    kv4_widen(codes, h);
+    const float s = kv4_scale(byte);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        w[i] = pack_bf16x2(f.x * s, f.y * s);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constant__ Kv4Params P) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dep_wait();
+    grid_dep_launch();
+    auto units = [&](int r, bool report) {
+        const LoadRow s = load_row(P, r, report);
+        return static_cast<long long>(groups_of(s.a, s.b));
+    };
+    Stretch st;
+    if (!stretch_of(P.S, units, st)) return;
+    LoadRow row = load_row(P, st.r, false);
+    for (; st.u < st.end; ++st.u) {
+        while (st.u >= st.base + groups_of(row.a, row.b)) {
+            st.base += groups_of(row.a, row.b);
+            if (++st.r >= P.S) return;  // the ranges changed under the call
+            row = load_row(P, st.r, false);
+        }
+        const int slot0 = ((row.a >> 4) + static_cast<int>(st.u - st.base)) << 4;
+        const int t_lo = row.a > slot0 ? row.a - slot0 : 0;
+        const int t_hi = row.b - slot0 < kKv4Group ? row.b - slot0 : kKv4Group;
+        const int id = P.pg.table[static_cast<size_t>(st.r) * P.pg.max_pages +
+                                  (slot0 >> P.pg.page_shift)];
+        const int to = P.to_table[static_cast<size_t>(st.r) * P.to_max_pages +
+                                  (slot0 >> P.to_page_shift)];
+        const bool held = id >= 0 && id < P.pg.n_pages;
+        if (!held || to < 0 || to >= P.to_n_pages) {
+            if (tid == 0) atomicOr(P.status, kErrPage);
+            if (to < 0 || to >= P.to_n_pages) continue;
+        }
+        for (int task = warp; task < P.Hkv * 8; task += kWarps) {
+            const int h = task >> 3, quad = task & 3;
+            const bool key = !(task & 4);
+            uint32_t codes[4] = {0, 0, 0, 0};
+            unsigned bytes = 0;  // of slots 4 quad .., in order
+            if (held) {
+                const uint8_t *group = (key ? P.pg.k : P.pg.v) + P.pg.group(id, h, P.Hkv, slot0);
+                if (key) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = 4 * quad + j;
+                        codes[j] = __ldcs(
+                            reinterpret_cast<const uint32_t *>(group + kv4_key_at(lane, t)));
+                        bytes |= static_cast<unsigned>(
+                                     __ldcs(group + kv4_key_scale_at(lane >> 1, t)))
+                                 << (8 * j);
+                    }
+                } else {
+                    const uint4 w =
+                        __ldcs(reinterpret_cast<const uint4 *>(group + kv4_value_at(lane, quad)));
+                    bytes = __byte_perm(__ldcs(reinterpret_cast<const unsigned *>(
+                                            group + kv4_value_scale_at(lane >> 1, quad))),
+                                        0, 0x3120);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) codes[j] = kv4_value_codes(w, j);
+                }
+            }
+            __nv_bfloat16 *dst =
+                (key ? P.k_pages : P.v_pages) +
+                (((static_cast<size_t>(to) * P.Hkv + h) << P.to_page_shift) +
+                 (slot0 & ((1 << P.to_page_shift) - 1))) * kHeadDim + lane * 8;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = 4 * quad + j;
+                if (t >= t_lo && t < t_hi)
+                    *reinterpret_cast<uint4 *>(dst + t * kHeadDim) =
+                        kv4_to_bf16(codes[j], bytes >> (8 * j) & 255u);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+spark_status done(cudaError_t e) {
+    if (e == cudaSuccess) return SPARK_OK;
+    cudaGetLastError();
+    return SPARK_ERR_CUDA;
+}
+
+void set_layer(Kv4Params &P, const spark_layer_desc *desc, int H, int Hkv) {
+    P.H = H;
+    P.Hkv = Hkv;
+    P.G = H / Hkv;
+    P.kind = desc->kind;
+    constexpr int kMostWindow = 1 << 30;  // (positions stay below it)
+    P.window = desc->kind != SPARK_LAYER_SLIDING ? 0
+               : desc->window < kMostWindow     ? desc->window
+                                                : kMostWindow;
+    P.gate_mode = desc->gate_mode;
+    fill_rope_table(desc, &P.rope);
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int k = 0; k < desc->rot_dim / 2; ++k)
+        P.turns[k] = std::pow(desc->rope_theta, -2.0 * k / desc->rot_dim) / two_pi;
+}
+
+void set_pages(Kv4Params &P, void *k4, void *v4, int n_pages, int page_size, const int32_t *table,
+               int max_pages) {
+    P.pg.k = static_cast<uint8_t *>(k4);
+    P.pg.v = static_cast<uint8_t *>(v4);
+    P.pg.table = table;
+    P.pg.n_pages = n_pages;
+    P.pg.page_shift = page_shift_of(page_size);
+    P.pg.max_pages = max_pages;
+}
+
+struct DecodeKv4Plan {
+    int grid;
+    size_t bytes;
+};
+
+DecodeKv4Plan plan_decode_kv4(int, int, int) { return DecodeKv4Plan{0, kWorkspaceHeader}; }
+
+}  // namespace
+}  // namespace spark
+
+using namespace spark;
+
+extern "C" {
+
+size_t spark_attn_kv4_store_workspace_size(int n_tokens, int S, int H, int Hkv,
+                                           const spark_layer_desc *desc) {
+    if (check_layer_desc(desc, H, Hkv) != SPARK_OK || n_tokens < 0 || S < 0) return 0;
+    return kWorkspaceHeader;
+}
+
+spark_status spark_attn_kv4_store(const void *qkv, const int32_t *pos, const int32_t *cu_seqlens,
+                                  const int32_t *start, void *k4_pages, void *v4_pages, int n_pages,
+                                  int page_size, const int32_t *page_table, int max_pages,
+                                  const spark_layer_desc *desc, int n_tokens, int S, int H,
+                                  int Hkv, void *workspace, size_t workspace_bytes, void *stream) {
+    spark_status st = check_layer_desc(desc, H, Hkv);
+    if (st != SPARK_OK) return st;
+    if (n_tokens < 0 || S < 0) return SPARK_ERR_SHAPE;
+    if (n_tokens == 0 || S == 0) return SPARK_OK;
+    if (!qkv || !pos || !cu_seqlens || !start || !workspace) return SPARK_ERR_NULL;
+    if (!aligned(qkv, 16) || !aligned(pos, 4) || !aligned(cu_seqlens, 4) || !aligned(start, 4) ||
+        !aligned(workspace, 256))
+        return SPARK_ERR_ALIGN;
+    st = check_pages(k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
+    if (st != SPARK_OK) return st;
+    if (workspace_bytes < kWorkspaceHeader) return SPARK_ERR_WORKSPACE;
+    int sms;
+    st = device_ready(&sms);
+    if (st != SPARK_OK) return st;
+    Kv4Params P;
+    std::memset(&P, 0, sizeof(P));
+    P.qkv = static_cast<const __nv_bfloat16 *>(qkv);
+    P.pos = pos;
+    P.cu = cu_seqlens;
+    P.begin = start;
+    P.N = n_tokens;
+    P.S = S;
+    P.status = static_cast<unsigned *>(workspace);
+    set_layer(P, desc, H, Hkv);
+    set_pages(P, k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
+    P.heads = Hkv;
+    return done(launch_overlapped(kv4_store_kernel, dim3(sms * 4), dim3(kThreads), 0,
+                                  static_cast<cudaStream_t>(stream), P));
+}
+
+size_t spark_attn_kv4_load_workspace_size(int S, int Hkv) {
+    if (S < 0 || Hkv < 1) return 0;
+    return kWorkspaceHeader;
+}
+
+spark_status spark_attn_kv4_load(const void *k4_pages, const void *v4_pages, int n_pages,
+                                 int page_size, const int32_t *page_table, int max_pages,
+                                 const int32_t *begin, const int32_t *end, void *k_pages,
+                                 void *v_pages, int to_n_pages, int to_page_size,
+                                 const int32_t *to_page_table, int to_max_pages, int S, int Hkv,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (S < 0 || Hkv < 1) return SPARK_ERR_SHAPE;
+    if (S == 0) return SPARK_OK;
+    if (!begin || !end || !workspace) return SPARK_ERR_NULL;
+    if (!aligned(begin, 4) || !aligned(end, 4) || !aligned(workspace, 256)) return SPARK_ERR_ALIGN;
+    spark_status st = check_pages(k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
+    if (st != SPARK_OK) return st;
+    st = check_pages(k_pages, v_pages, to_n_pages, to_page_size, to_page_table, to_max_pages);
+    if (st != SPARK_OK) return st;
+    if (workspace_bytes < kWorkspaceHeader) return SPARK_ERR_WORKSPACE;
+    int sms;
+    st = device_ready(&sms);
+    if (st != SPARK_OK) return st;
+    Kv4Params P;
+    std::memset(&P, 0, sizeof(P));
+    P.begin = begin;
+    P.end = end;
+    P.S = S;
+    P.Hkv = Hkv;
+    P.status = static_cast<unsigned *>(workspace);
+    set_pages(P, const_cast<void *>(k4_pages), const_cast<void *>(v4_pages), n_pages, page_size,
+              page_table, max_pages);
+    P.k_pages = static_cast<__nv_bfloat16 *>(k_pages);
+    P.v_pages = static_cast<__nv_bfloat16 *>(v_pages);
+    P.to_table = to_page_table;
+    P.to_n_pages = to_n_pages;
+    P.to_page_shift = page_shift_of(to_page_size);
+    P.to_max_pages = to_max_pages;
+    return done(launch_overlapped(kv4_load_kernel, dim3(sms * 4), dim3(kThreads), 0,
+                                  static_cast<cudaStream_t>(stream), P));
+}
+
+size_t spark_attn_decode_kv4_workspace_size(int B, int H, int Hkv, const spark_layer_desc *desc) {
+    if (check_layer_desc(desc, H, Hkv) != SPARK_OK || B < 0) return 0;
+    int sms;
+    device_ready(&sms);
+    return plan_decode_kv4(H, Hkv, sms).bytes;
+}
+
+spark_status spark_attn_decode_kv4(const void *qkv, const float *gate, const int32_t *pos,
+                                   void *k4_pages, void *v4_pages, int n_pages, int page_size,
+                                   const int32_t *page_table, int max_pages,
+                                   const spark_layer_desc *desc, int B, int H, int Hkv, void *out,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+    spark_status st = check_layer_desc(desc, H, Hkv);
+    if (st != SPARK_OK) return st;
+    if (B < 0) return SPARK_ERR_SHAPE;
+    if (B == 0) return SPARK_OK;
+    if (!qkv || !gate || !pos || !out || !workspace) return SPARK_ERR_NULL;
+    if (!aligned(qkv, 16) || !aligned(out, 16) || !aligned(gate, 4) || !aligned(pos, 4) ||
+        !aligned(workspace, 256))
+        return SPARK_ERR_ALIGN;
+    st = check_pages(k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
+    if (st != SPARK_OK) return st;
+    int sms;
+    const spark_status ready = device_ready(&sms);
+    const DecodeKv4Plan pl = plan_decode_kv4(H, Hkv, sms);
+    if (workspace_bytes < pl.bytes) return SPARK_ERR_WORKSPACE;
+    if (ready != SPARK_OK) return ready;
+    Kv4Params P;
+    std::memset(&P, 0, sizeof(P));
+    P.qkv = static_cast<const __nv_bfloat16 *>(qkv);
+    P.gate = gate;
+    P.pos = pos;
+    P.out = static_cast<__nv_bfloat16 *>(out);
+    P.N = P.S = B;
+    P.status = static_cast<unsigned *>(workspace);
+    set_layer(P, desc, H, Hkv);
+    set_pages(P, k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
+    P.pos_end = max_pages << P.pg.page_shift;
+    if (P.rope.rot_dim > 0 && P.pos_end > kRopePositions) P.pos_end = kRopePositions;
+    return done(launch_decode_kv4(P, pl.grid, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

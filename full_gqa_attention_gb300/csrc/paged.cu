@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(
     if (hit & 0x80008000u) atomicOr(&P.odd_values[*P.call & 1], 1u);
 }
 
+}  // namespace
+
 // ---------------------------------------------------------------- host side
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -405,6 +407,8 @@ spark_status check_pages(const void *k_pages, const void *v_pages, int n_pages, 
         return SPARK_ERR_ALIGN;
     return SPARK_OK;
 }
+
+namespace {
 
 spark_status check_packed(int n_tokens, int S, int H, int Hkv, const spark_layer_desc *desc) {
     const spark_status st = check_layer_desc(desc, H, Hkv);

@@ -508,7 +508,9 @@ spark_status check_pool(const spark_page_pool *pool, const void *workspace,
     return SPARK_OK;
 }
 
-PoolParams pool_params(const spark_page_pool *pool, void *workspace) {
+// token_bytes: of a token's key, or value, of one KV head.
+PoolParams pool_params(const spark_page_pool *pool, void *workspace,
+                       int token_bytes = kHeadDim * 2) {
     const PoolPlan pl = plan_pool(pool);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const size_t rows = up256(static_cast<size_t>(pool->n_rows > 0 ? pool->n_rows : 1) * 4);
@@ -524,7 +526,7 @@ PoolParams pool_params(const spark_page_pool *pool, void *workspace) {
     P.page_size = pool->page_size;
     P.n_rows = pool->n_rows;
     P.max_pages = pool->max_pages;
-    P.page_bytes = static_cast<long long>(pool->Hkv) * pool->page_size * kHeadDim * 2;
+    P.page_bytes = static_cast<long long>(pool->Hkv) * pool->page_size * token_bytes;
     P.status = reinterpret_cast<unsigned *>(ws);
     P.n_copies = reinterpret_cast<int32_t *>(ws + pl.counts);
     P.n_live = P.n_copies + 1;
@@ -558,6 +560,44 @@ cudaError_t launch_copies(const PoolParams &P, long long most, int sms, cudaStre
 
 // spark_attn.cu
 spark_status device_ready(int *sms);
+
+namespace {
+
+spark_status reserve(const spark_page_pool *pool, const int32_t *add, int32_t *taken,
+                     void *workspace, size_t workspace_bytes, void *stream, int token_bytes) {
+    spark_status st = check_pool(pool, workspace, workspace_bytes);
+    if (st != SPARK_OK) return st;
+    if (pool->n_rows > 0 && !add) return SPARK_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(add) % 4 || reinterpret_cast<uintptr_t>(taken) % 4)
+        return SPARK_ERR_ALIGN;
+    int sms;
+    st = device_ready(&sms);
+    if (st != SPARK_OK) return st;
+    const PoolParams P = pool_params(pool, workspace, token_bytes);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = done(launch_overlapped(reserve_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, P, add,
+                                taken));
+    const long long most = pool->n_rows < pool->n_pages ? pool->n_rows : pool->n_pages;
+    if (st != SPARK_OK || most == 0) return st;
+    return done(launch_copies<false>(P, most, sms, s));
+}
+
+spark_status compact(const spark_page_pool *pool, int32_t *live, void *workspace,
+                     size_t workspace_bytes, void *stream, int token_bytes) {
+    spark_status st = check_pool(pool, workspace, workspace_bytes);
+    if (st != SPARK_OK) return st;
+    if (reinterpret_cast<uintptr_t>(live) % 4) return SPARK_ERR_ALIGN;
+    int sms;
+    st = device_ready(&sms);
+    if (st != SPARK_OK) return st;
+    const PoolParams P = pool_params(pool, workspace, token_bytes);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = done(launch_overlapped(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, P, live));
+    if (st != SPARK_OK || pool->n_rows == 0 || pool->n_pages == 0) return st;
+    return done(launch_copies<true>(P, pool->n_pages / 2 + 1, sms, s));
+}
+
+}  // namespace
 
 }  // namespace spark
 
@@ -598,21 +638,13 @@ spark_status spark_attn_pages_fork(const spark_page_pool *pool, const int32_t *s
 spark_status spark_attn_pages_reserve(const spark_page_pool *pool, const int32_t *add,
                                       int32_t *taken, void *workspace, size_t workspace_bytes,
                                       void *stream) {
-    spark_status st = check_pool(pool, workspace, workspace_bytes);
-    if (st != SPARK_OK) return st;
-    if (pool->n_rows > 0 && !add) return SPARK_ERR_NULL;
-    if (reinterpret_cast<uintptr_t>(add) % 4 || reinterpret_cast<uintptr_t>(taken) % 4)
-        return SPARK_ERR_ALIGN;
-    int sms;
-    st = device_ready(&sms);
-    if (st != SPARK_OK) return st;
-    const PoolParams P = pool_params(pool, workspace);
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = done(launch_overlapped(reserve_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, P, add,
-                                taken));
-    const long long most = pool->n_rows < pool->n_pages ? pool->n_rows : pool->n_pages;
-    if (st != SPARK_OK || most == 0) return st;
-    return done(launch_copies<false>(P, most, sms, s));
+    return reserve(pool, add, taken, workspace, workspace_bytes, stream, kHeadDim * 2);
+}
+
+spark_status spark_attn_kv4_pages_reserve(const spark_page_pool *pool, const int32_t *add,
+                                          int32_t *taken, void *workspace, size_t workspace_bytes,
+                                          void *stream) {
+    return reserve(pool, add, taken, workspace, workspace_bytes, stream, kKv4TokenBytes);
 }
 
 spark_status spark_attn_pages_free(const spark_page_pool *pool, const int32_t *rows,
@@ -635,17 +667,12 @@ spark_status spark_attn_pages_free(const spark_page_pool *pool, const int32_t *r
 
 spark_status spark_attn_pages_compact(const spark_page_pool *pool, int32_t *live, void *workspace,
                                       size_t workspace_bytes, void *stream) {
-    spark_status st = check_pool(pool, workspace, workspace_bytes);
-    if (st != SPARK_OK) return st;
-    if (reinterpret_cast<uintptr_t>(live) % 4) return SPARK_ERR_ALIGN;
-    int sms;
-    st = device_ready(&sms);
-    if (st != SPARK_OK) return st;
-    const PoolParams P = pool_params(pool, workspace);
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = done(launch_overlapped(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, P, live));
-    if (st != SPARK_OK || pool->n_rows == 0 || pool->n_pages == 0) return st;
-    return done(launch_copies<true>(P, pool->n_pages / 2 + 1, sms, s));
+    return compact(pool, live, workspace, workspace_bytes, stream, kHeadDim * 2);
+}
+
+spark_status spark_attn_kv4_pages_compact(const spark_page_pool *pool, int32_t *live,
+                                          void *workspace, size_t workspace_bytes, void *stream) {
+    return compact(pool, live, workspace, workspace_bytes, stream, kKv4TokenBytes);
 }
 
 }  // extern "C"

@@ -543,6 +543,124 @@ spark_status spark_attn_pages_compact(const spark_page_pool *pool, int32_t *live
                                       size_t workspace_bytes, void *stream);
 
 /*
+ * A cache in 4 bits.
+ *
+ * The decode step of a long context is bound by the bytes of its cache.  Here
+ * a token's key (rotated) and value take 144 bytes per KV head instead of 512:
+ * of every 16 dims x a scale s and 16 numbers c, read as c * s, with
+ *     s = max |x| / 6, rounded to 5 bits of exponent (bias 15) and 3 of mantissa
+ *         without a sign (subnormal ones too), 10240 at most;
+ *     c = x / s, rounded to one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *         negatives (codes 0 .. 7, a set upper bit being the sign; larger
+ *         quotients become 6 or -6; 0 where s is 0).
+ * Both round to nearest, ties to the even code, and what is stored is the
+ * nearest to the exact key or value: a key is not rounded after its rotation.
+ * So values hold to about a tenth of their size, those below 2^-18 * 6 in all
+ * of a block become zeros, and those beyond 61440 become 61440.  A block with a
+ * value that is not finite is stored with the scale's byte 0xff and reads as
+ * NaN.  Every c * s is a bf16 number.
+ *
+ *   k4_pages, v4_pages  [n_pages, Hkv, page_size, 144] bytes, one layer's pool;
+ *               page sizes, tables and limits as for the paged calls above.  A
+ *               page of a KV head is its slots in groups of 16, 2304 bytes each:
+ *               2048 bytes of codes, then 256 of scales.
+ *       key, slot t of the group:
+ *           dims d, d + 1 (d even; d in the low half): byte
+ *               1024 * (d / 128) + 64 * t + d % 128 / 2
+ *           the scale of dims 16 b ..: byte
+ *               2048 + 16 * t + 4 * (b / 2 % 4) + 2 * (b / 8) + b % 2
+ *       value, slots t, t + 1 (t even; t in the low half):
+ *           dim d: byte
+ *               512 * (d / 8 % 4) + 64 * (d / 32) + 16 * (t / 4) + 4 * (d / 2 % 4)
+ *               + 2 * (t / 2 % 2) + d % 2
+ *           the scale of dims 16 b .. of slot t: byte
+ *               2048 + 32 * (b / 2) + 8 * (t / 4) + 4 * (b % 2) + 2 * (t % 2) + t / 2 % 2
+ *
+ * Cached tokens take part in attention as they are held; the tokens that a call
+ * brings itself take part as they are, and are held in 4 bits from then on.  A
+ * prompt behind cached tokens: read them back (spark_attn_kv4_load) into pages
+ * of bf16, call spark_attn_prefill_paged there, and store the new tokens
+ * (spark_attn_kv4_store); a first prompt: spark_attn_prefill_packed and store.
+ */
+
+/*
+ * Stores the keys (rotated) and values of packed prompts, or chunks of them,
+ * in 4 bits: token t of sequence s goes to slot start[s] + t of its row.
+ *
+ *   qkv, pos, cu_seqlens, start, page_table  as for spark_attn_prefill_paged
+ *         (the query heads are not read)
+ *   workspace  >= the size query's bytes, 256-byte aligned, zeroed once before
+ *         first use: its status word
+ * Slots beside the call's keep what they hold.  A sequence with offsets that
+ * decrease or leave [0, n_tokens] is skipped and SPARK_DEVERR_SEQLENS set; one
+ * with start < 0 or start + length > max_pages * page_size is skipped and
+ * SPARK_DEVERR_POSITION set; tokens whose page is not in the pool are not
+ * stored and SPARK_DEVERR_PAGE set.
+ */
+size_t spark_attn_kv4_store_workspace_size(int n_tokens, int S, int H, int Hkv,
+                                           const spark_layer_desc *desc);
+
+spark_status spark_attn_kv4_store(const void *qkv, const int32_t *pos, const int32_t *cu_seqlens,
+                                  const int32_t *start, void *k4_pages, void *v4_pages,
+                                  int n_pages, int page_size, const int32_t *page_table,
+                                  int max_pages, const spark_layer_desc *desc, int n_tokens, int S,
+                                  int H, int Hkv, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/*
+ * Reads tokens begin[r] .. end[r] - 1 of every row r back into pages of bf16,
+ * each at its own index: token j to slot j % to_page_size of page
+ * to_page_table[r][j / to_page_size].  The values are exact.
+ *
+ *   begin, end  int32 [S] (device); begin == end: an idle row.  A row with
+ *         begin < 0, end < begin or end past either table is skipped and
+ *         SPARK_DEVERR_POSITION set.
+ *   k_pages, v_pages, to_page_table  as for spark_attn_prefill_paged; no two
+ *         rows may write the same slot
+ *   workspace  as for spark_attn_kv4_store
+ * Slots beside the rows' tokens stay as they are.  Pages outside the pool:
+ * SPARK_DEVERR_PAGE, read as zeros, never written.
+ */
+size_t spark_attn_kv4_load_workspace_size(int S, int Hkv);
+
+spark_status spark_attn_kv4_load(const void *k4_pages, const void *v4_pages, int n_pages,
+                                 int page_size, const int32_t *page_table, int max_pages,
+                                 const int32_t *begin, const int32_t *end, void *k_pages,
+                                 void *v_pages, int to_n_pages, int to_page_size,
+                                 const int32_t *to_page_table, int to_max_pages, int S, int Hkv,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One new token per row over a cache in 4 bits: what spark_attn_decode_paged
+ * computes, with the same arguments (pos -1: an idle row) and its own workspace
+ * size.  The new token's key and value are stored in 4 bits in slot pos[b].
+ * Queries, probabilities and the new token are not rounded to bf16: cached keys
+ * and values are exact halves, and each query and probability enters the
+ * products as a sum of two halves (H / Hkv of 8: as one, 11 bits).  A query
+ * that is not finite makes its head's output NaN.
+ */
+size_t spark_attn_decode_kv4_workspace_size(int B, int H, int Hkv, const spark_layer_desc *desc);
+
+spark_status spark_attn_decode_kv4(const void *qkv, const float *gate, const int32_t *pos,
+                                   void *k4_pages, void *v4_pages, int n_pages, int page_size,
+                                   const int32_t *page_table, int max_pages,
+                                   const spark_layer_desc *desc, int B, int H, int Hkv, void *out,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * spark_attn_pages_reserve and _compact for a pool whose pages hold 4 bits
+ * (k_pages, v_pages [n_layers, n_pages, Hkv, page_size, 144] bytes): the pages
+ * that they copy have another size.  The other page operations do not touch
+ * pages and serve both.
+ */
+spark_status spark_attn_kv4_pages_reserve(const spark_page_pool *pool, const int32_t *add,
+                                          int32_t *taken, void *workspace, size_t workspace_bytes,
+                                          void *stream);
+
+spark_status spark_attn_kv4_pages_compact(const spark_page_pool *pool, int32_t *live,
+                                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Copies the sticky device status word out of a workspace (synchronizes on
  * `stream`).  If `clear` is non-zero the word is reset to 0 afterwards.
  */
