@@ -5,172 +5,805 @@
 // token itself, as it is:
 //     out = sigma(gate) * sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
 // with s_j = q.k_j / 16.  The new token's key and value are quantised into
-// slot pos.
+// slot pos.  The step reads 288 bytes per slot and KV head.
+//
+// The work is shared out as the bf16 step's is (decode_paged.cu): the tiles of
+// 64 slots of all pairs are one list, every CTA takes its stretch of it, and a
+// pair that several CTAs share is joined by the one that arrives last, in the
+// order of the CTAs.  No CTA waits for another.  Two CTAs per SM: one warp each
+// feeds a ring of stages by bulk copies, as many bytes of a page as the row
+// sees; four warps take 16 slots of a tile each.
+//
+// Widening 4 bits is what the SM has to do besides: a code pair is one
+// conversion to two halves and one product with the scale, exact, in the
+// registers in which the matrix instructions take them (the pages hold the
+// operands' order).  Keys and values are the instructions' A operand, 16 slots
+// or dims; B has 8 columns, which hold up to 4 heads as a sum of two halves
+// each (22 bits of a query or a probability), or 8 heads as one half (11 bits,
+// where a second product would cost as much as the widening).
+#include "decode_walk.cuh"
 #include "kv4.cuh"
 
 namespace spark {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kPairCost = 3;
+constexpr int kTile = 64;                                 // slots per stage
+constexpr int kStages = 4;
+constexpr int kWarps = 4;                                 // consumers, a group of 16 slots each
+constexpr int kThreads = (kWarps + 1) * 32;               // + one producer warp
+constexpr int kCtasPerSm = 2;
+constexpr int kTileBytes = kTile * kKv4TokenBytes;        // K or V
+constexpr int kStageBytes = 2 * kTileBytes;
+constexpr int kQBytes = 8 * kHeadDim * 2;                 // 8 columns
+constexpr int kRowBytes = kHeadDim * 2;
+constexpr int kNewBytes = 10 * kRowBytes;                 // a pair's new token: q, key, value
+constexpr int kPairs = 2;                                 // pairs handed over at a time
+constexpr int kJoin = 6;                                  // partial states joined at once
+constexpr int kRedHeads = 4;                              // heads reduced over the warps at once
+constexpr int kRedBytes = kWarps * kRedHeads * kHeadDim * 4;
+constexpr int kSmemBytes = 128 + kStages * kStageBytes + kPairs * kNewBytes + kQBytes + kRedBytes +
+                           2 * kHeadDim * 4;
+
+using Row = DecodeRow<kTile, kPairCost>;
+using Walk = DecodeWalk<kTile, kPairCost>;
+
+__device__ __forceinline__ Row row_of(const Kv4Params &P, int b) {
+    return decode_row<kTile, kPairCost>(P, b);
+}
+
+// A pair as the producer hands it over: its tiles [t0, t1) for this CTA (none:
+// the end), the CTAs [c0, c1] that share it, which of its two places in the
+// workspace is this CTA's.
+struct Pair {
+    int pos, lo, b, g, t0, t1, c0, c1, place;
+    long long first;           // its first unit in the list
+};
+
+__device__ __forceinline__ void consumer_bar() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a),
+                              *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Two numbers as halves, and what they leave.
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t pack_half2_rest(float lo, float hi, uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_half2(lo - f.x, hi - f.y);
+}
+
+// Byte i of four scales, as the two halves of a word.
+template <int i>
+__device__ __forceinline__ uint32_t twice_scale(uint32_t scales) {
+    return __byte_perm(scales, 0, 0x4040 | i | i << 8) << 7;
+}
+
+__device__ __forceinline__ float nonfinite_part(float x) { return isfinite(x) ? 0.f : x; }
+
+// Where dims 2 p, 2 p + 1 of a head lie among the sums of the warps, in pairs:
+// a warp writes them 16 pairs apart and reads them 4 pairs a lane.
+__device__ __forceinline__ int red_at(int head, int p) {
+    return head * (kHeadDim / 2) + (p ^ (p >> 4) ^ ((head >> 1 & 1) << 3));
+}
 
 }  // namespace
 
-// One CTA per pair of a row and a KV head, a warp per slot in turn.
-__global__ void __launch_bounds__(kThreads) decode_kv4_kernel(const __grid_constant__ Kv4Params P) {
-    __shared__ float2 cs[kMaxRopePairs];
-    __shared__ float sm_m[kWarps][8], sm_l[kWarps][8];
-    __shared__ float sm_o[kWarps][8][kHeadDim];
+// kTwo: queries and probabilities as sums of two halves (4 heads at most).
+template <bool kTwo>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    decode_kv4_kernel(const __grid_constant__ Kv4Params P) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *stages = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    uint8_t *new_rows = stages + kStages * kStageBytes;
+    uint8_t *qs = new_rows + kPairs * kNewBytes;  // [8 columns][256] halves
+    float2 *red_o = reinterpret_cast<float2 *>(qs + kQBytes);
+    float *kn = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(red_o) + kRedBytes);
+    float *vn = kn + kHeadDim;  // the new token's key (rotated) and value
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ uint64_t pair_full[kPairs], pair_empty[kPairs];
+    __shared__ Pair pairs[kPairs];
+    __shared__ int abort_flag, seg_bad, lost, last_cta;
+    __shared__ int s_row;
+    __shared__ long long s_base;
+    __shared__ long long warp_sum[kThreads / 32];
+    __shared__ float red_m[kWarps][8], red_l[kWarps][8];
+    __shared__ float q_unit[8];                 // of the queries' halves, in base-2 score units
+    __shared__ float2 freq[kHeadDim / 2], cs[kHeadDim / 2];
+    __shared__ uint32_t new_codes[2][32];       // the new token's key and value, quantised
+    __shared__ uint8_t new_scale[2][32];
+
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = blockIdx.y, g = blockIdx.x;
-    grid_dep_wait();
-    grid_dep_launch();
-    const int pos = P.pos[b];
-    if (pos < 0 || pos >= P.pos_end) {
-        if (g == 0 && tid == 0 && pos != -1) atomicOr(P.status, kErrPosition);
-        return;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kWarps);
+        }
+        for (int s = 0; s < kPairs; ++s) {
+            mbar_init(&pair_full[s], 1);
+            mbar_init(&pair_empty[s], kWarps);
+        }
+        fence_mbar_init();
+        abort_flag = 0;
+        seg_bad = 0;
+        lost = 0;
     }
     const int half = P.rope.rot_dim / 2;
-    if (tid < half) rope_cos_sin_fine(pos, P.rope.u[tid], cs[tid].x, cs[tid].y);
+    if (tid < half) freq[tid] = P.rope.u[tid];
+    grid_dep_wait();  // positions, tables and pages may come from the kernel before
+
+    // ---------------------------------------------------------- this CTA's stretch
+    const int per = (P.N + kThreads - 1) / kThreads;  // rows per thread
+    const int b0 = tid * per;
+    long long mine = 0;
+    for (int b = b0; b < b0 + per && b < P.N; ++b) {
+        const int p = P.pos[b];
+        if (blockIdx.x == 0 && (p < -1 || p >= P.pos_end))
+            atomicOr(P.status, kErrPosition);
+        mine += row_of(P, b).units();
+    }
+    long long before = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += y;
+    }
+    if (lane == 31) warp_sum[warp] = before;
+    before -= mine;
     __syncthreads();
-    const __nv_bfloat16 *x = P.qkv + static_cast<size_t>(b) * (P.H + 2 * P.Hkv) * kHeadDim;
-    float q[8][8];
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        if (h >= P.G) break;
-        const uint4 raw = *reinterpret_cast<const uint4 *>(x + (g * P.G + h) * kHeadDim + lane * 8);
-        kv4_rotate(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, q[h]);
+    long long total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
     }
-    const int lo = P.kind == 1 && pos >= P.window ? pos - P.window + 1 : 0;
-    const int32_t *table = P.pg.table + static_cast<size_t>(b) * P.pg.max_pages;
-    float m[8], l[8], o[8][8];
-#pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[h][i] = 0.f;
+    total *= P.Hkv;
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    Walk wk{};
+    wk.u = share * blockIdx.x;
+    wk.end = wk.u + share < total ? wk.u + share : total;
+    if (wk.u >= wk.end) return;
+    if (wk.u >= before * P.Hkv && wk.u < (before + mine) * P.Hkv) {
+        int b = b0;
+        long long base = before * P.Hkv;
+        for (;; ++b) {
+            const long long n = P.Hkv * row_of(P, b).units();
+            if (wk.u < base + n || b + 1 >= P.N) break;
+            base += n;
+        }
+        s_row = b;
+        s_base = base;
     }
-    auto add = [&](const float (&k)[8], const float (&v)[8]) {
+    __syncthreads();
+    wk.b = s_row;
+    wk.base = s_base;
+    wk.row = row_of(P, wk.b);
+
+    if (warp == kWarps) {
+        // ------------------------------------------------------ producer
+        // Lane l copies K (or V: bit 0) of piece l / 2 of a tile; a piece is
+        // what lies in one page, of it the groups that the row sees.
+        const int page = 1 << P.pg.page_shift;
+        const int piece_slots = page < kTile ? page : kTile;
+        const int pieces = kTile / piece_slots;
+        const int piece = lane >> 1, which = lane & 1;
+        const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
+        int it = 0, n_pairs = 0;
+        bool ok = true;
+        // Hands over a pair (or the end).  After an abort too: every shared
+        // pair has to be counted, so that the counters are 0 again.
+        auto hand_over = [&](bool end) {
+            const int s = n_pairs % kPairs;
+            if (lane == 0) {
+                if (n_pairs >= kPairs)
+                    mbar_wait_plain(&pair_empty[s], ((n_pairs / kPairs) - 1) & 1);
+                Pair &p = pairs[s];
+                p.pos = wk.row.pos;
+                p.lo = wk.row.lo;
+                p.b = wk.b;
+                p.g = wk.g;
+                p.t0 = wk.t0;
+                p.t1 = end ? wk.t0 : wk.t1;
+                p.c0 = static_cast<int>((wk.first + kPairCost) / share);
+                p.c1 = static_cast<int>((wk.first + wk.row.units() - 1) / share);
+                p.place = share * blockIdx.x < wk.first ? 1 : 0;  // not its first pair
+                p.first = wk.first;
+                if (end || !ok) {
+                    mbar_arrive(&pair_full[s]);
+                } else {
+                    uint8_t *dst = new_rows + s * kNewBytes;
+                    const __nv_bfloat16 *src = P.qkv + wk.b * width;
+                    mbar_arrive_expect_tx(&pair_full[s], (P.G + 2) * kRowBytes);
+                    bulk_load(dst, src + static_cast<size_t>(wk.g) * P.G * kHeadDim,
+                              P.G * kRowBytes, &pair_full[s]);
+                    bulk_load(dst + P.G * kRowBytes,
+                              src + static_cast<size_t>(P.H + wk.g) * kHeadDim, kRowBytes,
+                              &pair_full[s]);
+                    bulk_load(dst + (P.G + 1) * kRowBytes,
+                              src + static_cast<size_t>(P.H + P.Hkv + wk.g) * kHeadDim, kRowBytes,
+                              &pair_full[s]);
+                }
+            }
+            __syncwarp();
+            ++n_pairs;
+        };
+        while (wk.load(P)) {
+            hand_over(false);
+            if (!ok) continue;
+            const int32_t *row = P.pg.table + static_cast<size_t>(wk.b) * P.pg.max_pages;
+            const int slot0 = wk.row.slot0();
+            const int lo = wk.row.lo & ~15, hi = (wk.row.pos + 15) & ~15;  // groups seen
+            int ids = 0;
+            for (int t = wk.t0; t < wk.t1; ++t) {
+                // page numbers of the next 32 pieces, one per lane; -1: none
+                const int in = (t - wk.t0) * pieces & 31;
+                if (in == 0) {
+                    const int slot = slot0 + t * kTile + lane * piece_slots;
+                    ids = -1;
+                    if (slot < hi && slot + piece_slots > lo && slot < slot0 + wk.t1 * kTile) {
+                        ids = row[slot >> P.pg.page_shift];
+                        if (ids < 0 || ids >= P.pg.n_pages) {
+                            atomicOr(P.status, kErrPage);
+                            ids = -1;
+                        }
+                    }
+                }
+                const int s = it % kStages;
+                if (it >= kStages && lane == 0)
+                    ok = mbar_wait(&empty[s], ((it / kStages) - 1) & 1, &abort_flag, P.status);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const int id = __shfl_sync(0xffffffffu, ids, (in + piece) & 31);
+                const int at = slot0 + t * kTile + piece * piece_slots;
+                const int a = at > lo ? at : lo;
+                const int b = at + piece_slots < hi ? at + piece_slots : hi;
+                uint8_t *dst = stages + s * kStageBytes + which * kTileBytes +
+                               (a & (kTile - 1)) * kKv4TokenBytes;
+                const int bytes = piece < pieces && a < b ? (b - a) * kKv4TokenBytes : 0;
+                if (bytes && id < 0) {  // a page that is not in the pool reads as zeros
+                    for (int i = 0; i < bytes; i += 16)
+                        *reinterpret_cast<uint4 *>(dst + i) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();  // copies come here later
+                }
+                const unsigned all =
+                    __reduce_add_sync(0xffffffffu, id < 0 ? 0u : static_cast<unsigned>(bytes));
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], all);
+                __syncwarp();
+                if (bytes && id >= 0)
+                    bulk_load(dst, (which ? P.pg.v : P.pg.k) + P.pg.group(id, wk.g, P.Hkv, a),
+                              bytes, &full[s]);
+                ++it;
+            }
+        }
+        hand_over(true);
+        __syncthreads();
+        // copies still in flight after an abort must land before the CTA ends
+        if (lane == 0 && abort_flag)
+            for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
+                mbar_wait_plain(&full[i % kStages], (i / kStages) & 1);
+        if (lane == 0 && abort_flag)
+            for (int i = n_pairs > kPairs ? n_pairs - kPairs : 0; i < n_pairs; ++i)
+                mbar_wait_plain(&pair_full[i % kPairs], (i / kPairs) & 1);
+        return;
+    }
+
+    // ---------------------------------------------------------- consumers
+    const int row8 = lane >> 2, c4 = lane & 3;           // row and column pair of fragments
+    const int tok = 4 * (row8 >> 1) + (row8 & 1);        // slot of row row8; row8 + 8: + 2
+    // the heads of this thread's two columns
+    const int h0 = kTwo ? 2 * (c4 & 1) : 2 * c4, h1 = h0 + 1;
+    for (int i = tid; i < 8 * (kHeadDim / 8); i += kWarps * 32)
+        *reinterpret_cast<uint4 *>(qs + i * 16) = make_uint4(0, 0, 0, 0);
+    if (tid < 8) q_unit[tid] = 0.f;
+    int it = 0;
+    bool aborted = false;  // the same in every consumer thread
+    // Waits for a pair; the barrier behind it tells every warp whether all have it.
+    auto await_pair = [&](int n) {
+        if (!mbar_wait_plain(&pair_full[n % kPairs], (n / kPairs) & 1)) {
+            atomicOr(P.status, kErrTimeout);
+            abort_flag = 1;
+            lost = 1;
+        }
+        consumer_bar();
+    };
+    await_pair(0);
+    for (int n = 0; !lost; ++n) {
+        // The next pair; its new token's projections: q of the group's heads,
+        // the key, the value, warp w taking rows w, w + 4, ... of them.
+        const Pair &pair = pairs[n % kPairs];
+        const uint8_t *rows = new_rows + n % kPairs * kNewBytes;
+        const int pos = pair.pos, lo = pair.lo, t0 = pair.t0, t1 = pair.t1;
+        if (t0 >= t1) break;
+        const int b = pair.b, g = pair.g;
+        float gate[2] = {0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
-            if (h >= P.G) break;
-            float d = 0.f;
+        for (int i = 0; i < 2; ++i) {
+            const int hq = warp + i * kRedHeads;
+            if (hq < P.G) gate[i] = P.gate[static_cast<size_t>(b) * P.H + g * P.G + hq];
+        }
+        if (tid < half) rope_cos_sin_fine(pos, freq[tid], cs[tid].x, cs[tid].y);
+        consumer_bar();
+        // q, the new key and the new value of the warp's rows
+        float q[2][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d = fmaf(q[h][i], k[i], d);
+        for (int i = 0; i < 3; ++i) {
+            const int hh = warp + i * kWarps;
+            if (hh >= P.G + 2) break;
+            const uint4 raw = *reinterpret_cast<const uint4 *>(rows + hh * kRowBytes + lane * 16);
+            if (hh < P.G) {
+                // in halves, scaled by a power of two so that the largest is 1 to 2
+                float(&y)[8] = q[i & 1];
+                kv4_rotate(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, y);
+                float a = 0.f, z = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    a = fmaxf(a, fabsf(y[j]));
+                    z += y[j] * 0.f;
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) {
+                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+                    z += __shfl_xor_sync(0xffffffffu, z, off);
+                }
+                const unsigned e = __float_as_uint(a) >> 23;
+                const unsigned up = (e < 253u ? 254u - e : 1u) << 23;
+                const float f = __uint_as_float(up);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // (z: a query that is not finite is NaN throughout)
+                    const float u = fmaf(y[2 * j], f, z), v = fmaf(y[2 * j + 1], f, z);
+                    hi[j] = pack_half2(u, v);
+                    lo[j] = pack_half2_rest(u, v, hi[j]);
+                }
+                *reinterpret_cast<uint4 *>(qs + hh * kHeadDim * 2 + lane * 16) =
+                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if (kTwo)
+                    *reinterpret_cast<uint4 *>(qs + (hh + 4) * kHeadDim * 2 + lane * 16) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (lane == 0)
+                    q_unit[hh] = kScaleLog2 * __uint_as_float((254u << 23) - up);
+            } else {
+                float y[8];
+                uint32_t codes;
+                unsigned byte;
+                const int v = hh - P.G;
+                if (v == 0) {
+                    kv4_key_row(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, pos,
+                                P.turns, y, codes, byte);
+                } else {
+                    kv4_value_row(raw, codes, byte);
+                    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y[2 * j] = bf16_lo(w[j]);
+                        y[2 * j + 1] = bf16_hi(w[j]);
+                    }
+                }
+                float4 *dst = reinterpret_cast<float4 *>((v ? vn : kn) + lane * 8);
+                dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                new_codes[v][lane] = codes;
+                new_scale[v][lane] = static_cast<uint8_t>(byte);
+            }
+        }
+        consumer_bar();
+        const int c0 = pair.c0, c1 = pair.c1, place = pair.place;
+        const long long first_unit = pair.first;
+        const int slot0 = lo & ~(kTile - 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair_empty[n % kPairs]);
+        // the new token's scores
+        float x_new[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (warp + i * kWarps >= P.G) break;
+            const float4 ka = *reinterpret_cast<const float4 *>(kn + lane * 8);
+            const float4 kb = *reinterpret_cast<const float4 *>(kn + lane * 8 + 4);
+            float d = q[i][0] * ka.x;
+            d = fmaf(q[i][1], ka.y, d);
+            d = fmaf(q[i][2], ka.z, d);
+            d = fmaf(q[i][3], ka.w, d);
+            d = fmaf(q[i][4], kb.x, d);
+            d = fmaf(q[i][5], kb.y, d);
+            d = fmaf(q[i][6], kb.z, d);
+            d = fmaf(q[i][7], kb.w, d);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-            const float s = d * kScaleLog2, n = fmaxf(m[h], s), z = n == -INFINITY ? 0.f : n;
-            const float w = fast_exp2(m[h] - z), p = fast_exp2(s - z);
-            m[h] = n;
-            l[h] = l[h] * w + p;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[h][i] = o[h][i] * w + p * v[i];
+            x_new[i] = d * kScaleLog2;
         }
-    };
-    for (int j = lo + warp; j < pos; j += kWarps) {
-        const int id = table[j >> P.pg.page_shift], t = j & 15;
-        uint32_t kc = 0, vc = 0;
-        float ks = 0.f, vs = 0.f;
-        if (id >= 0 && id < P.pg.n_pages) {
-            const size_t at = P.pg.group(id, g, P.Hkv, j);
-            kc = *reinterpret_cast<const uint32_t *>(P.pg.k + at + kv4_key_at(lane, t));
-            ks = kv4_scale(P.pg.k[at + kv4_key_scale_at(lane >> 1, t)]);
-            vc = kv4_value_codes(
-                *reinterpret_cast<const uint4 *>(P.pg.v + at + kv4_value_at(lane, t >> 2)), t & 3);
-            vs = kv4_scale(P.pg.v[at + kv4_value_scale_at(lane >> 1, t >> 2) + 2 * (t & 1) +
-                                  (t >> 1 & 1)]);
-        } else if (lane == 0) {
-            atomicOr(P.status, kErrPage);
-        }
-        uint32_t h[4];
-        float k[8], v[8];
-        kv4_widen(kc, h);
+        // Q^T as the B operand of S^T = K Q^T: 8 dims are two steps' (b0, b1)
+        uint32_t qf[16][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-            k[2 * i] = f.x * ks;
-            k[2 * i + 1] = f.y * ks;
+        for (int i = 0; i < 8; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(
+                qs + row8 * kHeadDim * 2 + (128 * (i >> 2) + 32 * c4 + 8 * (i & 3)) * 2);
+            qf[2 * i][0] = x.x;
+            qf[2 * i][1] = x.y;
+            qf[2 * i + 1][0] = x.z;
+            qf[2 * i + 1][1] = x.w;
         }
-        kv4_widen(vc, h);
+        const float unit0 = q_unit[h0], unit1 = q_unit[h1];
+        float o[16][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-            v[2 * i] = f.x * vs;
-            v[2 * i + 1] = f.y * vs;
-        }
-        add(k, v);
-    }
-    if (warp == 0) {  // the new token: joined as it is, stored in 4 bits
-        const uint4 kr = *reinterpret_cast<const uint4 *>(x + (P.H + g) * kHeadDim + lane * 8);
-        const uint4 vr =
-            *reinterpret_cast<const uint4 *>(x + (P.H + P.Hkv + g) * kHeadDim + lane * 8);
-        float k[8], v[8];
-        uint32_t kc, vc;
-        unsigned kb, vb;
-        kv4_key_row(kv4_key_turn(kr, P.rope.rot_dim, pos, lane), cs, pos, P.turns, k, kc, kb);
-        kv4_value_row(vr, vc, vb);
-        const uint32_t w[4] = {vr.x, vr.y, vr.z, vr.w};
+        for (int m = 0; m < 16; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        bool ok = !aborted;
+        for (int t = t0; ok && t < t1; ++t, ++it) {
+            const int s = it % kStages;
+            ok = mbar_wait(&full[s], (it / kStages) & 1, &abort_flag, P.status);
+            if (!ok) break;
+            const int first = slot0 + t * kTile + warp * kKv4Group;
+            if (first < pos && first + kKv4Group > lo) {
+                const uint8_t *kg = stages + s * kStageBytes + warp * kKv4GroupBytes;
+                const uint8_t *vg = kg + kTileBytes;
+                // S^T (16 slots x 8 columns) = K (16 x 256) Q^T (256 x 8)
+                const uint32_t sa =
+                    *reinterpret_cast<const uint32_t *>(kg + kKv4Codes + tok * 16 + c4 * 4);
+                const uint32_t sb =
+                    *reinterpret_cast<const uint32_t *>(kg + kKv4Codes + tok * 16 + 32 + c4 * 4);
+                float sc[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16_lo(w[i]);
-            v[2 * i + 1] = bf16_hi(w[i]);
-        }
-        add(k, v);
-        const int id = table[pos >> P.pg.page_shift], t = pos & 15;
-        if (id < 0 || id >= P.pg.n_pages) {
-            if (lane == 0) atomicOr(P.status, kErrPage);
-        } else {
-            const size_t at = P.pg.group(id, g, P.Hkv, pos);
-            *reinterpret_cast<uint32_t *>(P.pg.k + at + kv4_key_at(lane, t)) = kc;
-            uint8_t *dst = P.pg.v + at + kv4_value_at(lane, t >> 2) + 2 * (t >> 1 & 1);
+                for (int i = 0; i < 4; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint8_t &byte = dst[4 * (i >> 1) + (i & 1)];
-                const unsigned c = vc >> (4 * i) & 15u;
-                byte = t & 1 ? (byte & 0x0f) | c << 4 : (byte & 0xf0) | c;
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 ka =
+                        *reinterpret_cast<const uint4 *>(kg + h * 1024 + tok * 64 + c4 * 16);
+                    const uint4 kb =
+                        *reinterpret_cast<const uint4 *>(kg + h * 1024 + tok * 64 + 128 + c4 * 16);
+                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w};
+                    const uint32_t wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                    const uint32_t ua[2] = {h ? twice_scale<2>(sa) : twice_scale<0>(sa),
+                                            h ? twice_scale<3>(sa) : twice_scale<1>(sa)};
+                    const uint32_t ub[2] = {h ? twice_scale<2>(sb) : twice_scale<0>(sb),
+                                            h ? twice_scale<3>(sb) : twice_scale<1>(sb)};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a[4], b[4];
+                        kv4_widen(wa[i], a);
+                        kv4_widen(wb[i], b);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            a[j] = mul_half2(a[j], ua[i >> 1]);
+                            b[j] = mul_half2(b[j], ub[i >> 1]);
+                        }
+                        const int ks = 8 * h + 2 * i;
+                        mma_f16_16816(sc[2 * (i & 1)], a[0], b[0], a[1], b[1], qf[ks][0],
+                                      qf[ks][1]);
+                        mma_f16_16816(sc[2 * (i & 1) + 1], a[2], b[2], a[3], b[3], qf[ks + 1][0],
+                                      qf[ks + 1][1]);
+                    }
+                }
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = (sc[0][i] + sc[1][i]) + (sc[2][i] + sc[3][i]);
+                    if (kTwo) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);
+                }
+                // this thread's slots (rows row8 and row8 + 8) and heads
+                const bool va = first + tok >= lo && first + tok < pos;
+                const bool vb = first + tok + 2 >= lo && first + tok + 2 < pos;
+                x[0] = va ? x[0] * unit0 : -INFINITY;
+                x[1] = va ? x[1] * unit1 : -INFINITY;
+                x[2] = vb ? x[2] * unit0 : -INFINITY;
+                x[3] = vb ? x[3] * unit1 : -INFINITY;
+                float n0 = fmaxf(x[0], x[2]), n1 = fmaxf(x[1], x[3]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+                    n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+                }
+                if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+                    n0 = fmaxf(n0, m0);
+                    n1 = fmaxf(n1, m1);
+                    const float r0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
+                    const float r1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
+                    l0 *= r0;
+                    l1 *= r1;
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) {
+                        o[m][0] *= r0;
+                        o[m][1] *= r1;
+                        o[m][2] *= r0;
+                        o[m][3] *= r1;
+                    }
+                    m0 = n0;
+                    m1 = n1;
+                }
+                const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+                const float p0 = fast_exp2(x[0] - z0), p1 = fast_exp2(x[1] - z1);
+                const float p2 = fast_exp2(x[2] - z0), p3 = fast_exp2(x[3] - z1);
+                l0 += p0 + p2;
+                l1 += p1 + p3;
+                // P^T as the B operand of O^T += V^T P^T; the last columns take
+                // what the halves of the first leave
+                uint32_t pa = pack_half2(p0, p1), pb = pack_half2(p2, p3);
+                if (kTwo) {
+                    const uint32_t ra = pack_half2_rest(p0, p1, pa);
+                    const uint32_t rb = pack_half2_rest(p2, p3, pb);
+                    pa = c4 & 2 ? ra : pa;
+                    pb = c4 & 2 ? rb : pb;
+                }
+                pa = movmatrix_trans(pa);
+                pb = movmatrix_trans(pb);
+                uint2 sv = *reinterpret_cast<const uint2 *>(vg + kKv4Codes + lane * 8);
+                if (first < lo || first + kKv4Group > pos) {
+                    // Slots that hold no visible token may hold anything: a
+                    // scale of zero makes zeros of it.
+                    uint32_t seen = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int slot = first + 4 * c4 + j;
+                        if (slot >= lo && slot < pos)
+                            seen |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
+                    }
+                    sv.x &= seen;
+                    sv.y &= seen;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(vg + j * 512 + lane * 16);
+                    const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t u = j >> 1 ? sv.y : sv.x;
+                    const uint32_t u0 = (u & 0x00ff00ffu) << 7, u1 = (u >> 1) & 0x7f807f80u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a[4];
+                        kv4_widen(wv[i], a);
+                        mma_f16_16816(o[4 * j + i], mul_half2(a[0], u0), mul_half2(a[1], u0),
+                                      mul_half2(a[2], u1), mul_half2(a[3], u1), pa, pb);
+                    }
+                }
             }
-            if (!(lane & 1)) {
-                P.pg.k[at + kv4_key_scale_at(lane >> 1, t)] = kb;
-                P.pg.v[at + kv4_value_scale_at(lane >> 1, t >> 2) + 2 * (t & 1) + (t >> 1 & 1)] =
-                    vb;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+        }
+
+        // ------------------------------------------------------ join the warps
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+        }
+        if (lane < (kTwo ? 2 : 4)) {
+            red_m[warp][h0] = m0;
+            red_m[warp][h1] = m1;
+            red_l[warp][h0] = l0;
+            red_l[warp][h1] = l1;
+        }
+        if (!ok) seg_bad = 1;
+        consumer_bar();
+        aborted = seg_bad != 0;  // written before the barrier, never reset
+        float M0 = red_m[0][h0], M1 = red_m[0][h1];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            M0 = fmaxf(M0, red_m[w][h0]);
+            M1 = fmaxf(M1, red_m[w][h1]);
+        }
+        const float s0 = M0 == -INFINITY ? 0.f : fast_exp2(m0 - M0);
+        const float s1 = M1 == -INFINITY ? 0.f : fast_exp2(m1 - M1);
+        // head hq of this warp, lane l its dims 8l..8l+7; the sums of the warps
+        // go through shared memory kRedHeads heads at a time
+        HeadState st[2];
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            if (pass * kRedHeads >= P.G) break;
+            if (pass) consumer_bar();  // the heads before are read
+            float2 *dst = red_o + warp * kRedHeads * (kHeadDim / 2);
+            if (kTwo) {
+                // columns j and j + 4 are one head's: each lane of the two takes
+                // half of the dims
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float give = c4 & 2 ? o[m][i] : o[m + 8][i];
+                        const float keep = c4 & 2 ? o[m + 8][i] : o[m][i];
+                        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+                    }
+                    const int p = 16 * row8 + m + 4 * (c4 & 2);
+                    dst[red_at(h0, p)] = make_float2(v[0] * s0, v[2] * s0);
+                    dst[red_at(h1, p)] = make_float2(v[1] * s1, v[3] * s1);
+                }
+            } else if (c4 >> 1 == pass) {
+#pragma unroll
+                for (int m = 0; m < 16; ++m) {
+                    const int p = 16 * row8 + m;
+                    dst[red_at(h0 & 3, p)] = make_float2(o[m][0] * s0, o[m][2] * s0);
+                    dst[red_at(h1 & 3, p)] = make_float2(o[m][1] * s1, o[m][3] * s1);
+                }
+            }
+            consumer_bar();
+            const int hq = warp + pass * kRedHeads;
+            HeadState &h = st[pass];
+            h.m = -INFINITY;
+            h.l = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h.o[i] = 0.f;
+            if (hq < P.G && !aborted) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) h.m = fmaxf(h.m, red_m[w][hq]);
+                // (a NaN among the sums has to stay one, whatever the maximum)
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    h.l += red_l[w][hq] *
+                           (h.m == -INFINITY ? 1.f : fast_exp2(red_m[w][hq] - h.m));
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = red_o[w * kRedHeads * (kHeadDim / 2) +
+                                               red_at(warp, 4 * lane + i)];
+                        h.o[2 * i] += v.x;
+                        h.o[2 * i + 1] += v.y;
+                    }
             }
         }
-    }
+
+        // ------------------------------------------------------ finish or hand over
+        bool finish = c0 == c1;
+        if (!finish) {
+            // this CTA's partial state, then the count
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
-        if (h >= P.G) break;
-        if (lane == 0) {
-            sm_m[warp][h] = m[h];
-            sm_l[warp][h] = l[h];
+            for (int i = 0; i < 2; ++i) {
+                const int hq = warp + i * kRedHeads;
+                if (hq >= P.G) break;
+                const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + place) * P.G + hq;
+                float4 *dst = reinterpret_cast<float4 *>(P.part_o + at * kHeadDim + lane * 8);
+                dst[0] = make_float4(st[i].o[0], st[i].o[1], st[i].o[2], st[i].o[3]);
+                dst[1] = make_float4(st[i].o[4], st[i].o[5], st[i].o[6], st[i].o[7]);
+                if (lane == 0)
+                    reinterpret_cast<float2 *>(P.part_ml)[at] = make_float2(st[i].m, st[i].l);
+            }
+            __threadfence();
+            consumer_bar();
+            if (tid == 0) {
+                // c0 is the first CTA of one shared pair at most, which the
+                // counter is named by
+                last_cta = atomicAdd(P.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+                // everyone has counted: back to 0 for the next call
+                if (last_cta) P.counters[c0] = 0;
+            }
+            consumer_bar();
+            finish = last_cta != 0;
+            if (finish) {
+                __threadfence();  // the others' states are read after the count
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int hq = warp + i * kRedHeads;
+                    if (hq >= P.G) break;
+                    HeadState &h = st[i];
+                    auto at = [&](int cta) {
+                        const int pl = static_cast<long long>(cta) * share < first_unit ? 1 : 0;
+                        return (static_cast<size_t>(cta) * 2 + pl) * P.G + hq;
+                    };
+                    // kJoin states at a time, all their loads in flight
+                    h.m = -INFINITY;
+                    h.l = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h.o[j] = 0.f;
+                    for (int cta = c0; cta <= c1; cta += kJoin) {
+                        float2 ml[kJoin];
+                        float4 x[kJoin], y[kJoin];
+#pragma unroll
+                        for (int k = 0; k < kJoin; ++k) {
+                            ml[k] = make_float2(-INFINITY, 0.f);
+                            x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (cta + k > c1) continue;
+                            const size_t a = at(cta + k);
+                            ml[k] = __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + a);
+                            const float4 *src = reinterpret_cast<const float4 *>(
+                                P.part_o + a * kHeadDim + lane * 8);
+                            x[k] = __ldcg(src);
+                            y[k] = __ldcg(src + 1);
+                        }
+                        float m = h.m;
+#pragma unroll
+                        for (int k = 0; k < kJoin; ++k) m = fmaxf(m, ml[k].x);
+                        const float z = m == -INFINITY ? 0.f : m;
+                        const float wo = fast_exp2(h.m - z);
+                        h.m = m;
+                        h.l *= wo;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) h.o[j] *= wo;
+#pragma unroll
+                        for (int k = 0; k < kJoin; ++k) {
+                            const float w = fast_exp2(ml[k].x - z);
+                            const float v[8] = {x[k].x, x[k].y, x[k].z, x[k].w,
+                                                y[k].x, y[k].y, y[k].z, y[k].w};
+                            h.l += ml[k].y * w;
+                            add_scaled(h, w, v);
+                        }
+                    }
+                }
+            }
         }
+        if (finish) {
+            // the new token joins, the gate applies
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sm_o[warp][h][lane * 8 + i] = o[h][i];
-    }
-    __syncthreads();
-    for (int h = warp; h < P.G; h += kWarps) {
-        float M = -INFINITY, L = 0.f, y[8] = {};
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][h]);
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = fast_exp2(sm_m[w][h] - M);
-            L += sm_l[w][h] * f;
+            for (int i = 0; i < 2; ++i) {
+                const int hq = warp + i * kRedHeads;
+                if (hq >= P.G) break;
+                HeadState &h = st[i];
+                const int head = g * P.G + hq;
+                const float4 va = *reinterpret_cast<const float4 *>(vn + lane * 8);
+                const float4 vb = *reinterpret_cast<const float4 *>(vn + lane * 8 + 4);
+                const float v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+                const float m = fmaxf(h.m, x_new[i]);
+                const float z = m == -INFINITY ? 0.f : m;
+                const float wo = h.m == -INFINITY ? 1.f : fast_exp2(h.m - z);
+                const float wn = fast_exp2(x_new[i] - z);
+                const float scale = gate_act(gate[i], P.gate_mode) / (h.l * wo + wn);
+                float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] += sm_o[w][h][lane * 8 + i] * f;
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = (h.o[j] * wo + v[j] * wn) * scale;
+                    // an infinity is one however small its weight
+                    if (!isfinite(v[j])) y[j] = (v[j] + nonfinite_part(h.o[j])) * scale;
+                }
+                *reinterpret_cast<uint4 *>(
+                    P.out + (static_cast<size_t>(b) * P.H + head) * kHeadDim + lane * 8) =
+                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                               pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+            }
+            if (warp == 0) {
+                // the new token's slot: every read of this pair is done
+                const int id = P.pg.table[static_cast<size_t>(b) * P.pg.max_pages +
+                                          (pos >> P.pg.page_shift)];
+                const int t = pos & 15;
+                if (id < 0 || id >= P.pg.n_pages) {
+                    if (lane == 0) atomicOr(P.status, kErrPage);
+                } else {
+                    const size_t at = P.pg.group(id, g, P.Hkv, pos);
+                    *reinterpret_cast<uint32_t *>(P.pg.k + at + kv4_key_at(lane, t)) =
+                        new_codes[0][lane];
+                    // the other slot of each byte stays
+                    const uint32_t codes = new_codes[1][lane];
+                    uint8_t *dst = P.pg.v + at + kv4_value_at(lane, t >> 2) + 2 * (t >> 1 & 1);
+                    unsigned old[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        old[j] = *reinterpret_cast<const uint16_t *>(dst + 4 * j);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const unsigned pair = codes >> (8 * j);
+                        const unsigned n = (pair & 15u) | (pair & 0xf0u) << 4;
+                        *reinterpret_cast<uint16_t *>(dst + 4 * j) = static_cast<uint16_t>(
+                            t & 1 ? (old[j] & 0x0f0fu) | n << 4 : (old[j] & 0xf0f0u) | n);
+                    }
+                    if (!(lane & 1)) {
+                        P.pg.k[at + kv4_key_scale_at(lane >> 1, t)] = new_scale[0][lane];
+                        P.pg.v[at + kv4_value_scale_at(lane >> 1, t >> 2) + 2 * (t & 1) +
+                               (t >> 1 & 1)] = new_scale[1][lane];
+                    }
+                }
+            }
         }
-        const int head = g * P.G + h;
-        const float c = gate_act(P.gate[static_cast<size_t>(b) * P.H + head], P.gate_mode) / L;
-        *reinterpret_cast<uint4 *>(P.out + (static_cast<size_t>(b) * P.H + head) * kHeadDim +
-                                   lane * 8) =
-            make_uint4(pack_bf16x2(y[0] * c, y[1] * c), pack_bf16x2(y[2] * c, y[3] * c),
-                       pack_bf16x2(y[4] * c, y[5] * c), pack_bf16x2(y[6] * c, y[7] * c));
+        await_pair(n + 1);  // (q, the new token and the sums are read)
     }
+    grid_dep_launch();
+    __syncthreads();  // with the producer
 }
 
 // ---------------------------------------------------------------- launcher
 
-cudaError_t launch_decode_kv4(const Kv4Params &P, int, cudaStream_t stream) {
-    return launch_overlapped(decode_kv4_kernel, dim3(P.Hkv, P.S), dim3(kThreads), 0, stream, P);
+int decode_kv4_ctas(int sms) { return sms * kCtasPerSm; }
+
+cudaError_t launch_decode_kv4(const Kv4Params &P, int grid, cudaStream_t stream) {
+    auto kernel = P.G <= 4 ? decode_kv4_kernel<true> : decode_kv4_kernel<false>;
+    cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (err != cudaSuccess) return err;
+    return launch_overlapped(kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, P);
 }
 
 }  // namespace spark

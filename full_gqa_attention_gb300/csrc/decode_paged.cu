@@ -24,13 +24,13 @@
 // enough -- and the CTA that arrives last at the pair's counter joins them in
 // the order of the CTAs, so the result does not depend on which one that is.
 // No CTA waits for another.
-#include "paged.cuh"
+#include "decode_walk.cuh"
 
 namespace spark {
 
 namespace {
 
-// A pair's own units (Row::units).  None: the ragged batch of 48 rows takes 129
+// A pair's own units (DecodeRow::units).  None: the ragged batch of 48 rows takes 129
 // us; 2, 3 and 5: 93 us, 64 sliding rows 33 to 34.
 constexpr int kPairCost = 3;
 constexpr int kTile = 64;                                 // slots per stage
@@ -52,69 +52,11 @@ __device__ __forceinline__ void consumer_bar() {
     asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
 }
 
-// What a row asks for: its position, first visible slot and tiles (0: nothing).
-struct Row {
-    int pos, lo, tiles;
-    __device__ __forceinline__ int slot0() const { return lo & ~(kTile - 1); }
-    // Units of one of its pairs in the list: its tiles, and what setting a pair
-    // up and finishing it costs besides, in tiles.
-    __device__ __forceinline__ long long units() const {
-        return tiles ? tiles + kPairCost : 0;
-    }
-};
+using Row = DecodeRow<kTile, kPairCost>;
+using Walk = DecodeWalk<kTile, kPairCost>;
 
 __device__ __forceinline__ Row row_of(const PagedParams &P, int b) {
-    Row r;
-    r.pos = P.pos[b];
-    r.lo = 0;
-    r.tiles = 0;
-    if (r.pos < 0 || r.pos >= P.pos_end) return r;
-    if (P.kind == kLayerSliding && r.pos >= P.window) r.lo = r.pos - P.window + 1;
-    const int n = (r.pos - r.slot0() + kTile - 1) / kTile;
-    r.tiles = n > 0 ? n : 1;  // a row with nothing cached still has its new token
-    return r;
-}
-
-// A CTA's walk over its stretch of the list: the pair (b, g) and the tiles
-// [t0, t1) of it.  A pair's units are kPairCost for itself, then its tiles.
-struct Walk {
-    long long u, end;   // next unit of the stretch, its end
-    long long base;     // first unit of row b
-    long long first;    // first unit of the pair
-    int b, g, t0, t1;
-    Row row;
-
-    // The next pair with tiles in the stretch, from unit u on; false at the
-    // end.  b and base are at or before it.
-    __device__ __forceinline__ bool load(const PagedParams &P) {
-        while (u < end) {
-            while (u >= base + P.Hkv * row.units()) {
-                if (b + 1 >= P.N) return false;  // the positions changed under the call
-                base += P.Hkv * row.units();
-                row = row_of(P, ++b);
-            }
-            const long long n = row.units();
-            g = static_cast<int>((u - base) / n);
-            first = base + g * n;
-            const int from = static_cast<int>(u - first) - kPairCost;
-            const int to = static_cast<int>(end - first < n ? end - first : n) - kPairCost;
-            u = first + to + kPairCost;
-            t0 = from > 0 ? from : 0;
-            t1 = to;
-            if (t1 > t0) return true;
-        }
-        return false;
-    }
-};
-
-// The running state of one query head: this lane's 8 dims.
-struct HeadState {
-    float m, l, o[8];
-};
-
-__device__ __forceinline__ void add_scaled(HeadState &s, float w, const float *o) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s.o[i] += o[i] * w;
+    return decode_row<kTile, kPairCost>(P, b);
 }
 
 // Values that are not finite.  A visible infinity is infinite in its dims,

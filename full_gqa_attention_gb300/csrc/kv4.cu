@@ -23,6 +23,7 @@ bool aligned(const void *p, size_t a);
 int page_shift_of(int page_size);
 spark_status check_pages(const void *k_pages, const void *v_pages, int n_pages, int page_size,
                          const int32_t *table, int max_pages);
+int decode_kv4_ctas(int sms);
 cudaError_t launch_decode_kv4(const Kv4Params &P, int grid, cudaStream_t stream);
 
 namespace {
@@ -372,12 +373,25 @@ void set_pages(Kv4Params &P, void *k4, void *v4, int n_pages, int page_size, con
     P.pg.max_pages = max_pages;
 }
 
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace of a decode: the header, a counter per CTA (of the finished parts of
+// a shared pair; every call leaves them at 0), two partial states per CTA.
 struct DecodeKv4Plan {
     int grid;
-    size_t bytes;
+    size_t counters, ml, o, bytes;
 };
 
-DecodeKv4Plan plan_decode_kv4(int, int, int) { return DecodeKv4Plan{0, kWorkspaceHeader}; }
+DecodeKv4Plan plan_decode_kv4(int H, int Hkv, int sms) {
+    DecodeKv4Plan pl{};
+    pl.grid = decode_kv4_ctas(sms);
+    const size_t parts = static_cast<size_t>(pl.grid) * 2 * (H / Hkv);
+    pl.counters = kWorkspaceHeader;
+    pl.ml = pl.counters + up256(static_cast<size_t>(pl.grid) * 4);
+    pl.o = pl.ml + up256(parts * 2 * 4);
+    pl.bytes = pl.o + up256(parts * kHeadDim * 4);
+    return pl;
+}
 
 }  // namespace
 }  // namespace spark
@@ -508,6 +522,10 @@ spark_status spark_attn_decode_kv4(const void *qkv, const float *gate, const int
     set_pages(P, k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
     P.pos_end = max_pages << P.pg.page_shift;
     if (P.rope.rot_dim > 0 && P.pos_end > kRopePositions) P.pos_end = kRopePositions;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    P.counters = reinterpret_cast<unsigned *>(ws + pl.counters);
+    P.part_ml = reinterpret_cast<float *>(ws + pl.ml);
+    P.part_o = reinterpret_cast<float *>(ws + pl.o);
     return done(launch_decode_kv4(P, pl.grid, static_cast<cudaStream_t>(stream)));
 }
 
