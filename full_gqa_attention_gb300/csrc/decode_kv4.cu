@@ -40,7 +40,7 @@ constexpr int kQBytes = 8 * kHeadDim * 2;                 // 8 columns
 constexpr int kRowBytes = kHeadDim * 2;
 constexpr int kNewBytes = 10 * kRowBytes;                 // a pair's new token: q, key, value
 constexpr int kPairs = 2;                                 // pairs handed over at a time
-constexpr int kJoin = 6;                                  // partial states joined at once
+constexpr int kFan = 8;                                   // partial states joined at once
 constexpr int kRedHeads = 4;                              // heads reduced over the warps at once
 constexpr int kRedBytes = kWarps * kRedHeads * kHeadDim * 4;
 constexpr int kSmemBytes = 128 + kStages * kStageBytes + kPairs * kNewBytes + kQBytes + kRedBytes +
@@ -54,11 +54,11 @@ __device__ __forceinline__ Row row_of(const Kv4Params &P, int b) {
 }
 
 // A pair as the producer hands it over: its tiles [t0, t1) for this CTA (none:
-// the end), the CTAs [c0, c1] that share it, which of its two places in the
-// workspace is this CTA's.
+// the end), the CTAs [c0, c1] that share it.  A CTA shares its first and its
+// last pair at most, and has two places for a state: `second` is 1 where the
+// pair is not the first of c0 (it is the first of every other).
 struct Pair {
-    int pos, lo, b, g, t0, t1, c0, c1, place;
-    long long first;           // its first unit in the list
+    int pos, lo, b, g, t0, t1, c0, c1, second;
 };
 
 __device__ __forceinline__ void consumer_bar() {
@@ -82,8 +82,7 @@ __device__ __forceinline__ uint32_t pack_half2_rest(float lo, float hi, uint32_t
 }
 
 // Byte i of four scales, as the two halves of a word.
-template <int i>
-__device__ __forceinline__ uint32_t twice_scale(uint32_t scales) {
+__device__ __forceinline__ uint32_t twice_scale(uint32_t scales, int i) {
     return __byte_perm(scales, 0, 0x4040 | i | i << 8) << 7;
 }
 
@@ -118,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __shared__ long long warp_sum[kThreads / 32];
     __shared__ float red_m[kWarps][8], red_l[kWarps][8];
     __shared__ float q_unit[8];                 // of the queries' halves, in base-2 score units
+    __shared__ float s_new[8], s_gate[8];       // the new token's scores, the gates
     __shared__ float2 freq[kHeadDim / 2], cs[kHeadDim / 2];
     __shared__ uint32_t new_codes[2][32];       // the new token's key and value, quantised
     __shared__ uint8_t new_scale[2][32];
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kWarps);
+            mbar_init(&empty[s], kWarps / 2);
         }
         for (int s = 0; s < kPairs; ++s) {
             mbar_init(&pair_full[s], 1);
@@ -214,8 +214,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 p.t1 = end ? wk.t0 : wk.t1;
                 p.c0 = static_cast<int>((wk.first + kPairCost) / share);
                 p.c1 = static_cast<int>((wk.first + wk.row.units() - 1) / share);
-                p.place = share * blockIdx.x < wk.first ? 1 : 0;  // not its first pair
-                p.first = wk.first;
+                p.second = share * p.c0 < wk.first ? 1 : 0;
                 if (end || !ok) {
                     mbar_arrive(&pair_full[s]);
                 } else {
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int tok = 4 * (row8 >> 1) + (row8 & 1);        // slot of row row8; row8 + 8: + 2
     // the heads of this thread's two columns
     const int h0 = kTwo ? 2 * (c4 & 1) : 2 * c4, h1 = h0 + 1;
-    for (int i = tid; i < 8 * (kHeadDim / 8); i += kWarps * 32)
+    for (int i = tid; i < kQBytes / 16; i += kWarps * 32)
         *reinterpret_cast<uint4 *>(qs + i * 16) = make_uint4(0, 0, 0, 0);
     if (tid < 8) q_unit[tid] = 0.f;
     int it = 0;
@@ -316,96 +315,89 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
     await_pair(0);
     for (int n = 0; !lost; ++n) {
-        // The next pair; its new token's projections: q of the group's heads,
-        // the key, the value, warp w taking rows w, w + 4, ... of them.
         const Pair &pair = pairs[n % kPairs];
-        const uint8_t *rows = new_rows + n % kPairs * kNewBytes;
         const int pos = pair.pos, lo = pair.lo, t0 = pair.t0, t1 = pair.t1;
         if (t0 >= t1) break;
-        const int b = pair.b, g = pair.g;
+        // The new token's projections: q of the group's heads (warp w takes w and
+        // w + 4), the value (warp 2), the key (warp 3).
+        const uint8_t *rows = new_rows + n % kPairs * kNewBytes;
         float gate[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int hq = warp + i * kRedHeads;
-            if (hq < P.G) gate[i] = P.gate[static_cast<size_t>(b) * P.H + g * P.G + hq];
+            if (hq < P.G)
+                gate[i] = P.gate[static_cast<size_t>(pair.b) * P.H + pair.g * P.G + hq];
         }
         if (tid < half) rope_cos_sin_fine(pos, freq[tid], cs[tid].x, cs[tid].y);
         consumer_bar();
-        // q, the new key and the new value of the warp's rows
         float q[2][8];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int hh = warp + i * kWarps;
-            if (hh >= P.G + 2) break;
+        for (int i = 0; i < 2; ++i) {
+            const int hh = warp + i * kRedHeads;
+            if (hh >= P.G) break;
+            // in halves, scaled by a power of two so that the largest is 1 to 2
             const uint4 raw = *reinterpret_cast<const uint4 *>(rows + hh * kRowBytes + lane * 16);
-            if (hh < P.G) {
-                // in halves, scaled by a power of two so that the largest is 1 to 2
-                float(&y)[8] = q[i & 1];
-                kv4_rotate(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, y);
-                float a = 0.f, z = 0.f;
+            float(&y)[8] = q[i];
+            kv4_rotate(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, y);
+            float a = 0.f, z = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    a = fmaxf(a, fabsf(y[j]));
-                    z += y[j] * 0.f;
-                }
+            for (int j = 0; j < 8; ++j) {
+                a = fmaxf(a, fabsf(y[j]));
+                z += y[j] * 0.f;
+            }
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) {
-                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-                    z += __shfl_xor_sync(0xffffffffu, z, off);
-                }
-                const unsigned e = __float_as_uint(a) >> 23;
-                const unsigned up = (e < 253u ? 254u - e : 1u) << 23;
-                const float f = __uint_as_float(up);
-                uint32_t hi[4], lo[4];
+            for (int off = 16; off > 0; off >>= 1) {
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+                z += __shfl_xor_sync(0xffffffffu, z, off);
+            }
+            const unsigned e = __float_as_uint(a) >> 23;
+            const unsigned up = (e < 253u ? 254u - e : 1u) << 23;
+            const float f = __uint_as_float(up);
+            uint32_t hi[4], rest[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // (z: a query that is not finite is NaN throughout)
-                    const float u = fmaf(y[2 * j], f, z), v = fmaf(y[2 * j + 1], f, z);
-                    hi[j] = pack_half2(u, v);
-                    lo[j] = pack_half2_rest(u, v, hi[j]);
-                }
-                *reinterpret_cast<uint4 *>(qs + hh * kHeadDim * 2 + lane * 16) =
-                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if (kTwo)
-                    *reinterpret_cast<uint4 *>(qs + (hh + 4) * kHeadDim * 2 + lane * 16) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                if (lane == 0)
-                    q_unit[hh] = kScaleLog2 * __uint_as_float((254u << 23) - up);
-            } else {
-                float y[8];
-                uint32_t codes;
-                unsigned byte;
-                const int v = hh - P.G;
-                if (v == 0) {
-                    kv4_key_row(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, pos,
-                                P.turns, y, codes, byte);
-                } else {
-                    kv4_value_row(raw, codes, byte);
-                    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[2 * j] = bf16_lo(w[j]);
-                        y[2 * j + 1] = bf16_hi(w[j]);
-                    }
-                }
-                float4 *dst = reinterpret_cast<float4 *>((v ? vn : kn) + lane * 8);
-                dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-                new_codes[v][lane] = codes;
-                new_scale[v][lane] = static_cast<uint8_t>(byte);
+            for (int j = 0; j < 4; ++j) {
+                // (z: a query that is not finite is NaN throughout)
+                const float u = fmaf(y[2 * j], f, z), v = fmaf(y[2 * j + 1], f, z);
+                hi[j] = pack_half2(u, v);
+                rest[j] = pack_half2_rest(u, v, hi[j]);
+            }
+            // in the order in which the lanes take B: dims 8 l .. are step
+            // 4 (l / 16) + l % 4 of lane 4 column + l % 16 / 4
+            uint8_t *dst = qs + (4 * (lane >> 4) + (lane & 3)) * 512 + (lane >> 2 & 3) * 16;
+            *reinterpret_cast<uint4 *>(dst + hh * 64) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (kTwo)
+                *reinterpret_cast<uint4 *>(dst + (hh + 4) * 64) =
+                    make_uint4(rest[0], rest[1], rest[2], rest[3]);
+            if (lane == 0) {
+                q_unit[hh] = kScaleLog2 * __uint_as_float((254u << 23) - up);
+                s_gate[hh] = gate[i];
             }
         }
+        if (warp >= 2) {
+            const int v = warp == 2;
+            const uint4 raw =
+                *reinterpret_cast<const uint4 *>(rows + (P.G + v) * kRowBytes + lane * 16);
+            float y[8];
+            uint32_t codes;
+            unsigned byte;
+            if (v) {
+                kv4_floats(raw, y);
+                kv4_value_row(y, codes, byte);
+            } else {
+                kv4_key_row(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, pos, P.turns, y,
+                            codes, byte);
+            }
+            float4 *dst = reinterpret_cast<float4 *>((v ? vn : kn) + lane * 8);
+            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+            new_codes[v][lane] = codes;
+            new_scale[v][lane] = static_cast<uint8_t>(byte);
+        }
         consumer_bar();
-        const int c0 = pair.c0, c1 = pair.c1, place = pair.place;
-        const long long first_unit = pair.first;
-        const int slot0 = lo & ~(kTile - 1);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pair_empty[n % kPairs]);
         // the new token's scores
-        float x_new[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (warp + i * kWarps >= P.G) break;
+            if (warp + i * kRedHeads >= P.G) break;
             const float4 ka = *reinterpret_cast<const float4 *>(kn + lane * 8);
             const float4 kb = *reinterpret_cast<const float4 *>(kn + lane * 8 + 4);
             float d = q[i][0] * ka.x;
@@ -418,84 +410,83 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             d = fmaf(q[i][7], kb.w, d);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-            x_new[i] = d * kScaleLog2;
+            if (lane == 0) s_new[warp + i * kRedHeads] = d * kScaleLog2;  // (this warp's alone)
         }
-        // Q^T as the B operand of S^T = K Q^T: 8 dims are two steps' (b0, b1)
-        uint32_t qf[16][2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(
-                qs + row8 * kHeadDim * 2 + (128 * (i >> 2) + 32 * c4 + 8 * (i & 3)) * 2);
-            qf[2 * i][0] = x.x;
-            qf[2 * i][1] = x.y;
-            qf[2 * i + 1][0] = x.z;
-            qf[2 * i + 1][1] = x.w;
-        }
-        const float unit0 = q_unit[h0], unit1 = q_unit[h1];
         float o[16][4];
 #pragma unroll
         for (int m = 0; m < 16; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         bool ok = !aborted;
+        // Two warps take the two halves of a tile, two groups of 16 slots each;
+        // the other two the next tile's.
         for (int t = t0; ok && t < t1; ++t, ++it) {
+            if ((it & 1) != warp >> 1) continue;
             const int s = it % kStages;
             ok = mbar_wait(&full[s], (it / kStages) & 1, &abort_flag, P.status);
             if (!ok) break;
-            const int first = slot0 + t * kTile + warp * kKv4Group;
-            if (first < pos && first + kKv4Group > lo) {
-                const uint8_t *kg = stages + s * kStageBytes + warp * kKv4GroupBytes;
+            const int first = (lo & ~(kTile - 1)) + t * kTile + (warp & 1) * 2 * kKv4Group;
+            if (first < pos && first + 2 * kKv4Group > lo) {
+                const uint8_t *kg = stages + s * kStageBytes + (warp & 1) * 2 * kKv4GroupBytes;
                 const uint8_t *vg = kg + kTileBytes;
-                // S^T (16 slots x 8 columns) = K (16 x 256) Q^T (256 x 8)
-                const uint32_t sa =
-                    *reinterpret_cast<const uint32_t *>(kg + kKv4Codes + tok * 16 + c4 * 4);
-                const uint32_t sb =
-                    *reinterpret_cast<const uint32_t *>(kg + kKv4Codes + tok * 16 + 32 + c4 * 4);
-                float sc[4][4];
+                // S^T (2 x 16 slots x 8 columns) = K (16 x 256) Q^T (256 x 8)
+                uint32_t sa[2], sb[2];
+                float sc[2][2][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+                for (int u = 0; u < 2; ++u) {
+                    const uint8_t *ks = kg + u * kKv4GroupBytes + kKv4Codes + tok * 16 + c4 * 4;
+                    sa[u] = *reinterpret_cast<const uint32_t *>(ks);
+                    sb[u] = *reinterpret_cast<const uint32_t *>(ks + 32);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[u][0][i] = sc[u][1][i] = 0.f;
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint4 ka =
-                        *reinterpret_cast<const uint4 *>(kg + h * 1024 + tok * 64 + c4 * 16);
-                    const uint4 kb =
-                        *reinterpret_cast<const uint4 *>(kg + h * 1024 + tok * 64 + 128 + c4 * 16);
-                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w};
-                    const uint32_t wb[4] = {kb.x, kb.y, kb.z, kb.w};
-                    const uint32_t ua[2] = {h ? twice_scale<2>(sa) : twice_scale<0>(sa),
-                                            h ? twice_scale<3>(sa) : twice_scale<1>(sa)};
-                    const uint32_t ub[2] = {h ? twice_scale<2>(sb) : twice_scale<0>(sb),
-                                            h ? twice_scale<3>(sb) : twice_scale<1>(sb)};
+                    uint32_t wa[2][4], wb[2][4];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint8_t *kc = kg + u * kKv4GroupBytes + h * 1024 + tok * 64 + c4 * 16;
+                        const uint4 ka = *reinterpret_cast<const uint4 *>(kc);
+                        const uint4 kb = *reinterpret_cast<const uint4 *>(kc + 128);
+                        wa[u][0] = ka.x, wa[u][1] = ka.y, wa[u][2] = ka.z, wa[u][3] = ka.w;
+                        wb[u][0] = kb.x, wb[u][1] = kb.y, wb[u][2] = kb.z, wb[u][3] = kb.w;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t a[4], b[4];
-                        kv4_widen(wa[i], a);
-                        kv4_widen(wb[i], b);
+                        const uint4 qf = *reinterpret_cast<const uint4 *>(
+                            qs + (4 * h + i) * 512 + lane * 16);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            a[j] = mul_half2(a[j], ua[i >> 1]);
-                            b[j] = mul_half2(b[j], ub[i >> 1]);
+                        for (int u = 0; u < 2; ++u) {
+                            const uint32_t ua = twice_scale(sa[u], 2 * h + (i >> 1));
+                            const uint32_t ub = twice_scale(sb[u], 2 * h + (i >> 1));
+                            uint32_t a[4], b[4];
+                            kv4_widen(wa[u][i], a);
+                            kv4_widen(wb[u][i], b);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                a[j] = mul_half2(a[j], ua);
+                                b[j] = mul_half2(b[j], ub);
+                            }
+                            mma_f16_16816(sc[u][0], a[0], b[0], a[1], b[1], qf.x, qf.y);
+                            mma_f16_16816(sc[u][1], a[2], b[2], a[3], b[3], qf.z, qf.w);
                         }
-                        const int ks = 8 * h + 2 * i;
-                        mma_f16_16816(sc[2 * (i & 1)], a[0], b[0], a[1], b[1], qf[ks][0],
-                                      qf[ks][1]);
-                        mma_f16_16816(sc[2 * (i & 1) + 1], a[2], b[2], a[3], b[3], qf[ks + 1][0],
-                                      qf[ks + 1][1]);
                     }
                 }
-                float x[4];
+                const float unit0 = q_unit[h0], unit1 = q_unit[h1];
+                // this thread's slots (rows row8 and row8 + 8 of both) and heads
+                float x[2][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = (sc[0][i] + sc[1][i]) + (sc[2][i] + sc[3][i]);
-                    if (kTwo) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[u][i] = sc[u][0][i] + sc[u][1][i];
+                        if (kTwo) x[u][i] += __shfl_xor_sync(0xffffffffu, x[u][i], 2);
+                        const int slot = first + u * kKv4Group + tok + (i & 2);
+                        x[u][i] = slot >= lo && slot < pos ? x[u][i] * (i & 1 ? unit1 : unit0)
+                                                           : -INFINITY;
+                    }
                 }
-                // this thread's slots (rows row8 and row8 + 8) and heads
-                const bool va = first + tok >= lo && first + tok < pos;
-                const bool vb = first + tok + 2 >= lo && first + tok + 2 < pos;
-                x[0] = va ? x[0] * unit0 : -INFINITY;
-                x[1] = va ? x[1] * unit1 : -INFINITY;
-                x[2] = vb ? x[2] * unit0 : -INFINITY;
-                x[3] = vb ? x[3] * unit1 : -INFINITY;
-                float n0 = fmaxf(x[0], x[2]), n1 = fmaxf(x[1], x[3]);
+                float n0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+                float n1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
@@ -519,52 +510,80 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     m1 = n1;
                 }
                 const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-                const float p0 = fast_exp2(x[0] - z0), p1 = fast_exp2(x[1] - z1);
-                const float p2 = fast_exp2(x[2] - z0), p3 = fast_exp2(x[3] - z1);
-                l0 += p0 + p2;
-                l1 += p1 + p3;
                 // P^T as the B operand of O^T += V^T P^T; the last columns take
                 // what the halves of the first leave
-                uint32_t pa = pack_half2(p0, p1), pb = pack_half2(p2, p3);
-                if (kTwo) {
-                    const uint32_t ra = pack_half2_rest(p0, p1, pa);
-                    const uint32_t rb = pack_half2_rest(p2, p3, pb);
-                    pa = c4 & 2 ? ra : pa;
-                    pb = c4 & 2 ? rb : pb;
+                uint32_t pt[2][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float p0 = fast_exp2(x[u][0] - z0), p1 = fast_exp2(x[u][1] - z1);
+                    const float p2 = fast_exp2(x[u][2] - z0), p3 = fast_exp2(x[u][3] - z1);
+                    l0 += p0 + p2;
+                    l1 += p1 + p3;
+                    uint32_t pa = pack_half2(p0, p1), pb = pack_half2(p2, p3);
+                    if (kTwo) {
+                        const uint32_t ra = pack_half2_rest(p0, p1, pa);
+                        const uint32_t rb = pack_half2_rest(p2, p3, pb);
+                        pa = c4 & 2 ? ra : pa;
+                        pb = c4 & 2 ? rb : pb;
+                    }
+                    pt[u][0] = movmatrix_trans(pa);
+                    pt[u][1] = movmatrix_trans(pb);
                 }
-                pa = movmatrix_trans(pa);
-                pb = movmatrix_trans(pb);
-                uint2 sv = *reinterpret_cast<const uint2 *>(vg + kKv4Codes + lane * 8);
-                if (first < lo || first + kKv4Group > pos) {
-                    // Slots that hold no visible token may hold anything: a
-                    // scale of zero makes zeros of it.
-                    uint32_t seen = 0;
+                const bool edge = first < lo || first + 2 * kKv4Group > pos;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint8_t *vu = vg + u * kKv4GroupBytes;
+                    uint2 sv = *reinterpret_cast<const uint2 *>(vu + kKv4Codes + lane * 8);
+                    if (edge) {
+                        // Slots that hold no visible token may hold anything: a
+                        // scale of zero makes zeros of it.
+                        uint32_t seen = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int slot = first + u * kKv4Group + 4 * c4 + j;
+                            if (slot >= lo && slot < pos)
+                                seen |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
+                        }
+                        sv.x &= seen;
+                        sv.y &= seen;
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int slot = first + 4 * c4 + j;
-                        if (slot >= lo && slot < pos)
-                            seen |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
-                    }
-                    sv.x &= seen;
-                    sv.y &= seen;
-                }
+                        const uint4 v = *reinterpret_cast<const uint4 *>(vu + j * 512 + lane * 16);
+                        const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+                        const uint32_t w = j >> 1 ? sv.y : sv.x;
+                        const uint32_t u0 = (w & 0x00ff00ffu) << 7, u1 = (w >> 1) & 0x7f807f80u;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(vg + j * 512 + lane * 16);
-                    const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
-                    const uint32_t u = j >> 1 ? sv.y : sv.x;
-                    const uint32_t u0 = (u & 0x00ff00ffu) << 7, u1 = (u >> 1) & 0x7f807f80u;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t a[4];
-                        kv4_widen(wv[i], a);
-                        mma_f16_16816(o[4 * j + i], mul_half2(a[0], u0), mul_half2(a[1], u0),
-                                      mul_half2(a[2], u1), mul_half2(a[3], u1), pa, pb);
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t a[4];
+                            kv4_widen(wv[i], a);
+                            mma_f16_16816(o[4 * j + i], mul_half2(a[0], u0), mul_half2(a[1], u0),
+                                          mul_half2(a[2], u1), mul_half2(a[3], u1), pt[u][0],
+                                          pt[u][1]);
+                        }
                     }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
+        }
+        // Where the new token goes; read now, written when the pair is finished.
+        const int t_new = pos & 15;
+        uint8_t *k_new = nullptr, *v_new = nullptr;
+        unsigned old[4] = {0, 0, 0, 0};
+        if (warp == 0) {
+            const int id = P.pg.table[static_cast<size_t>(pair.b) * P.pg.max_pages +
+                                      (pos >> P.pg.page_shift)];
+            if (id >= 0 && id < P.pg.n_pages) {
+                const size_t at = P.pg.group(id, pair.g, P.Hkv, pos);
+                k_new = P.pg.k + at;
+                v_new = P.pg.v + at;
+                const uint8_t *src =
+                    v_new + kv4_value_at(lane, t_new >> 2) + 2 * (t_new >> 1 & 1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    old[j] = *reinterpret_cast<const uint16_t *>(src + 4 * j);
+            }
         }
 
         // ------------------------------------------------------ join the warps
@@ -650,65 +669,74 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
 
         // ------------------------------------------------------ finish or hand over
+        // A pair of one CTA is finished.  Of others the states are joined in two
+        // steps, kFan of them and then what those leave, each by the CTA that
+        // counts last; in the order of the CTAs, so that the result does not
+        // depend on which one that is.
+        const int c0 = pair.c0, c1 = pair.c1, second = pair.second;
         bool finish = c0 == c1;
         if (!finish) {
-            // this CTA's partial state, then the count
+            const int me = static_cast<int>(blockIdx.x);
+            auto place = [&](int cta) { return 2 * cta + (cta == c0 ? second : 0); };
+            auto leave = [&](int cta) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int hq = warp + i * kRedHeads;
-                if (hq >= P.G) break;
-                const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + place) * P.G + hq;
-                float4 *dst = reinterpret_cast<float4 *>(P.part_o + at * kHeadDim + lane * 8);
-                dst[0] = make_float4(st[i].o[0], st[i].o[1], st[i].o[2], st[i].o[3]);
-                dst[1] = make_float4(st[i].o[4], st[i].o[5], st[i].o[6], st[i].o[7]);
-                if (lane == 0)
-                    reinterpret_cast<float2 *>(P.part_ml)[at] = make_float2(st[i].m, st[i].l);
-            }
-            __threadfence();
-            consumer_bar();
-            if (tid == 0) {
-                // c0 is the first CTA of one shared pair at most, which the
-                // counter is named by
-                last_cta = atomicAdd(P.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
-                // everyone has counted: back to 0 for the next call
-                if (last_cta) P.counters[c0] = 0;
-            }
-            consumer_bar();
-            finish = last_cta != 0;
-            if (finish) {
-                __threadfence();  // the others' states are read after the count
+                for (int i = 0; i < 2; ++i) {
+                    const int hq = warp + i * kRedHeads;
+                    if (hq >= P.G) break;
+                    const size_t at = static_cast<size_t>(place(cta)) * P.G + hq;
+                    float4 *dst = reinterpret_cast<float4 *>(P.part_o + at * kHeadDim + lane * 8);
+                    dst[0] = make_float4(st[i].o[0], st[i].o[1], st[i].o[2], st[i].o[3]);
+                    dst[1] = make_float4(st[i].o[4], st[i].o[5], st[i].o[6], st[i].o[7]);
+                    if (lane == 0)
+                        reinterpret_cast<float2 *>(P.part_ml)[at] = make_float2(st[i].m, st[i].l);
+                }
+                __threadfence();
+                consumer_bar();
+            };
+            // Whether this CTA is the last of `all` to count.
+            auto last = [&](unsigned *counter, int all) {
+                if (tid == 0) {
+                    last_cta = atomicAdd(counter, 1u) == static_cast<unsigned>(all - 1);
+                    // everyone has counted: back to 0 for the next call
+                    if (last_cta) *counter = 0;
+                }
+                consumer_bar();
+                const bool mine = last_cta != 0;
+                if (mine) __threadfence();  // the others' states are read after the count
+                consumer_bar();             // (last_cta is read)
+                return mine;
+            };
+            // The states of CTAs from, from + step, .. up to `to`.
+            auto join = [&](int from, int to, int step) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int hq = warp + i * kRedHeads;
                     if (hq >= P.G) break;
                     HeadState &h = st[i];
-                    auto at = [&](int cta) {
-                        const int pl = static_cast<long long>(cta) * share < first_unit ? 1 : 0;
-                        return (static_cast<size_t>(cta) * 2 + pl) * P.G + hq;
-                    };
-                    // kJoin states at a time, all their loads in flight
                     h.m = -INFINITY;
                     h.l = 0.f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) h.o[j] = 0.f;
-                    for (int cta = c0; cta <= c1; cta += kJoin) {
-                        float2 ml[kJoin];
-                        float4 x[kJoin], y[kJoin];
+                    for (int cta = from; cta <= to; cta += kFan * step) {
+                        float2 ml[kFan];
+                        float4 x[kFan], y[kFan];
 #pragma unroll
-                        for (int k = 0; k < kJoin; ++k) {
+                        for (int k = 0; k < kFan; ++k) {
                             ml[k] = make_float2(-INFINITY, 0.f);
                             x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (cta + k > c1) continue;
-                            const size_t a = at(cta + k);
-                            ml[k] = __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + a);
-                            const float4 *src = reinterpret_cast<const float4 *>(
-                                P.part_o + a * kHeadDim + lane * 8);
-                            x[k] = __ldcg(src);
-                            y[k] = __ldcg(src + 1);
+                            const int from_cta = cta + k * step;
+                            if (from_cta <= to) {
+                                const size_t a = static_cast<size_t>(place(from_cta)) * P.G + hq;
+                                ml[k] = __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + a);
+                                const float4 *src = reinterpret_cast<const float4 *>(
+                                    P.part_o + a * kHeadDim + lane * 8);
+                                x[k] = __ldcg(src);
+                                y[k] = __ldcg(src + 1);
+                            }
                         }
                         float m = h.m;
 #pragma unroll
-                        for (int k = 0; k < kJoin; ++k) m = fmaxf(m, ml[k].x);
+                        for (int k = 0; k < kFan; ++k) m = fmaxf(m, ml[k].x);
                         const float z = m == -INFINITY ? 0.f : m;
                         const float wo = fast_exp2(h.m - z);
                         h.m = m;
@@ -716,13 +744,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) h.o[j] *= wo;
 #pragma unroll
-                        for (int k = 0; k < kJoin; ++k) {
+                        for (int k = 0; k < kFan; ++k) {
                             const float w = fast_exp2(ml[k].x - z);
                             const float v[8] = {x[k].x, x[k].y, x[k].z, x[k].w,
                                                 y[k].x, y[k].y, y[k].z, y[k].w};
                             h.l += ml[k].y * w;
                             add_scaled(h, w, v);
                         }
+                    }
+                }
+            };
+            const int sub = (me - c0) / kFan, subs = (c1 - c0) / kFan + 1;
+            const int from = c0 + sub * kFan, to = from + kFan - 1 < c1 ? from + kFan - 1 : c1;
+            leave(me);
+            if (last(P.counters + place(from), to - from + 1)) {
+                join(from, to, 1);
+                finish = subs == 1;
+                if (!finish) {
+                    leave(from);
+                    // (c0 is the first CTA of one shared pair at most)
+                    if (last(P.counters + 2 * gridDim.x + c0, subs)) {
+                        join(c0, c1, kFan);
+                        finish = true;
                     }
                 }
             }
@@ -734,15 +777,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const int hq = warp + i * kRedHeads;
                 if (hq >= P.G) break;
                 HeadState &h = st[i];
-                const int head = g * P.G + hq;
+                const float x_new = s_new[hq];
                 const float4 va = *reinterpret_cast<const float4 *>(vn + lane * 8);
                 const float4 vb = *reinterpret_cast<const float4 *>(vn + lane * 8 + 4);
                 const float v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-                const float m = fmaxf(h.m, x_new[i]);
+                const float m = fmaxf(h.m, x_new);
                 const float z = m == -INFINITY ? 0.f : m;
                 const float wo = h.m == -INFINITY ? 1.f : fast_exp2(h.m - z);
-                const float wn = fast_exp2(x_new[i] - z);
-                const float scale = gate_act(gate[i], P.gate_mode) / (h.l * wo + wn);
+                const float wn = fast_exp2(x_new - z);
+                const float scale = gate_act(s_gate[hq], P.gate_mode) / (h.l * wo + wn);
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -751,43 +794,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     if (!isfinite(v[j])) y[j] = (v[j] + nonfinite_part(h.o[j])) * scale;
                 }
                 *reinterpret_cast<uint4 *>(
-                    P.out + (static_cast<size_t>(b) * P.H + head) * kHeadDim + lane * 8) =
-                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                               pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+                    P.out +
+                    (static_cast<size_t>(pair.b) * P.H + pair.g * P.G + hq) * kHeadDim +
+                    lane * 8) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
             }
             if (warp == 0) {
                 // the new token's slot: every read of this pair is done
-                const int id = P.pg.table[static_cast<size_t>(b) * P.pg.max_pages +
-                                          (pos >> P.pg.page_shift)];
-                const int t = pos & 15;
-                if (id < 0 || id >= P.pg.n_pages) {
+                if (!k_new) {
                     if (lane == 0) atomicOr(P.status, kErrPage);
                 } else {
-                    const size_t at = P.pg.group(id, g, P.Hkv, pos);
-                    *reinterpret_cast<uint32_t *>(P.pg.k + at + kv4_key_at(lane, t)) =
+                    *reinterpret_cast<uint32_t *>(k_new + kv4_key_at(lane, t_new)) =
                         new_codes[0][lane];
                     // the other slot of each byte stays
                     const uint32_t codes = new_codes[1][lane];
-                    uint8_t *dst = P.pg.v + at + kv4_value_at(lane, t >> 2) + 2 * (t >> 1 & 1);
-                    unsigned old[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        old[j] = *reinterpret_cast<const uint16_t *>(dst + 4 * j);
+                    uint8_t *dst = v_new + kv4_value_at(lane, t_new >> 2) + 2 * (t_new >> 1 & 1);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const unsigned pair = codes >> (8 * j);
-                        const unsigned n = (pair & 15u) | (pair & 0xf0u) << 4;
+                        const unsigned two = codes >> (8 * j);
+                        const unsigned c = (two & 15u) | (two & 0xf0u) << 4;
                         *reinterpret_cast<uint16_t *>(dst + 4 * j) = static_cast<uint16_t>(
-                            t & 1 ? (old[j] & 0x0f0fu) | n << 4 : (old[j] & 0xf0f0u) | n);
+                            t_new & 1 ? (old[j] & 0x0f0fu) | c << 4 : (old[j] & 0xf0f0u) | c);
                     }
                     if (!(lane & 1)) {
-                        P.pg.k[at + kv4_key_scale_at(lane >> 1, t)] = new_scale[0][lane];
-                        P.pg.v[at + kv4_value_scale_at(lane >> 1, t >> 2) + 2 * (t & 1) +
-                               (t >> 1 & 1)] = new_scale[1][lane];
+                        k_new[kv4_key_scale_at(lane >> 1, t_new)] = new_scale[0][lane];
+                        v_new[kv4_value_scale_at(lane >> 1, t_new >> 2) + 2 * (t_new & 1) +
+                              (t_new >> 1 & 1)] = new_scale[1][lane];
                     }
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair_empty[n % kPairs]);
         await_pair(n + 1);  // (q, the new token and the sums are read)
     }
     grid_dep_launch();

@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
                 for (int j = 0; j < 4; ++j) {
                     const int t = 4 * quad + j;
                     unsigned byte;
-                    kv4_value_row(raw[j], codes[j], byte);
+                    float x[8];
+                    kv4_floats(raw[j], x);
+                    kv4_value_row(x, codes[j], byte);
                     scales |= byte << (8 * (2 * (j & 1) + (j >> 1)));
                     if (t < t_lo || t >= t_hi) {
                         keep |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
@@ -375,8 +377,9 @@ void set_pages(Kv4Params &P, void *k4, void *v4, int n_pages, int page_size, con
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Workspace of a decode: the header, a counter per CTA (of the finished parts of
-// a shared pair; every call leaves them at 0), two partial states per CTA.
+// Workspace of a decode: the header; counters of states left (one per place, one
+// per CTA that is the first of a shared pair; every call leaves them at 0); two
+// partial states per CTA.
 struct DecodeKv4Plan {
     int grid;
     size_t counters, ml, o, bytes;
@@ -387,7 +390,7 @@ DecodeKv4Plan plan_decode_kv4(int H, int Hkv, int sms) {
     pl.grid = decode_kv4_ctas(sms);
     const size_t parts = static_cast<size_t>(pl.grid) * 2 * (H / Hkv);
     pl.counters = kWorkspaceHeader;
-    pl.ml = pl.counters + up256(static_cast<size_t>(pl.grid) * 4);
+    pl.ml = pl.counters + up256(static_cast<size_t>(pl.grid) * 3 * 4);
     pl.o = pl.ml + up256(parts * 2 * 4);
     pl.bytes = pl.o + up256(parts * kHeadDim * 4);
     return pl;

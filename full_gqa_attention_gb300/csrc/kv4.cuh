@@ -165,28 +165,39 @@ __device__ __forceinline__ float kv4_block_max(const float (&x)[8], bool &finite
     return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
 }
 
-// A value's row: bf16, so that the quotients round as exact ones would (x / s
-// lies on a border between two codes, where 32 bits hold it, or 2^-12 of itself
-// away from it; so does max / 6).
-__device__ __forceinline__ void kv4_value_row(const uint4 &raw, uint32_t &codes, unsigned &byte) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
+// What an exact quotient by a scale (or by 6) rounds to is told by one that is
+// off by 2^-22, where the number divided is bf16: the quotient lies on a border
+// between two codes (or scales), which have few bits, or 2^-9 of itself away
+// from it.  Sixteen bits of it are kept.
+__device__ __forceinline__ float kv4_snap(float y) {
+    return __uint_as_float((__float_as_uint(y) + 0x80u) & 0xffffff00u);
+}
+
+constexpr float kSixth = 1.0f / 6.0f;
+
+// A value's row.
+__device__ __forceinline__ void kv4_value_row(const float (&x)[8], uint32_t &codes,
+                                              unsigned &byte) {
     bool finite;
     const float a = kv4_block_max(x, finite);
-    byte = kv4_scale_byte(__fdiv_rn(a, 6.f));
-    const float s = kv4_scale(byte);
+    byte = kv4_scale_byte(kv4_snap(a * kSixth));
+    const float s = kv4_scale(byte), r = s > 0.f ? __frcp_rn(s) : 0.f;
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = s > 0.f ? __fdiv_rn(x[i], s) : 0.f;
+    for (int i = 0; i < 8; ++i) y[i] = kv4_snap(x[i] * r);
     codes = kv4_codes(y);
     if (!finite) {
         codes = 0;
         byte = kKv4NanScale;
+    }
+}
+
+__device__ __forceinline__ void kv4_floats(const uint4 &raw, float (&x)[8]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
     }
 }
 
@@ -229,55 +240,72 @@ __device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float2 *cs, f
     }
 }
 
-// Value i of a turned key in 64 bits.
-__device__ __noinline__ inline double kv4_exact_turn(float x, float z, bool upper, int pos, double u) {
+// Value i of a turned key in 64 bits: sine and cosine by their series, to
+// x^15 / 15!, of an angle of an eighth of a turn at most (1e-15).  64-bit
+// products are few on this chip: each takes a warp 16 cycles.
+__device__ __noinline__ inline double kv4_exact_turn(float x, float z, bool upper, int pos,
+                                                     double u) {
     const double p = pos * u;
     const double t = (p - rint(p)) + fma(static_cast<double>(pos), u, -p);
-    double s, c;
-    sincospi(2.0 * t, &s, &c);
-    return upper ? x * c + z * s : x * c - z * s;
+    const double quarter = rint(4.0 * t);
+    const double a = (t - 0.25 * quarter) * 6.283185307179586476925286766559, a2 = a * a;
+    double s = -1.0 / 1307674368000.0, c = -1.0 / 87178291200.0;
+    s = fma(s, a2, 1.0 / 6227020800.0);
+    c = fma(c, a2, 1.0 / 479001600.0);
+    s = fma(s, a2, -1.0 / 39916800.0);
+    c = fma(c, a2, -1.0 / 3628800.0);
+    s = fma(s, a2, 1.0 / 362880.0);
+    c = fma(c, a2, 1.0 / 40320.0);
+    s = fma(s, a2, -1.0 / 5040.0);
+    c = fma(c, a2, -1.0 / 720.0);
+    s = fma(s, a2, 1.0 / 120.0);
+    c = fma(c, a2, 1.0 / 24.0);
+    s = fma(s, a2, -1.0 / 6.0);
+    c = fma(c, a2, -0.5);
+    s = fma(s * a2, a, a);
+    c = fma(c, a2, 1.0);
+    const int q = static_cast<int>(quarter) & 3;  // turned on by quarters
+    const double cq = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
+    const double sq = q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c;
+    return upper ? x * cq + z * sq : x * cq - z * sq;
 }
 
-// Settles what 32 bits leave open of a key's row: its scales where `open_scale`,
-// and the codes of the dims in `open`, from the rotation in 64 bits.  All lanes
-// of the warp; `open_scale` is the same in the two lanes of a block.
-__device__ __noinline__ inline void kv4_settle(const KeyTurn &t, int pos, const double *turns,
-                                        bool open_scale, unsigned open, uint32_t &codes,
-                                        unsigned &byte) {
-    auto exact = [&](int i) {
-        return t.turns ? kv4_exact_turn(t.x[i], t.z[i], t.upper, pos, turns[t.k0 + i])
-                       : static_cast<double>(t.x[i]);
-    };
-    if (__any_sync(0xffffffffu, open_scale)) {
-        double a = 0.0;
-        if (open_scale) {
-            open = 0xff;
-            for (int i = 0; i < 8; ++i) a = fmax(a, fabs(exact(i)));
-        }
-        a = fmax(a, __shfl_xor_sync(0xffffffffu, a, 1));
-        if (open_scale) {
-            // the two scales around a / 6, and their middle
-            const double want = a / 6.0;
-            unsigned lo = kv4_scale_byte(static_cast<float>(want));
-            if (lo > 0 && kv4_scale(lo) > want) --lo;
-            byte = lo;
-            if (lo < kKv4MaxScale) {
-                const double mid = 0.5 * (static_cast<double>(kv4_scale(lo)) + kv4_scale(lo + 1));
-                if (want > mid || (want == mid && (lo & 1u))) byte = lo + 1;
-            }
-        }
-    }
-    const double s = kv4_scale(byte);
+// Settles the scale of the blocks in `open` (the same in a block's two lanes)
+// in 64 bits, from the values that can be its largest.  All lanes.
+__device__ __noinline__ inline unsigned kv4_settle_scale(const KeyTurn &t, int pos,
+                                                         const double *turns, const float (&y)[8],
+                                                         float least, bool open, unsigned byte) {
+    // (a block whose dims nearly cancel in their turn can have any scale)
+    double a = 0.0;
+    if (open)
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(y[i]) >= least)
+                a = fmax(a, fabs(kv4_exact_turn(t.x[i], t.z[i], t.upper, pos, turns[t.k0 + i])));
+    a = fmax(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    if (!open) return byte;
+    // the scale below a / 6, the next one, and their middle
+    unsigned lo = kv4_scale_byte(static_cast<float>(a / 6.0));
+    if (lo > 0 && 6.0 * kv4_scale(lo) > a) --lo;
+    if (lo == kKv4MaxScale) return lo;
+    const double mid = 3.0 * (static_cast<double>(kv4_scale(lo)) + kv4_scale(lo + 1));
+    return a > mid || (a == mid && (lo & 1u)) ? lo + 1 : lo;
+}
+
+// Settles the codes of the dims in `open`, in 64 bits.
+__device__ __noinline__ inline uint32_t kv4_settle_codes(const KeyTurn &t, int pos,
+                                                         const double *turns, float scale,
+                                                         unsigned open, uint32_t codes) {
+    const double s = scale;
     for (int i = 0; i < 8; ++i) {
-        if (!(open >> i & 1u)) continue;
-        const double v = exact(i), m = fabs(v);
-        unsigned c = 0;
-        if (s > 0.0)
-            c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) +
-                (m > 2.5 * s) + (m >= 3.5 * s) + (m > 5.0 * s);
+        if (!(open >> (4 * i) & 1u)) continue;
+        const double v = kv4_exact_turn(t.x[i], t.z[i], t.upper, pos, turns[t.k0 + i]);
+        const double m = fabs(v);
+        unsigned c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) +
+                     (m > 2.5 * s) + (m >= 3.5 * s) + (m > 5.0 * s);
         if (v < 0.0) c |= 8u;
         codes = (codes & ~(15u << (4 * i))) | c << (4 * i);
     }
+    return codes;
 }
 
 // A key's row, rotated (y, in 32 bits) and quantised.  What the pages hold is
@@ -286,11 +314,11 @@ __device__ __noinline__ inline void kv4_settle(const KeyTurn &t, int pos, const 
 // |y| is off by 2^-22 (|x| + |z|) at most: cos and sin by 2^-23 each (1 ulp of
 // sincospif, and 2^-24 that the frequencies' two parts leave of the angle below
 // 2^24 positions), the product and the sum by 2^-24 each.  Twice that is allowed.
-// Dims that do not turn are bf16 and lie on borders often; they divide exactly,
-// as a value's do.
+// Dims that do not turn are bf16: kv4_snap.
 __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float2 *cs, int pos,
                                             const double *turns, float (&y)[8], uint32_t &codes,
                                             unsigned &byte) {
+    constexpr float kRel = 2.38418579e-7f, kAbs = 4.76837158e-7f;  // 2^-22, 2^-21
     kv4_rotate(t, cs, y);
     bool finite;
     const float a = kv4_block_max(y, finite);
@@ -298,37 +326,32 @@ __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float2 *cs, 
     if (t.turns)
 #pragma unroll
         for (int i = 0; i < 8; ++i) e = fmaxf(e, fabsf(t.x[i]) + fabsf(t.z[i]));
-    e *= 4.76837158e-7f;  // 2^-21
+    e *= kAbs;
     const float other = __shfl_xor_sync(0xffffffffu, e, 1);  // (a block turns as a whole)
-    const float most = t.turns ? fmaf(a, 2.38418579e-7f, fmaxf(e, other)) : 0.f;
-    byte = kv4_scale_byte(__fdiv_rn(fmaxf(a - most, 0.f), 6.f));
-    const bool open_scale = byte != kv4_scale_byte(__fdiv_rn(a + most, 6.f));
-    const float s = kv4_scale(byte);
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    const float most = t.turns ? fmaf(a, kRel, fmaxf(e, other)) : 0.f;
+    const float lo_a = fmaxf(a - most, 0.f) * kSixth, hi_a = (a + most) * kSixth;
+    byte = kv4_scale_byte(t.turns ? lo_a : kv4_snap(lo_a));
+    const bool open_scale = t.turns && finite && byte != kv4_scale_byte(hi_a);
+    if (__any_sync(0xffffffffu, open_scale))
+        byte = kv4_settle_scale(t, pos, turns, y, a - 2.f * most, open_scale, byte);
+    const float s = kv4_scale(byte), r = s > 0.f ? __frcp_rn(s) : 0.f;
     float lo[8], hi[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = t.turns ? y[i] * r : s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
-        const float d = t.turns ? __fmaf_rn(fabsf(q), 2.38418579e-7f, e * r) : 0.f;
-        lo[i] = q - d;
-        hi[i] = q + d;
+        const float q = y[i] * r, d = __fmaf_rn(fabsf(q), kRel, e * r);
+        lo[i] = t.turns ? q - d : kv4_snap(q);
+        hi[i] = t.turns ? q + d : lo[i];
     }
     codes = kv4_codes(hi);
     // (a sign that differs beside zero stands for the same value)
-    unsigned differ = codes ^ kv4_codes(lo);
-    differ = (differ | differ >> 1 | differ >> 2) & 0x11111111u;
+    unsigned open = codes ^ kv4_codes(lo);
+    open = (open | open >> 1 | open >> 2) & 0x11111111u;
     if (!finite) {
-        codes = 0;
+        codes = open = 0;
         byte = kKv4NanScale;
-        differ = 0;
     }
-    const bool settle = differ != 0 || (open_scale && finite);
-    if (__any_sync(0xffffffffu, settle)) {
-        unsigned open = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) open |= (differ >> (4 * i) & 1u) << i;
-        kv4_settle(t, pos, turns, open_scale && finite, open, codes, byte);
-    }
+    if (__any_sync(0xffffffffu, open != 0))
+        codes = kv4_settle_codes(t, pos, turns, s, open, codes);
 }
 
 }  // namespace spark
