@@ -9,18 +9,29 @@
 //
 // The work is shared out as the bf16 step's is (decode_paged.cu): the tiles of
 // 64 slots of all pairs are one list, every CTA takes its stretch of it, and a
-// pair that several CTAs share is joined by the one that arrives last, in the
-// order of the CTAs.  No CTA waits for another.  Two CTAs per SM: one warp each
-// feeds a ring of stages by bulk copies, as many bytes of a page as the row
-// sees; four warps take 16 slots of a tile each.
+// pair that several CTAs share is joined by those that arrive last, in the order
+// of the CTAs.  No CTA waits for another.  Three CTAs per SM: one warp each feeds
+// a ring of stages by bulk copies, as many bytes of a page as the row sees; four
+// warps compute.
 //
 // Widening 4 bits is what the SM has to do besides: a code pair is one
 // conversion to two halves and one product with the scale, exact, in the
 // registers in which the matrix instructions take them (the pages hold the
 // operands' order).  Keys and values are the instructions' A operand, 16 slots
-// or dims; B has 8 columns, which hold up to 4 heads as a sum of two halves
-// each (22 bits of a query or a probability), or 8 heads as one half (11 bits,
-// where a second product would cost as much as the widening).
+// or dims.  A warp takes 16 slots' scores, and after a barrier a quarter of the
+// dims of all 64 slots' values: sums over all dims in every warp would take 64
+// registers a thread instead of 16, and with fewer warps on an SM the latency of
+// a tile's chain -- scores, maximum, exponentials, products -- shows (71 us
+// instead of 54 for 262,139 tokens).  So there is nothing to join over the warps either.
+//
+// B has 8 columns.  Up to 4 heads' queries are a sum of two halves each (22
+// bits), in two columns; 8 heads' are one half each (11 bits).  Probabilities are
+// one half: their roundings are independent and 16 times smaller than that of the
+// output.  They are taken relative to a reference that all warps share, the
+// largest score so far or up to 2^4 less, so that most tiles need neither a
+// maximum over the warps nor a second barrier; they are times 2^11, so that none
+// overflows, all of more than 2^-25 of the largest have 11 bits, and smaller ones
+// are off by 2^-36 of it.  Their sums are of the same ones in 32 bits.
 #include "decode_walk.cuh"
 #include "kv4.cuh"
 
@@ -28,23 +39,29 @@ namespace spark {
 
 namespace {
 
-constexpr int kPairCost = 3;
+constexpr int kPairCost = 6;
 constexpr int kTile = 64;                                 // slots per stage
-constexpr int kStages = 4;
-constexpr int kWarps = 4;                                 // consumers, a group of 16 slots each
+constexpr int kStages = 3;
+constexpr int kWarps = 4;                                 // consumers
 constexpr int kThreads = (kWarps + 1) * 32;               // + one producer warp
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 3;
 constexpr int kTileBytes = kTile * kKv4TokenBytes;        // K or V
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kQBytes = 8 * kHeadDim * 2;                 // 8 columns
 constexpr int kRowBytes = kHeadDim * 2;
-constexpr int kNewBytes = 10 * kRowBytes;                 // a pair's new token: q, key, value
 constexpr int kPairs = 2;                                 // pairs handed over at a time
 constexpr int kFan = 8;                                   // partial states joined at once
-constexpr int kRedHeads = 4;                              // heads reduced over the warps at once
-constexpr int kRedBytes = kWarps * kRedHeads * kHeadDim * 4;
-constexpr int kSmemBytes = 128 + kStages * kStageBytes + kPairs * kNewBytes + kQBytes + kRedBytes +
-                           2 * kHeadDim * 4;
+constexpr int kProbBytes = 2 * kWarps * 32 * 8;           // two tiles' probabilities
+constexpr float kHeadroom = 4.f;                          // scores may pass the reference by this
+constexpr float kProbShift = 11.f;                        // probabilities are times 2^11
+
+// Shared memory: the stages, a pair's new token (q of `heads` heads, key, value)
+// twice, the queries' halves, two tiles' probabilities, the new key and value.
+__host__ __device__ constexpr int new_bytes(int heads) { return (heads + 2) * kRowBytes; }
+__host__ __device__ constexpr int smem_bytes(int heads) {
+    return kStages * kStageBytes + kPairs * new_bytes(heads) + kQBytes + kProbBytes +
+           2 * kHeadDim * 4;
+}
 
 using Row = DecodeRow<kTile, kPairCost>;
 using Walk = DecodeWalk<kTile, kPairCost>;
@@ -88,34 +105,32 @@ __device__ __forceinline__ uint32_t twice_scale(uint32_t scales, int i) {
 
 __device__ __forceinline__ float nonfinite_part(float x) { return isfinite(x) ? 0.f : x; }
 
-// Where dims 2 p, 2 p + 1 of a head lie among the sums of the warps, in pairs:
-// a warp writes them 16 pairs apart and reads them 4 pairs a lane.
-__device__ __forceinline__ int red_at(int head, int p) {
-    return head * (kHeadDim / 2) + (p ^ (p >> 4) ^ ((head >> 1 & 1) << 3));
-}
-
 }  // namespace
 
-// kTwo: queries and probabilities as sums of two halves (4 heads at most).
+// kTwo: queries as sums of two halves (4 heads at most).
 template <bool kTwo>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_kv4_kernel(const __grid_constant__ Kv4Params P) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *stages = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    constexpr int kHeads = kTwo ? 4 : 8;
+    constexpr int kNewBytes = new_bytes(kHeads);
+    constexpr int kRows = kHeads / kWarps;               // heads of a warp: warp, warp + 4
+    extern __shared__ __align__(128) uint8_t stages[];
     uint8_t *new_rows = stages + kStages * kStageBytes;
-    uint8_t *qs = new_rows + kPairs * kNewBytes;  // [8 columns][256] halves
-    float2 *red_o = reinterpret_cast<float2 *>(qs + kQBytes);
-    float *kn = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(red_o) + kRedBytes);
-    float *vn = kn + kHeadDim;  // the new token's key (rotated) and value
+    uint8_t *qs = new_rows + kPairs * kNewBytes;         // queries' halves, as B takes them
+    uint2 *probs = reinterpret_cast<uint2 *>(qs + kQBytes);  // [2][4 groups][32 lanes]
+    float *kn = reinterpret_cast<float *>(probs + kProbBytes / 8);  // the new key (rotated), value
+    float *vn = kn + kHeadDim;
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ uint64_t pair_full[kPairs], pair_empty[kPairs];
     __shared__ Pair pairs[kPairs];
-    __shared__ int abort_flag, seg_bad, lost, last_cta;
+    __shared__ int abort_flag, lost, last_cta;
+    // Of a tile, by the last bit of its number: someone gave up waiting; some
+    // score passes the reference by too much.
+    __shared__ int gave_up[2], passed[2];
+    __shared__ float red[kWarps][8];            // the warps' maxima, or sums
     __shared__ int s_row;
     __shared__ long long s_base;
     __shared__ long long warp_sum[kThreads / 32];
-    __shared__ float red_m[kWarps][8], red_l[kWarps][8];
     __shared__ float q_unit[8];                 // of the queries' halves, in base-2 score units
     __shared__ float s_new[8], s_gate[8];       // the new token's scores, the gates
     __shared__ float2 freq[kHeadDim / 2], cs[kHeadDim / 2];
@@ -126,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kWarps / 2);
+            mbar_init(&empty[s], kWarps);
         }
         for (int s = 0; s < kPairs; ++s) {
             mbar_init(&pair_full[s], 1);
@@ -134,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         fence_mbar_init();
         abort_flag = 0;
-        seg_bad = 0;
+        gave_up[0] = gave_up[1] = passed[0] = passed[1] = 0;
         lost = 0;
     }
     const int half = P.rope.rot_dim / 2;
@@ -297,8 +312,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---------------------------------------------------------- consumers
     const int row8 = lane >> 2, c4 = lane & 3;           // row and column pair of fragments
     const int tok = 4 * (row8 >> 1) + (row8 & 1);        // slot of row row8; row8 + 8: + 2
-    // the heads of this thread's two columns
-    const int h0 = kTwo ? 2 * (c4 & 1) : 2 * c4, h1 = h0 + 1;
+    // Of the sums a thread has two heads, of which it is to hand on kDims dims
+    // from d0 (with two columns a head, two threads have the same: half each).
+    constexpr int kDims = kTwo ? 4 : 8;
+    const int h0 = kTwo ? 2 * (c4 & 1) : 2 * c4;
+    const int d0 = 32 * row8 + 8 * warp + (kTwo ? 2 * (c4 & 2) : 0);
     for (int i = tid; i < kQBytes / 16; i += kWarps * 32)
         *reinterpret_cast<uint4 *>(qs + i * 16) = make_uint4(0, 0, 0, 0);
     if (tid < 8) q_unit[tid] = 0.f;
@@ -321,19 +339,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // The new token's projections: q of the group's heads (warp w takes w and
         // w + 4), the value (warp 2), the key (warp 3).
         const uint8_t *rows = new_rows + n % kPairs * kNewBytes;
-        float gate[2] = {0.f, 0.f};
+        float gate[kRows];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int hq = warp + i * kRedHeads;
+        for (int i = 0; i < kRows; ++i) {
+            const int hq = warp + i * kWarps;
             if (hq < P.G)
                 gate[i] = P.gate[static_cast<size_t>(pair.b) * P.H + pair.g * P.G + hq];
         }
         if (tid < half) rope_cos_sin_fine(pos, freq[tid], cs[tid].x, cs[tid].y);
         consumer_bar();
-        float q[2][8];
+        float q[kRows][8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int hh = warp + i * kRedHeads;
+        for (int i = 0; i < kRows; ++i) {
+            const int hh = warp + i * kWarps;
             if (hh >= P.G) break;
             // in halves, scaled by a power of two so that the largest is 1 to 2
             const uint4 raw = *reinterpret_cast<const uint4 *>(rows + hh * kRowBytes + lane * 16);
@@ -396,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         consumer_bar();
         // the new token's scores
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (warp + i * kRedHeads >= P.G) break;
+        for (int i = 0; i < kRows; ++i) {
+            if (warp + i * kWarps >= P.G) break;
             const float4 ka = *reinterpret_cast<const float4 *>(kn + lane * 8);
             const float4 kb = *reinterpret_cast<const float4 *>(kn + lane * 8 + 4);
             float d = q[i][0] * ka.x;
@@ -410,158 +428,156 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             d = fmaf(q[i][7], kb.w, d);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-            if (lane == 0) s_new[warp + i * kRedHeads] = d * kScaleLog2;  // (this warp's alone)
+            if (lane == 0) s_new[warp + i * kWarps] = d * kScaleLog2;
         }
-        float o[16][4];
+        const float unit0 = q_unit[h0], unit1 = q_unit[h0 + 1];
+        float o[4][4];
 #pragma unroll
-        for (int m = 0; m < 16; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
+        for (int i = 0; i < 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        // References and sums of the thread's two heads.  All warps have the same
+        // references: a head's largest score so far, or up to kHeadroom less.
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         bool ok = !aborted;
-        // Two warps take the two halves of a tile, two groups of 16 slots each;
-        // the other two the next tile's.
         for (int t = t0; ok && t < t1; ++t, ++it) {
-            if ((it & 1) != warp >> 1) continue;
             const int s = it % kStages;
             ok = mbar_wait(&full[s], (it / kStages) & 1, &abort_flag, P.status);
-            if (!ok) break;
-            const int first = (lo & ~(kTile - 1)) + t * kTile + (warp & 1) * 2 * kKv4Group;
-            if (first < pos && first + 2 * kKv4Group > lo) {
-                const uint8_t *kg = stages + s * kStageBytes + (warp & 1) * 2 * kKv4GroupBytes;
-                const uint8_t *vg = kg + kTileBytes;
-                // S^T (2 x 16 slots x 8 columns) = K (16 x 256) Q^T (256 x 8)
-                uint32_t sa[2], sb[2];
-                float sc[2][2][4];
+            const int first = (lo & ~(kTile - 1)) + t * kTile;
+            const bool edge = first < lo || first + kTile > pos;
+            const uint8_t *kt = stages + s * kStageBytes;
+            uint2 *pt = probs + (it & 1) * kWarps * 32;
+            // S^T (16 slots x 8 columns) = K (16 x 256) Q^T (256 x 8)
+            float x[4];
+            {
+                const uint8_t *kg = kt + warp * kKv4GroupBytes;
+                const uint8_t *ks = kg + kKv4Codes + tok * 16 + c4 * 4;
+                const uint32_t sa = *reinterpret_cast<const uint32_t *>(ks);
+                const uint32_t sb = *reinterpret_cast<const uint32_t *>(ks + 32);
+                float acc[2][4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint8_t *ks = kg + u * kKv4GroupBytes + kKv4Codes + tok * 16 + c4 * 4;
-                    sa[u] = *reinterpret_cast<const uint32_t *>(ks);
-                    sb[u] = *reinterpret_cast<const uint32_t *>(ks + 32);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[u][0][i] = sc[u][1][i] = 0.f;
-                }
+                for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t wa[2][4], wb[2][4];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint8_t *kc = kg + u * kKv4GroupBytes + h * 1024 + tok * 64 + c4 * 16;
-                        const uint4 ka = *reinterpret_cast<const uint4 *>(kc);
-                        const uint4 kb = *reinterpret_cast<const uint4 *>(kc + 128);
-                        wa[u][0] = ka.x, wa[u][1] = ka.y, wa[u][2] = ka.z, wa[u][3] = ka.w;
-                        wb[u][0] = kb.x, wb[u][1] = kb.y, wb[u][2] = kb.z, wb[u][3] = kb.w;
-                    }
+                    const uint8_t *kc = kg + h * 1024 + tok * 64 + c4 * 16;
+                    const uint4 ka = *reinterpret_cast<const uint4 *>(kc);
+                    const uint4 kb = *reinterpret_cast<const uint4 *>(kc + 128);
+                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w};
+                    const uint32_t wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint4 qf = *reinterpret_cast<const uint4 *>(
                             qs + (4 * h + i) * 512 + lane * 16);
+                        const uint32_t ua = twice_scale(sa, 2 * h + (i >> 1));
+                        const uint32_t ub = twice_scale(sb, 2 * h + (i >> 1));
+                        uint32_t a[4], b[4];
+                        kv4_widen(wa[i], a);
+                        kv4_widen(wb[i], b);
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const uint32_t ua = twice_scale(sa[u], 2 * h + (i >> 1));
-                            const uint32_t ub = twice_scale(sb[u], 2 * h + (i >> 1));
-                            uint32_t a[4], b[4];
-                            kv4_widen(wa[u][i], a);
-                            kv4_widen(wb[u][i], b);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                a[j] = mul_half2(a[j], ua);
-                                b[j] = mul_half2(b[j], ub);
-                            }
-                            mma_f16_16816(sc[u][0], a[0], b[0], a[1], b[1], qf.x, qf.y);
-                            mma_f16_16816(sc[u][1], a[2], b[2], a[3], b[3], qf.z, qf.w);
+                        for (int j = 0; j < 4; ++j) {
+                            a[j] = mul_half2(a[j], ua);
+                            b[j] = mul_half2(b[j], ub);
                         }
+                        mma_f16_16816(acc[0], a[0], b[0], a[1], b[1], qf.x, qf.y);
+                        mma_f16_16816(acc[1], a[2], b[2], a[3], b[3], qf.z, qf.w);
                     }
                 }
-                const float unit0 = q_unit[h0], unit1 = q_unit[h1];
-                // this thread's slots (rows row8 and row8 + 8 of both) and heads
-                float x[2][4];
+                // this thread's slots (rows row8 and row8 + 8) and heads
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = acc[0][i] + acc[1][i];
+                    if (kTwo) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);
+                    x[i] *= i & 1 ? unit1 : unit0;
+                }
+                if (edge)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[u][i] = sc[u][0][i] + sc[u][1][i];
-                        if (kTwo) x[u][i] += __shfl_xor_sync(0xffffffffu, x[u][i], 2);
-                        const int slot = first + u * kKv4Group + tok + (i & 2);
-                        x[u][i] = slot >= lo && slot < pos ? x[u][i] * (i & 1 ? unit1 : unit0)
-                                                           : -INFINITY;
+                        const int slot = first + warp * kKv4Group + tok + (i & 2);
+                        if (slot < lo || slot >= pos) x[i] = -INFINITY;
                     }
-                }
-                float n0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-                float n1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+            }
+            // P^T of these slots, in the order in which the lanes take B
+            float p[4];
+            auto exponentiate = [&]() {
+                const float z0 = m0 == -INFINITY ? 0.f : m0 - kProbShift;
+                const float z1 = m1 == -INFINITY ? 0.f : m1 - kProbShift;
+                p[0] = fast_exp2(x[0] - z0);
+                p[1] = fast_exp2(x[1] - z1);
+                p[2] = fast_exp2(x[2] - z0);
+                p[3] = fast_exp2(x[3] - z1);
+                pt[warp * 32 + lane] = make_uint2(movmatrix_trans(pack_half2(p[0], p[1])),
+                                                  movmatrix_trans(pack_half2(p[2], p[3])));
+            };
+            exponentiate();
+            if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > m0 + kHeadroom ||
+                                            fmaxf(x[1], x[3]) > m1 + kHeadroom))
+                passed[it & 1] = 1;
+            if (!ok) gave_up[it & 1] = 1;
+            consumer_bar();
+            if (gave_up[it & 1]) break;  // (all of them: the next tile has its own word)
+            if (passed[it & 1]) {
+                // new references: the largest scores so far
+                float n0 = fmaxf(x[0], x[2]), n1 = fmaxf(x[1], x[3]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
                     n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
                 }
-                if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-                    n0 = fmaxf(n0, m0);
-                    n1 = fmaxf(n1, m1);
-                    const float r0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
-                    const float r1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
-                    l0 *= r0;
-                    l1 *= r1;
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) {
-                        o[m][0] *= r0;
-                        o[m][1] *= r1;
-                        o[m][2] *= r0;
-                        o[m][3] *= r1;
-                    }
-                    m0 = n0;
-                    m1 = n1;
+                if (row8 == 0 && (!kTwo || c4 < 2)) {
+                    red[warp][h0] = n0;
+                    red[warp][h0 + 1] = n1;
                 }
-                const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-                // P^T as the B operand of O^T += V^T P^T; the last columns take
-                // what the halves of the first leave
-                uint32_t pt[2][2];
+                consumer_bar();
+                if (tid == 0) passed[it & 1] = 0;
+                n0 = m0;
+                n1 = m1;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float p0 = fast_exp2(x[u][0] - z0), p1 = fast_exp2(x[u][1] - z1);
-                    const float p2 = fast_exp2(x[u][2] - z0), p3 = fast_exp2(x[u][3] - z1);
-                    l0 += p0 + p2;
-                    l1 += p1 + p3;
-                    uint32_t pa = pack_half2(p0, p1), pb = pack_half2(p2, p3);
-                    if (kTwo) {
-                        const uint32_t ra = pack_half2_rest(p0, p1, pa);
-                        const uint32_t rb = pack_half2_rest(p2, p3, pb);
-                        pa = c4 & 2 ? ra : pa;
-                        pb = c4 & 2 ? rb : pb;
-                    }
-                    pt[u][0] = movmatrix_trans(pa);
-                    pt[u][1] = movmatrix_trans(pb);
+                for (int w = 0; w < kWarps; ++w) {
+                    n0 = fmaxf(n0, red[w][h0]);
+                    n1 = fmaxf(n1, red[w][h0 + 1]);
                 }
-                const bool edge = first < lo || first + 2 * kKv4Group > pos;
+                const float r0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
+                const float r1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= r0;
+                l1 *= r1;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint8_t *vu = vg + u * kKv4GroupBytes;
-                    uint2 sv = *reinterpret_cast<const uint2 *>(vu + kKv4Codes + lane * 8);
-                    if (edge) {
-                        // Slots that hold no visible token may hold anything: a
-                        // scale of zero makes zeros of it.
-                        uint32_t seen = 0;
+                for (int i = 0; i < 4; ++i) {
+                    o[i][0] *= r0;
+                    o[i][1] *= r1;
+                    o[i][2] *= r0;
+                    o[i][3] *= r1;
+                }
+                exponentiate();
+                consumer_bar();
+            }
+            l0 += p[0] + p[2];
+            l1 += p[1] + p[3];
+            // O^T += V^T P^T, 64 dims of all slots
+            const uint8_t *vt = kt + kTileBytes;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int slot = first + u * kKv4Group + 4 * c4 + j;
-                            if (slot >= lo && slot < pos)
-                                seen |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
-                        }
-                        sv.x &= seen;
-                        sv.y &= seen;
-                    }
+            for (int u = 0; u < 4; ++u) {
+                const uint2 pb = pt[u * 32 + lane];
+                const uint8_t *vu = vt + u * kKv4GroupBytes;
+                const uint4 v = *reinterpret_cast<const uint4 *>(vu + warp * 512 + lane * 16);
+                uint32_t w = *reinterpret_cast<const uint32_t *>(vu + kKv4Codes + lane * 8 +
+                                                                 4 * (warp >> 1));
+                if (edge) {
+                    // Slots that hold no visible token may hold anything: a
+                    // scale of zero makes zeros of it.
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(vu + j * 512 + lane * 16);
-                        const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
-                        const uint32_t w = j >> 1 ? sv.y : sv.x;
-                        const uint32_t u0 = (w & 0x00ff00ffu) << 7, u1 = (w >> 1) & 0x7f807f80u;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t a[4];
-                            kv4_widen(wv[i], a);
-                            mma_f16_16816(o[4 * j + i], mul_half2(a[0], u0), mul_half2(a[1], u0),
-                                          mul_half2(a[2], u1), mul_half2(a[3], u1), pt[u][0],
-                                          pt[u][1]);
-                        }
+                        const int slot = first + u * kKv4Group + 4 * c4 + j;
+                        if (slot < lo || slot >= pos) w &= ~(0xffu << (8 * (2 * (j & 1) + (j >> 1))));
                     }
+                }
+                const uint32_t u0 = (w & 0x00ff00ffu) << 7, u1 = (w >> 1) & 0x7f807f80u;
+                const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a[4];
+                    kv4_widen(wv[i], a);
+                    mma_f16_16816(o[i], mul_half2(a[0], u0), mul_half2(a[1], u0),
+                                  mul_half2(a[2], u1), mul_half2(a[3], u1), pb.x, pb.y);
                 }
             }
             __syncwarp();
@@ -585,86 +601,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     old[j] = *reinterpret_cast<const uint16_t *>(src + 4 * j);
             }
         }
+        aborted = gave_up[0] || gave_up[1];  // (never reset; all have left the loop by one)
 
-        // ------------------------------------------------------ join the warps
+        // This CTA's state of the thread's two heads, kDims dims from d0.
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, off);
             l1 += __shfl_xor_sync(0xffffffffu, l1, off);
         }
-        if (lane < (kTwo ? 2 : 4)) {
-            red_m[warp][h0] = m0;
-            red_m[warp][h1] = m1;
-            red_l[warp][h0] = l0;
-            red_l[warp][h1] = l1;
+        if (row8 == 0 && (!kTwo || c4 < 2)) {
+            red[warp][h0] = l0;
+            red[warp][h0 + 1] = l1;
         }
-        if (!ok) seg_bad = 1;
         consumer_bar();
-        aborted = seg_bad != 0;  // written before the barrier, never reset
-        float M0 = red_m[0][h0], M1 = red_m[0][h1];
+        struct {
+            float m, l, o[kDims];
+        } st[2];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            M0 = fmaxf(M0, red_m[w][h0]);
-            M1 = fmaxf(M1, red_m[w][h1]);
-        }
-        const float s0 = M0 == -INFINITY ? 0.f : fast_exp2(m0 - M0);
-        const float s1 = M1 == -INFINITY ? 0.f : fast_exp2(m1 - M1);
-        // head hq of this warp, lane l its dims 8l..8l+7; the sums of the warps
-        // go through shared memory kRedHeads heads at a time
-        HeadState st[2];
+        for (int i = 0; i < 2; ++i) {
+            st[i].m = i ? m1 : m0;
+            st[i].l = 0.f;
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-            if (pass * kRedHeads >= P.G) break;
-            if (pass) consumer_bar();  // the heads before are read
-            float2 *dst = red_o + warp * kRedHeads * (kHeadDim / 2);
-            if (kTwo) {
-                // columns j and j + 4 are one head's: each lane of the two takes
-                // half of the dims
+            for (int w = 0; w < kWarps; ++w) st[i].l += red[w][h0 + i];
+            st[i].l *= 0x1p-11f;
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    float v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float give = c4 & 2 ? o[m][i] : o[m + 8][i];
-                        const float keep = c4 & 2 ? o[m + 8][i] : o[m][i];
-                        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
-                    }
-                    const int p = 16 * row8 + m + 4 * (c4 & 2);
-                    dst[red_at(h0, p)] = make_float2(v[0] * s0, v[2] * s0);
-                    dst[red_at(h1, p)] = make_float2(v[1] * s1, v[3] * s1);
-                }
-            } else if (c4 >> 1 == pass) {
-#pragma unroll
-                for (int m = 0; m < 16; ++m) {
-                    const int p = 16 * row8 + m;
-                    dst[red_at(h0 & 3, p)] = make_float2(o[m][0] * s0, o[m][2] * s0);
-                    dst[red_at(h1 & 3, p)] = make_float2(o[m][1] * s1, o[m][3] * s1);
-                }
-            }
-            consumer_bar();
-            const int hq = warp + pass * kRedHeads;
-            HeadState &h = st[pass];
-            h.m = -INFINITY;
-            h.l = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h.o[i] = 0.f;
-            if (hq < P.G && !aborted) {
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) h.m = fmaxf(h.m, red_m[w][hq]);
-                // (a NaN among the sums has to stay one, whatever the maximum)
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    h.l += red_l[w][hq] *
-                           (h.m == -INFINITY ? 1.f : fast_exp2(red_m[w][hq] - h.m));
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 v = red_o[w * kRedHeads * (kHeadDim / 2) +
-                                               red_at(warp, 4 * lane + i)];
-                        h.o[2 * i] += v.x;
-                        h.o[2 * i + 1] += v.y;
-                    }
+            for (int j = 0; j < kDims / 2; ++j) {
+                const float(&a)[4] = o[j];
+                const float(&b)[4] = o[kTwo ? j + 2 : j];
+                st[i].o[2 * j] = (kTwo && (c4 & 2) ? b[i] : a[i]) * 0x1p-11f;
+                st[i].o[2 * j + 1] = (kTwo && (c4 & 2) ? b[i + 2] : a[i + 2]) * 0x1p-11f;
             }
         }
 
@@ -681,13 +646,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             auto leave = [&](int cta) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int hq = warp + i * kRedHeads;
-                    if (hq >= P.G) break;
-                    const size_t at = static_cast<size_t>(place(cta)) * P.G + hq;
-                    float4 *dst = reinterpret_cast<float4 *>(P.part_o + at * kHeadDim + lane * 8);
-                    dst[0] = make_float4(st[i].o[0], st[i].o[1], st[i].o[2], st[i].o[3]);
-                    dst[1] = make_float4(st[i].o[4], st[i].o[5], st[i].o[6], st[i].o[7]);
-                    if (lane == 0)
+                    if (h0 + i >= P.G) break;
+                    const size_t at = static_cast<size_t>(place(cta)) * P.G + h0 + i;
+                    float4 *dst = reinterpret_cast<float4 *>(P.part_o + at * kHeadDim + d0);
+#pragma unroll
+                    for (int j = 0; j < kDims; j += 4)
+                        dst[j / 4] = make_float4(st[i].o[j], st[i].o[j + 1], st[i].o[j + 2],
+                                                 st[i].o[j + 3]);
+                    if (warp == 0 && row8 == 0 && (!kTwo || c4 < 2))
                         reinterpret_cast<float2 *>(P.part_ml)[at] = make_float2(st[i].m, st[i].l);
                 }
                 __threadfence();
@@ -710,46 +676,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             auto join = [&](int from, int to, int step) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int hq = warp + i * kRedHeads;
-                    if (hq >= P.G) break;
-                    HeadState &h = st[i];
+                    if (h0 + i >= P.G) break;
+                    auto &h = st[i];
                     h.m = -INFINITY;
                     h.l = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) h.o[j] = 0.f;
+                    for (int j = 0; j < kDims; ++j) h.o[j] = 0.f;
                     for (int cta = from; cta <= to; cta += kFan * step) {
                         float2 ml[kFan];
-                        float4 x[kFan], y[kFan];
+                        float4 x[kFan][kDims / 4];
 #pragma unroll
                         for (int k = 0; k < kFan; ++k) {
                             ml[k] = make_float2(-INFINITY, 0.f);
-                            x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int j = 0; j < kDims / 4; ++j)
+                                x[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
                             const int from_cta = cta + k * step;
                             if (from_cta <= to) {
-                                const size_t a = static_cast<size_t>(place(from_cta)) * P.G + hq;
+                                const size_t a = static_cast<size_t>(place(from_cta)) * P.G + h0 + i;
                                 ml[k] = __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + a);
                                 const float4 *src = reinterpret_cast<const float4 *>(
-                                    P.part_o + a * kHeadDim + lane * 8);
-                                x[k] = __ldcg(src);
-                                y[k] = __ldcg(src + 1);
+                                    P.part_o + a * kHeadDim + d0);
+#pragma unroll
+                                for (int j = 0; j < kDims / 4; ++j) x[k][j] = __ldcg(src + j);
                             }
                         }
-                        float m = h.m;
+                        float top = h.m;
 #pragma unroll
-                        for (int k = 0; k < kFan; ++k) m = fmaxf(m, ml[k].x);
-                        const float z = m == -INFINITY ? 0.f : m;
+                        for (int k = 0; k < kFan; ++k) top = fmaxf(top, ml[k].x);
+                        const float z = top == -INFINITY ? 0.f : top;
                         const float wo = fast_exp2(h.m - z);
-                        h.m = m;
+                        h.m = top;
                         h.l *= wo;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) h.o[j] *= wo;
+                        for (int j = 0; j < kDims; ++j) h.o[j] *= wo;
 #pragma unroll
                         for (int k = 0; k < kFan; ++k) {
-                            const float w = fast_exp2(ml[k].x - z);
-                            const float v[8] = {x[k].x, x[k].y, x[k].z, x[k].w,
-                                                y[k].x, y[k].y, y[k].z, y[k].w};
+                            // (an empty state's sums are 0, or NaN, whatever their weight)
+                            const float w = ml[k].x == -INFINITY ? 1.f : fast_exp2(ml[k].x - z);
                             h.l += ml[k].y * w;
-                            add_scaled(h, w, v);
+#pragma unroll
+                            for (int j = 0; j < kDims; j += 4) {
+                                h.o[j] += x[k][j / 4].x * w;
+                                h.o[j + 1] += x[k][j / 4].y * w;
+                                h.o[j + 2] += x[k][j / 4].z * w;
+                                h.o[j + 3] += x[k][j / 4].w * w;
+                            }
                         }
                     }
                 }
@@ -774,30 +746,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // the new token joins, the gate applies
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int hq = warp + i * kRedHeads;
-                if (hq >= P.G) break;
-                HeadState &h = st[i];
-                const float x_new = s_new[hq];
-                const float4 va = *reinterpret_cast<const float4 *>(vn + lane * 8);
-                const float4 vb = *reinterpret_cast<const float4 *>(vn + lane * 8 + 4);
-                const float v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-                const float m = fmaxf(h.m, x_new);
-                const float z = m == -INFINITY ? 0.f : m;
+                if (h0 + i >= P.G) break;
+                auto &h = st[i];
+                const float x_new = s_new[h0 + i];
+                const float top = fmaxf(h.m, x_new);
+                const float z = top == -INFINITY ? 0.f : top;
                 const float wo = h.m == -INFINITY ? 1.f : fast_exp2(h.m - z);
                 const float wn = fast_exp2(x_new - z);
-                const float scale = gate_act(s_gate[hq], P.gate_mode) / (h.l * wo + wn);
-                float y[8];
+                const float scale = gate_act(s_gate[h0 + i], P.gate_mode) / (h.l * wo + wn);
+                uint32_t y[kDims / 2];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    y[j] = (h.o[j] * wo + v[j] * wn) * scale;
-                    // an infinity is one however small its weight
-                    if (!isfinite(v[j])) y[j] = (v[j] + nonfinite_part(h.o[j])) * scale;
+                for (int j = 0; j < kDims; j += 4) {
+                    const float4 v4 = *reinterpret_cast<const float4 *>(vn + d0 + j);
+                    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+                    float r[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        r[k] = (h.o[j + k] * wo + v[k] * wn) * scale;
+                        // an infinity is one however small its weight
+                        if (!isfinite(v[k])) r[k] = (v[k] + nonfinite_part(h.o[j + k])) * scale;
+                    }
+                    y[j / 2] = pack_bf16x2(r[0], r[1]);
+                    y[j / 2 + 1] = pack_bf16x2(r[2], r[3]);
                 }
-                *reinterpret_cast<uint4 *>(
+                __nv_bfloat16 *dst =
                     P.out +
-                    (static_cast<size_t>(pair.b) * P.H + pair.g * P.G + hq) * kHeadDim +
-                    lane * 8) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+                    (static_cast<size_t>(pair.b) * P.H + pair.g * P.G + h0 + i) * kHeadDim + d0;
+                if (kTwo)
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(y[0], y[1]);
+                else
+                    *reinterpret_cast<uint4 *>(dst) =
+                        make_uint4(y[0], y[1], y[kDims / 2 - 2], y[kDims / 2 - 1]);
             }
             if (warp == 0) {
                 // the new token's slot: every read of this pair is done
@@ -837,11 +816,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 int decode_kv4_ctas(int sms) { return sms * kCtasPerSm; }
 
 cudaError_t launch_decode_kv4(const Kv4Params &P, int grid, cudaStream_t stream) {
-    auto kernel = P.G <= 4 ? decode_kv4_kernel<true> : decode_kv4_kernel<false>;
+    const bool two = P.G <= 4;
+    auto kernel = two ? decode_kv4_kernel<true> : decode_kv4_kernel<false>;
+    const int smem = smem_bytes(two ? 4 : 8);
     cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
-    return launch_overlapped(kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, P);
+    return launch_overlapped(kernel, dim3(grid), dim3(kThreads), smem, stream, P);
 }
 
 }  // namespace spark

@@ -119,11 +119,12 @@ def project(qkv, pos, H, Hkv, layer):
 def decode(qkv, gate, pos, k4, v4, table, H, Hkv, layer):
     """Out [B, H * 256] float64 (NaN rows where nothing is written) and how far a result may be
     from it; the pages k4, v4 are updated.  The bound, per value: half a step of bf16 (2^-8);
-    and, with A = sum_j p_j |v_j| and S the largest sum_i |q_i k_ji| / 16, twice A times what a
-    probability may be off -- S times the rounding of a query (a sum of two halves leaves 2^-22,
-    one half 2^-11) and of its sum of 256 products in 32 bits (2^-16), the probability's own
-    rounding (the same halves) and 2^-20 for the exponential and the gate -- and A times 2^-24
-    per token summed."""
+    and, with A = sum_j p_j |v_j| and S the largest sum_i |q_i k_ji| / 16, A times what a
+    numerator's probability may be off and again what the denominator's may: each S times the
+    rounding of a query (a sum of two halves leaves 2^-22, one half 2^-11) and of its sum of 256
+    products in 32 bits (2^-16), and 2^-20 for the exponential and the gate; the numerator's also
+    its own rounding to a half, 2^-11, or 2^-36 of the largest where it is subnormal; and A times
+    2^-24 per token summed."""
     B, G = len(pos), H // Hkv
     q, k, v = project(qkv, torch.clamp(pos, min=0), H, Hkv, layer)
     out, tol = np.full((B, H, D), np.nan), np.zeros((B, H, D))
@@ -144,7 +145,9 @@ def decode(qkv, gate, pos, k4, v4, table, H, Hkv, layer):
             out[b, h] = p @ vs[:, h // G] * act
             A = p @ np.abs(vs[:, h // G]) * abs(act)
             S = (np.abs(ks[:, h // G]) @ np.abs(q[b, h])).max() / 16.0
-            off = S * (halves + 2.0 ** -16) + halves + 2.0 ** -20
-            tol[b, h] = 2.0 ** -8 * np.abs(out[b, h]) + A * (2 * off + len(s) * 2.0 ** -24)
+            off = S * (halves + 2.0 ** -16) + 2.0 ** -20
+            tol[b, h] = 2.0 ** -8 * np.abs(out[b, h]) + A * (2 * off + 2.0 ** -11
+                                                                + len(s) * 2.0 ** -24)
+            tol[b, h] += 2.0 ** -36 * np.abs(vs[:, h // G]).sum(0) * abs(act)
         write(k4, v4, table[b], n, k[b], v[b])
     return out.reshape(B, H * D), tol.reshape(B, H * D)
