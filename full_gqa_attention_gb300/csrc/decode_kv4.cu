@@ -50,17 +50,20 @@ constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kQBytes = 8 * kHeadDim * 2;                 // 8 columns
 constexpr int kRowBytes = kHeadDim * 2;
 constexpr int kPairs = 2;                                 // pairs handed over at a time
-constexpr int kFan = 8;                                   // partial states joined at once
+constexpr int kFan = 8;                                   // partial states loaded at once
+constexpr int kSub = 16;                                  // ... joined in the first step
 constexpr int kProbBytes = 2 * kWarps * 32 * 8;           // two tiles' probabilities
 constexpr float kHeadroom = 4.f;                          // scores may pass the reference by this
 constexpr float kProbShift = 11.f;                        // probabilities are times 2^11
+constexpr float kProbScale = 2048.f;
+constexpr int kSumRow = kHeadDim;                         // floats
 
 // Shared memory: the stages, a pair's new token (q of `heads` heads, key, value)
-// twice, the queries' halves, two tiles' probabilities, the new key and value.
+// twice, the queries' halves (after the tiles: 4 heads' sums), two tiles'
+// probabilities.
 __host__ __device__ constexpr int new_bytes(int heads) { return (heads + 2) * kRowBytes; }
 __host__ __device__ constexpr int smem_bytes(int heads) {
-    return kStages * kStageBytes + kPairs * new_bytes(heads) + kQBytes + kProbBytes +
-           2 * kHeadDim * 4;
+    return kStages * kStageBytes + kPairs * new_bytes(heads) + kQBytes + kProbBytes;
 }
 
 using Row = DecodeRow<kTile, kPairCost>;
@@ -118,10 +121,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint8_t *new_rows = stages + kStages * kStageBytes;
     uint8_t *qs = new_rows + kPairs * kNewBytes;         // queries' halves, as B takes them
     uint2 *probs = reinterpret_cast<uint2 *>(qs + kQBytes);  // [2][4 groups][32 lanes]
-    float *kn = reinterpret_cast<float *>(probs + kProbBytes / 8);  // the new key (rotated), value
-    float *vn = kn + kHeadDim;
+    // the sums of 4 heads [4][kSumRow] in the queries' place
+    float *sums = reinterpret_cast<float *>(qs);
     __shared__ uint64_t full[kStages], empty[kStages];
-    __shared__ uint64_t pair_full[kPairs], pair_empty[kPairs];
+    __shared__ uint64_t pair_full[kPairs], rows_full[kPairs], new_full[kPairs];
+    __shared__ uint64_t pair_empty[kPairs];
     __shared__ Pair pairs[kPairs];
     __shared__ int abort_flag, lost, last_cta;
     // Of a tile, by the last bit of its number: someone gave up waiting; some
@@ -133,9 +137,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __shared__ long long warp_sum[kThreads / 32];
     __shared__ float q_unit[8];                 // of the queries' halves, in base-2 score units
     __shared__ float s_new[8], s_gate[8];       // the new token's scores, the gates
-    __shared__ float2 freq[kHeadDim / 2], cs[kHeadDim / 2];
-    __shared__ uint32_t new_codes[2][32];       // the new token's key and value, quantised
-    __shared__ uint8_t new_scale[2][32];
+    // cos and sin of the pair's position: the consumers', the producer's
+    __shared__ float2 cs[kHeadDim / 2], cs_new[kHeadDim / 2];
+    // the new token's key and value, quantised
+    __shared__ uint32_t new_codes[kPairs][2][32];
+    __shared__ uint8_t new_scale[kPairs][2][32];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -145,6 +151,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         for (int s = 0; s < kPairs; ++s) {
             mbar_init(&pair_full[s], 1);
+            mbar_init(&rows_full[s], 1);
+            mbar_init(&new_full[s], 1);
             mbar_init(&pair_empty[s], kWarps);
         }
         fence_mbar_init();
@@ -153,7 +161,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         lost = 0;
     }
     const int half = P.rope.rot_dim / 2;
-    if (tid < half) freq[tid] = P.rope.u[tid];
     grid_dep_wait();  // positions, tables and pages may come from the kernel before
 
     // ---------------------------------------------------------- this CTA's stretch
@@ -181,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         total += warp_sum[w];
     }
     total *= P.Hkv;
-    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    const long long share = quotient(total + gridDim.x - 1, gridDim.x);
     Walk wk{};
     wk.u = share * blockIdx.x;
     wk.end = wk.u + share < total ? wk.u + share : total;
@@ -213,8 +220,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
         int it = 0, n_pairs = 0;
         bool ok = true;
-        // Hands over a pair (or the end).  After an abort too: every shared
-        // pair has to be counted, so that the counters are 0 again.
+        // Hands over a pair (or the end), and fetches its new token.  After an
+        // abort too: every shared pair has to be counted, so that the counters
+        // are 0 again.
         auto hand_over = [&](bool end) {
             const int s = n_pairs % kPairs;
             if (lane == 0) {
@@ -227,36 +235,58 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 p.g = wk.g;
                 p.t0 = wk.t0;
                 p.t1 = end ? wk.t0 : wk.t1;
-                p.c0 = static_cast<int>((wk.first + kPairCost) / share);
-                p.c1 = static_cast<int>((wk.first + wk.row.units() - 1) / share);
-                p.second = share * p.c0 < wk.first ? 1 : 0;
-                if (end || !ok) {
-                    mbar_arrive(&pair_full[s]);
-                } else {
+                if (!end) {
                     uint8_t *dst = new_rows + s * kNewBytes;
                     const __nv_bfloat16 *src = P.qkv + wk.b * width;
-                    mbar_arrive_expect_tx(&pair_full[s], (P.G + 2) * kRowBytes);
+                    mbar_arrive_expect_tx(&rows_full[s], (P.G + 2) * kRowBytes);
                     bulk_load(dst, src + static_cast<size_t>(wk.g) * P.G * kHeadDim,
-                              P.G * kRowBytes, &pair_full[s]);
+                              P.G * kRowBytes, &rows_full[s]);
                     bulk_load(dst + P.G * kRowBytes,
                               src + static_cast<size_t>(P.H + wk.g) * kHeadDim, kRowBytes,
-                              &pair_full[s]);
+                              &rows_full[s]);
                     bulk_load(dst + (P.G + 1) * kRowBytes,
                               src + static_cast<size_t>(P.H + P.Hkv + wk.g) * kHeadDim, kRowBytes,
-                              &pair_full[s]);
+                              &rows_full[s]);
+                    p.c0 = static_cast<int>(quotient(wk.first + kPairCost, share));
+                    p.c1 = static_cast<int>(quotient(wk.first + wk.row.units() - 1, share));
+                    p.second = share * p.c0 < wk.first ? 1 : 0;
                 }
+                mbar_arrive(&pair_full[s]);
             }
             __syncwarp();
             ++n_pairs;
         };
+        // Quantises the new token of the pair handed over last, while the copies
+        // of its first tiles are on their way.
+        auto quantise_new = [&]() {
+            const int s = (n_pairs - 1) % kPairs;
+#pragma unroll 1
+            for (int k = lane; k < half; k += 32)
+                rope_cos_sin_fine(wk.row.pos, P.rope.u[k], cs_new[k].x, cs_new[k].y);
+            mbar_wait_plain(&rows_full[s], ((n_pairs - 1) / kPairs) & 1);
+            __syncwarp();
+            const uint8_t *src = new_rows + s * kNewBytes + P.G * kRowBytes + lane * 16;
+            float y[8];
+            unsigned byte;
+            kv4_key_row(kv4_key_turn(*reinterpret_cast<const uint4 *>(src), P.rope.rot_dim,
+                                     wk.row.pos, lane),
+                        cs_new, wk.row.pos, P.turns, y, new_codes[s][0][lane], byte);
+            new_scale[s][0][lane] = static_cast<uint8_t>(byte);
+            kv4_floats(*reinterpret_cast<const uint4 *>(src + kRowBytes), y);
+            kv4_value_row(y, new_codes[s][1][lane], byte);
+            new_scale[s][1][lane] = static_cast<uint8_t>(byte);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&new_full[s]);
+        };
         while (wk.load(P)) {
             hand_over(false);
-            if (!ok) continue;
+            int early = kStages;  // tiles before the new token's turn comes
             const int32_t *row = P.pg.table + static_cast<size_t>(wk.b) * P.pg.max_pages;
             const int slot0 = wk.row.slot0();
             const int lo = wk.row.lo & ~15, hi = (wk.row.pos + 15) & ~15;  // groups seen
             int ids = 0;
-            for (int t = wk.t0; t < wk.t1; ++t) {
+            for (int t = wk.t0; ok && t < wk.t1; ++t) {
+                if (early-- == 0) quantise_new();
                 // page numbers of the next 32 pieces, one per lane; -1: none
                 const int in = (t - wk.t0) * pieces & 31;
                 if (in == 0) {
@@ -296,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                               bytes, &full[s]);
                 ++it;
             }
+            if (early >= 0) quantise_new();
         }
         hand_over(true);
         __syncthreads();
@@ -304,22 +335,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
                 mbar_wait_plain(&full[i % kStages], (i / kStages) & 1);
         if (lane == 0 && abort_flag)
-            for (int i = n_pairs > kPairs ? n_pairs - kPairs : 0; i < n_pairs; ++i)
-                mbar_wait_plain(&pair_full[i % kPairs], (i / kPairs) & 1);
+            for (int i = n_pairs - 1 > kPairs ? n_pairs - 1 - kPairs : 0; i < n_pairs - 1; ++i)
+                mbar_wait_plain(&rows_full[i % kPairs], (i / kPairs) & 1);
         return;
     }
 
     // ---------------------------------------------------------- consumers
     const int row8 = lane >> 2, c4 = lane & 3;           // row and column pair of fragments
     const int tok = 4 * (row8 >> 1) + (row8 & 1);        // slot of row row8; row8 + 8: + 2
-    // Of the sums a thread has two heads, of which it is to hand on kDims dims
-    // from d0 (with two columns a head, two threads have the same: half each).
-    constexpr int kDims = kTwo ? 4 : 8;
-    const int h0 = kTwo ? 2 * (c4 & 1) : 2 * c4;
-    const int d0 = 32 * row8 + 8 * warp + (kTwo ? 2 * (c4 & 2) : 0);
-    for (int i = tid; i < kQBytes / 16; i += kWarps * 32)
-        *reinterpret_cast<uint4 *>(qs + i * 16) = make_uint4(0, 0, 0, 0);
+    const int h0 = kTwo ? 2 * (c4 & 1) : 2 * c4;         // the first of its two heads
+    // (columns of no head keep what they hold: their sums are nobody's)
     if (tid < 8) q_unit[tid] = 0.f;
+    float2 freq = make_float2(0.f, 0.f);
+    if (tid < half) freq = P.rope.u[tid];
     int it = 0;
     bool aborted = false;  // the same in every consumer thread
     // Waits for a pair; the barrier behind it tells every warp whether all have it.
@@ -336,9 +364,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const Pair &pair = pairs[n % kPairs];
         const int pos = pair.pos, lo = pair.lo, t0 = pair.t0, t1 = pair.t1;
         if (t0 >= t1) break;
-        // The new token's projections: q of the group's heads (warp w takes w and
-        // w + 4), the value (warp 2), the key (warp 3).
-        const uint8_t *rows = new_rows + n % kPairs * kNewBytes;
+        // The new token's queries, warp w taking heads w and w + 4, and its score
+        // (the turns of q and k cancel).
+        const int s_pair = n % kPairs, pair_turn = (n / kPairs) & 1;
+        const uint8_t *rows = new_rows + s_pair * kNewBytes;
         float gate[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
@@ -346,35 +375,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (hq < P.G)
                 gate[i] = P.gate[static_cast<size_t>(pair.b) * P.H + pair.g * P.G + hq];
         }
-        if (tid < half) rope_cos_sin_fine(pos, freq[tid], cs[tid].x, cs[tid].y);
+        int id_new = 0;
+        if (warp == 0)
+            id_new = P.pg.table[static_cast<size_t>(pair.b) * P.pg.max_pages +
+                                (pos >> P.pg.page_shift)];
+        if (tid < half) rope_cos_sin_fine(pos, freq, cs[tid].x, cs[tid].y);
+        if (!mbar_wait_plain(&rows_full[s_pair], pair_turn)) {
+            atomicOr(P.status, kErrTimeout);
+            abort_flag = 1;
+            gave_up[0] = 1;
+        }
         consumer_bar();
-        float q[kRows][8];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int hh = warp + i * kWarps;
             if (hh >= P.G) break;
             // in halves, scaled by a power of two so that the largest is 1 to 2
             const uint4 raw = *reinterpret_cast<const uint4 *>(rows + hh * kRowBytes + lane * 16);
-            float(&y)[8] = q[i];
-            kv4_rotate(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, y);
-            float a = 0.f, z = 0.f;
+            const KeyTurn turn = kv4_key_turn(raw, P.rope.rot_dim, pos, lane);
+            float y[8], k[8];
+            kv4_floats(*reinterpret_cast<const uint4 *>(rows + P.G * kRowBytes + lane * 16), k);
+            float d = 0.f, a = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d = fmaf(turn.x[j], k[j], d);
+            kv4_rotate(turn, cs, y);
+            bool odd = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 a = fmaxf(a, fabsf(y[j]));
-                z += y[j] * 0.f;
+                odd = odd || !isfinite(y[j]);
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) {
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-                z += __shfl_xor_sync(0xffffffffu, z, off);
+                d += __shfl_xor_sync(0xffffffffu, d, off);
             }
+            // (a query that is not finite is NaN throughout)
+            const float z = __any_sync(0xffffffffu, odd) ? NAN : 0.f;
             const unsigned e = __float_as_uint(a) >> 23;
             const unsigned up = (e < 253u ? 254u - e : 1u) << 23;
             const float f = __uint_as_float(up);
             uint32_t hi[4], rest[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                // (z: a query that is not finite is NaN throughout)
                 const float u = fmaf(y[2 * j], f, z), v = fmaf(y[2 * j + 1], f, z);
                 hi[j] = pack_half2(u, v);
                 rest[j] = pack_half2_rest(u, v, hi[j]);
@@ -388,48 +431,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     make_uint4(rest[0], rest[1], rest[2], rest[3]);
             if (lane == 0) {
                 q_unit[hh] = kScaleLog2 * __uint_as_float((254u << 23) - up);
+                s_new[hh] = fmaf(d, kScaleLog2, z);
                 s_gate[hh] = gate[i];
             }
         }
-        if (warp >= 2) {
-            const int v = warp == 2;
-            const uint4 raw =
-                *reinterpret_cast<const uint4 *>(rows + (P.G + v) * kRowBytes + lane * 16);
-            float y[8];
-            uint32_t codes;
-            unsigned byte;
-            if (v) {
-                kv4_floats(raw, y);
-                kv4_value_row(y, codes, byte);
-            } else {
-                kv4_key_row(kv4_key_turn(raw, P.rope.rot_dim, pos, lane), cs, pos, P.turns, y,
-                            codes, byte);
-            }
-            float4 *dst = reinterpret_cast<float4 *>((v ? vn : kn) + lane * 8);
-            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-            new_codes[v][lane] = codes;
-            new_scale[v][lane] = static_cast<uint8_t>(byte);
-        }
         consumer_bar();
-        // the new token's scores
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (warp + i * kWarps >= P.G) break;
-            const float4 ka = *reinterpret_cast<const float4 *>(kn + lane * 8);
-            const float4 kb = *reinterpret_cast<const float4 *>(kn + lane * 8 + 4);
-            float d = q[i][0] * ka.x;
-            d = fmaf(q[i][1], ka.y, d);
-            d = fmaf(q[i][2], ka.z, d);
-            d = fmaf(q[i][3], ka.w, d);
-            d = fmaf(q[i][4], kb.x, d);
-            d = fmaf(q[i][5], kb.y, d);
-            d = fmaf(q[i][6], kb.z, d);
-            d = fmaf(q[i][7], kb.w, d);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-            if (lane == 0) s_new[warp + i * kWarps] = d * kScaleLog2;
-        }
         const float unit0 = q_unit[h0], unit1 = q_unit[h0 + 1];
         float o[4][4];
 #pragma unroll
@@ -583,27 +589,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
         }
+        aborted = gave_up[0] || gave_up[1];  // (never reset; all have left the loop by one)
         // Where the new token goes; read now, written when the pair is finished.
         const int t_new = pos & 15;
         uint8_t *k_new = nullptr, *v_new = nullptr;
         unsigned old[4] = {0, 0, 0, 0};
-        if (warp == 0) {
-            const int id = P.pg.table[static_cast<size_t>(pair.b) * P.pg.max_pages +
-                                      (pos >> P.pg.page_shift)];
-            if (id >= 0 && id < P.pg.n_pages) {
-                const size_t at = P.pg.group(id, pair.g, P.Hkv, pos);
-                k_new = P.pg.k + at;
-                v_new = P.pg.v + at;
-                const uint8_t *src =
-                    v_new + kv4_value_at(lane, t_new >> 2) + 2 * (t_new >> 1 & 1);
+        if (warp == 0 && id_new >= 0 && id_new < P.pg.n_pages) {
+            const size_t at = P.pg.group(id_new, pair.g, P.Hkv, pos);
+            k_new = P.pg.k + at;
+            v_new = P.pg.v + at;
+            const uint8_t *src = v_new + kv4_value_at(lane, t_new >> 2) + 2 * (t_new >> 1 & 1);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    old[j] = *reinterpret_cast<const uint16_t *>(src + 4 * j);
-            }
+            for (int j = 0; j < 4; ++j) old[j] = *reinterpret_cast<const uint16_t *>(src + 4 * j);
         }
-        aborted = gave_up[0] || gave_up[1];  // (never reset; all have left the loop by one)
 
-        // This CTA's state of the thread's two heads, kDims dims from d0.
+        // ---------------------------------------------- this CTA's state of the heads
+        // Warp w has heads w and w + 4, lane l their dims 8 l ..
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, off);
@@ -613,92 +614,105 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             red[warp][h0] = l0;
             red[warp][h0 + 1] = l1;
         }
-        consumer_bar();
-        struct {
-            float m, l, o[kDims];
-        } st[2];
+        HeadState st[kRows];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            st[i].m = i ? m1 : m0;
-            st[i].l = 0.f;
+        for (int i = 0; i < kRows; ++i) {
+            if (i) consumer_bar();  // (the heads before are read)
+            // dims 32 row8 + 8 warp .. + 7 of two heads; with two columns a head
+            // two threads have the same: half each
+            if (kTwo || c4 >> 1 == i) {
+                const bool upper = kTwo && (c4 & 2);
+                float *dst = sums + (h0 & 3) * kSumRow + 32 * row8 + 8 * warp + (upper ? 4 : 0);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) st[i].l += red[w][h0 + i];
-            st[i].l *= 0x1p-11f;
+                for (int j = 0; j < (kTwo ? 2 : 4); j += 2) {
+                    float a[4], b[4];
 #pragma unroll
-            for (int j = 0; j < kDims / 2; ++j) {
-                const float(&a)[4] = o[j];
-                const float(&b)[4] = o[kTwo ? j + 2 : j];
-                st[i].o[2 * j] = (kTwo && (c4 & 2) ? b[i] : a[i]) * 0x1p-11f;
-                st[i].o[2 * j + 1] = (kTwo && (c4 & 2) ? b[i + 2] : a[i + 2]) * 0x1p-11f;
+                    for (int k = 0; k < 4; ++k) {
+                        a[k] = upper ? o[kTwo ? 2 : j][k] : o[j][k];
+                        b[k] = upper ? o[3][k] : o[j + 1][k];
+                    }
+                    *reinterpret_cast<float4 *>(dst + 2 * j) = make_float4(a[0], a[2], b[0], b[2]);
+                    *reinterpret_cast<float4 *>(dst + kSumRow + 2 * j) =
+                        make_float4(a[1], a[3], b[1], b[3]);
+                }
             }
+            consumer_bar();
+            const int hq = warp + i * kWarps;
+            HeadState &h = st[i];
+            h.m = __shfl_sync(0xffffffffu, hq & 1 ? m1 : m0, hq >> 1);
+            h.l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) h.l += red[w][hq];
+            h.l *= 1.f / kProbScale;
+            const float4 *src = reinterpret_cast<const float4 *>(sums + warp * kSumRow + 8 * lane);
+            const float4 a = src[0], b = src[1];
+            const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h.o[j] = v[j] * (1.f / kProbScale);
         }
 
         // ------------------------------------------------------ finish or hand over
-        // A pair of one CTA is finished.  Of others the states are joined in two
-        // steps, kFan of them and then what those leave, each by the CTA that
-        // counts last; in the order of the CTAs, so that the result does not
-        // depend on which one that is.
-        const int c0 = pair.c0, c1 = pair.c1, second = pair.second;
+        // A pair of one CTA is finished.  Of others the states are joined by the
+        // CTA that leaves its own last; of more than kSub in two steps, kSub of
+        // them and then what those leave.  The order is that of the CTAs, so that
+        // the result does not depend on which one is last.
+        const int c0 = pair.c0, c1 = pair.c1;
         bool finish = c0 == c1;
         if (!finish) {
-            const int me = static_cast<int>(blockIdx.x);
+            const int me = static_cast<int>(blockIdx.x), second = pair.second;
             auto place = [&](int cta) { return 2 * cta + (cta == c0 ? second : 0); };
-            auto leave = [&](int cta) {
+            // Leaves the state in that CTA's place; whether it was the last of `all`.
+            auto leave = [&](int cta, unsigned *counter, int all) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (h0 + i >= P.G) break;
-                    const size_t at = static_cast<size_t>(place(cta)) * P.G + h0 + i;
-                    float4 *dst = reinterpret_cast<float4 *>(P.part_o + at * kHeadDim + d0);
-#pragma unroll
-                    for (int j = 0; j < kDims; j += 4)
-                        dst[j / 4] = make_float4(st[i].o[j], st[i].o[j + 1], st[i].o[j + 2],
-                                                 st[i].o[j + 3]);
-                    if (warp == 0 && row8 == 0 && (!kTwo || c4 < 2))
+                for (int i = 0; i < kRows; ++i) {
+                    const int hq = warp + i * kWarps;
+                    if (hq >= P.G) break;
+                    const size_t at = static_cast<size_t>(place(cta)) * P.G + hq;
+                    float4 *dst = reinterpret_cast<float4 *>(P.part_o + at * kHeadDim + lane * 8);
+                    dst[0] = make_float4(st[i].o[0], st[i].o[1], st[i].o[2], st[i].o[3]);
+                    dst[1] = make_float4(st[i].o[4], st[i].o[5], st[i].o[6], st[i].o[7]);
+                    if (lane == 0)
                         reinterpret_cast<float2 *>(P.part_ml)[at] = make_float2(st[i].m, st[i].l);
                 }
-                __threadfence();
                 consumer_bar();
-            };
-            // Whether this CTA is the last of `all` to count.
-            auto last = [&](unsigned *counter, int all) {
                 if (tid == 0) {
-                    last_cta = atomicAdd(counter, 1u) == static_cast<unsigned>(all - 1);
+                    __threadfence();  // the whole CTA's state, before the count
+                    const bool is_last = atomicAdd(counter, 1u) == static_cast<unsigned>(all - 1);
+                    __threadfence();  // the others' states are read after it
                     // everyone has counted: back to 0 for the next call
-                    if (last_cta) *counter = 0;
+                    if (is_last) *counter = 0;
+                    last_cta = is_last;
                 }
                 consumer_bar();
-                const bool mine = last_cta != 0;
-                if (mine) __threadfence();  // the others' states are read after the count
-                consumer_bar();             // (last_cta is read)
-                return mine;
+                return last_cta != 0;
             };
             // The states of CTAs from, from + step, .. up to `to`.
             auto join = [&](int from, int to, int step) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (h0 + i >= P.G) break;
-                    auto &h = st[i];
+                for (int i = 0; i < kRows; ++i) {
+                    const int hq = warp + i * kWarps;
+                    if (hq >= P.G) break;
+                    HeadState &h = st[i];
                     h.m = -INFINITY;
                     h.l = 0.f;
 #pragma unroll
-                    for (int j = 0; j < kDims; ++j) h.o[j] = 0.f;
+                    for (int j = 0; j < 8; ++j) h.o[j] = 0.f;
+#pragma unroll 1
                     for (int cta = from; cta <= to; cta += kFan * step) {
                         float2 ml[kFan];
-                        float4 x[kFan][kDims / 4];
+                        float4 x[kFan], y[kFan];
 #pragma unroll
                         for (int k = 0; k < kFan; ++k) {
                             ml[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-                            for (int j = 0; j < kDims / 4; ++j)
-                                x[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            const int from_cta = cta + k * step;
-                            if (from_cta <= to) {
-                                const size_t a = static_cast<size_t>(place(from_cta)) * P.G + h0 + i;
+                            x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (cta + k * step <= to) {
+                                const size_t a =
+                                    static_cast<size_t>(place(cta + k * step)) * P.G + hq;
                                 ml[k] = __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + a);
                                 const float4 *src = reinterpret_cast<const float4 *>(
-                                    P.part_o + a * kHeadDim + d0);
-#pragma unroll
-                                for (int j = 0; j < kDims / 4; ++j) x[k][j] = __ldcg(src + j);
+                                    P.part_o + a * kHeadDim + lane * 8);
+                                x[k] = __ldcg(src);
+                                y[k] = __ldcg(src + 1);
                             }
                         }
                         float top = h.m;
@@ -709,84 +723,71 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         h.m = top;
                         h.l *= wo;
 #pragma unroll
-                        for (int j = 0; j < kDims; ++j) h.o[j] *= wo;
+                        for (int j = 0; j < 8; ++j) h.o[j] *= wo;
 #pragma unroll
                         for (int k = 0; k < kFan; ++k) {
                             // (an empty state's sums are 0, or NaN, whatever their weight)
                             const float w = ml[k].x == -INFINITY ? 1.f : fast_exp2(ml[k].x - z);
+                            const float v[8] = {x[k].x, x[k].y, x[k].z, x[k].w,
+                                                y[k].x, y[k].y, y[k].z, y[k].w};
                             h.l += ml[k].y * w;
-#pragma unroll
-                            for (int j = 0; j < kDims; j += 4) {
-                                h.o[j] += x[k][j / 4].x * w;
-                                h.o[j + 1] += x[k][j / 4].y * w;
-                                h.o[j + 2] += x[k][j / 4].z * w;
-                                h.o[j + 3] += x[k][j / 4].w * w;
-                            }
+                            add_scaled(h, w, v);
                         }
                     }
                 }
             };
-            const int sub = (me - c0) / kFan, subs = (c1 - c0) / kFan + 1;
-            const int from = c0 + sub * kFan, to = from + kFan - 1 < c1 ? from + kFan - 1 : c1;
-            leave(me);
-            if (last(P.counters + place(from), to - from + 1)) {
-                join(from, to, 1);
-                finish = subs == 1;
-                if (!finish) {
-                    leave(from);
-                    // (c0 is the first CTA of one shared pair at most)
-                    if (last(P.counters + 2 * gridDim.x + c0, subs)) {
-                        join(c0, c1, kFan);
-                        finish = true;
-                    }
-                }
+            const int sub = (me - c0) / kSub, subs = (c1 - c0) / kSub + 1;
+            const int from = c0 + sub * kSub, to = from + kSub - 1 < c1 ? from + kSub - 1 : c1;
+            int a = from, b = to, step = 1;
+            finish = leave(me, P.counters + place(from), to - from + 1);
+#pragma unroll 1
+            while (finish) {
+                join(a, b, step);
+                if (subs == 1 || step != 1) break;
+                // (c0 is the first CTA of one shared pair at most)
+                finish = leave(from, P.counters + 2 * gridDim.x + c0, subs);
+                a = c0;
+                b = c1;
+                step = kSub;
             }
         }
         if (finish) {
             // the new token joins, the gate applies
+            float v[8];
+            kv4_floats(*reinterpret_cast<const uint4 *>(rows + (P.G + 1) * kRowBytes + lane * 16),
+                       v);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (h0 + i >= P.G) break;
-                auto &h = st[i];
-                const float x_new = s_new[h0 + i];
+            for (int i = 0; i < kRows; ++i) {
+                const int hq = warp + i * kWarps;
+                if (hq >= P.G) break;
+                HeadState &h = st[i];
+                const float x_new = s_new[hq];
                 const float top = fmaxf(h.m, x_new);
                 const float z = top == -INFINITY ? 0.f : top;
                 const float wo = h.m == -INFINITY ? 1.f : fast_exp2(h.m - z);
                 const float wn = fast_exp2(x_new - z);
-                const float scale = gate_act(s_gate[h0 + i], P.gate_mode) / (h.l * wo + wn);
-                uint32_t y[kDims / 2];
+                const float scale = gate_act(s_gate[hq], P.gate_mode) / (h.l * wo + wn);
+                float y[8];
 #pragma unroll
-                for (int j = 0; j < kDims; j += 4) {
-                    const float4 v4 = *reinterpret_cast<const float4 *>(vn + d0 + j);
-                    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-                    float r[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        r[k] = (h.o[j + k] * wo + v[k] * wn) * scale;
-                        // an infinity is one however small its weight
-                        if (!isfinite(v[k])) r[k] = (v[k] + nonfinite_part(h.o[j + k])) * scale;
-                    }
-                    y[j / 2] = pack_bf16x2(r[0], r[1]);
-                    y[j / 2 + 1] = pack_bf16x2(r[2], r[3]);
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = (h.o[j] * wo + v[j] * wn) * scale;
+                    // an infinity is one however small its weight
+                    if (!isfinite(v[j])) y[j] = (v[j] + nonfinite_part(h.o[j])) * scale;
                 }
-                __nv_bfloat16 *dst =
-                    P.out +
-                    (static_cast<size_t>(pair.b) * P.H + pair.g * P.G + h0 + i) * kHeadDim + d0;
-                if (kTwo)
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(y[0], y[1]);
-                else
-                    *reinterpret_cast<uint4 *>(dst) =
-                        make_uint4(y[0], y[1], y[kDims / 2 - 2], y[kDims / 2 - 1]);
+                *reinterpret_cast<uint4 *>(
+                    P.out + (static_cast<size_t>(pair.b) * P.H + pair.g * P.G + hq) * kHeadDim +
+                    lane * 8) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
             }
             if (warp == 0) {
                 // the new token's slot: every read of this pair is done
                 if (!k_new) {
                     if (lane == 0) atomicOr(P.status, kErrPage);
-                } else {
+                } else if (mbar_wait_plain(&new_full[s_pair], pair_turn)) {
                     *reinterpret_cast<uint32_t *>(k_new + kv4_key_at(lane, t_new)) =
-                        new_codes[0][lane];
+                        new_codes[s_pair][0][lane];
                     // the other slot of each byte stays
-                    const uint32_t codes = new_codes[1][lane];
+                    const uint32_t codes = new_codes[s_pair][1][lane];
                     uint8_t *dst = v_new + kv4_value_at(lane, t_new >> 2) + 2 * (t_new >> 1 & 1);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -796,15 +797,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             t_new & 1 ? (old[j] & 0x0f0fu) | c << 4 : (old[j] & 0xf0f0u) | c);
                     }
                     if (!(lane & 1)) {
-                        k_new[kv4_key_scale_at(lane >> 1, t_new)] = new_scale[0][lane];
+                        k_new[kv4_key_scale_at(lane >> 1, t_new)] = new_scale[s_pair][0][lane];
                         v_new[kv4_value_scale_at(lane >> 1, t_new >> 2) + 2 * (t_new & 1) +
-                              (t_new >> 1 & 1)] = new_scale[1][lane];
+                              (t_new >> 1 & 1)] = new_scale[s_pair][1][lane];
                     }
+                } else {
+                    atomicOr(P.status, kErrTimeout);
                 }
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pair_empty[n % kPairs]);
+        if (lane == 0) mbar_arrive(&pair_empty[s_pair]);
         await_pair(n + 1);  // (q, the new token and the sums are read)
     }
     grid_dep_launch();

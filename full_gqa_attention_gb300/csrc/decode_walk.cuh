@@ -7,6 +7,12 @@
 
 namespace spark {
 
+// A quotient of numbers >= 0 that nearly always have 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
+
 // What a row asks for: its position, first visible slot and tiles (0: nothing).
 // kTile: slots of a tile.  kPairCost: what setting a pair up and finishing it
 // costs besides, in tiles.
@@ -54,7 +60,7 @@ struct DecodeWalk {
                 row = decode_row<kTile, kPairCost>(P, ++b);
             }
             const long long n = row.units();
-            g = static_cast<int>((u - base) / n);
+            g = static_cast<int>(quotient(u - base, n));
             first = base + g * n;
             const int from = static_cast<int>(u - first) - kPairCost;
             const int to = static_cast<int>(end - first < n ? end - first : n) - kPairCost;
