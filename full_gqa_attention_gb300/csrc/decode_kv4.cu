@@ -101,9 +101,22 @@ __device__ __forceinline__ uint32_t pack_half2_rest(float lo, float hi, uint32_t
     return pack_half2(lo - f.x, hi - f.y);
 }
 
-// Byte i of four scales, as the two halves of a word.
-__device__ __forceinline__ uint32_t twice_scale(uint32_t scales, int i) {
-    return __byte_perm(scales, 0, 0x4040 | i | i << 8) << 7;
+// Two halves times scale `upper` (0, 1) of two.
+__device__ __forceinline__ uint32_t mul_scale(uint32_t a, uint32_t scales, int upper) {
+    const __half2 s = *reinterpret_cast<const __half2 *>(&scales);
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a),
+                              upper ? __high2half2(s) : __low2half2(s));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Counts one up: what was written before is seen by who counts later.
+__device__ __forceinline__ unsigned atomic_count(unsigned *counter) {
+    unsigned before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                 : "=r"(before)
+                 : "l"(counter)
+                 : "memory");
+    return before;
 }
 
 __device__ __forceinline__ float nonfinite_part(float x) { return isfinite(x) ? 0.f : x; }
@@ -144,18 +157,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __shared__ uint8_t new_scale[kPairs][2][32];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kWarps);
-        }
-        for (int s = 0; s < kPairs; ++s) {
-            mbar_init(&pair_full[s], 1);
-            mbar_init(&rows_full[s], 1);
-            mbar_init(&new_full[s], 1);
-            mbar_init(&pair_empty[s], kWarps);
-        }
+    if (tid < kStages) {
+        mbar_init(&full[tid], 1);
+        mbar_init(&empty[tid], kWarps);
         fence_mbar_init();
+    } else if (tid >= 32 && tid < 32 + kPairs) {
+        mbar_init(&pair_full[tid - 32], 1);
+        mbar_init(&rows_full[tid - 32], 1);
+        mbar_init(&new_full[tid - 32], 1);
+        mbar_init(&pair_empty[tid - 32], kWarps);
+        fence_mbar_init();
+    } else if (tid == 64) {
         abort_flag = 0;
         gave_up[0] = gave_up[1] = passed[0] = passed[1] = 0;
         lost = 0;
@@ -302,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 const int s = it % kStages;
                 if (it >= kStages && lane == 0)
-                    ok = mbar_wait(&empty[s], ((it / kStages) - 1) & 1, &abort_flag, P.status);
+                    ok = mbar_wait_suspended(&empty[s], ((it / kStages) - 1) & 1, &abort_flag, P.status);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 const int id = __shfl_sync(0xffffffffu, ids, (in + piece) & 31);
@@ -446,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         bool ok = !aborted;
         for (int t = t0; ok && t < t1; ++t, ++it) {
             const int s = it % kStages;
-            ok = mbar_wait(&full[s], (it / kStages) & 1, &abort_flag, P.status);
+            ok = mbar_wait_suspended(&full[s], (it / kStages) & 1, &abort_flag, P.status);
             const int first = (lo & ~(kTile - 1)) + t * kTile;
             const bool edge = first < lo || first + kTile > pos;
             const uint8_t *kt = stages + s * kStageBytes;
@@ -458,9 +470,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const uint8_t *ks = kg + kKv4Codes + tok * 16 + c4 * 4;
                 const uint32_t sa = *reinterpret_cast<const uint32_t *>(ks);
                 const uint32_t sb = *reinterpret_cast<const uint32_t *>(ks + 32);
-                float acc[2][4];
+                // blocks 2 c4 and 8 + 2 c4 (first words), and those behind them
+                const uint32_t ua[2] = {(sa & 0x00ff00ffu) << 7, (sa >> 1) & 0x7f807f80u};
+                const uint32_t ub[2] = {(sb & 0x00ff00ffu) << 7, (sb >> 1) & 0x7f807f80u};
+                float acc[4][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
+                for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = acc[2][i] = acc[3][i] = 0.f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint8_t *kc = kg + h * 1024 + tok * 64 + c4 * 16;
@@ -472,24 +487,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     for (int i = 0; i < 4; ++i) {
                         const uint4 qf = *reinterpret_cast<const uint4 *>(
                             qs + (4 * h + i) * 512 + lane * 16);
-                        const uint32_t ua = twice_scale(sa, 2 * h + (i >> 1));
-                        const uint32_t ub = twice_scale(sb, 2 * h + (i >> 1));
                         uint32_t a[4], b[4];
                         kv4_widen(wa[i], a);
                         kv4_widen(wb[i], b);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            a[j] = mul_half2(a[j], ua);
-                            b[j] = mul_half2(b[j], ub);
+                            a[j] = mul_scale(a[j], ua[i >> 1], h);
+                            b[j] = mul_scale(b[j], ub[i >> 1], h);
                         }
-                        mma_f16_16816(acc[0], a[0], b[0], a[1], b[1], qf.x, qf.y);
-                        mma_f16_16816(acc[1], a[2], b[2], a[3], b[3], qf.z, qf.w);
+                        mma_f16_16816(acc[2 * (i & 1)], a[0], b[0], a[1], b[1], qf.x, qf.y);
+                        mma_f16_16816(acc[2 * (i & 1) + 1], a[2], b[2], a[3], b[3], qf.z, qf.w);
                     }
                 }
                 // this thread's slots (rows row8 and row8 + 8) and heads
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[i] = acc[0][i] + acc[1][i];
+                    x[i] = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
                     if (kTwo) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);
                     x[i] *= i & 1 ? unit1 : unit0;
                 }
@@ -676,9 +689,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 consumer_bar();
                 if (tid == 0) {
-                    __threadfence();  // the whole CTA's state, before the count
-                    const bool is_last = atomicAdd(counter, 1u) == static_cast<unsigned>(all - 1);
-                    __threadfence();  // the others' states are read after it
+                    // behind the whole CTA's state, before the others' are read
+                    const bool is_last = atomic_count(counter) == static_cast<unsigned>(all - 1);
                     // everyone has counted: back to 0 for the next call
                     if (is_last) *counter = 0;
                     last_cta = is_last;
