@@ -280,12 +280,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const uint8_t *src = new_rows + s * kNewBytes + P.G * kRowBytes + lane * 16;
             float y[8];
             unsigned byte;
-            kv4_key_row(kv4_key_turn(*reinterpret_cast<const uint4 *>(src), P.rope.rot_dim,
-                                     wk.row.pos, lane),
-                        cs_new, wk.row.pos, P.turns, y, new_codes[s][0][lane], byte);
+            const KeyTurn turn = kv4_key_turn(*reinterpret_cast<const uint4 *>(src),
+                                              P.rope.rot_dim, wk.row.pos, lane);
+            kv4_rotate(turn, cs_new, y);
+            kv4_key_row(turn, y, wk.row.pos, P.turns, new_codes[s][0][lane], byte);
             new_scale[s][0][lane] = static_cast<uint8_t>(byte);
-            kv4_floats(*reinterpret_cast<const uint4 *>(src + kRowBytes), y);
-            kv4_value_row(y, new_codes[s][1][lane], byte);
+            kv4_value_row(*reinterpret_cast<const uint4 *>(src + kRowBytes),
+                          new_codes[s][1][lane], byte);
             new_scale[s][1][lane] = static_cast<uint8_t>(byte);
             __syncwarp();
             if (lane == 0) mbar_arrive(&new_full[s]);

@@ -115,12 +115,26 @@ __device__ __forceinline__ StoreRow store_row(const Kv4Params &P, int r, bool re
     return StoreRow{start, start + (c1 - c0), c0};
 }
 
-__global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_constant__ Kv4Params P) {
-    __shared__ float2 freq[kMaxRopePairs];
-    __shared__ float2 cs[kKv4Group][kMaxRopePairs];
+// Cosines and sines of a token, as the lanes read them: pairs 8 l + 2 i and the
+// next one are the 16 bytes i of lane l.
+__device__ __forceinline__ int angle_at(int k) {
+    return (k >> 1 & 3) * 32 + (k >> 3) * 2 + (k & 1);  // in float2
+}
+
+constexpr int kStoreSmem = (2 * kKv4Group * kMaxRopePairs) * 8;
+
+__global__ void __launch_bounds__(kThreads, 3)
+    kv4_store_kernel(const __grid_constant__ Kv4Params P) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    float2 *angles = reinterpret_cast<float2 *>(smem);       // [16 tokens][128]
+    float2 *steps = angles + kKv4Group * kMaxRopePairs;      // [16][128]: of 0 .. 15 positions
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int half = P.rope.rot_dim / 2;
-    if (tid < half) freq[tid] = P.rope.u[tid];
+    // This thread's pair, and the first of its tokens.
+    const int together = half ? kThreads / half : 1;         // tokens the threads take at once
+    const int k = half ? tid % half : 0, t_mine = half ? tid / half : kKv4Group;
+    float2 freq = make_float2(0.f, 0.f);
+    if (half) freq = P.rope.u[k];
     grid_dep_wait();
     grid_dep_launch();
     const int parts = (P.Hkv + P.heads - 1) / P.heads;
@@ -130,7 +144,19 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
     };
     Stretch st;
     if (!stretch_of(P.S, units, st)) return;
+    // Consecutive positions, as nearly always: a group's turns are its first
+    // token's and those of 0 .. 15 positions together, 8 instructions for some 70.
+    const bool stepwise = st.end - st.u > 2;
+    if (stepwise)
+#pragma unroll 1
+        for (int t = t_mine; t < kKv4Group; t += together) {
+            float2 c;
+            rope_cos_sin_fine(t, freq, c.x, c.y);
+            steps[t * kMaxRopePairs + k] = c;
+        }
     const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
+    const int turning = P.rope.rot_dim >> 4;                 // lanes of each half of a turn
+    const int lane_pairs = lane < turning ? lane : lane < 2 * turning ? lane - turning : 0;
     StoreRow row = store_row(P, st.r, false);
     for (; st.u < st.end; ++st.u) {
         while (st.u >= st.base + static_cast<long long>(groups_of(row.a, row.b)) * parts) {
@@ -147,18 +173,35 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
         const int first = row.row + (slot0 - row.a);  // packed row of slot 0 of the group
         const int id = P.pg.table[static_cast<size_t>(st.r) * P.pg.max_pages +
                                   (slot0 >> P.pg.page_shift)];
+        const int32_t *pos = P.pos + first;
+        // The angles; every warp looks at the positions itself.
+        const int my_t = lane < t_lo ? t_lo : lane < t_hi ? lane : t_hi - 1;
+        const int my_pos = half ? pos[my_t] : 0;
+        const int pos_lo = __shfl_sync(0xffffffffu, my_pos, t_lo);
+        const bool steady =
+            stepwise && __all_sync(0xffffffffu, my_pos == pos_lo + (my_t - t_lo));
+        __syncthreads();  // (the angles of the unit before are read)
+        if (steady) {
+            float2 c;
+            rope_cos_sin_fine(pos_lo, freq, c.x, c.y);
+            for (int t = t_lo + t_mine; t < t_hi; t += together) {
+                const float2 d = steps[(t - t_lo) * kMaxRopePairs + k];
+                angles[t * kMaxRopePairs + angle_at(k)] =
+                    make_float2(fmaf(c.x, d.x, -c.y * d.y), fmaf(c.y, d.x, c.x * d.y));
+            }
+        } else {
+#pragma unroll 1
+            for (int t = t_lo + t_mine; t < t_hi; t += together) {
+                float2 c;
+                rope_cos_sin_fine(pos[t], freq, c.x, c.y);
+                angles[t * kMaxRopePairs + angle_at(k)] = c;
+            }
+        }
+        __syncthreads();
         if (id < 0 || id >= P.pg.n_pages) {
             if (tid == 0) atomicOr(P.status, kErrPage);
             continue;
         }
-        __syncthreads();  // (the angles of the unit before are read)
-        for (int i = tid; i < (t_hi - t_lo) * half; i += kThreads) {
-            const int t = t_lo + i / half, k = i % half;
-            float2 c;
-            rope_cos_sin_fine(P.pos[first + t], freq[k], c.x, c.y);
-            cs[t][k] = c;
-        }
-        __syncthreads();
         for (int task = warp; task < heads * 8; task += kWarps) {
             const int h = h0 + (task >> 3), quad = task & 3;
             const bool key = !(task & 4);
@@ -174,17 +217,23 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
             }
             uint8_t *group = (key ? P.pg.k : P.pg.v) + P.pg.group(id, h, P.Hkv, slot0);
             if (key) {
-#pragma unroll 1
+#pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int t = 4 * quad + j;
                     if (t < t_lo || t >= t_hi) continue;
-                    const uint4 x = j == 0 ? raw[0] : j == 1 ? raw[1] : j == 2 ? raw[2] : raw[3];
-                    const int pos = half ? P.pos[first + t] : 0;
-                    const KeyTurn turn = kv4_key_turn(x, P.rope.rot_dim, pos, lane);
-                    float y[8];
+                    const int p = __shfl_sync(0xffffffffu, my_pos, t);
+                    const KeyTurn turn = kv4_key_turn(raw[j], P.rope.rot_dim, p, lane);
+                    float c[8], s[8], y[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 a = *reinterpret_cast<const float4 *>(
+                            angles + t * kMaxRopePairs + i * 32 + lane_pairs * 2);
+                        c[2 * i] = a.x, s[2 * i] = a.y, c[2 * i + 1] = a.z, s[2 * i + 1] = a.w;
+                    }
+                    kv4_rotate(turn, c, s, y);
                     uint32_t codes;
                     unsigned byte;
-                    kv4_key_row(turn, cs[t], pos, P.turns, y, codes, byte);
+                    kv4_key_row(turn, y, p, P.turns, codes, byte);
                     *reinterpret_cast<uint32_t *>(group + kv4_key_at(lane, t)) = codes;
                     if (!(lane & 1))
                         group[kv4_key_scale_at(lane >> 1, t)] = static_cast<uint8_t>(byte);
@@ -197,9 +246,7 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
                 for (int j = 0; j < 4; ++j) {
                     const int t = 4 * quad + j;
                     unsigned byte;
-                    float x[8];
-                    kv4_floats(raw[j], x);
-                    kv4_value_row(x, codes[j], byte);
+                    kv4_value_row(raw[j], codes[j], byte);
                     scales |= byte << (8 * (2 * (j & 1) + (j >> 1)));
                     if (t < t_lo || t >= t_hi) {
                         keep |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
@@ -210,10 +257,10 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
                 // dims 2 i, 2 i + 1 of slots 0 and 1, then of 2 and 3
                 uint32_t e[2], o[2];
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const uint32_t a = codes[2 * p], b = codes[2 * p + 1];
-                    e[p] = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
-                    o[p] = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t a = codes[2 * q], b = codes[2 * q + 1];
+                    e[q] = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
+                    o[q] = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
                 }
                 uint32_t w[4];
 #pragma unroll
@@ -440,7 +487,7 @@ spark_status spark_attn_kv4_store(const void *qkv, const int32_t *pos, const int
     set_layer(P, desc, H, Hkv);
     set_pages(P, k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
     P.heads = Hkv;
-    return done(launch_overlapped(kv4_store_kernel, dim3(sms * 4), dim3(kThreads), 0,
+    return done(launch_overlapped(kv4_store_kernel, dim3(sms * 3), dim3(kThreads), kStoreSmem,
                                   static_cast<cudaStream_t>(stream), P));
 }
 

@@ -152,45 +152,7 @@ __device__ __forceinline__ uint32_t kv4_codes(const float (&y)[8]) {
 }
 
 // A warp's row of 256 dims, dims 8 lane .. 8 lane + 7 in a lane: two lanes hold
-// a block.  The maximum of both, and whether all of both is finite.
-__device__ __forceinline__ float kv4_block_max(const float (&x)[8], bool &finite) {
-    float a = 0.f, z = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        a = fmaxf(a, fabsf(x[i]));
-        z += x[i] * 0.f;
-    }
-    z += __shfl_xor_sync(0xffffffffu, z, 1);
-    finite = z == 0.f;
-    return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-}
-
-// What an exact quotient by a scale (or by 6) rounds to is told by one that is
-// off by 2^-22, where the number divided is bf16: the quotient lies on a border
-// between two codes (or scales), which have few bits, or 2^-9 of itself away
-// from it.  Sixteen bits of it are kept.
-__device__ __forceinline__ float kv4_snap(float y) {
-    return __uint_as_float((__float_as_uint(y) + 0x80u) & 0xffffff00u);
-}
-
-constexpr float kSixth = 1.0f / 6.0f;
-
-// A value's row.
-__device__ __forceinline__ void kv4_value_row(const float (&x)[8], uint32_t &codes,
-                                              unsigned &byte) {
-    bool finite;
-    const float a = kv4_block_max(x, finite);
-    byte = kv4_scale_byte(kv4_snap(a * kSixth));
-    const float s = kv4_scale(byte), r = s > 0.f ? __frcp_rn(s) : 0.f;
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = kv4_snap(x[i] * r);
-    codes = kv4_codes(y);
-    if (!finite) {
-        codes = 0;
-        byte = kKv4NanScale;
-    }
-}
+// a block.
 
 __device__ __forceinline__ void kv4_floats(const uint4 &raw, float (&x)[8]) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -201,41 +163,102 @@ __device__ __forceinline__ void kv4_floats(const uint4 &raw, float (&x)[8]) {
     }
 }
 
-// Dims 8 lane .. of a key: the lane's own values, those they turn with, and
-// where in the turn they stand.
+// The largest of a lane's eight; infinite where one of the eight bf16 numbers of
+// `raw` is not finite (0 times it is NaN, in pairs).
+__device__ __forceinline__ float kv4_largest(const uint4 &raw, const float (&x)[8]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    __nv_bfloat162 odd = __floats2bfloat162_rn(0.f, 0.f);
+    const __nv_bfloat162 zero = odd;
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), zero, odd);
+        a = fmaxf(a, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    }
+    return __low2float(odd) + __high2float(odd) == 0.f ? a : INFINITY;
+}
+
+__device__ __forceinline__ float kv4_reciprocal(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return s > 0.f ? r : 0.f;
+}
+
+// What an exact quotient by a scale (or by 6) rounds to is told by one that is
+// off by 2^-22, where the number divided is bf16: the quotient lies on a border
+// between two codes (or scales), which have few bits, or 2^-9 of itself away
+// from it.  So a maximum's sixth keeps sixteen bits, and a quotient, which is 8 at
+// most or saturates, what is left of it beside kSnap: multiples of 2^-13.
+__device__ __forceinline__ float kv4_snap(float y) {
+    return __uint_as_float((__float_as_uint(y) + 0x80u) & 0xffffff00u);
+}
+
+constexpr float kSnap = 1536.0f;
+constexpr float kSixth = 1.0f / 6.0f;
+
+// A value's row.
+__device__ __forceinline__ void kv4_value_row(const uint4 &raw, uint32_t &codes, unsigned &byte) {
+    float x[8];
+    kv4_floats(raw, x);
+    float a = kv4_largest(raw, x);
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    byte = kv4_scale_byte(kv4_snap(a * kSixth));
+    const float r = kv4_reciprocal(kv4_scale(byte));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmaf_rn(x[i], r, kSnap), -kSnap);
+    codes = kv4_codes(x);
+    if (a == INFINITY) {
+        codes = 0;
+        byte = kKv4NanScale;
+    }
+}
+
+// Dims 8 lane .. of a key and of what they turn with: y = x cos + z sin (z has
+// its sign changed in the first of each pair).
 struct KeyTurn {
     float x[8], z[8];
+    float largest, others;     // kv4_largest of both
     int k0;                    // the first pair
-    bool turns, upper;         // upper: the second of each pair
+    bool turns;
 };
 
 __device__ __forceinline__ KeyTurn kv4_key_turn(const uint4 &raw, int rot_dim, int pos, int lane) {
     KeyTurn t;
     const int half = rot_dim >> 4;  // lanes of each half
     t.turns = lane < 2 * half && pos != 0;
-    t.upper = lane >= half;
-    const int other = !t.turns ? lane : t.upper ? lane - half : lane + half;
-    t.k0 = !t.turns ? 0 : (t.upper ? lane - half : lane) * 8;
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t o = __shfl_sync(0xffffffffu, w[i], other);
-        t.x[2 * i] = bf16_lo(w[i]);
-        t.x[2 * i + 1] = bf16_hi(w[i]);
-        t.z[2 * i] = bf16_lo(o);
-        t.z[2 * i + 1] = bf16_hi(o);
-    }
+    const bool upper = lane >= half;
+    const int other = !t.turns ? lane : upper ? lane - half : lane + half;
+    t.k0 = !t.turns ? 0 : (upper ? lane - half : lane) * 8;
+    const uint32_t sign = upper ? 0u : 0x80008000u;
+    kv4_floats(raw, t.x);
+    t.largest = kv4_largest(raw, t.x);
+    uint4 o;
+    o.x = __shfl_sync(0xffffffffu, raw.x, other) ^ sign;
+    o.y = __shfl_sync(0xffffffffu, raw.y, other) ^ sign;
+    o.z = __shfl_sync(0xffffffffu, raw.z, other) ^ sign;
+    o.w = __shfl_sync(0xffffffffu, raw.w, other) ^ sign;
+    t.others = __shfl_sync(0xffffffffu, t.largest, other);
+    kv4_floats(o, t.z);
     return t;
 }
 
-// The rotated values in 32 bits; cs: cos and sin of each pair.
+// The rotated values in 32 bits; c, s: cosines and sines of the lane's pairs.
+__device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float (&c)[8],
+                                           const float (&s)[8], float (&y)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float r = __fmaf_rn(t.x[i], c[i], __fmul_rn(t.z[i], s[i]));
+        y[i] = t.turns ? r : t.x[i];
+    }
+}
+// ... from a table of all pairs.
 __device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float2 *cs, float (&y)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         y[i] = t.x[i];
         if (t.turns) {
             const float2 c = cs[t.k0 + i];
-            y[i] = __fmaf_rn(t.x[i], c.x, t.upper ? __fmul_rn(t.z[i], c.y) : -__fmul_rn(t.z[i], c.y));
+            y[i] = __fmaf_rn(t.x[i], c.x, __fmul_rn(t.z[i], c.y));
         }
     }
 }
@@ -243,8 +266,7 @@ __device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float2 *cs, f
 // Value i of a turned key in 64 bits: sine and cosine by their series, to
 // x^15 / 15!, of an angle of an eighth of a turn at most (1e-15).  64-bit
 // products are few on this chip: each takes a warp 16 cycles.
-__device__ __noinline__ inline double kv4_exact_turn(float x, float z, bool upper, int pos,
-                                                     double u) {
+__device__ __noinline__ inline double kv4_exact_turn(float x, float z, int pos, double u) {
     const double p = pos * u;
     const double t = (p - rint(p)) + fma(static_cast<double>(pos), u, -p);
     const double quarter = rint(4.0 * t);
@@ -267,7 +289,7 @@ __device__ __noinline__ inline double kv4_exact_turn(float x, float z, bool uppe
     const int q = static_cast<int>(quarter) & 3;  // turned on by quarters
     const double cq = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
     const double sq = q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c;
-    return upper ? x * cq + z * sq : x * cq - z * sq;
+    return x * cq + z * sq;
 }
 
 // Settles the scale of the blocks in `open` (the same in a block's two lanes)
@@ -280,7 +302,7 @@ __device__ __noinline__ inline unsigned kv4_settle_scale(const KeyTurn &t, int p
     if (open)
         for (int i = 0; i < 8; ++i)
             if (fabsf(y[i]) >= least)
-                a = fmax(a, fabs(kv4_exact_turn(t.x[i], t.z[i], t.upper, pos, turns[t.k0 + i])));
+                a = fmax(a, fabs(kv4_exact_turn(t.x[i], t.z[i], pos, turns[t.k0 + i])));
     a = fmax(a, __shfl_xor_sync(0xffffffffu, a, 1));
     if (!open) return byte;
     // the scale below a / 6, the next one, and their middle
@@ -298,7 +320,7 @@ __device__ __noinline__ inline uint32_t kv4_settle_codes(const KeyTurn &t, int p
     const double s = scale;
     for (int i = 0; i < 8; ++i) {
         if (!(open >> (4 * i) & 1u)) continue;
-        const double v = kv4_exact_turn(t.x[i], t.z[i], t.upper, pos, turns[t.k0 + i]);
+        const double v = kv4_exact_turn(t.x[i], t.z[i], pos, turns[t.k0 + i]);
         const double m = fabs(v);
         unsigned c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) +
                      (m > 2.5 * s) + (m >= 3.5 * s) + (m > 5.0 * s);
@@ -308,39 +330,44 @@ __device__ __noinline__ inline uint32_t kv4_settle_codes(const KeyTurn &t, int p
     return codes;
 }
 
-// A key's row, rotated (y, in 32 bits) and quantised.  What the pages hold is
-// the nearest to the exact rotation: where 32 bits do not tell on which side of
-// a border a value or a scale lies (one row in some hundreds), 64 bits decide.
-// |y| is off by 2^-22 (|x| + |z|) at most: cos and sin by 2^-23 each (1 ulp of
-// sincospif, and 2^-24 that the frequencies' two parts leave of the angle below
-// 2^24 positions), the product and the sum by 2^-24 each.  Twice that is allowed.
-// Dims that do not turn are bf16: kv4_snap.
-__device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float2 *cs, int pos,
-                                            const double *turns, float (&y)[8], uint32_t &codes,
+// A key's row, rotated (y, in 32 bits), quantised.  What the pages hold is the
+// nearest to the exact rotation: where 32 bits do not tell on which side of a
+// border a value or a scale lies (one row in a hundred or two), 64 bits decide.
+// |y| is off by 2^-21 (|x| + |z|) at most: cos and sin by 2^-22 each (1 ulp of
+// sincospif and 2^-24 that the frequencies' two parts leave of the angle below
+// 2^24 positions; where two turns are put together, both, and the products'
+// roundings), the product and the sum by 2^-24 each.  Twice that is allowed, and
+// 2^-22 of a quotient (8 at most, or it saturates).  Dims that do not turn are
+// bf16: kSnap.
+__device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8], int pos,
+                                            const double *turns, uint32_t &codes,
                                             unsigned &byte) {
-    constexpr float kRel = 2.38418579e-7f, kAbs = 4.76837158e-7f;  // 2^-22, 2^-21
-    kv4_rotate(t, cs, y);
-    bool finite;
-    const float a = kv4_block_max(y, finite);
-    float e = 0.f;
-    if (t.turns)
+    constexpr float kRel = 2.38418579e-7f, kAbs = 9.53674316e-7f;  // 2^-22, 2^-20
+    float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e = fmaxf(e, fabsf(t.x[i]) + fabsf(t.z[i]));
-    e *= kAbs;
-    const float other = __shfl_xor_sync(0xffffffffu, e, 1);  // (a block turns as a whole)
-    const float most = t.turns ? fmaf(a, kRel, fmaxf(e, other)) : 0.f;
+    for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    // infinite where a value of the block is not finite (a block turns as a whole)
+    const float e = t.turns ? fmaf(t.largest, kAbs, t.others * kAbs)
+                            : t.largest == INFINITY ? INFINITY : 0.f;
+    const float worst = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
+    const bool finite = worst < INFINITY;
+    const float most = t.turns ? fmaf(a, kRel, worst) : 0.f;
     const float lo_a = fmaxf(a - most, 0.f) * kSixth, hi_a = (a + most) * kSixth;
     byte = kv4_scale_byte(t.turns ? lo_a : kv4_snap(lo_a));
     const bool open_scale = t.turns && finite && byte != kv4_scale_byte(hi_a);
     if (__any_sync(0xffffffffu, open_scale))
         byte = kv4_settle_scale(t, pos, turns, y, a - 2.f * most, open_scale, byte);
-    const float s = kv4_scale(byte), r = s > 0.f ? __frcp_rn(s) : 0.f;
+    const float s = kv4_scale(byte), r = kv4_reciprocal(s);
+    const float d = fmaf(worst, r, 8.f * kRel);
+    // what the quotient is told by: both ends of what it can be, or itself, snapped
+    const float down = t.turns ? -d : kSnap, up = t.turns ? d : kSnap;
+    const float back = t.turns ? 0.f : -kSnap;
     float lo[8], hi[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = y[i] * r, d = __fmaf_rn(fabsf(q), kRel, e * r);
-        lo[i] = t.turns ? q - d : kv4_snap(q);
-        hi[i] = t.turns ? q + d : lo[i];
+        lo[i] = __fadd_rn(__fmaf_rn(y[i], r, down), back);
+        hi[i] = __fadd_rn(__fmaf_rn(y[i], r, up), back);
     }
     codes = kv4_codes(hi);
     // (a sign that differs beside zero stands for the same value)
