@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const KeyTurn turn = kv4_key_turn(*reinterpret_cast<const uint4 *>(src),
                                               P.rope.rot_dim, wk.row.pos, lane);
             kv4_rotate(turn, cs_new, y);
-            kv4_key_row(turn, y, wk.row.pos, P.turns, new_codes[s][0][lane], byte);
+            kv4_key_row<false>(turn, y, wk.row.pos, P.turns, new_codes[s][0][lane], byte);
             new_scale[s][0][lane] = static_cast<uint8_t>(byte);
             kv4_value_row(*reinterpret_cast<const uint4 *>(src + kRowBytes),
                           new_codes[s][1][lane], byte);
@@ -407,10 +407,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const uint4 raw = *reinterpret_cast<const uint4 *>(rows + hh * kRowBytes + lane * 16);
             const KeyTurn turn = kv4_key_turn(raw, P.rope.rot_dim, pos, lane);
             float y[8], k[8];
+            kv4_floats(raw, y);
             kv4_floats(*reinterpret_cast<const uint4 *>(rows + P.G * kRowBytes + lane * 16), k);
             float d = 0.f, a = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d = fmaf(turn.x[j], k[j], d);
+            for (int j = 0; j < 8; ++j) d = fmaf(y[j], k[j], d);
             kv4_rotate(turn, cs, y);
             bool odd = false;
 #pragma unroll

@@ -121,13 +121,16 @@ __device__ __forceinline__ int angle_at(int k) {
     return (k >> 1 & 3) * 32 + (k >> 3) * 2 + (k & 1);  // in float2
 }
 
-constexpr int kStoreSmem = (2 * kKv4Group * kMaxRopePairs) * 8;
+constexpr int kStoreSmem = (3 * kKv4Group * kMaxRopePairs) * 8;
 
+// kAll: all 256 dims turn.
+template <bool kAll>
 __global__ void __launch_bounds__(kThreads, 3)
     kv4_store_kernel(const __grid_constant__ Kv4Params P) {
     extern __shared__ __align__(16) uint8_t smem[];
-    float2 *angles = reinterpret_cast<float2 *>(smem);       // [16 tokens][128]
-    float2 *steps = angles + kKv4Group * kMaxRopePairs;      // [16][128]: of 0 .. 15 positions
+    constexpr int kAngles = kKv4Group * kMaxRopePairs;       // of 16 tokens
+    float2 *angles = reinterpret_cast<float2 *>(smem);       // of a unit, and of the next
+    float2 *steps = angles + 2 * kAngles;                    // of 0 .. 15 positions
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int half = P.rope.rot_dim / 2;
     // This thread's pair, and the first of its tokens.
@@ -147,18 +150,23 @@ __global__ void __launch_bounds__(kThreads, 3)
     // Consecutive positions, as nearly always: a group's turns are its first
     // token's and those of 0 .. 15 positions together, 8 instructions for some 70.
     const bool stepwise = st.end - st.u > 2;
-    if (stepwise)
+    if (stepwise) {
 #pragma unroll 1
         for (int t = t_mine; t < kKv4Group; t += together) {
             float2 c;
             rope_cos_sin_fine(t, freq, c.x, c.y);
             steps[t * kMaxRopePairs + k] = c;
         }
+        __syncthreads();
+    }
     const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
     const int turning = P.rope.rot_dim >> 4;                 // lanes of each half of a turn
     const int lane_pairs = lane < turning ? lane : lane < 2 * turning ? lane - turning : 0;
     StoreRow row = store_row(P, st.r, false);
+    int turn_of = 0;
     for (; st.u < st.end; ++st.u) {
+        angles = reinterpret_cast<float2 *>(smem) + turn_of * kAngles;
+        turn_of ^= 1;
         while (st.u >= st.base + static_cast<long long>(groups_of(row.a, row.b)) * parts) {
             st.base += static_cast<long long>(groups_of(row.a, row.b)) * parts;
             if (++st.r >= P.S) return;  // the offsets changed under the call
@@ -180,7 +188,11 @@ __global__ void __launch_bounds__(kThreads, 3)
         const int pos_lo = __shfl_sync(0xffffffffu, my_pos, t_lo);
         const bool steady =
             stepwise && __all_sync(0xffffffffu, my_pos == pos_lo + (my_t - t_lo));
-        __syncthreads();  // (the angles of the unit before are read)
+        if (id < 0 || id >= P.pg.n_pages) {
+            if (tid == 0) atomicOr(P.status, kErrPage);
+            __syncthreads();  // (as in every unit)
+            continue;
+        }
         if (steady) {
             float2 c;
             rope_cos_sin_fine(pos_lo, freq, c.x, c.y);
@@ -197,91 +209,102 @@ __global__ void __launch_bounds__(kThreads, 3)
                 angles[t * kMaxRopePairs + angle_at(k)] = c;
             }
         }
-        __syncthreads();
-        if (id < 0 || id >= P.pg.n_pages) {
-            if (tid == 0) atomicOr(P.status, kErrPage);
-            continue;
-        }
-        for (int task = warp; task < heads * 8; task += kWarps) {
-            const int h = h0 + (task >> 3), quad = task & 3;
-            const bool key = !(task & 4);
-            uint4 raw[4];
+        const __nv_bfloat16 *base = P.qkv + first * static_cast<ptrdiff_t>(width) + lane * 8 +
+                                    static_cast<size_t>(P.H + h0) * kHeadDim;
+        // Four tokens of a head's keys or values.
+        auto fetch = [&](const __nv_bfloat16 *from, int quad, uint4(&raw)[4]) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = 4 * quad + j;
                 raw[j] = make_uint4(0, 0, 0, 0);
                 if (t >= t_lo && t < t_hi)
-                    raw[j] = __ldcs(reinterpret_cast<const uint4 *>(
-                        P.qkv + (first + t) * width +
-                        static_cast<size_t>(P.H + (key ? 0 : P.Hkv) + h) * kHeadDim + lane * 8));
+                    raw[j] = __ldcs(reinterpret_cast<const uint4 *>(from + t * width));
             }
-            uint8_t *group = (key ? P.pg.k : P.pg.v) + P.pg.group(id, h, P.Hkv, slot0);
-            if (key) {
+        };
+        const size_t head_bytes = static_cast<size_t>(kKv4GroupBytes) << (P.pg.page_shift - 4);
+        const size_t group0 = P.pg.group(id, h0, P.Hkv, slot0);
+        // Values first, which wait for no angles; warps take turns so that with one
+        // KV head some have its keys and others its values.
+        for (int task = (warp + 4) & (kWarps - 1); task < heads * 4; task += kWarps) {
+            const int h = task >> 2, quad = task & 3;
+            uint4 raw[4];
+            fetch(base + static_cast<size_t>(P.Hkv + h) * kHeadDim, quad, raw);
+            uint32_t codes[4];
+            unsigned scales = 0, keep = 0;  // keep: of the group's slots, as masks
+            uint32_t mask = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = 4 * quad + j;
-                    if (t < t_lo || t >= t_hi) continue;
-                    const int p = __shfl_sync(0xffffffffu, my_pos, t);
-                    const KeyTurn turn = kv4_key_turn(raw[j], P.rope.rot_dim, p, lane);
-                    float c[8], s[8], y[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 a = *reinterpret_cast<const float4 *>(
-                            angles + t * kMaxRopePairs + i * 32 + lane_pairs * 2);
-                        c[2 * i] = a.x, s[2 * i] = a.y, c[2 * i + 1] = a.z, s[2 * i + 1] = a.w;
-                    }
-                    kv4_rotate(turn, c, s, y);
-                    uint32_t codes;
-                    unsigned byte;
-                    kv4_key_row(turn, y, p, P.turns, codes, byte);
-                    *reinterpret_cast<uint32_t *>(group + kv4_key_at(lane, t)) = codes;
-                    if (!(lane & 1))
-                        group[kv4_key_scale_at(lane >> 1, t)] = static_cast<uint8_t>(byte);
+            for (int j = 0; j < 4; ++j) {
+                const int t = 4 * quad + j;
+                unsigned byte;
+                kv4_value_row(raw[j], codes[j], byte);
+                scales |= byte << (8 * (2 * (j & 1) + (j >> 1)));
+                if (t < t_lo || t >= t_hi) {
+                    keep |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
+                    mask |= (j & 1 ? 0xf0f0u : 0x0f0fu) << (16 * (j >> 1));
                 }
-            } else {
-                uint32_t codes[4];
-                unsigned scales = 0, keep = 0;  // keep: of the group's slots, as masks
-                uint32_t mask = 0;
+            }
+            if (mask == 0xffffffffu) continue;
+            // dims 2 i, 2 i + 1 of slots 0 and 1, then of 2 and 3
+            uint32_t e[2], o[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = 4 * quad + j;
-                    unsigned byte;
-                    kv4_value_row(raw[j], codes[j], byte);
-                    scales |= byte << (8 * (2 * (j & 1) + (j >> 1)));
-                    if (t < t_lo || t >= t_hi) {
-                        keep |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
-                        mask |= (j & 1 ? 0xf0f0u : 0x0f0fu) << (16 * (j >> 1));
-                    }
-                }
-                if (mask == 0xffffffffu) continue;
-                // dims 2 i, 2 i + 1 of slots 0 and 1, then of 2 and 3
-                uint32_t e[2], o[2];
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t a = codes[2 * q], b = codes[2 * q + 1];
+                e[q] = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
+                o[q] = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+            }
+            uint32_t w[4];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t a = codes[2 * q], b = codes[2 * q + 1];
-                    e[q] = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
-                    o[q] = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
-                }
-                uint32_t w[4];
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = __byte_perm(e[0], o[0], i | (i + 4) << 4);
+                const uint32_t hi = __byte_perm(e[1], o[1], i | (i + 4) << 4);
+                w[i] = __byte_perm(lo, hi, 0x5410);
+            }
+            uint8_t *group = P.pg.v + group0 + h * head_bytes;
+            uint4 *dst = reinterpret_cast<uint4 *>(group + kv4_value_at(lane, quad));
+            uint32_t *sdst = reinterpret_cast<uint32_t *>(group + kv4_value_scale_at(lane >> 1, quad));
+            if (mask) {  // slots beside the call's keep what they hold
+                const uint4 old = *dst;
+                w[0] = (w[0] & ~mask) | (old.x & mask);
+                w[1] = (w[1] & ~mask) | (old.y & mask);
+                w[2] = (w[2] & ~mask) | (old.z & mask);
+                w[3] = (w[3] & ~mask) | (old.w & mask);
+                scales = (scales & ~keep) | (*sdst & keep);
+            }
+            *dst = make_uint4(w[0], w[1], w[2], w[3]);
+            if (!(lane & 1)) *sdst = scales;
+        }
+        uint4 raw[4];
+        if (warp < heads * 4) fetch(base + static_cast<size_t>(warp >> 2) * kHeadDim, warp & 3, raw);
+        __syncthreads();  // the angles (of two units: those of the one before may be read still)
+        for (int task = warp; task < heads * 4; task += kWarps) {
+            const int h = task >> 2, quad = task & 3;
+            if (task != warp) fetch(base + static_cast<size_t>(h) * kHeadDim, quad, raw);
+            uint8_t *group = P.pg.k + group0 + h * head_bytes;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = 4 * quad + j;
+                if (t < t_lo || t >= t_hi) continue;
+                const int p = __shfl_sync(0xffffffffu, my_pos, t);
+                const KeyTurn turn = kv4_key_turn(raw[j], P.rope.rot_dim, p, lane);
+                float c[8], s[8], y[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo = __byte_perm(e[0], o[0], i | (i + 4) << 4);
-                    const uint32_t hi = __byte_perm(e[1], o[1], i | (i + 4) << 4);
-                    w[i] = __byte_perm(lo, hi, 0x5410);
+                    const float4 a = *reinterpret_cast<const float4 *>(
+                        angles + t * kMaxRopePairs + i * 32 + lane_pairs * 2);
+                    c[2 * i] = a.x, s[2 * i] = a.y, c[2 * i + 1] = a.z, s[2 * i + 1] = a.w;
                 }
-                uint4 *dst = reinterpret_cast<uint4 *>(group + kv4_value_at(lane, quad));
-                uint32_t *sdst = reinterpret_cast<uint32_t *>(
-                    group + kv4_value_scale_at(lane >> 1, quad));
-                if (mask) {  // slots beside the call's keep what they hold
-                    const uint4 old = *dst;
-                    w[0] = (w[0] & ~mask) | (old.x & mask);
-                    w[1] = (w[1] & ~mask) | (old.y & mask);
-                    w[2] = (w[2] & ~mask) | (old.z & mask);
-                    w[3] = (w[3] & ~mask) | (old.w & mask);
-                    scales = (scales & ~keep) | (*sdst & keep);
-                }
-                *dst = make_uint4(w[0], w[1], w[2], w[3]);
-                if (!(lane & 1)) *sdst = scales;
+                if (!kAll && lane >= 2 * turning)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+                kv4_rotate(turn, c, s, y);
+                uint32_t codes;
+                unsigned byte;
+                if (kAll && p != 0)
+                    kv4_key_row<true>(turn, y, p, P.turns, codes, byte);
+                else
+                    kv4_key_row<false>(turn, y, p, P.turns, codes, byte);
+                *reinterpret_cast<uint32_t *>(group + kv4_key_at(lane, t)) = codes;
+                if (!(lane & 1)) group[kv4_key_scale_at(lane >> 1, t)] = static_cast<uint8_t>(byte);
             }
         }
     }
@@ -487,7 +510,10 @@ spark_status spark_attn_kv4_store(const void *qkv, const int32_t *pos, const int
     set_layer(P, desc, H, Hkv);
     set_pages(P, k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
     P.heads = Hkv;
-    return done(launch_overlapped(kv4_store_kernel, dim3(sms * 3), dim3(kThreads), kStoreSmem,
+    auto kernel = desc->rot_dim == kHeadDim ? kv4_store_kernel<true> : kv4_store_kernel<false>;
+    st = done(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStoreSmem));
+    if (st != SPARK_OK) return st;
+    return done(launch_overlapped(kernel, dim3(sms * 3), dim3(kThreads), kStoreSmem,
                                   static_cast<cudaStream_t>(stream), P));
 }
 

@@ -41,6 +41,7 @@ constexpr int kKv4Codes = kKv4Group * kHeadDim / 2; // bytes of codes in a group
 constexpr int kKv4GroupBytes = kKv4Group * kKv4TokenBytes;
 constexpr unsigned kKv4MaxScale = 226;              // 10240: 6 * 10240 is a finite half
 constexpr unsigned kKv4NanScale = 0xff;
+constexpr float kKv4LeastNormal = 6.103515625e-5f;  // 2^-14, of a scale
 
 // Pages in 4 bits: [n_pages][Hkv][page / 16][2304], and the table of the rows.
 struct Kv4Pages {
@@ -130,12 +131,13 @@ __device__ __forceinline__ uint32_t kv4_value_codes(const uint4 &w, int t) {
 
 // ---------------------------------------------------------------- quantising
 
-// The scale nearest to t >= 0, in e5m3.
+// The scale nearest to t >= 0, in e5m3: the upper bits of a float, rounded, with
+// the exponent moved.  Below 2^-14 the steps stay those of the binade above, which
+// adding 2^-14 makes them.
 __device__ __forceinline__ unsigned kv4_scale_byte(float t) {
-    const unsigned bits = __float_as_uint(t);
-    const unsigned normal = ((bits + 0x7ffffu + ((bits >> 20) & 1u)) >> 20) - (112u << 3);
-    const unsigned small = static_cast<unsigned>(__float2int_rn(t * 131072.0f));
-    const unsigned b = t < 6.103515625e-5f ? small : normal;
+    const bool small = t < kKv4LeastNormal;
+    const unsigned bits = __float_as_uint(t + (small ? kKv4LeastNormal : 0.f));
+    const unsigned b = ((bits + 0x7ffffu + (bits >> 20 & 1u)) >> 20) - (small ? 904u : 896u);
     return b < kKv4MaxScale ? b : kKv4MaxScale;
 }
 
@@ -163,19 +165,21 @@ __device__ __forceinline__ void kv4_floats(const uint4 &raw, float (&x)[8]) {
     }
 }
 
-// The largest of a lane's eight; infinite where one of the eight bf16 numbers of
-// `raw` is not finite (0 times it is NaN, in pairs).
-__device__ __forceinline__ float kv4_largest(const uint4 &raw, const float (&x)[8]) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    __nv_bfloat162 odd = __floats2bfloat162_rn(0.f, 0.f);
-    const __nv_bfloat162 zero = odd;
+__device__ __forceinline__ bool kv4_finite(const uint4 &raw) {
+    // an exponent of all ones carries into the sign's place
+    const uint32_t c = ((raw.x & 0x7f807f80u) + 0x00800080u) | ((raw.y & 0x7f807f80u) + 0x00800080u) |
+                       ((raw.z & 0x7f807f80u) + 0x00800080u) | ((raw.w & 0x7f807f80u) + 0x00800080u);
+    return !(c & 0x80008000u);
+}
+
+// The largest of a lane's eight numbers, and their sum, which is not finite where
+// one of them is NaN (or very large).
+__device__ __forceinline__ float kv4_largest(const float (&x)[8], float &sum) {
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), zero, odd);
-        a = fmaxf(a, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-    }
-    return __low2float(odd) + __high2float(odd) == 0.f ? a : INFINITY;
+    for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    return a;
 }
 
 __device__ __forceinline__ float kv4_reciprocal(float s) {
@@ -198,26 +202,31 @@ constexpr float kSixth = 1.0f / 6.0f;
 
 // A value's row.
 __device__ __forceinline__ void kv4_value_row(const uint4 &raw, uint32_t &codes, unsigned &byte) {
-    float x[8];
+    float x[8], sum;
     kv4_floats(raw, x);
-    float a = kv4_largest(raw, x);
+    float a = kv4_largest(x, sum);
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
     byte = kv4_scale_byte(kv4_snap(a * kSixth));
     const float r = kv4_reciprocal(kv4_scale(byte));
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmaf_rn(x[i], r, kSnap), -kSnap);
     codes = kv4_codes(x);
-    if (a == INFINITY) {
-        codes = 0;
-        byte = kKv4NanScale;
+    const bool odd = !(fabsf(sum) + a < INFINITY);
+    if (__any_sync(0xffffffffu, odd)) {
+        int bad = !kv4_finite(raw);
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+        if (bad) {
+            codes = 0;
+            byte = kKv4NanScale;
+        }
     }
 }
 
-// Dims 8 lane .. of a key and of what they turn with: y = x cos + z sin (z has
-// its sign changed in the first of each pair).
+// Dims 8 lane .. of a key, as bf16, and of what they turn with: y = x cos + z sin
+// (z has its sign changed in the first of each pair).
 struct KeyTurn {
-    float x[8], z[8];
-    float largest, others;     // kv4_largest of both
+    uint4 own, other;
+    int partner;               // the lane that has the others
     int k0;                    // the first pair
     bool turns;
 };
@@ -225,41 +234,39 @@ struct KeyTurn {
 __device__ __forceinline__ KeyTurn kv4_key_turn(const uint4 &raw, int rot_dim, int pos, int lane) {
     KeyTurn t;
     const int half = rot_dim >> 4;  // lanes of each half
-    t.turns = lane < 2 * half && pos != 0;
-    const bool upper = lane >= half;
-    const int other = !t.turns ? lane : upper ? lane - half : lane + half;
-    t.k0 = !t.turns ? 0 : (upper ? lane - half : lane) * 8;
+    const bool inside = lane < 2 * half, upper = lane >= half;
+    t.turns = inside && pos != 0;
+    t.partner = !inside ? lane : upper ? lane - half : lane + half;
+    t.k0 = !inside ? 0 : (upper ? lane - half : lane) * 8;
     const uint32_t sign = upper ? 0u : 0x80008000u;
-    kv4_floats(raw, t.x);
-    t.largest = kv4_largest(raw, t.x);
-    uint4 o;
-    o.x = __shfl_sync(0xffffffffu, raw.x, other) ^ sign;
-    o.y = __shfl_sync(0xffffffffu, raw.y, other) ^ sign;
-    o.z = __shfl_sync(0xffffffffu, raw.z, other) ^ sign;
-    o.w = __shfl_sync(0xffffffffu, raw.w, other) ^ sign;
-    t.others = __shfl_sync(0xffffffffu, t.largest, other);
-    kv4_floats(o, t.z);
+    t.own = raw;
+    t.other.x = __shfl_sync(0xffffffffu, raw.x, t.partner) ^ sign;
+    t.other.y = __shfl_sync(0xffffffffu, raw.y, t.partner) ^ sign;
+    t.other.z = __shfl_sync(0xffffffffu, raw.z, t.partner) ^ sign;
+    t.other.w = __shfl_sync(0xffffffffu, raw.w, t.partner) ^ sign;
     return t;
 }
 
-// The rotated values in 32 bits; c, s: cosines and sines of the lane's pairs.
+// The rotated values in 32 bits; c, s: cosines and sines of the lane's pairs, 1 and
+// 0 for dims that do not turn.
 __device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float (&c)[8],
                                            const float (&s)[8], float (&y)[8]) {
+    float z[8];
+    kv4_floats(t.own, y);
+    kv4_floats(t.other, z);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float r = __fmaf_rn(t.x[i], c[i], __fmul_rn(t.z[i], s[i]));
-        y[i] = t.turns ? r : t.x[i];
-    }
+    for (int i = 0; i < 8; ++i) y[i] = __fmaf_rn(y[i], c[i], __fmul_rn(z[i], s[i]));
 }
 // ... from a table of all pairs.
 __device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float2 *cs, float (&y)[8]) {
+    kv4_floats(t.own, y);
+    if (!t.turns) return;
+    float z[8];
+    kv4_floats(t.other, z);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        y[i] = t.x[i];
-        if (t.turns) {
-            const float2 c = cs[t.k0 + i];
-            y[i] = __fmaf_rn(t.x[i], c.x, __fmul_rn(t.z[i], c.y));
-        }
+        const float2 c = cs[t.k0 + i];
+        y[i] = __fmaf_rn(y[i], c.x, __fmul_rn(z[i], c.y));
     }
 }
 
@@ -292,17 +299,28 @@ __device__ __noinline__ inline double kv4_exact_turn(float x, float z, int pos, 
     return x * cq + z * sq;
 }
 
-// Settles the scale of the blocks in `open` (the same in a block's two lanes)
-// in 64 bits, from the values that can be its largest.  All lanes.
-__device__ __noinline__ inline unsigned kv4_settle_scale(const KeyTurn &t, int pos,
-                                                         const double *turns, const float (&y)[8],
-                                                         float least, bool open, unsigned byte) {
-    // (a block whose dims nearly cancel in their turn can have any scale)
+__device__ __forceinline__ float kv4_pick(const uint4 &raw, int i) {
+    const uint32_t w = i < 4 ? (i < 2 ? raw.x : raw.y) : (i < 6 ? raw.z : raw.w);
+    return i & 1 ? bf16_hi(w) : bf16_lo(w);
+}
+
+// Settles the scale of the blocks in `open` (the same in a block's two lanes) in
+// 64 bits.  turns: the frequencies of the lane's pairs.  All lanes.  (Arguments by
+// value: they stay in registers where it is not called.)
+__device__ __noinline__ inline unsigned kv4_settle_scale(uint4 own, uint4 other, int pos,
+                                                         const double *turns, float4 y0,
+                                                         float4 y1, float least, bool open,
+                                                         unsigned byte) {
     double a = 0.0;
     if (open)
-        for (int i = 0; i < 8; ++i)
-            if (fabsf(y[i]) >= least)
-                a = fmax(a, fabs(kv4_exact_turn(t.x[i], t.z[i], pos, turns[t.k0 + i])));
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const float4 h = i < 4 ? y0 : y1;
+            const float y = i & 2 ? (i & 1 ? h.w : h.z) : (i & 1 ? h.y : h.x);
+            if (!(fabsf(y) < least))  // it can be the largest
+                a = fmax(a, fabs(kv4_exact_turn(kv4_pick(own, i), kv4_pick(other, i), pos,
+                                                turns[i])));
+        }
     a = fmax(a, __shfl_xor_sync(0xffffffffu, a, 1));
     if (!open) return byte;
     // the scale below a / 6, the next one, and their middle
@@ -313,14 +331,15 @@ __device__ __noinline__ inline unsigned kv4_settle_scale(const KeyTurn &t, int p
     return a > mid || (a == mid && (lo & 1u)) ? lo + 1 : lo;
 }
 
-// Settles the codes of the dims in `open`, in 64 bits.
-__device__ __noinline__ inline uint32_t kv4_settle_codes(const KeyTurn &t, int pos,
+// Settles the codes of the dims in `open` (bit 4 i), in 64 bits.
+__device__ __noinline__ inline uint32_t kv4_settle_codes(uint4 own, uint4 other, int pos,
                                                          const double *turns, float scale,
                                                          unsigned open, uint32_t codes) {
     const double s = scale;
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
         if (!(open >> (4 * i) & 1u)) continue;
-        const double v = kv4_exact_turn(t.x[i], t.z[i], pos, turns[t.k0 + i]);
+        const double v = kv4_exact_turn(kv4_pick(own, i), kv4_pick(other, i), pos, turns[i]);
         const double m = fabs(v);
         unsigned c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) +
                      (m > 2.5 * s) + (m >= 3.5 * s) + (m > 5.0 * s);
@@ -332,42 +351,64 @@ __device__ __noinline__ inline uint32_t kv4_settle_codes(const KeyTurn &t, int p
 
 // A key's row, rotated (y, in 32 bits), quantised.  What the pages hold is the
 // nearest to the exact rotation: where 32 bits do not tell on which side of a
-// border a value or a scale lies (one row in a hundred or two), 64 bits decide.
+// border a value or a scale lies (one row in a hundred or so), 64 bits decide.
 // |y| is off by 2^-21 (|x| + |z|) at most: cos and sin by 2^-22 each (1 ulp of
 // sincospif and 2^-24 that the frequencies' two parts leave of the angle below
 // 2^24 positions; where two turns are put together, both, and the products'
-// roundings), the product and the sum by 2^-24 each.  Twice that is allowed, and
-// 2^-22 of a quotient (8 at most, or it saturates).  Dims that do not turn are
-// bf16: kSnap.
+// roundings), the product and the sum by 2^-24 each.  |x| + |z| is at most 1.5
+// times the sum of the two blocks' largest |y| (a turn keeps x^2 + z^2).  Twice the
+// error is allowed, and 2^-22 of a quotient (8 at most, or it saturates).  Dims
+// that do not turn are bf16: kSnap.
+// kAll: every lane turns.
+template <bool kAll>
 __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8], int pos,
                                             const double *turns, uint32_t &codes,
                                             unsigned &byte) {
-    constexpr float kRel = 2.38418579e-7f, kAbs = 9.53674316e-7f;  // 2^-22, 2^-20
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+    constexpr float kRel = 2.38418579e-7f, kAbs = 1.43051147e-6f;  // 2^-22, 1.5 * 2^-20
+    float sum;
+    float a = kv4_largest(y, sum);
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    // infinite where a value of the block is not finite (a block turns as a whole)
-    const float e = t.turns ? fmaf(t.largest, kAbs, t.others * kAbs)
-                            : t.largest == INFINITY ? INFINITY : 0.f;
-    const float worst = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
-    const bool finite = worst < INFINITY;
-    const float most = t.turns ? fmaf(a, kRel, worst) : 0.f;
-    const float lo_a = fmaxf(a - most, 0.f) * kSixth, hi_a = (a + most) * kSixth;
-    byte = kv4_scale_byte(t.turns ? lo_a : kv4_snap(lo_a));
-    const bool open_scale = t.turns && finite && byte != kv4_scale_byte(hi_a);
-    if (__any_sync(0xffffffffu, open_scale))
-        byte = kv4_settle_scale(t, pos, turns, y, a - 2.f * most, open_scale, byte);
+    const float a_other = __shfl_sync(0xffffffffu, a, t.partner);
+    const bool turns_here = kAll || t.turns;
+    const float e = fmaf(a, kAbs, a_other * kAbs);
+    const float top = a * kSixth;
+    byte = kv4_scale_byte(turns_here ? top : kv4_snap(top));
+    // Does the maximum's error reach the border between this scale and a next one?
+    const float moved = top + (top < kKv4LeastNormal ? kKv4LeastNormal : 0.f);
+    const float border = __uint_as_float((__float_as_uint(moved) & 0xfff00000u) | 0x80000u);
+    const bool open_scale =
+        turns_here && fabsf(moved - border) <= fmaf(e, kSixth, moved * kRel);
+    const bool odd = !(fabsf(sum) + a < INFINITY);
+    bool finite = true;
+    if (__any_sync(0xffffffffu, odd || open_scale)) {
+        int bad = !kv4_finite(t.own) || !kv4_finite(t.other);
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+        finite = !bad;
+        int open = open_scale || odd;
+        open |= __shfl_xor_sync(0xffffffffu, open, 1);
+        byte = kv4_settle_scale(t.own, t.other, pos, turns + t.k0,
+                                make_float4(y[0], y[1], y[2], y[3]),
+                                make_float4(y[4], y[5], y[6], y[7]), a - 2.f * fmaf(a, kRel, e),
+                                turns_here && open && finite, byte);
+    }
     const float s = kv4_scale(byte), r = kv4_reciprocal(s);
-    const float d = fmaf(worst, r, 8.f * kRel);
-    // what the quotient is told by: both ends of what it can be, or itself, snapped
-    const float down = t.turns ? -d : kSnap, up = t.turns ? d : kSnap;
-    const float back = t.turns ? 0.f : -kSnap;
+    const float d = fmaf(e, r, 8.f * kRel);
     float lo[8], hi[8];
+    if (kAll) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo[i] = __fadd_rn(__fmaf_rn(y[i], r, down), back);
-        hi[i] = __fadd_rn(__fmaf_rn(y[i], r, up), back);
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = __fmaf_rn(y[i], r, -d);
+            hi[i] = __fmaf_rn(y[i], r, d);
+        }
+    } else {
+        // both ends of what a quotient can be, or itself, snapped
+        const float down = turns_here ? -d : kSnap, up = turns_here ? d : kSnap;
+        const float back = turns_here ? 0.f : -kSnap;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = __fadd_rn(__fmaf_rn(y[i], r, down), back);
+            hi[i] = __fadd_rn(__fmaf_rn(y[i], r, up), back);
+        }
     }
     codes = kv4_codes(hi);
     // (a sign that differs beside zero stands for the same value)
@@ -378,7 +419,7 @@ __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8
         byte = kKv4NanScale;
     }
     if (__any_sync(0xffffffffu, open != 0))
-        codes = kv4_settle_codes(t, pos, turns, s, open, codes);
+        codes = kv4_settle_codes(t.own, t.other, pos, turns + t.k0, s, open, codes);
 }
 
 }  // namespace spark
