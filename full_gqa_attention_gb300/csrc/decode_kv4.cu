@@ -39,7 +39,7 @@ namespace spark {
 
 namespace {
 
-constexpr int kPairCost = 6;
+constexpr int kPairCost = 5;
 constexpr int kTile = 64;                                 // slots per stage
 constexpr int kStages = 3;
 constexpr int kWarps = 4;                                 // consumers
@@ -50,7 +50,7 @@ constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kQBytes = 8 * kHeadDim * 2;                 // 8 columns
 constexpr int kRowBytes = kHeadDim * 2;
 constexpr int kPairs = 2;                                 // pairs handed over at a time
-constexpr int kFan = 8;                                   // partial states loaded at once
+constexpr int kFan = 4;                                   // partial states loaded at once
 constexpr int kSub = 16;                                  // ... joined in the first step
 constexpr int kProbBytes = 2 * kWarps * 32 * 8;           // two tiles' probabilities
 constexpr float kHeadroom = 4.f;                          // scores may pass the reference by this
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int s = n_pairs % kPairs;
             if (lane == 0) {
                 if (n_pairs >= kPairs)
-                    mbar_wait_plain(&pair_empty[s], ((n_pairs / kPairs) - 1) & 1);
+                    mbar_wait_plain_short(&pair_empty[s], ((n_pairs / kPairs) - 1) & 1);
                 Pair &p = pairs[s];
                 p.pos = wk.row.pos;
                 p.lo = wk.row.lo;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll 1
             for (int k = lane; k < half; k += 32)
                 rope_cos_sin_fine(wk.row.pos, P.rope.u[k], cs_new[k].x, cs_new[k].y);
-            mbar_wait_plain(&rows_full[s], ((n_pairs - 1) / kPairs) & 1);
+            mbar_wait_plain_short(&rows_full[s], ((n_pairs - 1) / kPairs) & 1);
             __syncwarp();
             const uint8_t *src = new_rows + s * kNewBytes + P.G * kRowBytes + lane * 16;
             float y[8];
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 const int s = it % kStages;
                 if (it >= kStages && lane == 0)
-                    ok = mbar_wait_suspended(&empty[s], ((it / kStages) - 1) & 1, &abort_flag, P.status);
+                    ok = mbar_wait_short(&empty[s], ((it / kStages) - 1) & 1, &abort_flag, P.status);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 const int id = __shfl_sync(0xffffffffu, ids, (in + piece) & 31);
@@ -346,10 +346,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // copies still in flight after an abort must land before the CTA ends
         if (lane == 0 && abort_flag)
             for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
-                mbar_wait_plain(&full[i % kStages], (i / kStages) & 1);
+                mbar_wait_plain_short(&full[i % kStages], (i / kStages) & 1);
         if (lane == 0 && abort_flag)
             for (int i = n_pairs - 1 > kPairs ? n_pairs - 1 - kPairs : 0; i < n_pairs - 1; ++i)
-                mbar_wait_plain(&rows_full[i % kPairs], (i / kPairs) & 1);
+                mbar_wait_plain_short(&rows_full[i % kPairs], (i / kPairs) & 1);
         return;
     }
 
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     bool aborted = false;  // the same in every consumer thread
     // Waits for a pair; the barrier behind it tells every warp whether all have it.
     auto await_pair = [&](int n) {
-        if (!mbar_wait_plain(&pair_full[n % kPairs], (n / kPairs) & 1)) {
+        if (!mbar_wait_plain_short(&pair_full[n % kPairs], (n / kPairs) & 1)) {
             atomicOr(P.status, kErrTimeout);
             abort_flag = 1;
             lost = 1;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             id_new = P.pg.table[static_cast<size_t>(pair.b) * P.pg.max_pages +
                                 (pos >> P.pg.page_shift)];
         if (tid < half) rope_cos_sin_fine(pos, freq, cs[tid].x, cs[tid].y);
-        if (!mbar_wait_plain(&rows_full[s_pair], pair_turn)) {
+        if (!mbar_wait_plain_short(&rows_full[s_pair], pair_turn)) {
             atomicOr(P.status, kErrTimeout);
             abort_flag = 1;
             gave_up[0] = 1;
@@ -460,9 +460,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         bool ok = !aborted;
         for (int t = t0; ok && t < t1; ++t, ++it) {
             const int s = it % kStages;
-            ok = mbar_wait_suspended(&full[s], (it / kStages) & 1, &abort_flag, P.status);
+            ok = mbar_wait_short(&full[s], (it / kStages) & 1, &abort_flag, P.status);
             const int first = (lo & ~(kTile - 1)) + t * kTile;
-            const bool edge = first < lo || first + kTile > pos;
             const uint8_t *kt = stages + s * kStageBytes;
             uint2 *pt = probs + (it & 1) * kWarps * 32;
             // S^T (16 slots x 8 columns) = K (16 x 256) Q^T (256 x 8)
@@ -508,12 +507,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     if (kTwo) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);
                     x[i] *= i & 1 ? unit1 : unit0;
                 }
-                if (edge)
+                if (first < lo || first + kTile > pos) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int slot = first + warp * kKv4Group + tok + (i & 2);
                         if (slot < lo || slot >= pos) x[i] = -INFINITY;
                     }
+                    // Slots that hold no visible token may hold anything: a scale of
+                    // zero makes zeros of their values, too.
+                    uint32_t seen = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int slot = first + warp * kKv4Group + 4 * c4 + j;
+                        if (slot >= lo && slot < pos)
+                            seen |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
+                    }
+                    uint2 *sv = reinterpret_cast<uint2 *>(
+                        stages + s * kStageBytes + kTileBytes + warp * kKv4GroupBytes + kKv4Codes +
+                        lane * 8);
+                    *sv = make_uint2(sv->x & seen, sv->y & seen);
+                    fence_proxy_async_smem();  // copies come here later
+                }
             }
             // P^T of these slots, in the order in which the lanes take B
             float p[4];
@@ -580,17 +594,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const uint2 pb = pt[u * 32 + lane];
                 const uint8_t *vu = vt + u * kKv4GroupBytes;
                 const uint4 v = *reinterpret_cast<const uint4 *>(vu + warp * 512 + lane * 16);
-                uint32_t w = *reinterpret_cast<const uint32_t *>(vu + kKv4Codes + lane * 8 +
-                                                                 4 * (warp >> 1));
-                if (edge) {
-                    // Slots that hold no visible token may hold anything: a
-                    // scale of zero makes zeros of it.
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int slot = first + u * kKv4Group + 4 * c4 + j;
-                        if (slot < lo || slot >= pos) w &= ~(0xffu << (8 * (2 * (j & 1) + (j >> 1))));
-                    }
-                }
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(vu + kKv4Codes + lane * 8 +
+                                                                       4 * (warp >> 1));
                 const uint32_t u0 = (w & 0x00ff00ffu) << 7, u1 = (w >> 1) & 0x7f807f80u;
                 const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -700,54 +705,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 consumer_bar();
                 return last_cta != 0;
             };
-            // The states of CTAs from, from + step, .. up to `to`.
+            // The states of CTAs from, from + step, .. up to `to`, 32 at most: a lane
+            // has one state's maximum and sum, all lanes its output.
             auto join = [&](int from, int to, int step) {
+                const int n = step == 1 ? to - from + 1 : (to - from) / kSub + 1;
+                auto at = [&](int k, int i) {  // (a warp without a head reads the first)
+                    const int hq = warp + i * kWarps < P.G ? warp + i * kWarps : 0;
+                    return place(from + (k < n ? k : n - 1) * step) * P.G + hq;
+                };
+                float w[kRows];
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
-                    const int hq = warp + i * kWarps;
-                    if (hq >= P.G) break;
                     HeadState &h = st[i];
-                    h.m = -INFINITY;
-                    h.l = 0.f;
+                    const float2 ml =
+                        __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + at(lane, i));
+                    const float m = lane < n ? ml.x : -INFINITY;
+                    h.m = m;
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+                        h.m = fmaxf(h.m, __shfl_xor_sync(0xffffffffu, h.m, off));
+                    // (an empty state's sums are 0, or NaN, whatever their weight)
+                    w[i] = lane >= n ? 0.f : m == -INFINITY ? 1.f : fast_exp2(m - h.m);
+                    h.l = lane < n ? ml.y * w[i] : 0.f;
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+                        h.l += __shfl_xor_sync(0xffffffffu, h.l, off);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) h.o[j] = 0.f;
+                }
 #pragma unroll 1
-                    for (int cta = from; cta <= to; cta += kFan * step) {
-                        float2 ml[kFan];
-                        float4 x[kFan], y[kFan];
+                for (int k0 = 0; k0 < n; k0 += kFan) {
+                    float4 x[kRows][kFan], y[kRows][kFan];
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
 #pragma unroll
                         for (int k = 0; k < kFan; ++k) {
-                            ml[k] = make_float2(-INFINITY, 0.f);
-                            x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (cta + k * step <= to) {
-                                const size_t a =
-                                    static_cast<size_t>(place(cta + k * step)) * P.G + hq;
-                                ml[k] = __ldcg(reinterpret_cast<const float2 *>(P.part_ml) + a);
-                                const float4 *src = reinterpret_cast<const float4 *>(
-                                    P.part_o + a * kHeadDim + lane * 8);
-                                x[k] = __ldcg(src);
-                                y[k] = __ldcg(src + 1);
-                            }
+                            const float4 *src = reinterpret_cast<const float4 *>(P.part_o) +
+                                                at(k0 + k, i) * (kHeadDim / 4) + lane * 2;
+                            x[i][k] = __ldcg(src);
+                            y[i][k] = __ldcg(src + 1);
                         }
-                        float top = h.m;
 #pragma unroll
-                        for (int k = 0; k < kFan; ++k) top = fmaxf(top, ml[k].x);
-                        const float z = top == -INFINITY ? 0.f : top;
-                        const float wo = fast_exp2(h.m - z);
-                        h.m = top;
-                        h.l *= wo;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) h.o[j] *= wo;
+                    for (int i = 0; i < kRows; ++i)
 #pragma unroll
                         for (int k = 0; k < kFan; ++k) {
-                            // (an empty state's sums are 0, or NaN, whatever their weight)
-                            const float w = ml[k].x == -INFINITY ? 1.f : fast_exp2(ml[k].x - z);
-                            const float v[8] = {x[k].x, x[k].y, x[k].z, x[k].w,
-                                                y[k].x, y[k].y, y[k].z, y[k].w};
-                            h.l += ml[k].y * w;
-                            add_scaled(h, w, v);
+                            const float v[8] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w,
+                                                y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
+                            add_scaled(st[i], __shfl_sync(0xffffffffu, w[i], (k0 + k) & 31), v);
                         }
-                    }
                 }
             };
             const int sub = (me - c0) / kSub, subs = (c1 - c0) / kSub + 1;
@@ -797,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 // the new token's slot: every read of this pair is done
                 if (!k_new) {
                     if (lane == 0) atomicOr(P.status, kErrPage);
-                } else if (mbar_wait_plain(&new_full[s_pair], pair_turn)) {
+                } else if (mbar_wait_plain_short(&new_full[s_pair], pair_turn)) {
                     *reinterpret_cast<uint32_t *>(k_new + kv4_key_at(lane, t_new)) =
                         new_codes[s_pair][0][lane];
                     // the other slot of each byte stays
@@ -830,7 +835,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 // ---------------------------------------------------------------- launcher
 
-int decode_kv4_ctas(int sms) { return sms * kCtasPerSm; }
+int decode_kv4_ctas(int sms) {
+    // (the second step of a join takes one state a lane)
+    constexpr int kMost = 32 * kSub;
+    return sms * kCtasPerSm < kMost ? sms * kCtasPerSm : kMost;
+}
 
 cudaError_t launch_decode_kv4(const Kv4Params &P, int grid, cudaStream_t stream) {
     const bool two = P.G <= 4;

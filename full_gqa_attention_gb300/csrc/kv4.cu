@@ -121,11 +121,12 @@ __device__ __forceinline__ int angle_at(int k) {
     return (k >> 1 & 3) * 32 + (k >> 3) * 2 + (k & 1);  // in float2
 }
 
+constexpr int kStoreCtas = 2;
 constexpr int kStoreSmem = (3 * kKv4Group * kMaxRopePairs) * 8;
 
 // kAll: all 256 dims turn.
 template <bool kAll>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kStoreCtas)
     kv4_store_kernel(const __grid_constant__ Kv4Params P) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int kAngles = kKv4Group * kMaxRopePairs;       // of 16 tokens
@@ -419,6 +420,34 @@ spark_status done(cudaError_t e) {
     return SPARK_ERR_CUDA;
 }
 
+// The turns of a layer's pairs, in two floats and in 64 bits.  A model has a few
+// kinds of layers and 128 powers take longer than a launch: each thread keeps the
+// last four kinds' (by base and width, nothing else goes into them).
+struct LayerTurns {
+    double theta = 0.0;
+    int rot_dim = -1;
+    RopeTable rope;
+    double turns[kMaxRopePairs];
+};
+
+const LayerTurns &turns_of(const spark_layer_desc *desc) {
+    constexpr int kKinds = 4;
+    static thread_local LayerTurns kept[kKinds];
+    static thread_local int oldest = 0;
+    for (const LayerTurns &t : kept)
+        if (t.rot_dim == desc->rot_dim && t.theta == desc->rope_theta) return t;
+    LayerTurns &t = kept[oldest];
+    oldest = (oldest + 1) % kKinds;
+    t.theta = desc->rope_theta;
+    t.rot_dim = desc->rot_dim;
+    fill_rope_table(desc, &t.rope);
+    std::memset(t.turns, 0, sizeof(t.turns));
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int k = 0; k < desc->rot_dim / 2; ++k)
+        t.turns[k] = std::pow(desc->rope_theta, -2.0 * k / desc->rot_dim) / two_pi;
+    return t;
+}
+
 void set_layer(Kv4Params &P, const spark_layer_desc *desc, int H, int Hkv) {
     P.H = H;
     P.Hkv = Hkv;
@@ -429,10 +458,9 @@ void set_layer(Kv4Params &P, const spark_layer_desc *desc, int H, int Hkv) {
                : desc->window < kMostWindow     ? desc->window
                                                 : kMostWindow;
     P.gate_mode = desc->gate_mode;
-    fill_rope_table(desc, &P.rope);
-    const double two_pi = 6.283185307179586476925286766559;
-    for (int k = 0; k < desc->rot_dim / 2; ++k)
-        P.turns[k] = std::pow(desc->rope_theta, -2.0 * k / desc->rot_dim) / two_pi;
+    const LayerTurns &t = turns_of(desc);
+    P.rope = t.rope;
+    std::memcpy(P.turns, t.turns, sizeof(P.turns));
 }
 
 void set_pages(Kv4Params &P, void *k4, void *v4, int n_pages, int page_size, const int32_t *table,
@@ -513,7 +541,7 @@ spark_status spark_attn_kv4_store(const void *qkv, const int32_t *pos, const int
     auto kernel = desc->rot_dim == kHeadDim ? kv4_store_kernel<true> : kv4_store_kernel<false>;
     st = done(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStoreSmem));
     if (st != SPARK_OK) return st;
-    return done(launch_overlapped(kernel, dim3(sms * 3), dim3(kThreads), kStoreSmem,
+    return done(launch_overlapped(kernel, dim3(sms * kStoreCtas), dim3(kThreads), kStoreSmem,
                                   static_cast<cudaStream_t>(stream), P));
 }
 

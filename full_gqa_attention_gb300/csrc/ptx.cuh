@@ -65,19 +65,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// The same, suspended for up to about `ns`: a warp that waits long takes few
-// issue slots of those that work.
-__device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-        : "memory");
-    return ok != 0;
-}
-
 // Waits for the phase of `bar` with the given parity to complete.  Gives up
 // when *abort is set by another thread or after kWaitLimitNs; in the latter
 // case it raises *abort and records kErrTimeout in *status.  Returns false
@@ -99,21 +86,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
-// Same, suspended meanwhile.
-__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity,
-                                                    volatile int *abort, unsigned *status) {
-    constexpr uint32_t kNs = 20000;
-    if (mbar_try_wait_for(bar, parity, kNs)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait_for(bar, parity, kNs)) {
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            *abort = 1;
-            atomicOr(status, kErrTimeout);
-            return false;
-        }
-    }
-    return true;
+// Same, the waiting itself out of line: instructions that are fetched for nothing
+// cost a short kernel its time.
+__device__ __noinline__ inline bool mbar_wait_out(uint64_t *bar, uint32_t parity,
+                                                  volatile int *abort, unsigned *status) {
+    return mbar_wait(bar, parity, abort, status);
+}
+
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity,
+                                                volatile int *abort, unsigned *status) {
+    return mbar_try_wait(bar, parity) || mbar_wait_out(bar, parity, abort, status);
 }
 
 // Same, with no abort flag to watch (used while cleaning up).
@@ -124,6 +106,15 @@ __device__ __forceinline__ bool mbar_wait_plain(uint64_t *bar, uint32_t parity) 
         if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) return false;
     }
+}
+
+// Same, out of line.
+__device__ __noinline__ inline bool mbar_wait_plain_out(uint64_t *bar, uint32_t parity) {
+    return mbar_wait_plain(bar, parity);
+}
+
+__device__ __forceinline__ bool mbar_wait_plain_short(uint64_t *bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || mbar_wait_plain_out(bar, parity);
 }
 
 // ---------------------------------------------------------------- launch overlap
