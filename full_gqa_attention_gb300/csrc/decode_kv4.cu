@@ -41,10 +41,8 @@ namespace {
 
 constexpr int kPairCost = 5;
 constexpr int kTile = 64;                                 // slots per stage
-constexpr int kStages = 3;
 constexpr int kWarps = 4;                                 // consumers
 constexpr int kThreads = (kWarps + 1) * 32;               // + one producer warp
-constexpr int kCtasPerSm = 3;
 constexpr int kTileBytes = kTile * kKv4TokenBytes;        // K or V
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kQBytes = 8 * kHeadDim * 2;                 // 8 columns
@@ -58,13 +56,21 @@ constexpr float kProbShift = 11.f;                        // probabilities are t
 constexpr float kProbScale = 2048.f;
 constexpr int kSumRow = kHeadDim;                         // floats
 
-// Shared memory: the stages, a pair's new token (q of `heads` heads, key, value)
-// twice, the queries' halves (after the tiles: 4 heads' sums), two tiles'
+// What goes by the query heads of a KV head.  With up to 4, three CTAs per SM of
+// three stages; 8 heads' states and joins take more registers, and two CTAs of
+// four stages are faster (20 rows of one KV head 25.9 -> 21.8 us, 500,000 tokens
+// 45.3 -> 41.9).  Shared memory: the stages, a pair's new token (queries, key,
+// value) twice, the queries' halves (after the tiles: 4 heads' sums), two tiles'
 // probabilities.
-__host__ __device__ constexpr int new_bytes(int heads) { return (heads + 2) * kRowBytes; }
-__host__ __device__ constexpr int smem_bytes(int heads) {
-    return kStages * kStageBytes + kPairs * new_bytes(heads) + kQBytes + kProbBytes;
-}
+template <bool kTwo>
+struct Shape {
+    static constexpr int kHeads = kTwo ? 4 : 8;
+    static constexpr int kCtasPerSm = kTwo ? 3 : 2;
+    static constexpr int kStages = kTwo ? 3 : 4;
+    static constexpr int kNewBytes = (kHeads + 2) * kRowBytes;
+    static constexpr int kSmemBytes =
+        kStages * kStageBytes + kPairs * kNewBytes + kQBytes + kProbBytes;
+};
 
 using Row = DecodeRow<kTile, kPairCost>;
 using Walk = DecodeWalk<kTile, kPairCost>;
@@ -125,11 +131,11 @@ __device__ __forceinline__ float nonfinite_part(float x) { return isfinite(x) ? 
 
 // kTwo: queries as sums of two halves (4 heads at most).
 template <bool kTwo>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
     decode_kv4_kernel(const __grid_constant__ Kv4Params P) {
-    constexpr int kHeads = kTwo ? 4 : 8;
-    constexpr int kNewBytes = new_bytes(kHeads);
-    constexpr int kRows = kHeads / kWarps;               // heads of a warp: warp, warp + 4
+    constexpr int kStages = Shape<kTwo>::kStages;
+    constexpr int kNewBytes = Shape<kTwo>::kNewBytes;
+    constexpr int kRows = Shape<kTwo>::kHeads / kWarps;                 // heads of a warp: warp, warp + 4
     extern __shared__ __align__(128) uint8_t stages[];
     uint8_t *new_rows = stages + kStages * kStageBytes;
     uint8_t *qs = new_rows + kPairs * kNewBytes;         // queries' halves, as B takes them
@@ -835,20 +841,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 // ---------------------------------------------------------------- launcher
 
-int decode_kv4_ctas(int sms) {
-    // (the second step of a join takes one state a lane)
-    constexpr int kMost = 32 * kSub;
-    return sms * kCtasPerSm < kMost ? sms * kCtasPerSm : kMost;
+int decode_kv4_ctas(int sms, int G) {
+    const int ctas = sms * (G <= 4 ? Shape<true>::kCtasPerSm : Shape<false>::kCtasPerSm);
+    constexpr int kMost = 32 * kSub;  // (the second step of a join takes one state a lane)
+    return ctas < kMost ? ctas : kMost;
+}
+
+template <bool kTwo>
+static cudaError_t launch(const Kv4Params &P, int grid, cudaStream_t stream) {
+    constexpr int kSmem = Shape<kTwo>::kSmemBytes;
+    const cudaError_t err = cudaFuncSetAttribute(
+        decode_kv4_kernel<kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (err != cudaSuccess) return err;
+    return launch_overlapped(decode_kv4_kernel<kTwo>, dim3(grid), dim3(kThreads), kSmem, stream,
+                             P);
 }
 
 cudaError_t launch_decode_kv4(const Kv4Params &P, int grid, cudaStream_t stream) {
-    const bool two = P.G <= 4;
-    auto kernel = two ? decode_kv4_kernel<true> : decode_kv4_kernel<false>;
-    const int smem = smem_bytes(two ? 4 : 8);
-    cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
-    return launch_overlapped(kernel, dim3(grid), dim3(kThreads), smem, stream, P);
+    return P.G <= 4 ? launch<true>(P, grid, stream) : launch<false>(P, grid, stream);
 }
 
 }  // namespace spark

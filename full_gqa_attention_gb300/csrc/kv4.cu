@@ -23,7 +23,7 @@ bool aligned(const void *p, size_t a);
 int page_shift_of(int page_size);
 spark_status check_pages(const void *k_pages, const void *v_pages, int n_pages, int page_size,
                          const int32_t *table, int max_pages);
-int decode_kv4_ctas(int sms);
+int decode_kv4_ctas(int sms, int G);
 cudaError_t launch_decode_kv4(const Kv4Params &P, int grid, cudaStream_t stream);
 
 namespace {
@@ -485,7 +485,7 @@ struct DecodeKv4Plan {
 
 DecodeKv4Plan plan_decode_kv4(int H, int Hkv, int sms) {
     DecodeKv4Plan pl{};
-    pl.grid = decode_kv4_ctas(sms);
+    pl.grid = decode_kv4_ctas(sms, H / Hkv);
     const size_t parts = static_cast<size_t>(pl.grid) * 2 * (H / Hkv);
     pl.counters = kWorkspaceHeader;
     pl.ml = pl.counters + up256(static_cast<size_t>(pl.grid) * 3 * 4);
