@@ -40,8 +40,9 @@ struct Stretch {
 
 // units(r, report): units of row r; report: the one place to note a fault of it.
 // False where nothing is left for this CTA.  All threads.
-template <typename Units>
+template <int kThreads, typename Units>
 __device__ __forceinline__ bool stretch_of(int S, Units &&units, Stretch &st) {
+    constexpr int kWarps = kThreads / 32;
     __shared__ long long sums[kWarps];
     __shared__ long long s_base;
     __shared__ int s_row;
@@ -121,33 +122,55 @@ __device__ __forceinline__ int angle_at(int k) {
     return (k >> 1 & 3) * 32 + (k >> 3) * 2 + (k & 1);  // in float2
 }
 
-constexpr int kStoreCtas = 2;
-constexpr int kStoreSmem = (3 * kKv4Group * kMaxRopePairs) * 8;
+// One CTA per SM, of 16 warps: a warp takes one of a unit's 16 tokens' keys, of one
+// KV head after another with the same angles, and 4 tokens of one KV head's
+// values.  The next unit's projections come by bulk copies meanwhile.
+constexpr int kStoreThreads = 512;
+constexpr int kStoreHeads = 4;                                   // of a unit, at most
+constexpr int kStoreRow = kStoreHeads * kHeadDim * 2;            // a token's keys, or values
+constexpr int kStoreStage = 2 * kKv4Group * kStoreRow;
+constexpr int kAngles = kKv4Group * kMaxRopePairs;               // of 16 tokens
+constexpr int kStoreSmem = 2 * kStoreStage + 3 * kAngles * 8;
+
+struct StoreUnit {
+    int r, slot0, h0, heads;
+    int t_lo, t_hi;            // the call's slots of the group
+    int first;                 // packed row of slot 0 of the group
+    int id;                    // its page
+};
 
 // kAll: all 256 dims turn.
 template <bool kAll>
-__global__ void __launch_bounds__(kThreads, kStoreCtas)
+__global__ void __launch_bounds__(kStoreThreads, 1)
     kv4_store_kernel(const __grid_constant__ Kv4Params P) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int kAngles = kKv4Group * kMaxRopePairs;       // of 16 tokens
-    float2 *angles = reinterpret_cast<float2 *>(smem);       // of a unit, and of the next
-    float2 *steps = angles + 2 * kAngles;                    // of 0 .. 15 positions
+    extern __shared__ __align__(128) uint8_t smem[];             // two stages: keys, values
+    float2 *angles = reinterpret_cast<float2 *>(smem + 2 * kStoreStage);  // of two units
+    float2 *steps = angles + 2 * kAngles;                        // of 0 .. 15 positions
+    __shared__ uint64_t full[2];
+    __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int half = P.rope.rot_dim / 2;
     // This thread's pair, and the first of its tokens.
-    const int together = half ? kThreads / half : 1;         // tokens the threads take at once
-    const int k = half ? tid % half : 0, t_mine = half ? tid / half : kKv4Group;
+    const int together = half ? kStoreThreads / half : 1;        // tokens the threads take at once
+    const int k = half ? tid % half : 0;
+    const int t_mine = half && tid < together * half ? tid / half : kKv4Group;
     float2 freq = make_float2(0.f, 0.f);
     if (half) freq = P.rope.u[k];
+    if (tid == 0) {
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        fence_mbar_init();
+        abort_flag = 0;
+    }
     grid_dep_wait();
     grid_dep_launch();
-    const int parts = (P.Hkv + P.heads - 1) / P.heads;
+    const int parts = (P.Hkv + kStoreHeads - 1) / kStoreHeads;
     auto units = [&](int r, bool report) {
         const StoreRow s = store_row(P, r, report);
         return static_cast<long long>(groups_of(s.a, s.b)) * parts;
     };
     Stretch st;
-    if (!stretch_of(P.S, units, st)) return;
+    if (!stretch_of<kStoreThreads>(P.S, units, st)) return;
     // Consecutive positions, as nearly always: a group's turns are its first
     // token's and those of 0 .. 15 positions together, 8 instructions for some 70.
     const bool stepwise = st.end - st.u > 2;
@@ -160,46 +183,64 @@ __global__ void __launch_bounds__(kThreads, kStoreCtas)
         }
         __syncthreads();
     }
-    const size_t width = static_cast<size_t>(P.H + 2 * P.Hkv) * kHeadDim;
-    const int turning = P.rope.rot_dim >> 4;                 // lanes of each half of a turn
+    const ptrdiff_t width = static_cast<ptrdiff_t>(P.H + 2 * P.Hkv) * kHeadDim;
+    const int turning = P.rope.rot_dim >> 4;                     // lanes of each half of a turn
     const int lane_pairs = lane < turning ? lane : lane < 2 * turning ? lane - turning : 0;
     StoreRow row = store_row(P, st.r, false);
-    int turn_of = 0;
-    for (; st.u < st.end; ++st.u) {
-        angles = reinterpret_cast<float2 *>(smem) + turn_of * kAngles;
-        turn_of ^= 1;
-        while (st.u >= st.base + static_cast<long long>(groups_of(row.a, row.b)) * parts) {
-            st.base += static_cast<long long>(groups_of(row.a, row.b)) * parts;
-            if (++st.r >= P.S) return;  // the offsets changed under the call
+    // Unit u, at or behind the one located last; false where the offsets changed
+    // under the call.
+    auto locate = [&](long long u, StoreUnit &unit) {
+        for (;;) {
+            const long long n = static_cast<long long>(groups_of(row.a, row.b)) * parts;
+            if (u < st.base + n) break;
+            st.base += n;
+            if (++st.r >= P.S) return false;
             row = store_row(P, st.r, false);
         }
-        const int at = static_cast<int>(st.u - st.base);
-        const int slot0 = ((row.a >> 4) + at / parts) << 4;
-        const int h0 = at % parts * P.heads;
-        const int heads = P.Hkv - h0 < P.heads ? P.Hkv - h0 : P.heads;
-        const int t_lo = row.a > slot0 ? row.a - slot0 : 0;
-        const int t_hi = row.b - slot0 < kKv4Group ? row.b - slot0 : kKv4Group;
-        const int first = row.row + (slot0 - row.a);  // packed row of slot 0 of the group
-        const int id = P.pg.table[static_cast<size_t>(st.r) * P.pg.max_pages +
-                                  (slot0 >> P.pg.page_shift)];
-        const int32_t *pos = P.pos + first;
+        const int at = static_cast<int>(u - st.base);
+        unit.r = st.r;
+        unit.slot0 = ((row.a >> 4) + at / parts) << 4;
+        unit.h0 = at % parts * kStoreHeads;
+        unit.heads = P.Hkv - unit.h0 < kStoreHeads ? P.Hkv - unit.h0 : kStoreHeads;
+        unit.t_lo = row.a > unit.slot0 ? row.a - unit.slot0 : 0;
+        unit.t_hi = row.b - unit.slot0 < kKv4Group ? row.b - unit.slot0 : kKv4Group;
+        unit.first = row.row + (unit.slot0 - row.a);
+        unit.id = P.pg.table[static_cast<size_t>(st.r) * P.pg.max_pages +
+                             (unit.slot0 >> P.pg.page_shift)];
+        return true;
+    };
+    // (one warp: lanes 0 .. 15 the tokens' keys, the others their values)
+    auto fetch = [&](const StoreUnit &unit, int s) {
+        const int t = lane & 15, value = lane >> 4, bytes = unit.heads * kHeadDim * 2;
+        if (lane == 0)
+            mbar_arrive_expect_tx(&full[s], 2 * (unit.t_hi - unit.t_lo) * bytes);
+        __syncwarp();
+        if (t >= unit.t_lo && t < unit.t_hi)
+            bulk_load(smem + s * kStoreStage + lane * kStoreRow,
+                      P.qkv + (unit.first + t) * width +
+                          static_cast<ptrdiff_t>(P.H + value * P.Hkv + unit.h0) * kHeadDim,
+                      bytes, &full[s]);
+    };
+    StoreUnit next;
+    bool more = locate(st.u, next);
+    if (more && warp == 0) fetch(next, 0);
+    int n = 0;
+    for (; more; ++n) {
+        const StoreUnit unit = next;
+        const int s = n & 1, t_lo = unit.t_lo, t_hi = unit.t_hi;
+        float2 *turns = angles + s * kAngles;
         // The angles; every warp looks at the positions itself.
+        const int32_t *pos = P.pos + unit.first;
         const int my_t = lane < t_lo ? t_lo : lane < t_hi ? lane : t_hi - 1;
         const int my_pos = half ? pos[my_t] : 0;
         const int pos_lo = __shfl_sync(0xffffffffu, my_pos, t_lo);
-        const bool steady =
-            stepwise && __all_sync(0xffffffffu, my_pos == pos_lo + (my_t - t_lo));
-        if (id < 0 || id >= P.pg.n_pages) {
-            if (tid == 0) atomicOr(P.status, kErrPage);
-            __syncthreads();  // (as in every unit)
-            continue;
-        }
-        if (steady) {
+        more = ++st.u < st.end && locate(st.u, next);
+        if (stepwise && __all_sync(0xffffffffu, my_pos == pos_lo + (my_t - t_lo))) {
             float2 c;
             rope_cos_sin_fine(pos_lo, freq, c.x, c.y);
             for (int t = t_lo + t_mine; t < t_hi; t += together) {
                 const float2 d = steps[(t - t_lo) * kMaxRopePairs + k];
-                angles[t * kMaxRopePairs + angle_at(k)] =
+                turns[t * kMaxRopePairs + angle_at(k)] =
                     make_float2(fmaf(c.x, d.x, -c.y * d.y), fmaf(c.y, d.x, c.x * d.y));
             }
         } else {
@@ -207,29 +248,21 @@ __global__ void __launch_bounds__(kThreads, kStoreCtas)
             for (int t = t_lo + t_mine; t < t_hi; t += together) {
                 float2 c;
                 rope_cos_sin_fine(pos[t], freq, c.x, c.y);
-                angles[t * kMaxRopePairs + angle_at(k)] = c;
+                turns[t * kMaxRopePairs + angle_at(k)] = c;
             }
         }
-        const __nv_bfloat16 *base = P.qkv + first * static_cast<ptrdiff_t>(width) + lane * 8 +
-                                    static_cast<size_t>(P.H + h0) * kHeadDim;
-        // Four tokens of a head's keys or values.
-        auto fetch = [&](const __nv_bfloat16 *from, int quad, uint4(&raw)[4]) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 4 * quad + j;
-                raw[j] = make_uint4(0, 0, 0, 0);
-                if (t >= t_lo && t < t_hi)
-                    raw[j] = __ldcs(reinterpret_cast<const uint4 *>(from + t * width));
-            }
-        };
+        __syncthreads();  // the angles are written, the unit before is done
+        if (more && warp == 0) fetch(next, s ^ 1);
+        const bool ok = mbar_wait_short(&full[s], n >> 1 & 1, &abort_flag, P.status);
+        if (!ok || unit.id < 0 || unit.id >= P.pg.n_pages) {
+            if (tid == 0 && ok) atomicOr(P.status, kErrPage);
+            continue;
+        }
+        const uint8_t *keys = smem + s * kStoreStage, *values = keys + kKv4Group * kStoreRow;
         const size_t head_bytes = static_cast<size_t>(kKv4GroupBytes) << (P.pg.page_shift - 4);
-        const size_t group0 = P.pg.group(id, h0, P.Hkv, slot0);
-        // Values first, which wait for no angles; warps take turns so that with one
-        // KV head some have its keys and others its values.
-        for (int task = (warp + 4) & (kWarps - 1); task < heads * 4; task += kWarps) {
-            const int h = task >> 2, quad = task & 3;
-            uint4 raw[4];
-            fetch(base + static_cast<size_t>(P.Hkv + h) * kHeadDim, quad, raw);
+        const size_t group0 = P.pg.group(unit.id, unit.h0, P.Hkv, unit.slot0);
+        if (warp < unit.heads * 4) {
+            const int h = warp >> 2, quad = warp & 3;
             uint32_t codes[4];
             unsigned scales = 0, keep = 0;  // keep: of the group's slots, as masks
             uint32_t mask = 0;
@@ -237,78 +270,84 @@ __global__ void __launch_bounds__(kThreads, kStoreCtas)
             for (int j = 0; j < 4; ++j) {
                 const int t = 4 * quad + j;
                 unsigned byte;
-                kv4_value_row(raw[j], codes[j], byte);
+                // (rows beside the call's hold anything and are masked)
+                kv4_value_row(*reinterpret_cast<const uint4 *>(values + t * kStoreRow +
+                                                               h * (kHeadDim * 2) + lane * 16),
+                              codes[j], byte);
                 scales |= byte << (8 * (2 * (j & 1) + (j >> 1)));
                 if (t < t_lo || t >= t_hi) {
                     keep |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
                     mask |= (j & 1 ? 0xf0f0u : 0x0f0fu) << (16 * (j >> 1));
                 }
             }
-            if (mask == 0xffffffffu) continue;
-            // dims 2 i, 2 i + 1 of slots 0 and 1, then of 2 and 3
-            uint32_t e[2], o[2];
+            if (mask != 0xffffffffu) {
+                // dims 2 i, 2 i + 1 of slots 0 and 1, then of 2 and 3
+                uint32_t e[2], o[2];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint32_t a = codes[2 * q], b = codes[2 * q + 1];
-                e[q] = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
-                o[q] = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = __byte_perm(e[0], o[0], i | (i + 4) << 4);
-                const uint32_t hi = __byte_perm(e[1], o[1], i | (i + 4) << 4);
-                w[i] = __byte_perm(lo, hi, 0x5410);
-            }
-            uint8_t *group = P.pg.v + group0 + h * head_bytes;
-            uint4 *dst = reinterpret_cast<uint4 *>(group + kv4_value_at(lane, quad));
-            uint32_t *sdst = reinterpret_cast<uint32_t *>(group + kv4_value_scale_at(lane >> 1, quad));
-            if (mask) {  // slots beside the call's keep what they hold
-                const uint4 old = *dst;
-                w[0] = (w[0] & ~mask) | (old.x & mask);
-                w[1] = (w[1] & ~mask) | (old.y & mask);
-                w[2] = (w[2] & ~mask) | (old.z & mask);
-                w[3] = (w[3] & ~mask) | (old.w & mask);
-                scales = (scales & ~keep) | (*sdst & keep);
-            }
-            *dst = make_uint4(w[0], w[1], w[2], w[3]);
-            if (!(lane & 1)) *sdst = scales;
-        }
-        uint4 raw[4];
-        if (warp < heads * 4) fetch(base + static_cast<size_t>(warp >> 2) * kHeadDim, warp & 3, raw);
-        __syncthreads();  // the angles (of two units: those of the one before may be read still)
-        for (int task = warp; task < heads * 4; task += kWarps) {
-            const int h = task >> 2, quad = task & 3;
-            if (task != warp) fetch(base + static_cast<size_t>(h) * kHeadDim, quad, raw);
-            uint8_t *group = P.pg.k + group0 + h * head_bytes;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 4 * quad + j;
-                if (t < t_lo || t >= t_hi) continue;
-                const int p = __shfl_sync(0xffffffffu, my_pos, t);
-                const KeyTurn turn = kv4_key_turn(raw[j], P.rope.rot_dim, p, lane);
-                float c[8], s[8], y[8];
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t a = codes[2 * q], b = codes[2 * q + 1];
+                    e[q] = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
+                    o[q] = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+                }
+                uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float4 a = *reinterpret_cast<const float4 *>(
-                        angles + t * kMaxRopePairs + i * 32 + lane_pairs * 2);
-                    c[2 * i] = a.x, s[2 * i] = a.y, c[2 * i + 1] = a.z, s[2 * i + 1] = a.w;
+                    const uint32_t lo = __byte_perm(e[0], o[0], i | (i + 4) << 4);
+                    const uint32_t hi = __byte_perm(e[1], o[1], i | (i + 4) << 4);
+                    w[i] = __byte_perm(lo, hi, 0x5410);
                 }
-                if (!kAll && lane >= 2 * turning)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-                kv4_rotate(turn, c, s, y);
-                uint32_t codes;
-                unsigned byte;
-                if (kAll && p != 0)
-                    kv4_key_row<true>(turn, y, p, P.turns, codes, byte);
-                else
-                    kv4_key_row<false>(turn, y, p, P.turns, codes, byte);
-                *reinterpret_cast<uint32_t *>(group + kv4_key_at(lane, t)) = codes;
-                if (!(lane & 1)) group[kv4_key_scale_at(lane >> 1, t)] = static_cast<uint8_t>(byte);
+                uint8_t *group = P.pg.v + group0 + h * head_bytes;
+                uint4 *dst = reinterpret_cast<uint4 *>(group + kv4_value_at(lane, quad));
+                uint32_t *sdst =
+                    reinterpret_cast<uint32_t *>(group + kv4_value_scale_at(lane >> 1, quad));
+                if (mask) {  // slots beside the call's keep what they hold
+                    const uint4 old = *dst;
+                    w[0] = (w[0] & ~mask) | (old.x & mask);
+                    w[1] = (w[1] & ~mask) | (old.y & mask);
+                    w[2] = (w[2] & ~mask) | (old.z & mask);
+                    w[3] = (w[3] & ~mask) | (old.w & mask);
+                    scales = (scales & ~keep) | (*sdst & keep);
+                }
+                *dst = make_uint4(w[0], w[1], w[2], w[3]);
+                if (!(lane & 1)) *sdst = scales;
             }
         }
+        const int t = warp;
+        if (t < t_lo || t >= t_hi) continue;
+        const int p = __shfl_sync(0xffffffffu, my_pos, t);
+        float c[8], sn[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 a =
+                *reinterpret_cast<const float4 *>(turns + t * kMaxRopePairs + i * 32 + lane_pairs * 2);
+            c[2 * i] = a.x, sn[2 * i] = a.y, c[2 * i + 1] = a.z, sn[2 * i + 1] = a.w;
+        }
+        if (!kAll && lane >= 2 * turning)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = 1.f, sn[i] = 0.f;
+        uint8_t *group = P.pg.k + group0;
+#pragma unroll 1
+        for (int h = 0; h < unit.heads; ++h, group += head_bytes) {
+            const KeyTurn turn = kv4_key_turn(
+                *reinterpret_cast<const uint4 *>(keys + t * kStoreRow + h * (kHeadDim * 2) +
+                                                 lane * 16),
+                P.rope.rot_dim, p, lane);
+            float y[8];
+            kv4_rotate(turn, c, sn, y);
+            uint32_t codes;
+            unsigned byte;
+            if (kAll && p != 0)
+                kv4_key_row<true>(turn, y, p, P.turns, codes, byte);
+            else
+                kv4_key_row<false>(turn, y, p, P.turns, codes, byte);
+            *reinterpret_cast<uint32_t *>(group + kv4_key_at(lane, t)) = codes;
+            if (!(lane & 1)) group[kv4_key_scale_at(lane >> 1, t)] = static_cast<uint8_t>(byte);
+        }
     }
+    // copies that were waited for in vain must land before the CTA ends
+    __syncthreads();
+    if (tid == 0 && abort_flag)
+        for (int i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait_plain_short(&full[i & 1], i >> 1 & 1);
 }
 
 // ---------------------------------------------------------------- load
@@ -350,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constan
         return static_cast<long long>(groups_of(s.a, s.b));
     };
     Stretch st;
-    if (!stretch_of(P.S, units, st)) return;
+    if (!stretch_of<kThreads>(P.S, units, st)) return;
     LoadRow row = load_row(P, st.r, false);
     for (; st.u < st.end; ++st.u) {
         while (st.u >= st.base + groups_of(row.a, row.b)) {
@@ -420,15 +459,20 @@ spark_status done(cudaError_t e) {
     return SPARK_ERR_CUDA;
 }
 
-// The turns of a layer's pairs, in two floats and in 64 bits.  A model has a few
+// The turns of a layer's pairs, in two floats and in units of 2^-64 turns.  A model has a few
 // kinds of layers and 128 powers take longer than a launch: each thread keeps the
 // last four kinds' (by base and width, nothing else goes into them).
 struct LayerTurns {
     double theta = 0.0;
     int rot_dim = -1;
     RopeTable rope;
-    double turns[kMaxRopePairs];
+    unsigned long long turns[kMaxRopePairs];
 };
+
+// (A base below 1 gives frequencies above a turn: whole turns leave no trace.)
+unsigned long long turns_in_units(double u) {
+    return static_cast<unsigned long long>(std::ldexp(u - std::floor(u), 64));
+}
 
 const LayerTurns &turns_of(const spark_layer_desc *desc) {
     constexpr int kKinds = 4;
@@ -444,7 +488,7 @@ const LayerTurns &turns_of(const spark_layer_desc *desc) {
     std::memset(t.turns, 0, sizeof(t.turns));
     const double two_pi = 6.283185307179586476925286766559;
     for (int k = 0; k < desc->rot_dim / 2; ++k)
-        t.turns[k] = std::pow(desc->rope_theta, -2.0 * k / desc->rot_dim) / two_pi;
+        t.turns[k] = turns_in_units(std::pow(desc->rope_theta, -2.0 * k / desc->rot_dim) / two_pi);
     return t;
 }
 
@@ -537,11 +581,10 @@ spark_status spark_attn_kv4_store(const void *qkv, const int32_t *pos, const int
     P.status = static_cast<unsigned *>(workspace);
     set_layer(P, desc, H, Hkv);
     set_pages(P, k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
-    P.heads = Hkv;
     auto kernel = desc->rot_dim == kHeadDim ? kv4_store_kernel<true> : kv4_store_kernel<false>;
     st = done(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStoreSmem));
     if (st != SPARK_OK) return st;
-    return done(launch_overlapped(kernel, dim3(sms * kStoreCtas), dim3(kThreads), kStoreSmem,
+    return done(launch_overlapped(kernel, dim3(sms), dim3(kStoreThreads), kStoreSmem,
                                   static_cast<cudaStream_t>(stream), P));
 }
 

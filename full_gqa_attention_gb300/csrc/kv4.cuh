@@ -76,9 +76,8 @@ struct Kv4Params {
     int N, S, H, Hkv, G;
     int kind, window, gate_mode;
     int pos_end;               // decode: positions end here
-    int heads;                 // store: KV heads of a unit of work
     RopeTable rope;
-    double turns[kMaxRopePairs];  // the frequencies in 64 bits
+    unsigned long long turns[kMaxRopePairs];  // the frequencies, in 2^-64 turns per position
 };
 
 // ---------------------------------------------------------------- reading
@@ -270,33 +269,52 @@ __device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float2 *cs, f
     }
 }
 
-// Value i of a turned key in 64 bits: sine and cosine by their series, to
-// x^15 / 15!, of an angle of an eighth of a turn at most (1e-15).  64-bit
-// products are few on this chip: each takes a warp 16 cycles.
-__device__ __noinline__ inline double kv4_exact_turn(float x, float z, int pos, double u) {
-    const double p = pos * u;
-    const double t = (p - rint(p)) + fma(static_cast<double>(pos), u, -p);
-    const double quarter = rint(4.0 * t);
-    const double a = (t - 0.25 * quarter) * 6.283185307179586476925286766559, a2 = a * a;
-    double s = -1.0 / 1307674368000.0, c = -1.0 / 87178291200.0;
-    s = fma(s, a2, 1.0 / 6227020800.0);
-    c = fma(c, a2, 1.0 / 479001600.0);
-    s = fma(s, a2, -1.0 / 39916800.0);
-    c = fma(c, a2, -1.0 / 3628800.0);
-    s = fma(s, a2, 1.0 / 362880.0);
-    c = fma(c, a2, 1.0 / 40320.0);
-    s = fma(s, a2, -1.0 / 5040.0);
-    c = fma(c, a2, -1.0 / 720.0);
-    s = fma(s, a2, 1.0 / 120.0);
-    c = fma(c, a2, 1.0 / 24.0);
-    s = fma(s, a2, -1.0 / 6.0);
-    c = fma(c, a2, -0.5);
-    s = fma(s * a2, a, a);
-    c = fma(c, a2, 1.0);
+// The product of two numbers in units of 2^-62.
+__device__ __forceinline__ long long kv4_mul62(long long a, long long b) {
+    return __mul64hi(a, b) << 2;
+}
+
+// A number in units of 2^-62 as the sum of two floats.
+__device__ __forceinline__ float2 kv4_two_floats(long long a) {
+    const float hi = __ll2float_rn(a);
+    const float lo = __ll2float_rn(a - __float2ll_rn(hi));
+    return make_float2(hi * 0x1p-62f, lo * 0x1p-62f);
+}
+
+// Cosine (x, y) and sine (z, w) of position `pos`'s turn, each as the sum of two
+// floats, to 2^-48: `turn` is a position's in units of 2^-64 turns, so that a
+// product of 64 bits leaves the part behind whole turns.  By the series, to the
+// 17th power of an angle of an eighth of a turn at most, in whole numbers: 64-bit
+// floats are some twenty times slower on this chip.
+__device__ __noinline__ inline float4 kv4_exact_turn(int pos, unsigned long long turn) {
+    const unsigned long long t = pos * turn;
+    const unsigned long long quarter = (t + (1ull << 61)) >> 62;
+    const long long r = static_cast<long long>(t - (quarter << 62));
+    const long long a = kv4_mul62(r, 7244019458077122842ll);  // half of pi
+    const long long a2 = kv4_mul62(a, a);
+    long long c = 220414ll;
+    c = -52899477ll + kv4_mul62(c, a2);
+    c = 9627704831ll + kv4_mul62(c, a2);
+    c = -1270857037706ll + kv4_mul62(c, a2);
+    c = 114377133393536ll + kv4_mul62(c, a2);
+    c = -6405119470038039ll + kv4_mul62(c, a2);
+    c = 192153584101141163ll + kv4_mul62(c, a2);
+    c = -2305843009213693952ll + kv4_mul62(c, a2);
+    long long s = 12966ll;
+    s = -3526632ll + kv4_mul62(s, a2);
+    s = 740592679ll + kv4_mul62(s, a2);
+    s = -115532457973ll + kv4_mul62(s, a2);
+    s = 12708570377060ll + kv4_mul62(s, a2);
+    s = -915017067148291ll + kv4_mul62(s, a2);
+    s = 38430716820228233ll + kv4_mul62(s, a2);
+    s = -768614336404564651ll + kv4_mul62(s, a2);
+    c = (1ll << 62) + kv4_mul62(c, a2);
+    s = a + kv4_mul62(kv4_mul62(s, a2), a);
     const int q = static_cast<int>(quarter) & 3;  // turned on by quarters
-    const double cq = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
-    const double sq = q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c;
-    return x * cq + z * sq;
+    const long long cq = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
+    const long long sq = q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c;
+    const float2 x = kv4_two_floats(cq), y = kv4_two_floats(sq);
+    return make_float4(x.x, x.y, y.x, y.y);
 }
 
 __device__ __forceinline__ float kv4_pick(const uint4 &raw, int i) {
@@ -304,46 +322,67 @@ __device__ __forceinline__ float kv4_pick(const uint4 &raw, int i) {
     return i & 1 ? bf16_hi(w) : bf16_lo(w);
 }
 
-// Settles the scale of the blocks in `open` (the same in a block's two lanes) in
-// 64 bits.  turns: the frequencies of the lane's pairs.  All lanes.  (Arguments by
-// value: they stay in registers where it is not called.)
+// |x cos + z sin| as the sum of two floats, and its sign.
+__device__ __forceinline__ float2 kv4_exact_size(float x, float z, int pos,
+                                                 unsigned long long turn, bool &negative) {
+    const float4 t = kv4_exact_turn(pos, turn);
+    const float p = __fmul_rn(x, t.x), q = __fmul_rn(z, t.z);
+    const float sum = __fadd_rn(p, q), back = __fadd_rn(sum, -p);
+    float rest = __fadd_rn(__fadd_rn(p, -__fadd_rn(sum, -back)), __fadd_rn(q, -back));
+    rest += __fmaf_rn(x, t.x, -p) + __fmaf_rn(z, t.z, -q) + __fmaf_rn(x, t.y, z * t.w);
+    const float hi = __fadd_rn(sum, rest), lo = __fadd_rn(rest, -__fadd_rn(hi, -sum));
+    negative = hi < 0.f;
+    return negative ? make_float2(-hi, -lo) : make_float2(hi, lo);
+}
+
+// Settles the scale of the blocks in `open` (the same in a block's two lanes) from
+// the exact rotation.  turns: the lane's pairs' (kv4_exact_turn).  All lanes.
+// (Arguments by value: they stay in registers where it is not called.)
 __device__ __noinline__ inline unsigned kv4_settle_scale(uint4 own, uint4 other, int pos,
-                                                         const double *turns, float4 y0,
-                                                         float4 y1, float least, bool open,
-                                                         unsigned byte) {
-    double a = 0.0;
+                                                         const unsigned long long *turns,
+                                                         float4 y0, float4 y1, float least,
+                                                         bool open, unsigned byte) {
+    float2 a = make_float2(0.f, 0.f);
     if (open)
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
             const float4 h = i < 4 ? y0 : y1;
             const float y = i & 2 ? (i & 1 ? h.w : h.z) : (i & 1 ? h.y : h.x);
-            if (!(fabsf(y) < least))  // it can be the largest
-                a = fmax(a, fabs(kv4_exact_turn(kv4_pick(own, i), kv4_pick(other, i), pos,
-                                                turns[i])));
+            if (fabsf(y) < least) continue;  // it cannot be the largest
+            bool negative;
+            const float2 v =
+                kv4_exact_size(kv4_pick(own, i), kv4_pick(other, i), pos, turns[i], negative);
+            if (v.x > a.x || (v.x == a.x && v.y > a.y)) a = v;
         }
-    a = fmax(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    const float2 b = make_float2(__shfl_xor_sync(0xffffffffu, a.x, 1),
+                                 __shfl_xor_sync(0xffffffffu, a.y, 1));
+    if (b.x > a.x || (b.x == a.x && b.y > a.y)) a = b;
     if (!open) return byte;
-    // the scale below a / 6, the next one, and their middle
-    unsigned lo = kv4_scale_byte(static_cast<float>(a / 6.0));
-    if (lo > 0 && 6.0 * kv4_scale(lo) > a) --lo;
+    // the scale below a / 6, the next one, and their middle (a few bits each: exact)
+    unsigned lo = kv4_scale_byte(a.x * kSixth);
+    if (lo > 0 && 6.f * kv4_scale(lo) > a.x) --lo;
     if (lo == kKv4MaxScale) return lo;
-    const double mid = 3.0 * (static_cast<double>(kv4_scale(lo)) + kv4_scale(lo + 1));
-    return a > mid || (a == mid && (lo & 1u)) ? lo + 1 : lo;
+    const float mid = 3.f * (kv4_scale(lo) + kv4_scale(lo + 1));
+    const float over = (a.x - mid) + a.y;
+    return over > 0.f || (over == 0.f && (lo & 1u)) ? lo + 1 : lo;
 }
 
-// Settles the codes of the dims in `open` (bit 4 i), in 64 bits.
+// Settles the codes of the dims in `open` (bit 4 i) from the exact rotation.
 __device__ __noinline__ inline uint32_t kv4_settle_codes(uint4 own, uint4 other, int pos,
-                                                         const double *turns, float scale,
+                                                         const unsigned long long *turns, float s,
                                                          unsigned open, uint32_t codes) {
-    const double s = scale;
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
         if (!(open >> (4 * i) & 1u)) continue;
-        const double v = kv4_exact_turn(kv4_pick(own, i), kv4_pick(other, i), pos, turns[i]);
-        const double m = fabs(v);
-        unsigned c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) +
-                     (m > 2.5 * s) + (m >= 3.5 * s) + (m > 5.0 * s);
-        if (v < 0.0) c |= 8u;
+        bool negative;
+        const float2 m =
+            kv4_exact_size(kv4_pick(own, i), kv4_pick(other, i), pos, turns[i], negative);
+        // (borders have few bits: exact; so is a difference from one nearby)
+        auto over = [&](float border) { return __fadd_rn(m.x, -border * s) + m.y; };
+        unsigned c = (over(0.25f) > 0.f) + (over(0.75f) >= 0.f) + (over(1.25f) > 0.f) +
+                     (over(1.75f) >= 0.f) + (over(2.5f) > 0.f) + (over(3.5f) >= 0.f) +
+                     (over(5.f) > 0.f);
+        if (negative) c |= 8u;
         codes = (codes & ~(15u << (4 * i))) | c << (4 * i);
     }
     return codes;
@@ -351,26 +390,28 @@ __device__ __noinline__ inline uint32_t kv4_settle_codes(uint4 own, uint4 other,
 
 // A key's row, rotated (y, in 32 bits), quantised.  What the pages hold is the
 // nearest to the exact rotation: where 32 bits do not tell on which side of a
-// border a value or a scale lies (one row in a hundred or so), 64 bits decide.
-// |y| is off by 2^-21 (|x| + |z|) at most: cos and sin by 2^-22 each (1 ulp of
-// sincospif and 2^-24 that the frequencies' two parts leave of the angle below
-// 2^24 positions; where two turns are put together, both, and the products'
-// roundings), the product and the sum by 2^-24 each.  |x| + |z| is at most 1.5
-// times the sum of the two blocks' largest |y| (a turn keeps x^2 + z^2).  Twice the
-// error is allowed, and 2^-22 of a quotient (8 at most, or it saturates).  Dims
-// that do not turn are bf16: kSnap.
+// border a value or a scale lies (one row in some hundreds), more bits decide.
+// Let N be the larger of the two blocks' largest |y| times 2^(1/2): a turn keeps
+// x^2 + z^2, so no (x, z) of the block is longer.  (cos, sin) is off by less than
+// 2^-21.2, as a vector: each of two turns put together by 2^-23.5 (1 ulp of
+// sincospif, 2^-24, in each component) and 2^-24.5 (its correction's rounding),
+// their product by 2^-23.5, and 2^-24 is the angle's, which the frequencies' two
+// parts leave below 2^24 positions.  The product and the sum round by 2^-24 N
+// each.  In all |y| is off by 2^-20.8 N at most; 2^-20.7 is allowed, and of a
+// quotient (7 at most, or it saturates) also 2^-22 of it.  Dims that do not turn
+// are bf16: kSnap.
 // kAll: every lane turns.
 template <bool kAll>
 __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8], int pos,
-                                            const double *turns, uint32_t &codes,
+                                            const unsigned long long *turns, uint32_t &codes,
                                             unsigned &byte) {
-    constexpr float kRel = 2.38418579e-7f, kAbs = 1.43051147e-6f;  // 2^-22, 1.5 * 2^-20
+    constexpr float kRel = 2.38418579e-7f, kAbs = 8.31e-7f;  // 2^-22, 2^(1/2 - 20.7)
     float sum;
     float a = kv4_largest(y, sum);
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
     const float a_other = __shfl_sync(0xffffffffu, a, t.partner);
     const bool turns_here = kAll || t.turns;
-    const float e = fmaf(a, kAbs, a_other * kAbs);
+    const float e = fmaxf(a, a_other) * kAbs;
     const float top = a * kSixth;
     byte = kv4_scale_byte(turns_here ? top : kv4_snap(top));
     // Does the maximum's error reach the border between this scale and a next one?
