@@ -469,11 +469,6 @@ struct LayerTurns {
     unsigned long long turns[kMaxRopePairs];
 };
 
-// (A base below 1 gives frequencies above a turn: whole turns leave no trace.)
-unsigned long long turns_in_units(double u) {
-    return static_cast<unsigned long long>(std::ldexp(u - std::floor(u), 64));
-}
-
 const LayerTurns &turns_of(const spark_layer_desc *desc) {
     constexpr int kKinds = 4;
     static thread_local LayerTurns kept[kKinds];
@@ -487,8 +482,16 @@ const LayerTurns &turns_of(const spark_layer_desc *desc) {
     fill_rope_table(desc, &t.rope);
     std::memset(t.turns, 0, sizeof(t.turns));
     const double two_pi = 6.283185307179586476925286766559;
-    for (int k = 0; k < desc->rot_dim / 2; ++k)
-        t.turns[k] = turns_in_units(std::pow(desc->rope_theta, -2.0 * k / desc->rot_dim) / two_pi);
+    for (int k = 0; k < desc->rot_dim / 2; ++k) {
+        double u = std::pow(desc->rope_theta, -2.0 * k / desc->rot_dim) / two_pi;
+        if (!(u <= 0.5)) {
+            // (a base below 1: whole turns per position leave no trace)
+            u = std::isfinite(u) ? u - std::rint(u) : 0.0;
+            const float hi = static_cast<float>(u);
+            t.rope.u[k] = make_float2(hi, static_cast<float>(u - hi));
+        }
+        t.turns[k] = static_cast<unsigned long long>(std::ldexp(u - std::floor(u), 64));
+    }
     return t;
 }
 

@@ -452,9 +452,11 @@ __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8
         }
     }
     codes = kv4_codes(hi);
-    // (a sign that differs beside zero stands for the same value)
+    // (a sign that differs beside zero stands for the same value; quotients that are
+    // known to a quarter only, of rotations that cancel, can be of either sign)
     unsigned open = codes ^ kv4_codes(lo);
     open = (open | open >> 1 | open >> 2) & 0x11111111u;
+    if (turns_here && d >= 0.25f) open = 0x11111111u;
     if (!finite) {
         codes = open = 0;
         byte = kKv4NanScale;
