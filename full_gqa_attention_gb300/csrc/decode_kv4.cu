@@ -285,15 +285,18 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
             __syncwarp();
             const uint8_t *src = new_rows + s * kNewBytes + P.G * kRowBytes + lane * 16;
             float y[8];
-            unsigned byte;
+            unsigned byte[1];
+            uint32_t codes[1];
             const KeyTurn turn = kv4_key_turn(*reinterpret_cast<const uint4 *>(src),
                                               P.rope.rot_dim, wk.row.pos, lane);
             kv4_rotate(turn, cs_new, y);
-            kv4_key_row<false>(turn, y, wk.row.pos, P.turns, new_codes[s][0][lane], byte);
-            new_scale[s][0][lane] = static_cast<uint8_t>(byte);
-            kv4_value_row(*reinterpret_cast<const uint4 *>(src + kRowBytes),
-                          new_codes[s][1][lane], byte);
-            new_scale[s][1][lane] = static_cast<uint8_t>(byte);
+            kv4_key_row<false>(turn, y, wk.row.pos, P.turns, codes[0], byte[0]);
+            new_codes[s][0][lane] = codes[0];
+            new_scale[s][0][lane] = static_cast<uint8_t>(byte[0]);
+            const uint4 value[1] = {*reinterpret_cast<const uint4 *>(src + kRowBytes)};
+            kv4_value_rows(value, codes, byte);
+            new_codes[s][1][lane] = codes[0];
+            new_scale[s][1][lane] = static_cast<uint8_t>(byte[0]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&new_full[s]);
         };

@@ -266,15 +266,17 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
             uint32_t codes[4];
             unsigned scales = 0, keep = 0;  // keep: of the group's slots, as masks
             uint32_t mask = 0;
+            uint4 raw[4];
+            unsigned byte[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // (rows beside the call's hold anything and are masked)
+                raw[j] = *reinterpret_cast<const uint4 *>(values + (4 * quad + j) * kStoreRow +
+                                                          h * (kHeadDim * 2) + lane * 16);
+            kv4_value_rows(raw, codes, byte);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t = 4 * quad + j;
-                unsigned byte;
-                // (rows beside the call's hold anything and are masked)
-                kv4_value_row(*reinterpret_cast<const uint4 *>(values + t * kStoreRow +
-                                                               h * (kHeadDim * 2) + lane * 16),
-                              codes[j], byte);
-                scales |= byte << (8 * (2 * (j & 1) + (j >> 1)));
+                scales |= byte[j] << (8 * (2 * (j & 1) + (j >> 1)));
                 if (t < t_lo || t >= t_hi) {
                     keep |= 0xffu << (8 * (2 * (j & 1) + (j >> 1)));
                     mask |= (j & 1 ? 0xf0f0u : 0x0f0fu) << (16 * (j >> 1));

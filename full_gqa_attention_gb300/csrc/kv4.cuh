@@ -171,14 +171,15 @@ __device__ __forceinline__ bool kv4_finite(const uint4 &raw) {
     return !(c & 0x80008000u);
 }
 
-// The largest of a lane's eight numbers, and their sum, which is not finite where
-// one of them is NaN (or very large).
-__device__ __forceinline__ float kv4_largest(const float (&x)[8], float &sum) {
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-    sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-    return a;
+// The largest of three sizes, NaN where one is; the largest of a lane's eight.
+__device__ __forceinline__ float kv4_larger(float a, float b, float c = 0.f) {
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+__device__ __forceinline__ float kv4_largest(const float (&x)[8]) {
+    return kv4_larger(kv4_larger(x[0], x[1], x[2]), kv4_larger(x[3], x[4], x[5]),
+                      kv4_larger(x[6], x[7]));
 }
 
 __device__ __forceinline__ float kv4_reciprocal(float s) {
@@ -199,26 +200,34 @@ __device__ __forceinline__ float kv4_snap(float y) {
 constexpr float kSnap = 1536.0f;
 constexpr float kSixth = 1.0f / 6.0f;
 
-// A value's row.
-__device__ __forceinline__ void kv4_value_row(const uint4 &raw, uint32_t &codes, unsigned &byte) {
-    float x[8], sum;
-    kv4_floats(raw, x);
-    float a = kv4_largest(x, sum);
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    byte = kv4_scale_byte(kv4_snap(a * kSixth));
-    const float r = kv4_reciprocal(kv4_scale(byte));
+// N values' rows: their chains interleave.
+template <int N>
+__device__ __forceinline__ void kv4_value_rows(const uint4 (&raw)[N], uint32_t (&codes)[N],
+                                               unsigned (&byte)[N]) {
+    bool odd = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmaf_rn(x[i], r, kSnap), -kSnap);
-    codes = kv4_codes(x);
-    const bool odd = !(fabsf(sum) + a < INFINITY);
-    if (__any_sync(0xffffffffu, odd)) {
-        int bad = !kv4_finite(raw);
-        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-        if (bad) {
-            codes = 0;
-            byte = kKv4NanScale;
-        }
+    for (int n = 0; n < N; ++n) {
+        float x[8];
+        kv4_floats(raw[n], x);
+        float a = kv4_largest(x);
+        a = kv4_larger(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        byte[n] = kv4_scale_byte(kv4_snap(a * kSixth));
+        const float r = kv4_reciprocal(kv4_scale(byte[n]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmaf_rn(x[i], r, kSnap), -kSnap);
+        codes[n] = kv4_codes(x);
+        odd = odd || !(a < INFINITY);
     }
+    if (__any_sync(0xffffffffu, odd))
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            int bad = !kv4_finite(raw[n]);
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+            if (bad) {
+                codes[n] = 0;
+                byte[n] = kKv4NanScale;
+            }
+        }
 }
 
 // Dims 8 lane .. of a key, as bf16, and of what they turn with: y = x cos + z sin
@@ -406,9 +415,8 @@ __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8
                                             const unsigned long long *turns, uint32_t &codes,
                                             unsigned &byte) {
     constexpr float kRel = 2.38418579e-7f, kAbs = 8.31e-7f;  // 2^-22, 2^(1/2 - 20.7)
-    float sum;
-    float a = kv4_largest(y, sum);
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    float a = kv4_largest(y);
+    a = kv4_larger(a, __shfl_xor_sync(0xffffffffu, a, 1));
     const float a_other = __shfl_sync(0xffffffffu, a, t.partner);
     const bool turns_here = kAll || t.turns;
     const float e = fmaxf(a, a_other) * kAbs;
@@ -419,13 +427,13 @@ __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8
     const float border = __uint_as_float((__float_as_uint(moved) & 0xfff00000u) | 0x80000u);
     const bool open_scale =
         turns_here && fabsf(moved - border) <= fmaf(e, kSixth, moved * kRel);
-    const bool odd = !(fabsf(sum) + a < INFINITY);
+    const bool odd = !(a < INFINITY);
     bool finite = true;
     if (__any_sync(0xffffffffu, odd || open_scale)) {
         int bad = !kv4_finite(t.own) || !kv4_finite(t.other);
         bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
         finite = !bad;
-        int open = open_scale || odd;
+        int open = open_scale || odd;  // (a block's lanes may turn with different blocks)
         open |= __shfl_xor_sync(0xffffffffu, open, 1);
         byte = kv4_settle_scale(t.own, t.other, pos, turns + t.k0,
                                 make_float4(y[0], y[1], y[2], y[3]),
