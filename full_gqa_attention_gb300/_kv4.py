@@ -41,10 +41,10 @@ def _pages4(k4_pages, v4_pages, page_table, rows: int, Hkv: int | None = None):
     return shape[0], shape[1], shape[2], table[1]
 
 
-def _space(dev: int, workspace, need: int):
-    """The caller's workspace or a new one, and whether it is ours."""
+def _space(dev: int, workspace, size, *args):
+    """The caller's workspace or a new one (size(*args) bytes), and whether it is ours."""
     if workspace is None:
-        return new_workspace(need, torch.device("cuda", dev)), True
+        return new_workspace(size(*args), torch.device("cuda", dev)), True
     _check(dev, (workspace, _U8, "workspace"))
     return workspace, False
 
@@ -80,18 +80,18 @@ def spark_attn_kv4_store(qkv: torch.Tensor, pos: torch.Tensor, cu_seqlens: torch
     _check(dev, (qkv, _BF16, "qkv"), (pos, _I32, "pos"), (cu_seqlens, _I32, "cu_seqlens"),
            (start, _I32, "start"), (k4_pages, _U8, "k4_pages"), (v4_pages, _U8, "v4_pages"),
            (page_table, _I32, "page_table"))
-    S = cu_seqlens.numel() - 1
-    if qkv.dim() != 2 or pos.shape != qkv.shape[:1] or cu_seqlens.dim() != 1 or start.shape != (S,):
+    tokens, offsets = qkv.shape, cu_seqlens.shape
+    S = offsets[0] - 1 if len(offsets) == 1 else -1
+    if len(tokens) != 2 or pos.shape != tokens[:1] or start.shape != (S,):
         raise ValueError("qkv must be [tokens, (H + 2 Hkv) * 256], pos [tokens], "
                          "cu_seqlens [S + 1], start [S]")
     n_pages, Hkv, page_size, max_pages = _pages4(k4_pages, v4_pages, page_table, S)
-    n, width = qkv.shape
+    n, width = tokens
     H = width // HEAD_DIM - 2 * Hkv
     if H < 1 or (H + 2 * Hkv) * HEAD_DIM != width:
         raise ValueError("qkv and k4_pages disagree on the heads")
     d = ctypes.byref(as_desc(layer))
-    ws, owned = _space(dev, workspace,
-                       lib.spark_attn_kv4_store_workspace_size(n, S, H, Hkv, d))
+    ws, owned = _space(dev, workspace, lib.spark_attn_kv4_store_workspace_size, n, S, H, Hkv, d)
     st = lib.spark_attn_kv4_store(
         qkv.data_ptr(), pos.data_ptr(), cu_seqlens.data_ptr(), start.data_ptr(),
         k4_pages.data_ptr(), v4_pages.data_ptr(), n_pages, page_size, page_table.data_ptr(),
@@ -117,12 +117,13 @@ def spark_attn_kv4_load(k4_pages: torch.Tensor, v4_pages: torch.Tensor, page_tab
            (page_table, _I32, "page_table"), (begin, _I32, "begin"), (end, _I32, "end"),
            (k_pages, _BF16, "k_pages"), (v_pages, _BF16, "v_pages"),
            (to_page_table, _I32, "to_page_table"))
-    if begin.dim() != 1 or end.shape != begin.shape:
+    rows = begin.shape
+    if len(rows) != 1 or end.shape != rows:
         raise ValueError("begin and end must be [S]")
-    S = begin.shape[0]
+    S = rows[0]
     n_pages, Hkv, page_size, max_pages = _pages4(k4_pages, v4_pages, page_table, S)
     to_n_pages, to_page_size, to_max_pages = _pages(k_pages, v_pages, to_page_table, S, Hkv)
-    ws, owned = _space(dev, workspace, lib.spark_attn_kv4_load_workspace_size(S, Hkv))
+    ws, owned = _space(dev, workspace, lib.spark_attn_kv4_load_workspace_size, S, Hkv)
     st = lib.spark_attn_kv4_load(
         k4_pages.data_ptr(), v4_pages.data_ptr(), n_pages, page_size, page_table.data_ptr(),
         max_pages, begin.data_ptr(), end.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
