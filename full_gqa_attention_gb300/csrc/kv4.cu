@@ -124,13 +124,16 @@ __device__ __forceinline__ int angle_at(int k) {
 
 // One CTA per SM, of 16 warps: a warp takes one of a unit's 16 tokens' keys, of one
 // KV head after another with the same angles, and 4 tokens of one KV head's
-// values.  The next unit's projections come by bulk copies meanwhile.
+// values.  The next unit's projections come by bulk copies meanwhile, and its
+// angles are written before a unit's rows are: a warp that is late (some rows take
+// more arithmetic) may be behind the others by nearly a unit.
 constexpr int kStoreThreads = 512;
 constexpr int kStoreHeads = 4;                                   // of a unit, at most
 constexpr int kStoreRow = kStoreHeads * kHeadDim * 2;            // a token's keys, or values
 constexpr int kStoreStage = 2 * kKv4Group * kStoreRow;
 constexpr int kAngles = kKv4Group * kMaxRopePairs;               // of 16 tokens
-constexpr int kStoreSmem = 2 * kStoreStage + 3 * kAngles * 8;
+constexpr int kAngleSets = 3;
+constexpr int kStoreSmem = 2 * kStoreStage + (kAngleSets + 1) * kAngles * 8;
 
 struct StoreUnit {
     int r, slot0, h0, heads;
@@ -144,14 +147,15 @@ template <bool kAll>
 __global__ void __launch_bounds__(kStoreThreads, 1)
     kv4_store_kernel(const __grid_constant__ Kv4Params P) {
     extern __shared__ __align__(128) uint8_t smem[];             // two stages: keys, values
-    float2 *angles = reinterpret_cast<float2 *>(smem + 2 * kStoreStage);  // of two units
-    float2 *steps = angles + 2 * kAngles;                        // of 0 .. 15 positions
-    __shared__ uint64_t full[2];
+    float2 *angles = reinterpret_cast<float2 *>(smem + 2 * kStoreStage);  // of three units
+    float2 *steps = angles + kAngleSets * kAngles;               // of 0 .. 15 positions
+    __shared__ uint64_t full[2];     // a stage's rows are there
+    __shared__ uint64_t turned;      // a unit's angles are, and the unit before the last is done
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int half = P.rope.rot_dim / 2;
     // This thread's pair, and the first of its tokens.
-    const int together = half ? kStoreThreads / half : 1;        // tokens the threads take at once
+    const int together = half ? kStoreThreads / half : 1;     // tokens the threads take at once
     const int k = half ? tid % half : 0;
     const int t_mine = half && tid < together * half ? tid / half : kKv4Group;
     float2 freq = make_float2(0.f, 0.f);
@@ -159,6 +163,7 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
     if (tid == 0) {
         mbar_init(&full[0], 1);
         mbar_init(&full[1], 1);
+        mbar_init(&turned, kStoreThreads / 32);
         fence_mbar_init();
         abort_flag = 0;
     }
@@ -183,13 +188,11 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
         }
         __syncthreads();
     }
-    const ptrdiff_t width = static_cast<ptrdiff_t>(P.H + 2 * P.Hkv) * kHeadDim;
-    const int turning = P.rope.rot_dim >> 4;                     // lanes of each half of a turn
-    const int lane_pairs = lane < turning ? lane : lane < 2 * turning ? lane - turning : 0;
     StoreRow row = store_row(P, st.r, false);
-    // Unit u, at or behind the one located last; false where the offsets changed
-    // under the call.
+    // Unit u, at or behind the one located last; false where there is none, or the
+    // offsets changed under the call.
     auto locate = [&](long long u, StoreUnit &unit) {
+        if (u >= st.end) return false;
         for (;;) {
             const long long n = static_cast<long long>(groups_of(row.a, row.b)) * parts;
             if (u < st.base + n) break;
@@ -209,6 +212,7 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
                              (unit.slot0 >> P.pg.page_shift)];
         return true;
     };
+    const ptrdiff_t width = static_cast<ptrdiff_t>(P.H + 2 * P.Hkv) * kHeadDim;
     // (one warp: lanes 0 .. 15 the tokens' keys, the others their values)
     auto fetch = [&](const StoreUnit &unit, int s) {
         const int t = lane & 15, value = lane >> 4, bytes = unit.heads * kHeadDim * 2;
@@ -221,20 +225,17 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
                           static_cast<ptrdiff_t>(P.H + value * P.Hkv + unit.h0) * kHeadDim,
                       bytes, &full[s]);
     };
-    StoreUnit next;
-    bool more = locate(st.u, next);
-    if (more && warp == 0) fetch(next, 0);
-    int n = 0;
-    for (; more; ++n) {
-        const StoreUnit unit = next;
-        const int s = n & 1, t_lo = unit.t_lo, t_hi = unit.t_hi;
-        float2 *turns = angles + s * kAngles;
-        // The angles; every warp looks at the positions itself.
+    const int turning = P.rope.rot_dim >> 4;                     // lanes of each half of a turn
+    const int lane_pairs = lane < turning ? lane : lane < 2 * turning ? lane - turning : 0;
+    // Writes unit n's angles, and says so; returns this lane's token's position.
+    auto turn = [&](const StoreUnit &unit, int n) {
+        // every warp looks at the positions itself
+        float2 *turns = angles + n % kAngleSets * kAngles;
+        const int t_lo = unit.t_lo, t_hi = unit.t_hi;
         const int32_t *pos = P.pos + unit.first;
         const int my_t = lane < t_lo ? t_lo : lane < t_hi ? lane : t_hi - 1;
         const int my_pos = half ? pos[my_t] : 0;
         const int pos_lo = __shfl_sync(0xffffffffu, my_pos, t_lo);
-        more = ++st.u < st.end && locate(st.u, next);
         if (stepwise && __all_sync(0xffffffffu, my_pos == pos_lo + (my_t - t_lo))) {
             float2 c;
             rope_cos_sin_fine(pos_lo, freq, c.x, c.y);
@@ -251,11 +252,46 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
                 turns[t * kMaxRopePairs + angle_at(k)] = c;
             }
         }
-        __syncthreads();  // the angles are written, the unit before is done
-        if (more && warp == 0) fetch(next, s ^ 1);
-        const bool ok = mbar_wait_short(&full[s], n >> 1 & 1, &abort_flag, P.status);
-        if (!ok || unit.id < 0 || unit.id >= P.pg.n_pages) {
-            if (tid == 0 && ok) atomicOr(P.status, kErrPage);
+        return my_pos;
+    };
+    auto arrive = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&turned);
+    };
+    StoreUnit next;
+    bool more = locate(st.u, next);
+    int next_pos = 0, fetched = 0;
+    bool alive = true;  // no wait has run out
+    if (more) {
+        if (warp == 0) fetch(next, fetched++);
+        next_pos = turn(next, 0);
+        arrive();
+    }
+    for (int n = 0; more; ++n) {
+        const StoreUnit unit = next;
+        const int s = n & 1, t_lo = unit.t_lo, t_hi = unit.t_hi, my_pos = next_pos;
+        const float2 *turns = angles + n % kAngleSets * kAngles;
+        more = locate(st.u + n + 1, next);
+        // All warps have done unit n - 2, whose place unit n + 1's angles take.
+        alive = alive && mbar_wait_short(&turned, n & 1, &abort_flag, P.status);
+        if (more) {
+            next_pos = turn(next, n + 1);
+            arrive();
+        }
+        alive = alive && mbar_wait_short(&full[s], n >> 1 & 1, &abort_flag, P.status);
+        alive = __all_sync(0xffffffffu, alive);
+        // Once all have done unit n - 1, whose stage the next one takes.
+        auto fetch_next = [&]() {
+            if (warp != 0 || !more) return;
+            alive = alive && (n == 0 || mbar_wait_short(&turned, (n + 1) & 1, &abort_flag, P.status));
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) return;
+            fetch(next, s ^ 1);
+            ++fetched;
+        };
+        if (!alive || unit.id < 0 || unit.id >= P.pg.n_pages) {
+            if (tid == 0 && alive) atomicOr(P.status, kErrPage);
+            fetch_next();
             continue;
         }
         const uint8_t *keys = smem + s * kStoreStage, *values = keys + kKv4Group * kStoreRow;
@@ -314,6 +350,7 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
                 if (!(lane & 1)) *sdst = scales;
             }
         }
+        fetch_next();
         const int t = warp;
         if (t < t_lo || t >= t_hi) continue;
         const int p = __shfl_sync(0xffffffffu, my_pos, t);
@@ -347,9 +384,9 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
         }
     }
     // copies that were waited for in vain must land before the CTA ends
-    __syncthreads();
-    if (tid == 0 && abort_flag)
-        for (int i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait_plain_short(&full[i & 1], i >> 1 & 1);
+    if (warp == 0 && *static_cast<volatile int *>(&abort_flag))
+        for (int i = fetched > 2 ? fetched - 2 : 0; i < fetched; ++i)
+            mbar_wait_plain_short(&full[i & 1], i >> 1 & 1);
 }
 
 // ---------------------------------------------------------------- load
