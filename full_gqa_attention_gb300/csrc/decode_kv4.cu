@@ -283,17 +283,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
                 rope_cos_sin_fine(wk.row.pos, P.rope.u[k], cs_new[k].x, cs_new[k].y);
             mbar_wait_plain_short(&rows_full[s], ((n_pairs - 1) / kPairs) & 1);
             __syncwarp();
-            const uint8_t *src = new_rows + s * kNewBytes + P.G * kRowBytes + lane * 16;
+            const uint8_t *src = new_rows + s * kNewBytes + P.G * kRowBytes;
             float y[8];
             unsigned byte[1];
             uint32_t codes[1];
-            const KeyTurn turn = kv4_key_turn(*reinterpret_cast<const uint4 *>(src),
-                                              P.rope.rot_dim, wk.row.pos, lane);
-            kv4_rotate(turn, cs_new, y);
-            kv4_key_row<false>(turn, y, wk.row.pos, P.turns, codes[0], byte[0]);
+            const KeyTurn turn = kv4_key_turn(P.rope.rot_dim, wk.row.pos, lane);
+            kv4_rotate(turn, src, lane, cs_new, y);
+            kv4_key_row<false>(turn, src, lane, y, wk.row.pos, P.turns, codes[0], byte[0]);
             new_codes[s][0][lane] = codes[0];
             new_scale[s][0][lane] = static_cast<uint8_t>(byte[0]);
-            const uint4 value[1] = {*reinterpret_cast<const uint4 *>(src + kRowBytes)};
+            const uint4 value[1] = {kv4_own(src + kRowBytes, lane)};
             kv4_value_rows(value, codes, byte);
             new_codes[s][1][lane] = codes[0];
             new_scale[s][1][lane] = static_cast<uint8_t>(byte[0]);
@@ -413,15 +412,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
             const int hh = warp + i * kWarps;
             if (hh >= P.G) break;
             // in halves, scaled by a power of two so that the largest is 1 to 2
-            const uint4 raw = *reinterpret_cast<const uint4 *>(rows + hh * kRowBytes + lane * 16);
-            const KeyTurn turn = kv4_key_turn(raw, P.rope.rot_dim, pos, lane);
+            const uint8_t *row = rows + hh * kRowBytes;
             float y[8], k[8];
-            kv4_floats(raw, y);
-            kv4_floats(*reinterpret_cast<const uint4 *>(rows + P.G * kRowBytes + lane * 16), k);
+            kv4_floats(kv4_own(row, lane), y);
+            kv4_floats(kv4_own(rows + P.G * kRowBytes, lane), k);
             float d = 0.f, a = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) d = fmaf(y[j], k[j], d);
-            kv4_rotate(turn, cs, y);
+            kv4_rotate(kv4_key_turn(P.rope.rot_dim, pos, lane), row, lane, cs, y);
             bool odd = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {

@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
     float2 *angles = reinterpret_cast<float2 *>(smem + 2 * kStoreStage);  // of three units
     float2 *steps = angles + kAngleSets * kAngles;               // of 0 .. 15 positions
     __shared__ uint64_t full[2];     // a stage's rows are there
-    __shared__ uint64_t turned;      // a unit's angles are, and the unit before the last is done
+    __shared__ uint64_t turned;      // a unit's angles are
+    __shared__ uint64_t emptied;     // all warps have read a unit's rows
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int half = P.rope.rot_dim / 2;
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
         mbar_init(&full[0], 1);
         mbar_init(&full[1], 1);
         mbar_init(&turned, kStoreThreads / 32);
+        mbar_init(&emptied, kStoreThreads / 32);
         fence_mbar_init();
         abort_flag = 0;
     }
@@ -227,14 +229,17 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
     };
     const int turning = P.rope.rot_dim >> 4;                     // lanes of each half of a turn
     const int lane_pairs = lane < turning ? lane : lane < 2 * turning ? lane - turning : 0;
-    // Writes unit n's angles, and says so; returns this lane's token's position.
-    auto turn = [&](const StoreUnit &unit, int n) {
-        // every warp looks at the positions itself
+    // The position of this lane's token of a unit: every warp looks at all of them.
+    auto token_of = [&](const StoreUnit &unit) {
+        return lane < unit.t_lo ? unit.t_lo : lane < unit.t_hi ? lane : unit.t_hi - 1;
+    };
+    auto position = [&](const StoreUnit &unit) {
+        return half ? P.pos[unit.first + token_of(unit)] : 0;
+    };
+    // Writes unit n's angles.
+    auto turn = [&](const StoreUnit &unit, int n, int my_pos) {
         float2 *turns = angles + n % kAngleSets * kAngles;
-        const int t_lo = unit.t_lo, t_hi = unit.t_hi;
-        const int32_t *pos = P.pos + unit.first;
-        const int my_t = lane < t_lo ? t_lo : lane < t_hi ? lane : t_hi - 1;
-        const int my_pos = half ? pos[my_t] : 0;
+        const int t_lo = unit.t_lo, t_hi = unit.t_hi, my_t = token_of(unit);
         const int pos_lo = __shfl_sync(0xffffffffu, my_pos, t_lo);
         if (stepwise && __all_sync(0xffffffffu, my_pos == pos_lo + (my_t - t_lo))) {
             float2 c;
@@ -248,13 +253,10 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
 #pragma unroll 1
             for (int t = t_lo + t_mine; t < t_hi; t += together) {
                 float2 c;
-                rope_cos_sin_fine(pos[t], freq, c.x, c.y);
+                rope_cos_sin_fine(P.pos[unit.first + t], freq, c.x, c.y);
                 turns[t * kMaxRopePairs + angle_at(k)] = c;
             }
         }
-        return my_pos;
-    };
-    auto arrive = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&turned);
     };
@@ -264,34 +266,41 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
     bool alive = true;  // no wait has run out
     if (more) {
         if (warp == 0) fetch(next, fetched++);
-        next_pos = turn(next, 0);
-        arrive();
+        next_pos = position(next);
+        turn(next, 0, next_pos);
     }
     for (int n = 0; more; ++n) {
         const StoreUnit unit = next;
         const int s = n & 1, t_lo = unit.t_lo, t_hi = unit.t_hi, my_pos = next_pos;
         const float2 *turns = angles + n % kAngleSets * kAngles;
         more = locate(st.u + n + 1, next);
-        // All warps have done unit n - 2, whose place unit n + 1's angles take.
-        alive = alive && mbar_wait_short(&turned, n & 1, &abort_flag, P.status);
-        if (more) {
-            next_pos = turn(next, n + 1);
-            arrive();
-        }
-        alive = alive && mbar_wait_short(&full[s], n >> 1 & 1, &abort_flag, P.status);
+        if (more) next_pos = position(next);
+        alive = alive && mbar_wait_short(&turned, n & 1, &abort_flag, P.status) &&
+                mbar_wait_short(&full[s], n >> 1 & 1, &abort_flag, P.status);
         alive = __all_sync(0xffffffffu, alive);
-        // Once all have done unit n - 1, whose stage the next one takes.
-        auto fetch_next = [&]() {
-            if (warp != 0 || !more) return;
-            alive = alive && (n == 0 || mbar_wait_short(&turned, (n + 1) & 1, &abort_flag, P.status));
+        // In the middle of a unit: the next one's angles (all warps have said that unit
+        // n's are there, so that unit n - 2's, whose place these take, are done with) and
+        // its rows, into the stage that unit n - 1's have left.
+        auto prepare = [&]() {
+            if (!more) return;
+            turn(next, n + 1, next_pos);
+            if (warp != 0) return;
+            if (n > 0)
+                alive = alive && mbar_wait_short(&emptied, (n - 1) & 1, &abort_flag, P.status);
             alive = __all_sync(0xffffffffu, alive);
             if (!alive) return;
             fetch(next, s ^ 1);
             ++fetched;
         };
+        // At its end.
+        auto leave = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&emptied);
+        };
         if (!alive || unit.id < 0 || unit.id >= P.pg.n_pages) {
             if (tid == 0 && alive) atomicOr(P.status, kErrPage);
-            fetch_next();
+            prepare();
+            leave();
             continue;
         }
         const uint8_t *keys = smem + s * kStoreStage, *values = keys + kKv4Group * kStoreRow;
@@ -350,9 +359,12 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
                 if (!(lane & 1)) *sdst = scales;
             }
         }
-        fetch_next();
+        prepare();
         const int t = warp;
-        if (t < t_lo || t >= t_hi) continue;
+        if (t < t_lo || t >= t_hi) {
+            leave();
+            continue;
+        }
         const int p = __shfl_sync(0xffffffffu, my_pos, t);
         float c[8], sn[8];
 #pragma unroll
@@ -364,24 +376,23 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
         if (!kAll && lane >= 2 * turning)
 #pragma unroll
             for (int i = 0; i < 8; ++i) c[i] = 1.f, sn[i] = 0.f;
+        const KeyTurn turn_of = kv4_key_turn(P.rope.rot_dim, p, lane);
+        const uint8_t *key = keys + t * kStoreRow;
         uint8_t *group = P.pg.k + group0;
 #pragma unroll 1
-        for (int h = 0; h < unit.heads; ++h, group += head_bytes) {
-            const KeyTurn turn = kv4_key_turn(
-                *reinterpret_cast<const uint4 *>(keys + t * kStoreRow + h * (kHeadDim * 2) +
-                                                 lane * 16),
-                P.rope.rot_dim, p, lane);
+        for (int h = 0; h < unit.heads; ++h, key += kHeadDim * 2, group += head_bytes) {
             float y[8];
-            kv4_rotate(turn, c, sn, y);
             uint32_t codes;
             unsigned byte;
+            kv4_rotate(turn_of, key, lane, c, sn, y);
             if (kAll && p != 0)
-                kv4_key_row<true>(turn, y, p, P.turns, codes, byte);
+                kv4_key_row<true>(turn_of, key, lane, y, p, P.turns, codes, byte);
             else
-                kv4_key_row<false>(turn, y, p, P.turns, codes, byte);
+                kv4_key_row<false>(turn_of, key, lane, y, p, P.turns, codes, byte);
             *reinterpret_cast<uint32_t *>(group + kv4_key_at(lane, t)) = codes;
             if (!(lane & 1)) group[kv4_key_scale_at(lane >> 1, t)] = static_cast<uint8_t>(byte);
         }
+        leave();
     }
     // copies that were waited for in vain must land before the CTA ends
     if (warp == 0 && *static_cast<volatile int *>(&abort_flag))

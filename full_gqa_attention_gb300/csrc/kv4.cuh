@@ -230,47 +230,53 @@ __device__ __forceinline__ void kv4_value_rows(const uint4 (&raw)[N], uint32_t (
         }
 }
 
-// Dims 8 lane .. of a key, as bf16, and of what they turn with: y = x cos + z sin
-// (z has its sign changed in the first of each pair).
+// How a lane's dims 8 lane .. of a key turn: y = x cos + z sin, where z are the dims
+// of the other end (with the sign changed in the first of each pair).
 struct KeyTurn {
-    uint4 own, other;
     int partner;               // the lane that has the others
     int k0;                    // the first pair
     bool turns;
+    uint32_t sign;
 };
 
-__device__ __forceinline__ KeyTurn kv4_key_turn(const uint4 &raw, int rot_dim, int pos, int lane) {
+__device__ __forceinline__ KeyTurn kv4_key_turn(int rot_dim, int pos, int lane) {
     KeyTurn t;
     const int half = rot_dim >> 4;  // lanes of each half
     const bool inside = lane < 2 * half, upper = lane >= half;
     t.turns = inside && pos != 0;
     t.partner = !inside ? lane : upper ? lane - half : lane + half;
     t.k0 = !inside ? 0 : (upper ? lane - half : lane) * 8;
-    const uint32_t sign = upper ? 0u : 0x80008000u;
-    t.own = raw;
-    t.other.x = __shfl_sync(0xffffffffu, raw.x, t.partner) ^ sign;
-    t.other.y = __shfl_sync(0xffffffffu, raw.y, t.partner) ^ sign;
-    t.other.z = __shfl_sync(0xffffffffu, raw.z, t.partner) ^ sign;
-    t.other.w = __shfl_sync(0xffffffffu, raw.w, t.partner) ^ sign;
+    t.sign = upper ? 0u : 0x80008000u;
     return t;
+}
+
+// The lane's dims of a row (512 bytes in shared memory), and the other end's.
+__device__ __forceinline__ uint4 kv4_own(const uint8_t *row, int lane) {
+    return *reinterpret_cast<const uint4 *>(row + lane * 16);
+}
+__device__ __forceinline__ uint4 kv4_other(const uint8_t *row, int partner, uint32_t sign) {
+    const uint4 z = *reinterpret_cast<const uint4 *>(row + partner * 16);
+    return make_uint4(z.x ^ sign, z.y ^ sign, z.z ^ sign, z.w ^ sign);
 }
 
 // The rotated values in 32 bits; c, s: cosines and sines of the lane's pairs, 1 and
 // 0 for dims that do not turn.
-__device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float (&c)[8],
-                                           const float (&s)[8], float (&y)[8]) {
+__device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const uint8_t *row, int lane,
+                                           const float (&c)[8], const float (&s)[8],
+                                           float (&y)[8]) {
     float z[8];
-    kv4_floats(t.own, y);
-    kv4_floats(t.other, z);
+    kv4_floats(kv4_own(row, lane), y);
+    kv4_floats(kv4_other(row, t.partner, t.sign), z);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __fmaf_rn(y[i], c[i], __fmul_rn(z[i], s[i]));
 }
 // ... from a table of all pairs.
-__device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const float2 *cs, float (&y)[8]) {
-    kv4_floats(t.own, y);
+__device__ __forceinline__ void kv4_rotate(const KeyTurn &t, const uint8_t *row, int lane,
+                                           const float2 *cs, float (&y)[8]) {
+    kv4_floats(kv4_own(row, lane), y);
     if (!t.turns) return;
     float z[8];
-    kv4_floats(t.other, z);
+    kv4_floats(kv4_other(row, t.partner, t.sign), z);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float2 c = cs[t.k0 + i];
@@ -345,19 +351,16 @@ __device__ __forceinline__ float2 kv4_exact_size(float x, float z, int pos,
 }
 
 // Settles the scale of the blocks in `open` (the same in a block's two lanes) from
-// the exact rotation.  turns: the lane's pairs' (kv4_exact_turn).  All lanes.
-// (Arguments by value: they stay in registers where it is not called.)
-__device__ __noinline__ inline unsigned kv4_settle_scale(uint4 own, uint4 other, int pos,
-                                                         const unsigned long long *turns,
-                                                         float4 y0, float4 y1, float least,
-                                                         bool open, unsigned byte) {
+// the exact rotation.  turns: the lane's pairs' (kv4_exact_turn); maybe: bit 4 i,
+// dims that can be the largest.  All lanes.
+__device__ __forceinline__ unsigned kv4_settle_scale(const uint4 &own, const uint4 &other, int pos,
+                                                     const unsigned long long *turns,
+                                                     unsigned maybe, bool open, unsigned byte) {
     float2 a = make_float2(0.f, 0.f);
     if (open)
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-            const float4 h = i < 4 ? y0 : y1;
-            const float y = i & 2 ? (i & 1 ? h.w : h.z) : (i & 1 ? h.y : h.x);
-            if (fabsf(y) < least) continue;  // it cannot be the largest
+            if (!(maybe >> (4 * i) & 1u)) continue;
             bool negative;
             const float2 v =
                 kv4_exact_size(kv4_pick(own, i), kv4_pick(other, i), pos, turns[i], negative);
@@ -377,9 +380,9 @@ __device__ __noinline__ inline unsigned kv4_settle_scale(uint4 own, uint4 other,
 }
 
 // Settles the codes of the dims in `open` (bit 4 i) from the exact rotation.
-__device__ __noinline__ inline uint32_t kv4_settle_codes(uint4 own, uint4 other, int pos,
-                                                         const unsigned long long *turns, float s,
-                                                         unsigned open, uint32_t codes) {
+__device__ __forceinline__ uint32_t kv4_settle_codes(const uint4 &own, const uint4 &other, int pos,
+                                                     const unsigned long long *turns, float s,
+                                                     unsigned open, uint32_t codes) {
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
         if (!(open >> (4 * i) & 1u)) continue;
@@ -409,39 +412,22 @@ __device__ __noinline__ inline uint32_t kv4_settle_codes(uint4 own, uint4 other,
 // each.  In all |y| is off by 2^-20.8 N at most; 2^-20.7 is allowed, and of a
 // quotient (7 at most, or it saturates) also 2^-22 of it.  Dims that do not turn
 // are bf16: kSnap.
-// kAll: every lane turns.
-template <bool kAll>
-__device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8], int pos,
-                                            const unsigned long long *turns, uint32_t &codes,
-                                            unsigned &byte) {
-    constexpr float kRel = 2.38418579e-7f, kAbs = 8.31e-7f;  // 2^-22, 2^(1/2 - 20.7)
-    float a = kv4_largest(y);
-    a = kv4_larger(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    const float a_other = __shfl_sync(0xffffffffu, a, t.partner);
-    const bool turns_here = kAll || t.turns;
-    const float e = fmaxf(a, a_other) * kAbs;
-    const float top = a * kSixth;
-    byte = kv4_scale_byte(turns_here ? top : kv4_snap(top));
-    // Does the maximum's error reach the border between this scale and a next one?
+constexpr float kKeyRel = 2.38418579e-7f, kKeyAbs = 8.31e-7f;  // 2^-22, 2^(1/2 - 20.7)
+
+// Does the error e of a block's maximum reach the border between its scale and a
+// next one?  top: a sixth of the maximum.
+__device__ __forceinline__ bool kv4_scale_open(float top, float e) {
     const float moved = top + (top < kKv4LeastNormal ? kKv4LeastNormal : 0.f);
     const float border = __uint_as_float((__float_as_uint(moved) & 0xfff00000u) | 0x80000u);
-    const bool open_scale =
-        turns_here && fabsf(moved - border) <= fmaf(e, kSixth, moved * kRel);
-    const bool odd = !(a < INFINITY);
-    bool finite = true;
-    if (__any_sync(0xffffffffu, odd || open_scale)) {
-        int bad = !kv4_finite(t.own) || !kv4_finite(t.other);
-        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-        finite = !bad;
-        int open = open_scale || odd;  // (a block's lanes may turn with different blocks)
-        open |= __shfl_xor_sync(0xffffffffu, open, 1);
-        byte = kv4_settle_scale(t.own, t.other, pos, turns + t.k0,
-                                make_float4(y[0], y[1], y[2], y[3]),
-                                make_float4(y[4], y[5], y[6], y[7]), a - 2.f * fmaf(a, kRel, e),
-                                turns_here && open && finite, byte);
-    }
-    const float s = kv4_scale(byte), r = kv4_reciprocal(s);
-    const float d = fmaf(e, r, 8.f * kRel);
+    return fabsf(moved - border) <= fmaf(e, kSixth, moved * kKeyRel);
+}
+
+// Codes of rotated values under scale s, and which of them (bit 4 i) the values'
+// error e leaves open.  kAll: every lane turns.
+template <bool kAll>
+__device__ __forceinline__ uint32_t kv4_key_codes(const float (&y)[8], float s, float e,
+                                                  bool turns_here, unsigned &open) {
+    const float r = kv4_reciprocal(s), d = fmaf(e, r, 8.f * kKeyRel);
     float lo[8], hi[8];
     if (kAll) {
 #pragma unroll
@@ -459,18 +445,62 @@ __device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const float (&y)[8
             hi[i] = __fadd_rn(__fmaf_rn(y[i], r, up), back);
         }
     }
-    codes = kv4_codes(hi);
+    const uint32_t codes = kv4_codes(hi);
     // (a sign that differs beside zero stands for the same value; quotients that are
     // known to a quarter only, of rotations that cancel, can be of either sign)
-    unsigned open = codes ^ kv4_codes(lo);
+    open = codes ^ kv4_codes(lo);
     open = (open | open >> 1 | open >> 2) & 0x11111111u;
     if (turns_here && d >= 0.25f) open = 0x11111111u;
-    if (!finite) {
-        codes = open = 0;
-        byte = kKv4NanScale;
+    return codes;
+}
+
+// Codes (x) and scale (y) of a row some block of which is open or not finite.
+// (Out of line, arguments by value: nothing of it is held where it is not called.)
+__device__ __noinline__ inline uint2 kv4_key_row_settled(KeyTurn t, const uint8_t *row, int lane,
+                                                         int pos, const unsigned long long *turns,
+                                                         float4 y0, float4 y1, float a, float e,
+                                                         bool turns_here, bool open_scale) {
+    const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+    const uint4 own = kv4_own(row, lane), other = kv4_other(row, t.partner, t.sign);
+    int bad = !kv4_finite(own) || !kv4_finite(other);
+    bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+    int settle = open_scale;  // (a block's lanes may turn with different blocks)
+    settle |= __shfl_xor_sync(0xffffffffu, settle, 1);
+    const float top = a * kSixth, least = a - 2.f * fmaf(a, kKeyRel, e);
+    unsigned byte = kv4_scale_byte(turns_here ? top : kv4_snap(top)), maybe = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) maybe |= fabsf(y[i]) < least ? 0u : 1u << (4 * i);
+    byte = kv4_settle_scale(own, other, pos, turns, maybe, turns_here && settle && !bad, byte);
+    const float s = kv4_scale(byte);
+    unsigned open;
+    uint32_t codes = kv4_key_codes<false>(y, s, e, turns_here, open);
+    if (bad) return make_uint2(0, kKv4NanScale);
+    return make_uint2(kv4_settle_codes(own, other, pos, turns, s, open, codes), byte);
+}
+
+// kAll: every lane turns.
+template <bool kAll>
+__device__ __forceinline__ void kv4_key_row(const KeyTurn &t, const uint8_t *row, int lane,
+                                            const float (&y)[8], int pos,
+                                            const unsigned long long *turns, uint32_t &codes,
+                                            unsigned &byte) {
+    const bool turns_here = kAll || t.turns;
+    float a = kv4_largest(y);
+    a = kv4_larger(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    const float a_other = __shfl_sync(0xffffffffu, a, t.partner);
+    const float e = fmaxf(a, a_other) * kKeyAbs, top = a * kSixth;
+    byte = kv4_scale_byte(turns_here ? top : kv4_snap(top));
+    unsigned open;
+    codes = kv4_key_codes<kAll>(y, kv4_scale(byte), e, turns_here, open);
+    const bool open_scale = (turns_here && kv4_scale_open(top, e)) || !(a < INFINITY);
+    if (__any_sync(0xffffffffu, open_scale || open)) {
+        const uint2 x = kv4_key_row_settled(t, row, lane, pos, turns + t.k0,
+                                            make_float4(y[0], y[1], y[2], y[3]),
+                                            make_float4(y[4], y[5], y[6], y[7]), a, e, turns_here,
+                                            open_scale);
+        codes = x.x;
+        byte = x.y;
     }
-    if (__any_sync(0xffffffffu, open != 0))
-        codes = kv4_settle_codes(t.own, t.other, pos, turns + t.k0, s, open, codes);
 }
 
 }  // namespace spark
