@@ -21,8 +21,14 @@
 // or dims.  A warp takes 16 slots' scores, and after a barrier a quarter of the
 // dims of all 64 slots' values: sums over all dims in every warp would take 64
 // registers a thread instead of 16, and with fewer warps on an SM the latency of
-// a tile's chain -- scores, maximum, exponentials, products -- shows (71 us
-// instead of 54 for 262,139 tokens).  So there is nothing to join over the warps either.
+// a tile's chain -- scores, maximum, exponentials, products -- shows (262,139
+// tokens of 4 KV heads 75 us instead of 67, with everything else as it then was).
+// So there is nothing to join over the warps either.
+//
+// 262,139 tokens of 4 KV heads take 60 us: 5.0 TB/s, 0.74 of a copy's rate.  A tile
+// takes an SM some 900 cycles -- 32 words a warp at 17 for their conversions,
+// scales and products, and the chain -- where HBM would need 784; 3 us go to the
+// start, 5 to the last tiles, the states and their joins.
 //
 // B has 8 columns.  Up to 4 heads' queries are a sum of two halves each (22
 // bits), in two columns; 8 heads' are one half each (11 bits).  Probabilities are
@@ -39,7 +45,10 @@ namespace spark {
 
 namespace {
 
-constexpr int kPairCost = 5;
+// What setting a pair up and finishing it costs, in tiles: 2 / 3 / 4 / 5 / 7 take
+// 27.2 / 27.8 / 28.0 / 28.2 / 29 us for 48 rows of 1 to 16,384 tokens, 29.8 / 29.6 /
+// 30.6 / 29.6 / 32 for 256 windows of 512.
+constexpr int kPairCost = 3;
 constexpr int kTile = 64;                                 // slots per stage
 constexpr int kWarps = 4;                                 // consumers
 constexpr int kThreads = (kWarps + 1) * 32;               // + one producer warp
@@ -47,11 +56,16 @@ constexpr int kTileBytes = kTile * kKv4TokenBytes;        // K or V
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kQBytes = 8 * kHeadDim * 2;                 // 8 columns
 constexpr int kRowBytes = kHeadDim * 2;
-constexpr int kPairs = 2;                                 // pairs handed over at a time
-constexpr int kFan = 4;                                   // partial states loaded at once
-constexpr int kSub = 16;                                  // ... joined in the first step
+// Pairs handed over at a time: with 2 the windows take 31 us, with 4 three CTAs no
+// longer fit an SM (42).
+constexpr int kPairs = 3;
+// Partial states loaded at once (2 or 8: 262,139 tokens 62.3 us instead of 60.6), and
+// joined in the first step (32: 20 rows of 8 query heads a KV head 23.5 instead of 21.6).
+constexpr int kFan = 4;
+constexpr int kSub = 16;
 constexpr int kProbBytes = 2 * kWarps * 32 * 8;           // two tiles' probabilities
-constexpr float kHeadroom = 4.f;                          // scores may pass the reference by this
+// Scores may pass the reference by this (by nothing: 2 to 5 % slower).
+constexpr float kHeadroom = 4.f;
 constexpr float kProbShift = 11.f;                        // probabilities are times 2^11
 constexpr float kProbScale = 2048.f;
 constexpr int kSumRow = kHeadDim;                         // floats
@@ -59,8 +73,8 @@ constexpr int kSumRow = kHeadDim;                         // floats
 // What goes by the query heads of a KV head.  With up to 4, three CTAs per SM of
 // three stages; 8 heads' states and joins take more registers, and two CTAs of
 // four stages are faster (20 rows of one KV head 25.9 -> 21.8 us, 500,000 tokens
-// 45.3 -> 41.9).  Shared memory: the stages, a pair's new token (queries, key,
-// value) twice, the queries' halves (after the tiles: 4 heads' sums), two tiles'
+// 45.3 -> 41.9).  Shared memory: the stages, the new tokens (queries, key, value) of
+// kPairs pairs, the queries' halves (after the tiles: 4 heads' sums), two tiles'
 // probabilities.
 template <bool kTwo>
 struct Shape {
