@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
     float2 *steps = angles + kAngleSets * kAngles;               // of 0 .. 15 positions
     __shared__ uint64_t full[2];     // a stage's rows are there
     __shared__ uint64_t turned;      // a unit's angles are
-    __shared__ uint64_t emptied;     // all warps have read a unit's rows
+    __shared__ uint64_t emptied[2];  // all warps have read a stage's rows
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int half = P.rope.rot_dim / 2;
@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
         mbar_init(&full[0], 1);
         mbar_init(&full[1], 1);
         mbar_init(&turned, kStoreThreads / 32);
-        mbar_init(&emptied, kStoreThreads / 32);
+        mbar_init(&emptied[0], kStoreThreads / 32);
+        mbar_init(&emptied[1], kStoreThreads / 32);
         fence_mbar_init();
         abort_flag = 0;
     }
@@ -293,16 +294,18 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
             turn(next, n + 1, next_pos);
             if (warp != 0) return;
             if (n > 0)
-                alive = alive && mbar_wait_short(&emptied, (n - 1) & 1, &abort_flag, P.status);
+                alive = alive && mbar_wait_short(&emptied[s ^ 1], (n - 1) >> 1 & 1, &abort_flag,
+                                                 P.status);
             alive = __all_sync(0xffffffffu, alive);
             if (!alive) return;
             fetch(next, s ^ 1);
             ++fetched;
         };
-        // At its end.
+        // At its end.  (A warp that says so of unit n + 2 has seen that all began unit
+        // n + 1: each phase counts every warp once.)
         auto leave = [&]() {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&emptied);
+            if (lane == 0) mbar_arrive(&emptied[s]);
         };
         if (!alive || unit.id < 0 || unit.id >= P.pg.n_pages) {
             if (tid == 0 && alive) atomicOr(P.status, kErrPage);

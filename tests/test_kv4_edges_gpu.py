@@ -64,6 +64,43 @@ def either_way(got, k, table, page, off):
         assert ((codes >> 3 == np.signbit(x)) | (codes & 7 == 0)).all()
 
 
+def cancel(x, c, s):
+    """Keys [n, heads, 2 half] whose first ends come out as next to nothing: x_lo c = x_hi s."""
+    half = x.shape[-1] // 2
+    lo, hi = x[..., :half], x[..., half:]
+    c, s = c[:, None], s[:, None]
+    steep = np.abs(c) > np.abs(s)
+    lo[:] = np.where(steep, hi * s / np.where(steep, c, 1), lo)
+    hi[:] = np.where(steep, hi, lo * c / np.where(steep, 1, s))
+
+
+def test_store_tokens_that_take_long(cuda):
+    """Many groups of tokens to an SM, in each some tokens that take many times as long as the
+    others (rotations that cancel): nobody overtakes them by more than there is room for."""
+    layer = layer_of("sliding")
+    n, H = 16 * 1100 + 5, 4
+    s = Store([n], [3], H=H, Hkv=H, page=128, seed=46)
+    s.pos = (torch.arange(n) % 2000).to(torch.int32)
+    slow = np.arange(n)[np.isin((np.arange(n) + 3) % 16, (2, 9))]
+    x = s.qkv.view(n, 3 * H, D)[slow, H:2 * H].double().numpy()
+    cancel(x, *turns(s.pos.numpy()[slow], layer))
+    s.qkv.view(n, 3 * H, D)[slow, H:2 * H] = torch.from_numpy(x).to(torch.bfloat16)
+    want = s.want(layer)
+    for _ in range(5):
+        got = s.run(layer)
+        assert kv4.same(got[0], want[0]) and kv4.same(got[1], want[1])
+
+
+def test_store_many_groups(cuda):
+    """The same without such tokens, on a layer that turns some dims, of several rows."""
+    s = Store([9000, 1, 5000, 3333], [3, 50, 0, 70], H=4, Hkv=4, page=64, seed=47)
+    layer = layer_of("full")
+    want = s.want(layer)
+    for _ in range(5):
+        got = s.run(layer)
+        assert kv4.same(got[0], want[0]) and kv4.same(got[1], want[1])
+
+
 def test_store_half_a_turn_alone(cuda):
     """Keys of which one end of each pair is zero, at angles from nothing to whole turns.  With
     the largest base cosines lie closer to 1 than 64 bits tell, beside values that lie on
