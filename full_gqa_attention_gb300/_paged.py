@@ -76,9 +76,12 @@ def _refuse(dev: int, t, dtype, name: str):
 def _check(dev: int, *wanted):
     """Each (tensor, dtype, name): contiguous, of that type, on that device."""
     for t, dtype, name in wanted:
-        if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev
-                or not t.is_contiguous()):
-            _refuse(dev, t, dtype, name)
+        try:
+            if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass  # not a tensor
+        _refuse(dev, t, dtype, name)
 
 
 @contextlib.contextmanager
