@@ -63,6 +63,18 @@ constexpr int kPairs = 3;
 // joined in the first step (32: 20 rows of 8 query heads a KV head 23.5 instead of 21.6).
 constexpr int kFan = 4;
 constexpr int kSub = 16;
+// The states left are counted in the workspace header's words behind the status
+// word, which every call leaves at 0, so that a workspace may serve any calls.
+// First step: a byte for two CTAs.  A CTA begins one group of two states or more at
+// most, and none inside another group: an even one's that ends in the next CTA
+// has 2 bits, the odd one's, or an even one's that is longer, the upper 5.  Second:
+// 5 bits (of 31 groups at most) for each kSub CTAs, of which one begins a pair of
+// more than kSub: the next such pair begins where it ends.
+constexpr int kMostCtas = 456;
+constexpr int kFirstWords = kMostCtas / 8;
+static_assert(kFirstWords + (kMostCtas / kSub + 6) / 6 <= kWorkspaceHeader / 4 - 1 &&
+                  kMostCtas / kSub + 1 <= 31 && kSub < 32,
+              "the counts fit the header");
 constexpr int kProbBytes = 2 * kWarps * 32 * 8;           // two tiles' probabilities
 // Scores may pass the reference by this (by nothing: 2 to 5 % slower).
 constexpr float kHeadroom = 4.f;
@@ -129,14 +141,23 @@ __device__ __forceinline__ uint32_t mul_scale(uint32_t a, uint32_t scales, int u
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Counts one up: what was written before is seen by who counts later.
-__device__ __forceinline__ unsigned atomic_count(unsigned *counter) {
+// A count of `bits` bits inside a word.
+struct Count {
+    unsigned *word;
+    int shift, bits;
+};
+
+// Counts one up, back to 0 from `all`, and whether that was it.  What was written
+// before is seen by who counts later.
+__device__ __forceinline__ bool count_last(const Count &c, unsigned all) {
     unsigned before;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
                  : "=r"(before)
-                 : "l"(counter)
+                 : "l"(c.word), "r"(1u << c.shift)
                  : "memory");
-    return before;
+    const bool last = (before >> c.shift & ((1u << c.bits) - 1u)) == all - 1;
+    if (last) atomicSub(c.word, all << c.shift);
+    return last;
 }
 
 __device__ __forceinline__ float nonfinite_part(float x) { return isfinite(x) ? 0.f : x; }
@@ -703,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
             const int me = static_cast<int>(blockIdx.x), second = pair.second;
             auto place = [&](int cta) { return 2 * cta + (cta == c0 ? second : 0); };
             // Leaves the state in that CTA's place; whether it was the last of `all`.
-            auto leave = [&](int cta, unsigned *counter, int all) {
+            auto leave = [&](int cta, const Count &count, int all) {
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
                     const int hq = warp + i * kWarps;
@@ -716,13 +737,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
                         reinterpret_cast<float2 *>(P.part_ml)[at] = make_float2(st[i].m, st[i].l);
                 }
                 consumer_bar();
-                if (tid == 0) {
-                    // behind the whole CTA's state, before the others' are read
-                    const bool is_last = atomic_count(counter) == static_cast<unsigned>(all - 1);
-                    // everyone has counted: back to 0 for the next call
-                    if (is_last) *counter = 0;
-                    last_cta = is_last;
-                }
+                // behind the whole CTA's state, before the others' are read
+                if (tid == 0) last_cta = count_last(count, all);
                 consumer_bar();
                 return last_cta != 0;
             };
@@ -779,13 +795,20 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
             const int sub = (me - c0) / kSub, subs = (c1 - c0) / kSub + 1;
             const int from = c0 + sub * kSub, to = from + kSub - 1 < c1 ? from + kSub - 1 : c1;
             int a = from, b = to, step = 1;
-            finish = leave(me, P.counters + place(from), to - from + 1);
+            const bool single = from == to;  // the state is at hand
+            const int byte = 8 * (from >> 1 & 3);
+            finish = single || leave(me,
+                                     (from & 1) || to - from > 1
+                                         ? Count{P.counters + (from >> 3), byte + 3, 5}
+                                         : Count{P.counters + (from >> 3), byte, 2},
+                                     to - from + 1);
 #pragma unroll 1
             while (finish) {
-                join(a, b, step);
+                if (!single || step != 1) join(a, b, step);
                 if (subs == 1 || step != 1) break;
-                // (c0 is the first CTA of one shared pair at most)
-                finish = leave(from, P.counters + 2 * gridDim.x + c0, subs);
+                const int at = c0 / kSub;
+                finish = leave(from, Count{P.counters + kFirstWords + at / 6, 5 * (at % 6), 5},
+                               subs);
                 a = c0;
                 b = c1;
                 step = kSub;
@@ -858,8 +881,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
 
 int decode_kv4_ctas(int sms, int G) {
     const int ctas = sms * (G <= 4 ? Shape<true>::kCtasPerSm : Shape<false>::kCtasPerSm);
-    constexpr int kMost = 32 * kSub;  // (the second step of a join takes one state a lane)
-    return ctas < kMost ? ctas : kMost;
+    return ctas < kMostCtas ? ctas : kMostCtas;
 }
 
 template <bool kTwo>

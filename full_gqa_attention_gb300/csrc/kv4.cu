@@ -585,20 +585,18 @@ void set_pages(Kv4Params &P, void *k4, void *v4, int n_pages, int page_size, con
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Workspace of a decode: the header; counters of states left (one per place, one
-// per CTA that is the first of a shared pair; every call leaves them at 0); two
-// partial states per CTA.
+// Workspace of a decode: the header (status word, counts of states left, which every
+// call leaves at 0); two partial states per CTA.
 struct DecodeKv4Plan {
     int grid;
-    size_t counters, ml, o, bytes;
+    size_t ml, o, bytes;
 };
 
 DecodeKv4Plan plan_decode_kv4(int H, int Hkv, int sms) {
     DecodeKv4Plan pl{};
     pl.grid = decode_kv4_ctas(sms, H / Hkv);
     const size_t parts = static_cast<size_t>(pl.grid) * 2 * (H / Hkv);
-    pl.counters = kWorkspaceHeader;
-    pl.ml = pl.counters + up256(static_cast<size_t>(pl.grid) * 3 * 4);
+    pl.ml = kWorkspaceHeader;
     pl.o = pl.ml + up256(parts * 2 * 4);
     pl.bytes = pl.o + up256(parts * kHeadDim * 4);
     return pl;
@@ -736,7 +734,7 @@ spark_status spark_attn_decode_kv4(const void *qkv, const float *gate, const int
     P.pos_end = max_pages << P.pg.page_shift;
     if (P.rope.rot_dim > 0 && P.pos_end > kRopePositions) P.pos_end = kRopePositions;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    P.counters = reinterpret_cast<unsigned *>(ws + pl.counters);
+    P.counters = P.status + 1;
     P.part_ml = reinterpret_cast<float *>(ws + pl.ml);
     P.part_o = reinterpret_cast<float *>(ws + pl.o);
     return done(launch_decode_kv4(P, pl.grid, static_cast<cudaStream_t>(stream)));

@@ -72,7 +72,7 @@ struct Kv4Params {
     unsigned *status;
     float *part_ml;            // decode: states of shared pairs, as PagedParams has them
     float *part_o;
-    unsigned *counters;
+    unsigned *counters;        // decode: the header's words behind the status word
     int N, S, H, Hkv, G;
     int kind, window, gate_mode;
     int pos_end;               // decode: positions end here

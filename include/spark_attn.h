@@ -633,7 +633,8 @@ spark_status spark_attn_kv4_load(const void *k4_pages, const void *v4_pages, int
 /*
  * One new token per row over a cache in 4 bits: what spark_attn_decode_paged
  * computes, with the same arguments (pos -1: an idle row) and its own workspace
- * size.  The new token's key and value are stored in 4 bits in slot pos[b].
+ * size (the counts in its first 256 bytes are left at 0 by every call).  The new
+ * token's key and value are stored in 4 bits in slot pos[b].
  * Nothing is rounded to bf16 but the output: cached keys and values are exact
  * halves, a query enters the products as a sum of two halves (H / Hkv of 8: as
  * one, 11 bits), a probability as one half.  A query that is not finite makes

@@ -274,6 +274,38 @@ def test_guards(cuda):
             assert fga.spark_attn_read_status(ws.t) == 0 and out.t.isfinite().all()
 
 
+@pytest.mark.parametrize("H,Hkv", [(4, 1), (8, 1), (6, 6)])
+def test_one_workspace_for_any_calls(cuda, H, Hkv):
+    """Scratch that other calls left, of other kinds or of this one with other heads: nothing of a
+    call is kept in it but counts at 0 in its header."""
+    pos = [9001, 40, 3000, 2 ** 13, 1500, 700, 64, 6000]
+    d = Decode(pos, H=H, Hkv=Hkv, page=128, seed=48 + H)
+    need = fga.spark_attn_decode_kv4_workspace_size(len(pos), H, Hkv, d.layer)
+    ws = fga.new_workspace(need)
+    args = d.device()
+    out = torch.full((len(pos), H * D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fga.spark_attn_decode_kv4(*args, d.layer, out=out, workspace=ws)
+    d.compare(out, args[3].clone(), args[4].clone())
+    first = out.clone()
+    for fill in (0xff, 0x7f, 0x01):
+        assert not ws[:256].any()
+        ws[256:] = fill
+        out.fill_(float("nan"))
+        fga.spark_attn_decode_kv4(*args, d.layer, out=out, workspace=ws)
+        assert torch.equal(out, first)
+    assert not ws[:256].any()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 7, 30, 31, 450, 460])
+def test_decode_shares_of_every_length(cuda, rows):
+    """Rows of which each takes some part of the CTAs: alone, in pairs, in groups of a few and of
+    more than are joined at once."""
+    rng = np.random.default_rng(rows)
+    n = 30000 // rows
+    pos = rng.integers(n // 2, n, rows).tolist()
+    Decode(pos, H=1, Hkv=1, page=256, seed=rows, unseen=False).check()
+
+
 def test_empty_calls(cuda):
     k4 = torch.zeros((1, 1, 16, 144), dtype=torch.uint8, device="cuda")
     wide = torch.full((1, 1, 16, D), 7.0, dtype=torch.bfloat16, device="cuda")
