@@ -416,7 +416,7 @@ struct LoadRow {
     int a, b;
 };
 
-__device__ __forceinline__ LoadRow load_row(const Kv4Params &P, int r, bool report) {
+__device__ __forceinline__ LoadRow load_row(const Kv4LoadParams &P, int r, bool report) {
     const int a = P.begin[r], b = P.end[r];
     if (a == b) return LoadRow{0, 0};
     const int from = P.pg.max_pages << P.pg.page_shift, to = P.to_max_pages << P.to_page_shift;
@@ -443,7 +443,7 @@ __device__ __forceinline__ uint4 kv4_to_bf16(uint32_t codes, unsigned byte) {
 // A warp takes 4 slots of a KV head's keys or values.  53,900 tokens of 4 KV heads:
 // 52 us, 5.4 TB/s, of which 4.2 are writes (a fill writes 4.0).  Six or eight CTAs
 // per SM instead of four, and shares by KV head, are no faster.
-__global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constant__ Kv4Params P) {
+__global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constant__ Kv4LoadParams P) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dep_wait();
     grid_dep_launch();
@@ -573,14 +573,16 @@ void set_layer(Kv4Params &P, const spark_layer_desc *desc, int H, int Hkv) {
     std::memcpy(P.turns, t.turns, sizeof(P.turns));
 }
 
-void set_pages(Kv4Params &P, void *k4, void *v4, int n_pages, int page_size, const int32_t *table,
-               int max_pages) {
-    P.pg.k = static_cast<uint8_t *>(k4);
-    P.pg.v = static_cast<uint8_t *>(v4);
-    P.pg.table = table;
-    P.pg.n_pages = n_pages;
-    P.pg.page_shift = page_shift_of(page_size);
-    P.pg.max_pages = max_pages;
+Kv4Pages pages_of(void *k4, void *v4, int n_pages, int page_size, const int32_t *table,
+                  int max_pages) {
+    Kv4Pages pg;
+    pg.k = static_cast<uint8_t *>(k4);
+    pg.v = static_cast<uint8_t *>(v4);
+    pg.table = table;
+    pg.n_pages = n_pages;
+    pg.page_shift = page_shift_of(page_size);
+    pg.max_pages = max_pages;
+    return pg;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -644,7 +646,7 @@ spark_status spark_attn_kv4_store(const void *qkv, const int32_t *pos, const int
     P.S = S;
     P.status = static_cast<unsigned *>(workspace);
     set_layer(P, desc, H, Hkv);
-    set_pages(P, k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
+    P.pg = pages_of(k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
     auto kernel = desc->rot_dim == kHeadDim ? kv4_store_kernel<true> : kv4_store_kernel<false>;
     st = done(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStoreSmem));
     if (st != SPARK_OK) return st;
@@ -675,14 +677,13 @@ spark_status spark_attn_kv4_load(const void *k4_pages, const void *v4_pages, int
     int sms;
     st = device_ready(&sms);
     if (st != SPARK_OK) return st;
-    Kv4Params P;
-    std::memset(&P, 0, sizeof(P));
+    Kv4LoadParams P{};
     P.begin = begin;
     P.end = end;
     P.S = S;
     P.Hkv = Hkv;
     P.status = static_cast<unsigned *>(workspace);
-    set_pages(P, const_cast<void *>(k4_pages), const_cast<void *>(v4_pages), n_pages, page_size,
+    P.pg = pages_of(const_cast<void *>(k4_pages), const_cast<void *>(v4_pages), n_pages, page_size,
               page_table, max_pages);
     P.k_pages = static_cast<__nv_bfloat16 *>(k_pages);
     P.v_pages = static_cast<__nv_bfloat16 *>(v_pages);
@@ -730,7 +731,7 @@ spark_status spark_attn_decode_kv4(const void *qkv, const float *gate, const int
     P.N = P.S = B;
     P.status = static_cast<unsigned *>(workspace);
     set_layer(P, desc, H, Hkv);
-    set_pages(P, k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
+    P.pg = pages_of(k4_pages, v4_pages, n_pages, page_size, page_table, max_pages);
     P.pos_end = max_pages << P.pg.page_shift;
     if (P.rope.rot_dim > 0 && P.pos_end > kRopePositions) P.pos_end = kRopePositions;
     uint8_t *ws = static_cast<uint8_t *>(workspace);

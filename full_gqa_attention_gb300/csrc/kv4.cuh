@@ -61,13 +61,8 @@ struct Kv4Params {
     const float *gate;         // [N, H] (decode)
     const int32_t *pos;        // [N] (decode: [S], -1 idle)
     const int32_t *cu;         // [S + 1] (store)
-    const int32_t *begin;      // [S]: first token (store: tokens in the pages; load)
-    const int32_t *end;        // [S]: behind the last one (load)
+    const int32_t *begin;      // [S]: tokens in the pages (store)
     Kv4Pages pg;
-    __nv_bfloat16 *k_pages;    // [n_pages, Hkv, page, 256]: where load writes to
-    __nv_bfloat16 *v_pages;
-    const int32_t *to_table;   // [S, to_max_pages]
-    int to_n_pages, to_page_shift, to_max_pages;
     __nv_bfloat16 *out;        // [S, H*256] (decode)
     unsigned *status;
     float *part_ml;            // decode: states of shared pairs, as PagedParams has them
@@ -78,6 +73,17 @@ struct Kv4Params {
     int pos_end;               // decode: positions end here
     RopeTable rope;
     unsigned long long turns[kMaxRopePairs];  // the frequencies, in 2^-64 turns per position
+};
+
+struct Kv4LoadParams {
+    const int32_t *begin, *end;  // [S]: first token, behind the last one
+    Kv4Pages pg;
+    __nv_bfloat16 *k_pages;    // [n_pages, Hkv, page, 256]
+    __nv_bfloat16 *v_pages;
+    const int32_t *to_table;   // [S, to_max_pages]
+    int to_n_pages, to_page_shift, to_max_pages;
+    unsigned *status;
+    int S, Hkv;
 };
 
 // ---------------------------------------------------------------- reading
