@@ -343,16 +343,22 @@ __device__ __forceinline__ float kv4_pick(const uint4 &raw, int i) {
     return i & 1 ? bf16_hi(w) : bf16_lo(w);
 }
 
-// |x cos + z sin| as the sum of two floats, and its sign.
+// |x cos + z sin| as the sum of two floats, and its sign.  Where finite numbers turn
+// into one past the largest, of which 32 bits have only the half, the first is infinity.
 __device__ __forceinline__ float2 kv4_exact_size(float x, float z, int pos,
                                                  unsigned long long turn, bool &negative) {
     const float4 t = kv4_exact_turn(pos, turn);
+    const bool large = fmaxf(fabsf(x), fabsf(z)) >= 0x1p126f;
+    x = large ? 0.5f * x : x;
+    z = large ? 0.5f * z : z;
     const float p = __fmul_rn(x, t.x), q = __fmul_rn(z, t.z);
     const float sum = __fadd_rn(p, q), back = __fadd_rn(sum, -p);
     float rest = __fadd_rn(__fadd_rn(p, -__fadd_rn(sum, -back)), __fadd_rn(q, -back));
     rest += __fmaf_rn(x, t.x, -p) + __fmaf_rn(z, t.z, -q) + __fmaf_rn(x, t.y, z * t.w);
-    const float hi = __fadd_rn(sum, rest), lo = __fadd_rn(rest, -__fadd_rn(hi, -sum));
+    float hi = __fadd_rn(sum, rest), lo = __fadd_rn(rest, -__fadd_rn(hi, -sum));
     negative = hi < 0.f;
+    hi = large ? 2.f * hi : hi;
+    lo = large ? 2.f * lo : lo;
     return negative ? make_float2(-hi, -lo) : make_float2(hi, lo);
 }
 
