@@ -476,8 +476,11 @@ __device__ __noinline__ inline uint2 kv4_key_row_settled(KeyTurn t, const uint8_
     const uint4 own = kv4_own(row, lane), other = kv4_other(row, t.partner, t.sign);
     int bad = !kv4_finite(own) || !kv4_finite(other);
     bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-    int settle = open_scale;  // (a block's lanes may turn with different blocks)
+    // A block's lanes may turn with different blocks: what the maximum may be off by, and
+    // whether that reaches a border, is the larger of what its lanes say.
+    int settle = open_scale;
     settle |= __shfl_xor_sync(0xffffffffu, settle, 1);
+    e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
     const float top = a * kSixth, least = a - 2.f * fmaf(a, kKeyRel, e);
     unsigned byte = kv4_scale_byte(turns_here ? top : kv4_snap(top)), maybe = 0;
 #pragma unroll

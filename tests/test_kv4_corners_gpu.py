@@ -1,5 +1,5 @@
 """Corners of a cache in 4 bits: keys whose rotation passes the largest 32-bit
-number."""
+number, and blocks of a key whose two halves turn with blocks of other sizes."""
 from __future__ import annotations
 
 import numpy as np
@@ -10,6 +10,10 @@ import kv4_ref as kv4
 from test_kv4_gpu import D, Decode, Store, layer_of
 
 pytestmark = pytest.mark.gpu
+
+
+def bf16(x):
+    return torch.as_tensor(np.asarray(x, dtype=np.float64)).to(torch.bfloat16).double().numpy()
 
 
 # ---------------------------------------------------------------- past 32 bits
@@ -42,4 +46,56 @@ def test_decode_rotation_past_32_bits(cuda):
     x = d.qkv.view(3, 8, D)
     x[:, :4] = 0
     x[:, 4:6] = huge((3, 2, D), 63)
+    d.check()
+
+
+# ---------------------------------------------------------------- halves of a block
+
+def crossed(n, seed):
+    """Positions and keys [n, 256] for 48 turned dims.  Of block 1, dims 16 to 31, the upper half
+    turns with block 0, whose values are about 1000, the lower half with block 2, of about 1.
+    Dim 25 comes out just below a border between two scales, as what two numbers of about 1000
+    leave, which 32 bits tell to some 2^-14; dim 16 just above it, to 2^-22."""
+    rng = np.random.default_rng(seed)
+    freq = 1e4 ** (-2.0 * np.arange(24) / 48)
+    borders = 3 * (kv4.SCALES[1:] + kv4.SCALES[:-1])
+    pos, keys = [402], [np.zeros(D)]
+    keys[0][[1, 25, 16, 40]] = 1032, -652, -0.00387573, -4.1875
+    while len(pos) < n:
+        p = int(rng.integers(1, 2000))
+        c, s = np.cos(p * freq[1]), np.sin(p * freq[1])
+        c2, s2 = np.cos(p * freq[16]), np.sin(p * freq[16])
+        if min(abs(s), abs(c), abs(s2), abs(c2)) < 0.25:
+            continue
+        x1 = bf16(rng.uniform(700, 1500, 4000))
+        x25 = bf16(-x1 * s / c + rng.uniform(-8, 8, 4000))
+        y25 = np.abs(x25 * c + x1 * s)
+        border = borders[np.searchsorted(borders, y25).clip(0, 225)]
+        near = np.nonzero((y25 < border) & (border - y25 < 1e-4) & (y25 > 0.5))[0]
+        if not len(near):
+            continue
+        i = near[0]
+        x40 = bf16(-border[i] / s2 * (1 + rng.uniform(-0.01, 0.01)))
+        x16 = bf16((border[i] * (1 + 4e-6) + x40 * s2) / c2)
+        if 0 < x16 * c2 - x40 * s2 - border[i] < 2e-5:
+            pos.append(p)
+            keys.append(np.zeros(D))
+            keys[-1][[1, 25, 16, 40]] = x1[i], x25[i], x16, x40
+    return np.array(pos, np.int32), np.array(keys)
+
+
+def test_store_scale_of_crossed_halves(cuda):
+    n = 200
+    pos, keys = crossed(n, 64)
+    s = Store([n], [0], H=1, Hkv=1, seed=64)
+    s.pos = torch.from_numpy(pos)
+    s.qkv.view(n, 3, D)[:, 1] = torch.from_numpy(keys).to(torch.bfloat16)
+    layer = layer_of("sliding", rot=48)
+    k = kv4.project(s.qkv, s.pos, 1, 1, layer)[1]
+    # (the border lies between the two of them)
+    assert (np.abs(k[:, 0, 16]) > np.abs(k[:, 0, 25])).all()
+    s.check(layer)
+    # of a step's new token, too
+    d = Decode(pos[:20].tolist(), H=1, Hkv=1, page=64, seed=65, layer=layer)
+    d.qkv.view(20, 3, D)[:, 1] = torch.from_numpy(keys[:20]).to(torch.bfloat16)
     d.check()
