@@ -368,10 +368,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
                 uint8_t *dst = stages + s * kStageBytes + which * kTileBytes +
                                (a & (kTile - 1)) * kKv4TokenBytes;
                 const int bytes = piece < pieces && a < b ? (b - a) * kKv4TokenBytes : 0;
-                if (bytes && id < 0) {  // a page that is not in the pool reads as zeros
-                    for (int i = 0; i < bytes; i += 16)
-                        *reinterpret_cast<uint4 *>(dst + i) = make_uint4(0, 0, 0, 0);
+                if (__any_sync(0xffffffffu, bytes && id < 0)) {
+                    // A page that is not in the pool reads as zeros: written once every lane
+                    // knows that the stage is free, and all before lane 0 tells that it is full.
+                    __syncwarp();
+                    if (id < 0)
+                        for (int i = 0; i < bytes; i += 16)
+                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();  // copies come here later
+                    __syncwarp();
                 }
                 const unsigned all =
                     __reduce_add_sync(0xffffffffu, id < 0 ? 0u : static_cast<unsigned>(bytes));

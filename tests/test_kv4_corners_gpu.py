@@ -1,11 +1,13 @@
 """Corners of a cache in 4 bits: keys whose rotation passes the largest 32-bit
-number, and blocks of a key whose two halves turn with blocks of other sizes."""
+number, blocks of a key whose two halves turn with blocks of other sizes, and
+pages that are not in the pool."""
 from __future__ import annotations
 
 import numpy as np
 import pytest
 import torch
 
+import full_gqa_attention_gb300 as fga
 import kv4_ref as kv4
 from test_kv4_gpu import D, Decode, Store, layer_of
 
@@ -99,3 +101,28 @@ def test_store_scale_of_crossed_halves(cuda):
     d = Decode(pos[:20].tolist(), H=1, Hkv=1, page=64, seed=65, layer=layer)
     d.qkv.view(20, 3, D)[:, 1] = torch.from_numpy(keys[:20]).to(torch.bfloat16)
     d.check()
+
+
+# ---------------------------------------------------------------- pages that are not there
+
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 1)])
+def test_decode_missing_pages_beside_nan(cuda, H, Hkv):
+    """Stages that held NaN before: missing pages of every place in a tile read as zeros."""
+    rng = np.random.default_rng(66 + H)
+    rows = 900
+    pos = [int(p) for p in rng.integers(70, 130, rows)]
+    d = Decode(pos, H=H, Hkv=Hkv, page=16, seed=66, unseen=False)
+    for r in range(rows):
+        if r % 2:     # some pages of every row that has one, never the new token's own
+            gone = rng.uniform(size=pos[r] // 16) < rng.choice([0.1, 0.5, 0.9])
+            d.table[r, :len(gone)][gone] = rng.choice([-1, 10 ** 6])
+        else:         # a row of NaN
+            for p in d.table[r, :pos[r] // 16 + 1]:
+                for pages in (d.k4, d.v4):
+                    pages[p].reshape(Hkv, -1, 2304)[..., 2048:] = 255
+    args = d.device()
+    ws = fga.new_workspace(fga.spark_attn_decode_kv4_workspace_size(rows, H, Hkv, d.layer))
+    out = torch.full((rows, H * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    fga.spark_attn_decode_kv4(*args, d.layer, out=out, workspace=ws)
+    assert fga.spark_attn_read_status(ws) == fga.SPARK_DEVERR_PAGE
+    d.compare(out, args[3], args[4])
