@@ -40,6 +40,7 @@
 // are off by 2^-36 of it.  Their sums are of the same ones in 32 bits.
 #include "decode_walk.cuh"
 #include "kv4.cuh"
+#include "kv4_counts.cuh"
 
 namespace spark {
 
@@ -59,22 +60,11 @@ constexpr int kRowBytes = kHeadDim * 2;
 // Pairs handed over at a time: with 2 the windows take 31 us, with 4 three CTAs no
 // longer fit an SM (42).
 constexpr int kPairs = 3;
-// Partial states loaded at once (2 or 8: 262,139 tokens 62.3 us instead of 60.6), and
-// joined in the first step (32: 20 rows of 8 query heads a KV head 23.5 instead of 21.6).
+// Partial states loaded at once (2 or 8: 262,139 tokens 62.3 us instead of 60.6).  In the
+// first step kSub are joined (kv4_counts.cuh; 32: 20 rows of 8 query heads a KV head 23.5
+// instead of 21.6).
 constexpr int kFan = 4;
-constexpr int kSub = 16;
-// The states left are counted in the workspace header's words behind the status
-// word, which every call leaves at 0, so that a workspace may serve any calls.
-// First step: a byte for two CTAs.  A CTA begins one group of two states or more at
-// most, and none inside another group: an even one's that ends in the next CTA
-// has 2 bits, the odd one's, or an even one's that is longer, the upper 5.  Second:
-// 5 bits (of 31 groups at most) for each kSub CTAs, of which one begins a pair of
-// more than kSub: the next such pair begins where it ends.
-constexpr int kMostCtas = 456;
-constexpr int kFirstWords = kMostCtas / 8;
-static_assert(kFirstWords + (kMostCtas / kSub + 6) / 6 <= kWorkspaceHeader / 4 - 1 &&
-                  kMostCtas / kSub + 1 <= 31 && kSub < 32,
-              "the counts fit the header");
+static_assert(kCountWords <= kWorkspaceHeader / 4 - 1, "the counts fit the header");
 constexpr int kProbBytes = 2 * kWarps * 32 * 8;           // two tiles' probabilities
 // Scores may pass the reference by this (by nothing: 2 to 5 % slower).
 constexpr float kHeadroom = 4.f;
@@ -141,23 +131,25 @@ __device__ __forceinline__ uint32_t mul_scale(uint32_t a, uint32_t scales, int u
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// A count of `bits` bits inside a word.
-struct Count {
-    unsigned *word;
-    int shift, bits;
-};
-
 // Counts one up, back to 0 from `all`, and whether that was it.  What was written
 // before is seen by who counts later.
-__device__ __forceinline__ bool count_last(const Count &c, unsigned all) {
+__device__ __forceinline__ bool count_last(unsigned *counters, const StateCount &c, unsigned all) {
     unsigned before;
     asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
                  : "=r"(before)
-                 : "l"(c.word), "r"(1u << c.shift)
+                 : "l"(counters + c.word), "r"(1u << c.shift)
                  : "memory");
     const bool last = (before >> c.shift & ((1u << c.bits) - 1u)) == all - 1;
-    if (last) atomicSub(c.word, all << c.shift);
+    if (last) atomicSub(counters + c.word, all << c.shift);
     return last;
+}
+
+// The CTAs that share a pair with units [first, first + units).
+__device__ __forceinline__ int first_cta(long long first, long long share) {
+    return static_cast<int>(quotient(first + kPairCost, share));
+}
+__device__ __forceinline__ int last_cta_of(long long first, long long units, long long share) {
+    return static_cast<int>(quotient(first + units - 1, share));
 }
 
 __device__ __forceinline__ float nonfinite_part(float x) { return isfinite(x) ? 0.f : x; }
@@ -300,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
                     bulk_load(dst + (P.G + 1) * kRowBytes,
                               src + static_cast<size_t>(P.H + P.Hkv + wk.g) * kHeadDim, kRowBytes,
                               &rows_full[s]);
-                    p.c0 = static_cast<int>(quotient(wk.first + kPairCost, share));
-                    p.c1 = static_cast<int>(quotient(wk.first + wk.row.units() - 1, share));
+                    p.c0 = first_cta(wk.first, share);
+                    p.c1 = last_cta_of(wk.first, wk.row.units(), share);
                     p.second = share * p.c0 < wk.first ? 1 : 0;
                 }
                 mbar_arrive(&pair_full[s]);
@@ -335,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
             if (lane == 0) mbar_arrive(&new_full[s]);
         };
         while (wk.load(P)) {
+            // (consumers that have left take no pair any more)
+            if (__shfl_sync(0xffffffffu, *static_cast<volatile int *>(&lost), 0)) break;
             hand_over(false);
             int early = kStages;  // tiles before the new token's turn comes
             const int32_t *row = P.pg.table + static_cast<size_t>(wk.b) * P.pg.max_pages;
@@ -398,6 +392,26 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
         if (lane == 0 && abort_flag)
             for (int i = n_pairs - 1 > kPairs ? n_pairs - 1 - kPairs : 0; i < n_pairs - 1; ++i)
                 mbar_wait_plain_short(&rows_full[i % kPairs], (i / kPairs) & 1);
+        // Pairs that the consumers have not come to are counted all the same, so that the
+        // counts are 0 again; what is joined of them is invalid, as the status word says.
+        if (lane == 0 && lost) {
+            Walk rest{};
+            rest.u = share * blockIdx.x;
+            rest.end = wk.end;
+            rest.b = s_row;
+            rest.base = s_base;
+            rest.row = row_of(P, rest.b);
+            for (int n = 1; rest.load(P); ++n) {
+                if (n < lost) continue;
+                const int c0 = first_cta(rest.first, share);
+                const StateGroup g = kv4_group(c0, last_cta_of(rest.first, rest.row.units(), share),
+                                               static_cast<int>(blockIdx.x));
+                if ((g.from == g.to || count_last(P.counters, kv4_first_count(g.from, g.to),
+                                                  g.to - g.from + 1)) &&
+                    g.groups > 1)
+                    count_last(P.counters, kv4_second_count(c0), g.groups);
+            }
+        }
         return;
     }
 
@@ -416,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
         if (!mbar_wait_plain_short(&pair_full[n % kPairs], (n / kPairs) & 1)) {
             atomicOr(P.status, kErrTimeout);
             abort_flag = 1;
-            lost = 1;
+            lost = n + 1;
         }
         consumer_bar();
     };
@@ -729,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
             const int me = static_cast<int>(blockIdx.x), second = pair.second;
             auto place = [&](int cta) { return 2 * cta + (cta == c0 ? second : 0); };
             // Leaves the state in that CTA's place; whether it was the last of `all`.
-            auto leave = [&](int cta, const Count &count, int all) {
+            auto leave = [&](int cta, const StateCount &count, int all) {
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
                     const int hq = warp + i * kWarps;
@@ -743,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
                 }
                 consumer_bar();
                 // behind the whole CTA's state, before the others' are read
-                if (tid == 0) last_cta = count_last(count, all);
+                if (tid == 0) last_cta = count_last(P.counters, count, all);
                 consumer_bar();
                 return last_cta != 0;
             };
@@ -797,23 +811,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
                         }
                 }
             };
-            const int sub = (me - c0) / kSub, subs = (c1 - c0) / kSub + 1;
-            const int from = c0 + sub * kSub, to = from + kSub - 1 < c1 ? from + kSub - 1 : c1;
+            const StateGroup group = kv4_group(c0, c1, me);
+            const int from = group.from, to = group.to, subs = group.groups;
             int a = from, b = to, step = 1;
             const bool single = from == to;  // the state is at hand
-            const int byte = 8 * (from >> 1 & 3);
-            finish = single || leave(me,
-                                     (from & 1) || to - from > 1
-                                         ? Count{P.counters + (from >> 3), byte + 3, 5}
-                                         : Count{P.counters + (from >> 3), byte, 2},
-                                     to - from + 1);
+            finish = single || leave(me, kv4_first_count(from, to), to - from + 1);
 #pragma unroll 1
             while (finish) {
                 if (!single || step != 1) join(a, b, step);
                 if (subs == 1 || step != 1) break;
-                const int at = c0 / kSub;
-                finish = leave(from, Count{P.counters + kFirstWords + at / 6, 5 * (at % 6), 5},
-                               subs);
+                finish = leave(from, kv4_second_count(c0), subs);
                 a = c0;
                 b = c1;
                 step = kSub;
