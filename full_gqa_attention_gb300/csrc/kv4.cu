@@ -117,6 +117,16 @@ __device__ __forceinline__ StoreRow store_row(const Kv4Params &P, int r, bool re
     return StoreRow{start, start + (c1 - c0), c0};
 }
 
+// Four words and one that other threads may be writing.
+__device__ __forceinline__ void load_relaxed(const uint32_t *four, const uint32_t *one,
+                                             uint32_t (&x)[5]) {
+    asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%5];\n\t"
+                 "ld.relaxed.gpu.global.b32 %4, [%6];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4])
+                 : "l"(four), "l"(one)
+                 : "memory");
+}
+
 // Cosines and sines of a token, as the lanes read them: pairs 8 l + 2 i and the
 // next one are the 16 bytes i of lane l.
 __device__ __forceinline__ int angle_at(int k) {
@@ -354,19 +364,22 @@ __global__ void __launch_bounds__(kStoreThreads, 1)
                     w[i] = __byte_perm(lo, hi, 0x5410);
                 }
                 uint8_t *group = P.pg.v + group0 + h * head_bytes;
-                uint4 *dst = reinterpret_cast<uint4 *>(group + kv4_value_at(lane, quad));
+                uint32_t *dst = reinterpret_cast<uint32_t *>(group + kv4_value_at(lane, quad));
                 uint32_t *sdst =
                     reinterpret_cast<uint32_t *>(group + kv4_value_scale_at(lane >> 1, quad));
-                if (mask) {  // slots beside the call's keep what they hold
-                    const uint4 old = *dst;
-                    w[0] = (w[0] & ~mask) | (old.x & mask);
-                    w[1] = (w[1] & ~mask) | (old.y & mask);
-                    w[2] = (w[2] & ~mask) | (old.z & mask);
-                    w[3] = (w[3] & ~mask) | (old.w & mask);
-                    scales = (scales & ~keep) | (*sdst & keep);
+                if (!mask) {
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (!(lane & 1)) *sdst = scales;
+                } else {
+                    // Slots beside the call's keep what they hold, and other sequences of the
+                    // call may be writing there (a row stored as several chunks): only the bits
+                    // of this one's slots, which nobody else changes, are turned over.
+                    uint32_t old[5];
+                    load_relaxed(dst, sdst, old);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) atomicXor(dst + i, (old[i] ^ w[i]) & ~mask);
+                    if (!(lane & 1)) atomicXor(sdst, (old[4] ^ scales) & ~keep);
                 }
-                *dst = make_uint4(w[0], w[1], w[2], w[3]);
-                if (!(lane & 1)) *sdst = scales;
             }
         }
         prepare();

@@ -591,7 +591,9 @@ spark_status spark_attn_pages_compact(const spark_page_pool *pool, int32_t *live
  *         (the query heads are not read)
  *   workspace  >= the size query's bytes, 256-byte aligned, zeroed once before
  *         first use: its status word
- * Slots beside the call's keep what they hold.  A sequence with offsets that
+ * Slots beside the call's keep what they hold.  Sequences of a call may write
+ * into the same page (one row stored as several chunks, with a table row
+ * each), but not the same slot.  A sequence with offsets that
  * decrease or leave [0, n_tokens] is skipped and SPARK_DEVERR_SEQLENS set; one
  * with start < 0 or start + length > max_pages * page_size is skipped and
  * SPARK_DEVERR_POSITION set; tokens whose page is not in the pool are not

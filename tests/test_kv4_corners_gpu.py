@@ -1,6 +1,6 @@
 """Corners of a cache in 4 bits: keys whose rotation passes the largest 32-bit
-number, blocks of a key whose two halves turn with blocks of other sizes, and
-pages that are not in the pool."""
+number, blocks of a key whose two halves turn with blocks of other sizes, pages
+that are not in the pool, and a row stored as several sequences of a call."""
 from __future__ import annotations
 
 import numpy as np
@@ -126,3 +126,28 @@ def test_decode_missing_pages_beside_nan(cuda, H, Hkv):
     fga.spark_attn_decode_kv4(*args, d.layer, out=out, workspace=ws)
     assert fga.spark_attn_read_status(ws) == fga.SPARK_DEVERR_PAGE
     d.compare(out, args[3], args[4])
+
+
+# ---------------------------------------------------------------- one row in chunks
+
+@pytest.mark.parametrize("page", [16, 256])
+@pytest.mark.parametrize("order", ["forward", "any"])
+def test_store_one_row_as_chunks(cuda, page, order):
+    """Neighbouring slots, which share bytes of values, written by sequences of one call that run
+    on different SMs: as one sequence."""
+    rng = np.random.default_rng(67)
+    new = rng.integers(1, 8, 600)
+    old = np.cumsum(new) - new
+    if order == "any":
+        p = rng.permutation(600)
+        new, old = new[p], old[p]
+    s = Store([int(new.sum())], [0], H=2, Hkv=2, page=page, seed=67)
+    s.new, s.old = new.tolist(), old.tolist()
+    s.cu = [0] + np.cumsum(new).tolist()
+    s.pos = torch.cat([torch.arange(b, b + a) for a, b in zip(s.new, s.old)]).to(torch.int32)
+    s.table = np.repeat(s.table, 600, axis=0)
+    layer = layer_of("full")
+    want = s.want(layer)
+    for _ in range(20):
+        got = s.run(layer)
+        assert kv4.same(got[0], want[0]) and kv4.same(got[1], want[1])
