@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
             const int slot0 = wk.row.slot0();
             const int lo = wk.row.lo & ~15, hi = (wk.row.pos + 15) & ~15;  // groups seen
             int ids = 0;
+            bool gaps = false;  // some page number is not in the pool
             for (int t = wk.t0; ok && t < wk.t1; ++t) {
                 if (early-- == 0) quantise_new();
                 // page numbers of the next 32 pieces, one per lane; -1: none
@@ -342,13 +343,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
                 if (in == 0) {
                     const int slot = slot0 + t * kTile + lane * piece_slots;
                     ids = -1;
+                    gaps = false;
                     if (slot < hi && slot + piece_slots > lo && slot < slot0 + wk.t1 * kTile) {
                         ids = row[slot >> P.pg.page_shift];
                         if (ids < 0 || ids >= P.pg.n_pages) {
                             atomicOr(P.status, kErrPage);
                             ids = -1;
+                            gaps = true;
                         }
                     }
+                    gaps = __any_sync(0xffffffffu, gaps);
                 }
                 const int s = it % kStages;
                 if (it >= kStages && lane == 0)
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTwo>::kCtasPerSm)
                 uint8_t *dst = stages + s * kStageBytes + which * kTileBytes +
                                (a & (kTile - 1)) * kKv4TokenBytes;
                 const int bytes = piece < pieces && a < b ? (b - a) * kKv4TokenBytes : 0;
-                if (__any_sync(0xffffffffu, bytes && id < 0)) {
+                if (gaps) {
                     // A page that is not in the pool reads as zeros: written once every lane
                     // knows that the stage is free, and all before lane 0 tells that it is full.
                     __syncwarp();
