@@ -303,8 +303,10 @@ __device__ __forceinline__ float2 kv4_two_floats(long long a) {
 }
 
 // Cosine (x, y) and sine (z, w) of position `pos`'s turn, each as the sum of two
-// floats, to 2^-48: `turn` is a position's in units of 2^-64 turns, so that a
-// product of 64 bits leaves the part behind whole turns.  By the series, to the
+// floats, to 2^-48 for the given `turn`: a position's in units of 2^-64 turns, so
+// that a product of 64 bits leaves the part behind whole turns.  (The turn itself is
+// the host's 64-bit float: the real number's at position p is p 2^-54 turns off at
+// most, 2^-36 at 262,144.  That float is what "exact" means.)  By the series, to the
 // 17th power of an angle of an eighth of a turn at most, in whole numbers: 64-bit
 // floats are some twenty times slower on this chip.
 __device__ __noinline__ inline float4 kv4_exact_turn(int pos, unsigned long long turn) {

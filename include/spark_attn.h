@@ -554,7 +554,8 @@ spark_status spark_attn_pages_compact(const spark_page_pool *pool, int32_t *live
  *         negatives (codes 0 .. 7, a set upper bit being the sign; larger
  *         quotients become 6 or -6; 0 where s is 0).
  * Both round to nearest, ties to the even code, and what is stored is the
- * nearest to the exact key or value: a key is not rounded after its rotation.
+ * nearest to the exact key or value: a key is not rounded after its rotation
+ * (by p times theta^(-2k/r) / (2 pi) turns, taken in a 64-bit float).
  * So values hold to about a tenth of their size, those below 2^-18 * 6 in all
  * of a block become zeros, and those beyond 61440 become 61440.  A block with a
  * value that is not finite is stored with the scale's byte 0xff and reads as
@@ -581,6 +582,10 @@ spark_status spark_attn_pages_compact(const spark_page_pool *pool, int32_t *live
  * prompt behind cached tokens: read them back (spark_attn_kv4_load) into pages
  * of bf16, call spark_attn_prefill_paged there, and store the new tokens
  * (spark_attn_kv4_store); a first prompt: spark_attn_prefill_packed and store.
+ *
+ * Store and decode take a layer's frequencies from what the calling thread
+ * keeps of the last four kinds of layers (rope_theta, rot_dim); a model that
+ * goes through more in turn pays up to 128 powers on the host per call.
  */
 
 /*
@@ -639,8 +644,8 @@ spark_status spark_attn_kv4_load(const void *k4_pages, const void *v4_pages, int
  * token's key and value are stored in 4 bits in slot pos[b].
  * Nothing is rounded to bf16 but the output: cached keys and values are exact
  * halves, a query enters the products as a sum of two halves (H / Hkv of 8: as
- * one, 11 bits), a probability as one half.  A query that is not finite makes
- * its head's output NaN.
+ * one, 11 bits), a probability as one half.  A query that is not finite, or
+ * whose rotation passes the largest 32-bit number, makes its head's output NaN.
  */
 size_t spark_attn_decode_kv4_workspace_size(int B, int H, int Hkv, const spark_layer_desc *desc);
 
